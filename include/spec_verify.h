@@ -61,13 +61,17 @@ typedef enum {
   SPEC_ETIMEOUT = 4       /* a bounded device-side wait ran out (error word) */
 } spec_status;
 
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
+/* SPEC_F16 and SPEC_E4M3 are types of spec_append_tokens and spec_decode_attn. */
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2, SPEC_E4M3 = 3 } spec_dtype;
 
 /* status_per_seq bits (OR-ed). */
 #define SPEC_SEQ_QZERO 1       /* a proposed token had q(x) == 0; it was accepted iff p(x) > 0 */
 #define SPEC_SEQ_NONFINITE 2   /* a target logit was NaN or +inf; that sequence's outputs are -1 */
 #define SPEC_SEQ_RESID_ZERO 4  /* residual mass was 0 after a rejection; the draw used p */
 #define SPEC_SEQ_BAD_TREE 8    /* parent array is not a tree in storage order */
+#define SPEC_SEQ_BAD_LEN 16    /* a length is negative or past the table or the token rows */
+#define SPEC_SEQ_NO_PAGES 32   /* the free list had no page left (or no room) for the sequence */
+#define SPEC_SEQ_BAD_PAGE 64   /* a page id the sequence needs is not in [0, num_pages) */
 
 /* Error words written to a workspace by a bounded wait that ran out. */
 #define SPEC_ERR_MBAR_TIMEOUT 0x100
@@ -428,6 +432,148 @@ spec_status spec_logits_penalize(float* logits, int B, int R, int V, const int32
                                  int H, const int32_t* block_tokens, const int32_t* parent,
                                  float penalty, const int32_t* banned, int n_banned,
                                  void* stream);
+
+/* ------------------------------------------------------------------------
+ * spec_extend_tables -- pages, block tables and slots for a step's new tokens,
+ * from the requests' lengths alone (nothing is read back to the host, so a
+ * captured step can run it).  It stands in front of spec_append_block /
+ * spec_append_tokens and the attention calls, which read what it writes.
+ *
+ *   ctx_len  [B] int32: tokens already stored per sequence; its first
+ *            ceil(ctx_len / page_size) block-table entries hold their pages.
+ *   add_len  [B] int32: new tokens of this step (0 allowed).
+ *   block_table [B,max_pages] int32, updated: entries ceil(ctx_len / P) ..
+ *            ceil((ctx_len + add_len) / P) - 1 get pages; the others stay.
+ *   free_list [num_pages] int32, free_count [1] int32: the pool's free pages
+ *            are entries 0 .. free_count - 1; the k-th page of the step (in
+ *            sequence order) is entry free_count - 1 - k.  Only read.
+ *   The step's tokens are packed in sequence order: sequence b's are rows
+ *   cu_len[b] .. cu_len[b + 1] - 1 of max_tokens rows.
+ *   slot_map [max_tokens] int64 out: page * page_size + offset of each token;
+ *            -1 for tokens of a refused sequence and rows behind the last.
+ *   positions [max_tokens] int32 out: ctx_len[b] + its place; -1 with slot -1.
+ *   cu_len   [B+1] int32 out (saturates at 2^31 - 1).
+ *   new_len  [B] int32 out: ctx_len + add_len; ctx_len if refused.
+ *   free_left [1] int32 out: pages left on the list; not the same memory as
+ *            free_count (the next call takes it as its free_count).
+ *   status_per_seq [B] int32 out: 0, or why the sequence was refused (all of
+ *            its tokens or none): SPEC_SEQ_BAD_LEN (a negative length, more
+ *            pages than max_pages, rows past max_tokens; it takes no page),
+ *            SPEC_SEQ_NO_PAGES (the pages needed by the sequences up to and
+ *            including this one exceed free_count; sequences that need no page
+ *            are never refused for it, every later one that needs some is).
+ *            SPEC_SEQ_BAD_PAGE: a table or free-list entry the new tokens fall
+ *            on is not a page id; those tokens' slots are -1, new_len is
+ *            ctx_len, and the pages taken stay in the table row.
+ *   B <= 8192; max_pages * page_size and max_tokens below 2^31.
+ * ---------------------------------------------------------------------- */
+spec_status spec_extend_tables(const int32_t* ctx_len, const int32_t* add_len, int B,
+                               int page_size, int32_t* block_table, int max_pages,
+                               const int32_t* free_list, int num_pages,
+                               const int32_t* free_count, int max_tokens, int64_t* slot_map,
+                               int32_t* positions, int32_t* cu_len, int32_t* new_len,
+                               int32_t* free_left, int32_t* status_per_seq, void* stream);
+
+/* ------------------------------------------------------------------------
+ * spec_release_pages -- the pages behind each sequence's kept ones go back on
+ * the free list: after spec_kv_commit, with its keep_pages ("later slots the
+ * block wrote may be released"), and keep_pages = 0 for a finished request.
+ *
+ *   len      [B] int32: tokens the table row was extended for (new_len of
+ *            spec_extend_tables): entries 0 .. ceil(len / page_size) - 1 are
+ *            held.  keep_pages [B] int32: entries that stay.
+ *   free_list, free_count: entries keep .. held - 1 of every sequence, in
+ *            sequence order, are written to free_list[free_count ..]; the
+ *            block table is not changed.
+ *   free_total [1] int32 out: the new count; not the same memory as free_count.
+ *   status_per_seq [B] int32 out (nullable): SPEC_SEQ_BAD_LEN (len < 0,
+ *            keep outside 0 .. held, held > max_pages: nothing released),
+ *            SPEC_SEQ_NO_PAGES (the list would exceed num_pages entries: the
+ *            sequence and every later one with pages to give release nothing),
+ *            SPEC_SEQ_BAD_PAGE (an entry is not a page id: -1 goes on the list
+ *            in its place, which spec_extend_tables reports when it draws it).
+ *   B <= 8192.
+ * ---------------------------------------------------------------------- */
+spec_status spec_release_pages(const int32_t* block_table, int max_pages, const int32_t* len,
+                               const int32_t* keep_pages, int B, int page_size,
+                               int32_t* free_list, int num_pages, const int32_t* free_count,
+                               int32_t* free_total, int32_t* status_per_seq, void* stream);
+
+/* ------------------------------------------------------------------------
+ * spec_append_tokens -- spec_append_block for packed tokens: T rows of any
+ * sequences (prompts, single draft tokens) stored at their slots, keys rotated
+ * for their positions, in a 16-bit, fp32 or e4m3 cache.
+ *
+ *   k_new, v_new rows of Hkv*D new_dtype elements, k_stride / v_stride elements
+ *            apart (slices of a fused projection are taken as they are).
+ *   q, q_out rows of Hq*D (nullable, both): q rotated into q_out; the same
+ *            memory with the same stride rotates in place.
+ *   slot_map [T] int64 (spec_extend_tables): row t goes to offset slot % P of
+ *            page slot / P.  Rows whose slot is outside 0 .. num_pages * P - 1
+ *            are skipped whole (their q_out row stays as it was).  Slots are
+ *            distinct; of rows with the same slot an unspecified mix is stored.
+ *   positions [T] int32 (may be NULL when rope_base is 0): the rotation's
+ *            positions; a row with a negative one is skipped.
+ *   k_cache, v_cache: element (page, token, head, d) is at page * page_stride +
+ *            token * token_stride + head * head_stride + d (elements), the same
+ *            for both.  cache_dtype is new_dtype, or SPEC_E4M3 with 16-bit rows:
+ *            then x / scale is stored, rounded to nearest even and limited to
+ *            +-448 (a NaN stays NaN).
+ *   k_scale, v_scale [Hkv] fp32, > 0 (NULL: 1; only with SPEC_E4M3): what a
+ *            stored 1.0 stands for.
+ *   rope_base 0: no rotation, else > 1: as in spec_append_block (split-half
+ *            form; angles in 64 bits, rotation in fp32, one rounding).
+ *   D in {64,128,256}.  Rows, strides and caches are 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+spec_status spec_append_tokens(const void* k_new, int64_t k_stride, const void* v_new,
+                               int64_t v_stride, const void* q, int64_t q_stride, void* q_out,
+                               int64_t q_out_stride, spec_dtype new_dtype, void* k_cache,
+                               void* v_cache, spec_dtype cache_dtype, const float* k_scale,
+                               const float* v_scale, int num_pages, int page_size,
+                               int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                               const int64_t* slot_map, const int32_t* positions, int T, int Hq,
+                               int Hkv, int D, double rope_base, void* stream);
+
+/* ------------------------------------------------------------------------
+ * spec_decode_attn -- attention of one new token per sequence over the paged
+ * cache: a drafter's own step between verify passes, or plain decoding.  It
+ * takes what spec_verify_attn does not: 16-bit and e4m3 caches, D of 64, 128
+ * and 256, any page size, a sliding window, strided caches and queries, idle
+ * rows in the batch.
+ *
+ *   q        [B,Hq,D] q_dtype (bf16 or fp16); element (b,h,d) at b * q_stride_b
+ *            + h * q_stride_h + d.
+ *   k_cache, v_cache cache_dtype (q's type, or SPEC_E4M3 with k_scale / v_scale
+ *            as in spec_append_tokens), strides as there; page_stride is a
+ *            multiple of token_stride.
+ *   block_table [B,max_pages] int32; seq_len [B] int32: stored tokens, the new
+ *            one included (append it first).  The token sees positions
+ *            max(0, seq_len - window) .. seq_len - 1 (window 0: all of them).
+ *            Positions past the table or whose page id is not in
+ *            [0, num_pages) are not seen.  Nothing behind seq_len is read as a
+ *            number: unwritten slots may hold anything.
+ *   scale    softmax scale; <= 0 selects 1/sqrt(D).
+ *   out      [B,Hq,D] q_dtype; lse_out [B,Hq] fp32 natural log (nullable).  A
+ *            sequence that sees nothing (seq_len <= 0) has zeros and -inf.
+ *   workspace >= spec_decode_attn_workspace_size(...) bytes, 256-byte aligned,
+ *            used for spec_decode_attn only; one workspace serves calls of any
+ *            shape whose own size fits in it.
+ *
+ * The result of a sequence does not depend on atomics' order; it may depend on
+ * the rest of the batch (by where the cache is split) within rounding.
+ * B * Hkv * ceil(Hq / Hkv / 16) <= 65536 (/ 8 instead of / 16 for D = 256).
+ * ---------------------------------------------------------------------- */
+size_t spec_decode_attn_workspace_size(int B, int Hq, int Hkv, int D);
+
+spec_status spec_decode_attn(const void* q, int64_t q_stride_b, int64_t q_stride_h,
+                             spec_dtype q_dtype, const void* k_cache, const void* v_cache,
+                             spec_dtype cache_dtype, const float* k_scale, const float* v_scale,
+                             int num_pages, int page_size, int64_t page_stride,
+                             int64_t token_stride, int64_t head_stride,
+                             const int32_t* block_table, int max_pages, const int32_t* seq_len,
+                             int B, int Hq, int Hkv, int D, int window, float scale,
+                             void* workspace, size_t workspace_bytes, void* out, float* lse_out,
+                             void* stream);
 
 #ifdef __cplusplus
 }

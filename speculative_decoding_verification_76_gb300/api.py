@@ -18,8 +18,9 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libspecverify.so")
 
 SPEC_OK, SPEC_EINVAL, SPEC_EUNSUPPORTED, SPEC_ECUDA, SPEC_ETIMEOUT = range(5)
-SPEC_F32, SPEC_BF16 = 0, 1
+SPEC_F32, SPEC_BF16, SPEC_F16, SPEC_E4M3 = 0, 1, 2, 3
 SEQ_QZERO, SEQ_NONFINITE, SEQ_RESID_ZERO, SEQ_BAD_TREE = 1, 2, 4, 8
+SEQ_BAD_LEN, SEQ_NO_PAGES, SEQ_BAD_PAGE = 16, 32, 64
 
 # every symbol include/spec_verify.h declares
 EXPORTS = (
@@ -30,6 +31,8 @@ EXPORTS = (
     "spec_accept_sample", "spec_accept_sample_tree", "spec_workspace_error",
     "spec_kv_commit", "spec_verify_attn_noalloc", "spec_verify_attn_noalloc_error",
     "spec_append_block", "spec_logits_penalize", "spec_debug_attn_fault",
+    "spec_extend_tables", "spec_release_pages", "spec_append_tokens",
+    "spec_decode_attn_workspace_size", "spec_decode_attn",
 )
 
 
@@ -58,9 +61,14 @@ class SamplerConfig:
                         1 if self.greedy else 0, int(self.eos_id))
 
 
+# the current stream's handle without a Stream object (2 us of host time a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 _SZ = ctypes.c_size_t
 
 
@@ -119,6 +127,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.spec_debug_attn_fault.argtypes = [_I, ctypes.c_ulonglong]
     lib.spec_verify_attn_noalloc_error.restype = _I
     lib.spec_verify_attn_noalloc_error.argtypes = [ctypes.POINTER(ctypes.c_int32), _P]
+    lib.spec_extend_tables.restype = _I
+    lib.spec_extend_tables.argtypes = [_P, _P, _I, _I, _P, _I, _P, _I, _P, _I, _P, _P, _P, _P, _P,
+                                       _P, _P]
+    lib.spec_release_pages.restype = _I
+    lib.spec_release_pages.argtypes = [_P, _I, _P, _P, _I, _I, _P, _I, _P, _P, _P, _P]
+    lib.spec_append_tokens.restype = _I
+    lib.spec_append_tokens.argtypes = [_P, _L, _P, _L, _P, _L, _P, _L, _I, _P, _P, _I, _P, _P, _I,
+                                       _I, _L, _L, _L, _P, _P, _I, _I, _I, _I, ctypes.c_double, _P]
+    lib.spec_decode_attn_workspace_size.restype = _SZ
+    lib.spec_decode_attn_workspace_size.argtypes = [_I] * 4
+    lib.spec_decode_attn.restype = _I
+    lib.spec_decode_attn.argtypes = [_P, _L, _L, _I, _P, _P, _I, _P, _P, _I, _I, _L, _L, _L, _P,
+                                     _I, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P, _SZ, _P, _P,
+                                     _P]
     _lib = lib
     return lib
 
@@ -444,3 +466,253 @@ def accept_sample_tree(logits, draft_probs, node_tokens, parent, uniforms, cfg: 
                                      _ptr(out["status"]), _stream(stream))
     _check("spec_accept_sample_tree", rc)
     return out
+
+
+# ------------------------------------------------------------------ the cache's side
+_DTYPE = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16,
+          torch.float8_e4m3fn: SPEC_E4M3}
+
+
+def _elsewhere(dev, stream):
+    """True when the call has to change the current device or stream first."""
+    return stream is not None or dev.index != torch.cuda.current_device()
+
+
+def _here(dev):
+    return _raw_stream(dev.index)
+
+
+def _tensor(t, name, dev, dtype, shape):
+    """The address of a contiguous tensor of this type and shape on `dev`."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor on {dev}")
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t.device != dev:
+        raise ValueError(f"{name} must be a tensor on {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _cuda_device(t, name):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _rows(t, name, dev, dtype, heads, D):
+    """[T, heads, D] rows whose heads lie side by side; returns (pointer, row stride)."""
+    if not isinstance(t, torch.Tensor) or t.device != dev:
+        raise ValueError(f"{name} must be a tensor on {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError(f"{name} must be [tokens, {heads}, {D}], got {tuple(t.shape)}")
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != D):
+        raise ValueError(f"{name}: a row's heads must lie side by side")
+    return t.data_ptr(), st[0]
+
+
+def _caches(k_cache, v_cache, dev, dtype):
+    """Checks the pair; returns its (page, token, head) strides."""
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor) or t.device != dev:
+            raise ValueError(f"{name} must be a tensor on {dev}")
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("caches must be [pages, page_size, Hkv, D], both alike")
+    if v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must have one dtype")
+    if k_cache.dtype != dtype and (k_cache.dtype != torch.float8_e4m3fn
+                                   or dtype == torch.float32):
+        raise ValueError(f"caches must be {dtype}" + ("" if dtype == torch.float32
+                                                      else " or float8_e4m3fn"))
+    st = k_cache.stride()
+    if st[3] != 1 or v_cache.stride() != st:
+        raise ValueError("caches must have the same strides, 1 over D")
+    return st
+
+
+def _scales(k_scale, v_scale, k_cache, dev):
+    if k_scale is None and v_scale is None:
+        return None, None
+    if k_cache.dtype != torch.float8_e4m3fn:
+        raise ValueError("scales belong to float8_e4m3fn caches")
+    shape = k_cache.shape[2:3]
+    return tuple(None if t is None else _tensor(t, name, dev, torch.float32, shape)
+                 for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")))
+
+
+def extend_tables(ctx_len, add_len, block_table, free_list, free_count, page_size: int,
+                  max_tokens: int, out=None, stream=None):
+    """Pages, slots and positions for a step's new tokens, from lengths on the GPU.
+
+    block_table [B, max_pages] int32 is updated; free_list [num_pages] and free_count
+    [1] (int32) are only read.  Returns dict(slot_map [max_tokens] int64, positions
+    [max_tokens], cu_len [B+1], new_len [B], free_count [1], status [B]); free_count is
+    what is left of the list, for the next call.  out: an earlier call's dict of these
+    shapes, written again (its free_count is not this call's)."""
+    dev = _cuda_device(ctx_len, "ctx_len")
+    if _elsewhere(dev, stream):
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return extend_tables(ctx_len, add_len, block_table, free_list, free_count, page_size,
+                                 max_tokens, out)
+    i32 = torch.int32
+    if ctx_len.dim() != 1 or block_table.dim() != 2 or free_list.dim() != 1:
+        raise ValueError("ctx_len [B], block_table [B, max_pages], free_list [num_pages]")
+    B, width = ctx_len.shape[0], block_table.shape[1]
+    ins = (_tensor(ctx_len, "ctx_len", dev, i32, (B,)),
+           _tensor(add_len, "add_len", dev, i32, (B,)))
+    table = _tensor(block_table, "block_table", dev, i32, (B, width))
+    n = free_list.shape[0]
+    lst = _tensor(free_list, "free_list", dev, i32, (n,))
+    cnt = _tensor(free_count, "free_count", dev, i32, (1,))
+    if out is None:
+        cu, new_len, left, status = torch.empty(3 * B + 2, dtype=i32, device=dev).split(
+            (B + 1, B, 1, B))
+        out = dict(slot_map=torch.empty(max_tokens, dtype=torch.int64, device=dev),
+                   positions=torch.empty(max_tokens, dtype=i32, device=dev), cu_len=cu,
+                   new_len=new_len, free_count=left, status=status)
+    _check("spec_extend_tables",
+           load().spec_extend_tables(
+               *ins, B, page_size, table, width, lst, n, cnt, max_tokens,
+               _tensor(out["slot_map"], "slot_map", dev, torch.int64, (max_tokens,)),
+               _tensor(out["positions"], "positions", dev, i32, (max_tokens,)),
+               _tensor(out["cu_len"], "cu_len", dev, i32, (B + 1,)),
+               _tensor(out["new_len"], "new_len", dev, i32, (B,)),
+               _tensor(out["free_count"], "free_count", dev, i32, (1,)),
+               _tensor(out["status"], "status", dev, i32, (B,)), _here(dev)))
+    return out
+
+
+def release_pages(block_table, length, keep_pages, free_list, free_count, page_size: int,
+                  total=None, status=None, stream=None):
+    """Pages behind each sequence's kept ones go back on the free list (in place).
+
+    length [B]: tokens the rows were extended for; keep_pages [B]: kv_commit's, or 0
+    for a finished request.  Returns (free_count [1], status [B])."""
+    dev = _cuda_device(length, "length")
+    if _elsewhere(dev, stream):
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return release_pages(block_table, length, keep_pages, free_list, free_count,
+                                 page_size, total, status)
+    i32 = torch.int32
+    if length.dim() != 1 or block_table.dim() != 2 or free_list.dim() != 1:
+        raise ValueError("length [B], block_table [B, max_pages], free_list [num_pages]")
+    B, width, n = length.shape[0], block_table.shape[1], free_list.shape[0]
+    table = _tensor(block_table, "block_table", dev, i32, (B, width))
+    held = _tensor(length, "length", dev, i32, (B,))
+    keep = _tensor(keep_pages, "keep_pages", dev, i32, (B,))
+    lst = _tensor(free_list, "free_list", dev, i32, (n,))
+    cnt = _tensor(free_count, "free_count", dev, i32, (1,))
+    total = torch.empty(1, dtype=i32, device=dev) if total is None else total
+    status = torch.empty(B, dtype=i32, device=dev) if status is None else status
+    _check("spec_release_pages",
+           load().spec_release_pages(table, width, held, keep, B, page_size, lst, n, cnt,
+                                     _tensor(total, "total", dev, i32, (1,)),
+                                     _tensor(status, "status", dev, i32, (B,)), _here(dev)))
+    return total, status
+
+
+def append_tokens(k_new, v_new, k_cache, v_cache, slot_map, positions=None, q=None, q_out=None,
+                  rope_base: float = 10000.0, k_scale=None, v_scale=None, stream=None):
+    """Packed rows [T, Hkv, D] into the paged cache at their slots, keys rotated at
+    `positions` (rope_base 0: not); with q [T, Hq, D] the rotated queries go to q_out
+    (allocated if not given; q itself rotates in place).  Rows with a slot outside the
+    cache are skipped.  Returns q_out (None without q)."""
+    dev = _cuda_device(k_new, "k_new")
+    if _elsewhere(dev, stream):
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return append_tokens(k_new, v_new, k_cache, v_cache, slot_map, positions, q, q_out,
+                                 rope_base, k_scale, v_scale)
+    dt = k_new.dtype
+    if dt not in _DTYPE or dt == torch.float8_e4m3fn:
+        raise ValueError("k_new must be bf16, fp16 or fp32")
+    sp, st, sh, _ = _caches(k_cache, v_cache, dev, dt)
+    npg, P, Hkv, D = k_cache.shape
+    k, ks = _rows(k_new, "k_new", dev, dt, Hkv, D)
+    v, vs = _rows(v_new, "v_new", dev, dt, Hkv, D)
+    T = k_new.shape[0]
+    slots = _tensor(slot_map, "slot_map", dev, torch.int64, (T,))
+    if v_new.shape[0] != T:
+        raise ValueError("v_new and k_new must have the same rows")
+    pos = None
+    if positions is not None:
+        pos = _tensor(positions, "positions", dev, torch.int32, (T,))
+    elif rope_base:
+        raise ValueError("positions are needed to rotate (rope_base 0: no rotation)")
+    Hq, qp, qs, op, os_ = 0, None, 0, None, 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T:
+            raise ValueError("q must be [tokens, Hq, D]")
+        Hq = q.shape[1]
+        qp, qs = _rows(q, "q", dev, dt, Hq, D)
+        if q_out is None:
+            q_out = torch.zeros((T, Hq, D), dtype=dt, device=dev)
+        op, os_ = _rows(q_out, "q_out", dev, dt, Hq, D)
+        if q_out.shape[0] != T:
+            raise ValueError("q_out and q must have the same rows")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    sk, sv = _scales(k_scale, v_scale, k_cache, dev)
+    _check("spec_append_tokens",
+           load().spec_append_tokens(k, ks, v, vs, qp, qs, op, os_, _DTYPE[dt],
+                                     k_cache.data_ptr(), v_cache.data_ptr(),
+                                     _DTYPE[k_cache.dtype], sk, sv, npg, P, sp, st, sh, slots,
+                                     pos, T, Hq, Hkv, D, rope_base, _here(dev)))
+    return q_out
+
+
+def decode_attn_workspace_size(B, Hq, Hkv, D) -> int:
+    return int(load().spec_decode_attn_workspace_size(B, Hq, Hkv, D))
+
+
+def decode_attn(q, k_cache, v_cache, block_table, seq_len, scale: float = 0.0, window: int = 0,
+                k_scale=None, v_scale=None, workspace=None, out=None, lse=None, stream=None):
+    """Attention of one new token per sequence over the paged cache.
+
+    q [B, Hq, D] bf16 or fp16 (strided over B and Hq as it comes); caches [pages, P,
+    Hkv, D] of q's dtype or float8_e4m3fn with scales [Hkv]; seq_len [B] counts the
+    stored tokens, the new one included.  Returns (out [B, Hq, D], lse [B, Hq])."""
+    dev = _cuda_device(q, "q")
+    if _elsewhere(dev, stream):
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return decode_attn(q, k_cache, v_cache, block_table, seq_len, scale, window, k_scale,
+                               v_scale, workspace, out, lse)
+    dt = q.dtype
+    if dt != torch.bfloat16 and dt != torch.float16:
+        raise ValueError("q must be bf16 or fp16")
+    if q.dim() != 3 or q.stride(2) != 1:
+        raise ValueError("q must be [B, Hq, D], contiguous over D")
+    B, Hq, D = q.shape
+    sp, st, sh, _ = _caches(k_cache, v_cache, dev, dt)
+    npg, P, Hkv, D2 = k_cache.shape
+    if D2 != D:
+        raise ValueError("head_dim mismatch")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    width = block_table.shape[1]
+    table = _tensor(block_table, "block_table", dev, torch.int32, (B, width))
+    lens = _tensor(seq_len, "seq_len", dev, torch.int32, (B,))
+    sk, sv = _scales(k_scale, v_scale, k_cache, dev)
+    lib = load()
+    if workspace is None:
+        workspace = new_workspace(lib.spec_decode_attn_workspace_size(B, Hq, Hkv, D), dev)
+    elif workspace.device != dev or workspace.dtype != torch.uint8 \
+            or not workspace.is_contiguous():
+        raise ValueError("workspace must come from new_workspace on q's device")
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=dt, device=dev)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    _check("spec_decode_attn",
+           lib.spec_decode_attn(q.data_ptr(), q.stride(0), q.stride(1), _DTYPE[dt],
+                                k_cache.data_ptr(), v_cache.data_ptr(), _DTYPE[k_cache.dtype], sk,
+                                sv, npg, P, sp, st, sh, table, width, lens, B, Hq, Hkv, D, window,
+                                scale, workspace.data_ptr(), workspace.numel(),
+                                _tensor(out, "out", dev, dt, (B, Hq, D)),
+                                _tensor(lse, "lse", dev, torch.float32, (B, Hq)), _here(dev)))
+    return out, lse

@@ -1,0 +1,840 @@
+// spec_decode_attn -- attention of one new token per sequence over the paged
+// cache, split over the cache's length and joined.
+//
+// Mathematics: query head h of sequence b over the seen positions t:
+//   x_t = scale * q . k_t,  out = sum_t e^(x_t - m) v_t / l,  l = sum_t e^(x_t - m),
+//   lse = m + ln l  for any reference m.
+// Parts of the positions give (m, l, sum) each, and parts join by e^(m_i - M)
+// ("Speculative Token Decoupling: Asynchronous Verification via Flash-Decoding",
+// section 03: split-K attention).  Everything runs in the log2 domain, in fp32.
+//
+// What bounds it: HBM.  Every K and V row is read once (512 bytes per position
+// and KV head at D = 128 in bf16, 256 in e4m3) for 4 D flops per query head.
+//
+// Design.  A CTA (4 warps) takes one KV head (up to 8 or 16 of its query heads)
+// and one contiguous range of the batch's positions; all CTAs of a launch are
+// resident at once and the ranges are cut evenly over the whole batch (units of
+// 64 positions, counted from seq_len on the device), so ragged batches, one long
+// sequence and the launch of a captured graph whose lengths change all fill the
+// GPU alike.  The CTAs of a range's heads are neighbours in the grid and walk the
+// same token rows together.
+// A warp streams its positions straight from HBM into registers: no shared
+// memory ring, no barrier in the loop.  That works because both products are
+// taken transposed, heads as the MMA's 8 columns (m16n8k16, fp32 accumulate):
+//   S^T = K Q^T: rows are 16 positions; a lane's 16-byte pieces of a K row are
+//     the A fragments of two (16-bit) or four (8-bit) k-steps, in an order of
+//     the D dimensions that Q's fragments share;
+//   O^T = V^T P^T: a lane holds 16-byte pieces of the four V rows that its
+//     fragment columns want, and byte permutes pair the rows; the rows of the
+//     output tile are whatever dimensions those pieces hold.
+//   P^T's fragments are S^T's accumulators, packed and transposed by movmatrix.
+// K's loads for the next tile go out when this tile's S is done, V's when its
+// product is; the page lookups are two tiles ahead.
+// P is fp16 beside fp16 and e4m3 caches (e4m3 converts to fp16 exactly) and a
+// sum of two bf16 parts beside bf16 ones, so that rounding P adds nothing to the
+// output's own rounding.  The reference m of a row stays until a score exceeds
+// it by 15 (it is set 7 below the maximum: P stays in fp16's range).
+#include <algorithm>
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kUnit = 64;             // positions: the granularity of the ranges
+constexpr int kMaxCounters = 65536;   // sequences x KV heads x head groups
+constexpr float kBelow = 7.f;         // the reference sits this far under the maximum
+constexpr float kSlack = 15.f;        // a score may exceed the reference by this much
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct DecodeParams {
+  const char *q, *k, *v;
+  const int32_t *table, *seq_len;
+  const float *k_scale, *v_scale;
+  char* out;
+  float *lse, *part_o, *part_ml;
+  int32_t* counters;
+  long long q_stride_b, q_stride_h;          // elements
+  long long head_stride;                     // bytes
+  uint32_t token_stride;                     // bytes
+  uint32_t page_rows;                        // page stride in token strides
+  int B, Hq, Hkv, G, groups, hpg, P, num_pages, max_pages, window, ranges, q_bf16;
+  float scale_log2;
+};
+
+// What is read in the place of positions that are not seen: an address instead of
+// a predicate on every load (a predicated load leaves its registers live).
+__device__ __align__(512) char kZeros[512];
+
+enum Cache { kBf16, kF16, kE4m3 };
+
+template <int CT>
+constexpr int elem_bytes() { return CT == kE4m3 ? 1 : 2; }
+
+// D = A(16x16, row) * B(16x8, col) + D (fp32), f16 or bf16 operands
+template <bool BF>
+SPEC_DEV void mma(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                  uint32_t b1) {
+  if constexpr (BF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+SPEC_DEV uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+SPEC_DEV uint32_t pack_f16(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+SPEC_DEV uint32_t e4m3_to_f16(uint32_t pair) {  // low two bytes
+  uint32_t r;
+  asm("{\n .reg .b16 x;\n cvt.u16.u32 x, %1;\n cvt.rn.f16x2.e4m3x2 %0, x;\n}\n" : "=r"(r) : "r"(pair));
+  return r;
+}
+
+// N words of the cache, read once: not kept in L1, first out of L2
+template <int N>
+SPEC_DEV void load_words(uint32_t* w, const char* p, uint64_t pol) {
+  if constexpr (N == 4)
+    asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.b32 {%0,%1,%2,%3}, [%4], %5;"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "l"(p), "l"(pol));
+  else
+    asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v2.b32 {%0,%1}, [%2], %3;"
+                 : "=r"(w[0]), "=r"(w[1])
+                 : "l"(p), "l"(pol));
+}
+
+SPEC_DEV int seen_from(const DecodeParams& p, int n) {
+  return p.window > 0 && n > p.window ? n - p.window : 0;
+}
+
+// stored tokens of sequence b (never more than its table row can name)
+SPEC_DEV int stored(const DecodeParams& p, int b) {
+  const int n = p.seq_len[b];
+  return n < 0 ? 0 : min(n, p.max_pages * p.P);
+}
+
+SPEC_DEV int units_of(const DecodeParams& p, int n) {
+  return (n - seen_from(p, n) + kUnit - 1) / kUnit;
+}
+
+template <int N>
+struct Row {  // a lane's N consecutive floats of a part's row
+  float x[N];
+  SPEC_DEV void load(const float* row, int lane) {
+    if constexpr (N == 2) {
+      const float2 y = __ldcg(reinterpret_cast<const float2*>(row) + lane);
+      x[0] = y.x, x[1] = y.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(row + N * lane + i));
+        x[i] = y.x, x[i + 1] = y.y, x[i + 2] = y.z, x[i + 3] = y.w;
+      }
+    }
+  }
+};
+
+// Block-wide sum of one value per thread (all threads get it).
+SPEC_DEV long long block_sum(long long v, long long* sh) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) v += sh[w];
+  __syncthreads();
+  return v;
+}
+
+SPEC_DEV long long warp_scan(long long v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  return v;
+}
+
+// floor(W r / nr): where range r of nr begins (32-bit division where it does)
+SPEC_DEV long long cut(long long W, int r, int nr) {
+  return W < 1 << 20 ? (long long)((uint32_t)W * (uint32_t)r / (uint32_t)nr) : W * r / nr;
+}
+
+// the range that holds unit x: the largest r with floor(W r / nr) <= x
+SPEC_DEV int range_of(long long x, long long W, int nr) {
+  return W < 1 << 20 ? (int)(((uint32_t)(x + 1) * (uint32_t)nr - 1) / (uint32_t)W)
+                     : (int)(((x + 1) * nr - 1) / W);
+}
+
+template <int CT, int D, int NT>
+struct Shape {
+  static constexpr int kBytes = D * elem_bytes<CT>();           // of a row
+  static constexpr int kTile = 16 * kBytes <= 2048 ? 32 : 16;   // positions of a warp's tile
+  static constexpr int kSub = kTile / 16;
+  static constexpr int kKPieces = kBytes / 64;                  // 16-byte pieces per lane and row
+  static constexpr int kVWords = kBytes >= 128 ? 4 : kBytes / 32;  // words of a lane's V piece
+  static constexpr int kVPieces = kBytes >= 128 ? kBytes / 128 : 1;
+  static constexpr int kSteps = D / 16;
+};
+
+// The parts of sequence b's head group, joined by one CTA in the parts' order:
+// a warp per head; lanes hold the weights of 32 parts at a time, and kFlight
+// parts' rows are loaded together.  `late`: the first part is its range's last
+// segment (slot 1).  Out of line: its registers are not the loop's.
+template <int D>
+__device__ __forceinline__ void join(const DecodeParams& p, int b, int r_first, int np, bool late,
+                                  int hv, int nh) {
+  constexpr int kPer = D / 32, kFlight = kPer > 4 ? 8 : 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, HV = p.Hkv * p.groups;
+  const int kvh = hv / p.groups, h0 = hv % p.groups * p.hpg;
+  const float vs = p.v_scale ? p.v_scale[kvh] : 1.f;
+#pragma unroll 1
+  for (int h = warp; h < nh; h += kWarps) {
+    // row of part 0 of head h (in slot 0), and the rows from part to part
+    const size_t row0 = ((size_t)r_first * 2 * HV + hv) * p.hpg + h;
+    const int step = 2 * HV * p.hpg, slot1 = late ? HV * p.hpg : 0;
+    float M = -INFINITY, L = 0.f, acc[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < np; i0 += 32) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (i0 + lane < np)
+        ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + row0 +
+                    (size_t)(i0 + lane) * step + (i0 + lane == 0 ? slot1 : 0));
+      const float now = fmaxf(M, warp_max(ml.x));
+      const float a = M == -INFINITY ? 0.f : fast_exp2(M - now);
+      const float e = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - now);
+      M = now;
+      L = L * a + warp_sum(e * ml.y);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] *= a;
+      const int cnt = min(32, np - i0);
+#pragma unroll 1
+      for (int j0 = 0; j0 < cnt; j0 += kFlight) {
+        Row<kPer> y[kFlight];
+        const float* src = p.part_o + (row0 + (size_t)(i0 + j0) * step) * D;
+        const size_t first = i0 + j0 == 0 ? (size_t)slot1 * D : 0;
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j)
+          y[j].load(src + (size_t)(min(j, cnt - 1 - j0) * step) * D + (j == 0 ? first : 0), lane);
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j) {
+          const float ej = __shfl_sync(0xffffffffu, e, (j0 + j) & 31);
+          if (j0 + j < cnt) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) acc[i] += ej * y[j].x[i];
+          }
+        }
+      }
+    }
+    const float f = L == 0.f ? 0.f : vs / L;
+#pragma unroll
+    for (int i = 0; i < kPer; i += 2) {
+      const uint32_t y = p.q_bf16 ? pack_bf16(acc[i] * f, acc[i + 1] * f)
+                                  : pack_f16(acc[i] * f, acc[i + 1] * f);
+      *reinterpret_cast<uint32_t*>(
+          p.out + (((size_t)b * p.Hq + kvh * p.G + h0 + h) * D + kPer * lane + i) * 2) = y;
+    }
+    if (lane == 0 && p.lse)
+      p.lse[(size_t)b * p.Hq + kvh * p.G + h0 + h] =
+          L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+  }
+}
+
+template <int CT, int D, int NT, int MINB>
+__global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
+    const __grid_constant__ DecodeParams p) {
+  using S = Shape<CT, D, NT>;
+  constexpr bool kBf = CT == kBf16;
+  constexpr int NS = S::kSub, KP = S::kKPieces, VW = S::kVWords, VP = S::kVPieces;
+  constexpr int kHeads = 8 * NT;
+  __shared__ __align__(16) float so[kWarps][kHeads][D];
+  __shared__ float sml[kWarps][kHeads][2];
+  __shared__ long long ssum[kWarps];
+  // the segment being worked on: in shared memory, read again behind the barriers,
+  // so that it holds no registers while the positions stream through
+  __shared__ struct {
+    long long W, w, w1, at;  // the batch's units; this CTA's next and end; in front of b
+    int nr, b;
+  } seg;
+  __shared__ int s_last;
+
+  const int hv = blockIdx.x % (p.Hkv * p.groups), r = blockIdx.x / (p.Hkv * p.groups);
+  const int kvh = hv / p.groups, h0 = hv % p.groups * p.hpg;   // first query head within G
+  const int nh = min(p.hpg, p.G - h0);                         // query heads of this CTA
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n8 = lane >> 2, c4 = lane & 3;
+  const int HV = p.Hkv * p.groups;
+
+  // ---- this CTA's units [w0, w1) of the batch's W, and the sequence that holds w0
+  auto nothing_seen = [&](int b) {  // zeros and -inf for this CTA's heads
+    for (int i = threadIdx.x; i < nh * D; i += kThreads)
+      reinterpret_cast<uint16_t*>(p.out)[((size_t)b * p.Hq + kvh * p.G + h0) * D + i] = 0;
+    if (p.lse && threadIdx.x < nh)
+      p.lse[(size_t)b * p.Hq + kvh * p.G + h0 + threadIdx.x] = -INFINITY;
+  };
+  if (p.B <= kThreads) {  // one sequence per thread: one load of the lengths, one scan
+    const int tid = threadIdx.x;
+    const int u = tid < p.B ? units_of(p, stored(p, tid)) : 0;
+    const bool idle = tid < p.B && u == 0;
+    const long long x = warp_scan(u, lane);
+    if (lane == 31) ssum[warp] = x;
+    const int idles = __syncthreads_count(idle && tid % p.ranges == r);
+    long long before = 0, W = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += ssum[w];
+      W += ssum[w];
+    }
+    if (idles)
+      for (int b = r; b < p.B; b += p.ranges)
+        if (units_of(p, stored(p, b)) == 0) nothing_seen(b);
+    const int nr = (int)min((long long)p.ranges, W);
+    if (r >= nr) return;
+    const long long w0 = cut(W, r, nr), pre = before + x - u;
+    if (u > 0 && pre <= w0 && w0 < pre + u)
+      seg = {W, w0, cut(W, r + 1, nr), pre, nr, tid};
+    __syncthreads();
+  } else {
+    for (int b = r; b < p.B; b += p.ranges)
+      if (units_of(p, stored(p, b)) == 0) nothing_seen(b);
+    long long mine = 0;
+    for (int b = threadIdx.x; b < p.B; b += kThreads) mine += units_of(p, stored(p, b));
+    const long long W = block_sum(mine, ssum);
+    const int nr = (int)min((long long)p.ranges, W);
+    if (r >= nr) return;
+    const long long w0 = cut(W, r, nr);
+    long long base = 0;  // units in front of these kThreads sequences
+    for (int b0 = 0; b0 < p.B && base <= w0; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      const int u = b < p.B ? units_of(p, stored(p, b)) : 0;
+      const long long x = warp_scan(u, lane);
+      if (lane == 31) ssum[warp] = x;
+      __syncthreads();
+      long long before = base;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += ssum[w];
+        base += ssum[w];
+      }
+      const long long pre = before + x - u;
+      if (u > 0 && pre <= w0 && w0 < pre + u)
+        seg = {W, w0, cut(W, r + 1, nr), pre, nr, b};
+      __syncthreads();
+    }
+  }
+
+  uint64_t pol;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
+  const char* kh = p.k + kvh * p.head_stride + c4 * 16;
+  const char* vh = p.v + kvh * p.head_stride + n8 * VW * 4;
+
+  while (true) {
+    const int b = seg.b;
+    int t_begin, t_end;
+    {
+      const int n = stored(p, b), first = seen_from(p, n);
+      t_begin = first + (int)(seg.w - seg.at) * kUnit;
+      t_end = (int)min((long long)n, first + (seg.w1 - seg.at) * kUnit);
+    }
+    const int32_t* bt = p.table + (size_t)b * p.max_pages;
+
+    // ---- Q fragments (column n8 of tile nt is query head h0 + 8 nt + n8)
+    uint32_t qf[NT][S::kSteps][2];
+    float sc[NT][2];   // log2-domain scale of this lane's accumulator columns
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int g = 8 * nt + n8;
+      const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + b * p.q_stride_b +
+                            (kvh * p.G + h0 + min(g, nh - 1)) * p.q_stride_h;
+      uint32_t raw[S::kSteps * 2];
+      if constexpr (CT == kE4m3) {  // 16 dimensions per lane and piece
+#pragma unroll
+        for (int j = 0; j < KP; ++j) {
+          const uint4* s4 = reinterpret_cast<const uint4*>(src + (j * 4 + c4) * 16);
+          const uint4 x = s4[0], y = s4[1];
+          raw[8 * j] = x.x, raw[8 * j + 1] = x.y, raw[8 * j + 2] = x.z, raw[8 * j + 3] = x.w;
+          raw[8 * j + 4] = y.x, raw[8 * j + 5] = y.y, raw[8 * j + 6] = y.z, raw[8 * j + 7] = y.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < KP; ++j) {
+          const uint4 x = *reinterpret_cast<const uint4*>(src + (j * 4 + c4) * 8);
+          raw[4 * j] = x.x, raw[4 * j + 1] = x.y, raw[4 * j + 2] = x.z, raw[4 * j + 3] = x.w;
+        }
+      }
+      float up = 1.f;
+      if (CT == kE4m3 && p.q_bf16) {
+        // bf16 q beside fp16 operands: scaled by a power of two that puts the
+        // head's largest element at 2^14, so that nothing overflows and what
+        // becomes subnormal is 2^-28 of the largest
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < S::kSteps * 2; ++i)
+          big = fmaxf(big, fmaxf(fabsf(__uint_as_float(raw[i] << 16)),
+                                 fabsf(__uint_as_float(raw[i] & 0xffff0000u))));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        int e = (int)(__float_as_uint(big) >> 23) - 127;   // exponent of the largest
+        if (!(big > 0.f) || e > 127) e = 14;               // zero, Inf or NaN: as it is
+        e = max(e, -100);
+        const float down = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+        up = __uint_as_float((uint32_t)(127 + e - 14) << 23);
+#pragma unroll
+        for (int i = 0; i < S::kSteps * 2; ++i)
+          raw[i] = pack_f16(__uint_as_float(raw[i] << 16) * down,
+                            __uint_as_float(raw[i] & 0xffff0000u) * down);
+      }
+#pragma unroll
+      for (int i = 0; i < S::kSteps; ++i) {
+        qf[nt][i][0] = raw[2 * i];
+        qf[nt][i][1] = raw[2 * i + 1];
+      }
+      const float mul = p.scale_log2 * (p.k_scale ? p.k_scale[kvh] : 1.f) * up;
+      sc[nt][0] = __shfl_sync(0xffffffffu, mul, 8 * c4);       // head 2 c4 of the tile
+      sc[nt][1] = __shfl_sync(0xffffffffu, mul, 8 * c4 + 4);   // head 2 c4 + 1
+    }
+
+    float o[NT][S::kSteps][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < S::kSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    // page of this lane's position of the tile at t0: the raw table entry (-1: none)
+    const int tl = lane % S::kTile;
+    auto entry = [&](int t0) {
+      const int t = t0 + tl;
+      return t < t_end ? bt[t / p.P] : -1;
+    };
+    // cache row of that position, in token strides (-1: not seen)
+    auto row_of = [&](int t0, int id) {
+      const int t = t0 + tl;
+      return id >= 0 && id < p.num_pages ? (int)(id * p.page_rows + t % p.P) : -1;
+    };
+    uint32_t kr[NS][2][KP][4], vr[NS][4][VP][VW];
+    bool seen[NS][2];
+    auto load_k = [&](int row) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int rr = __shfl_sync(0xffffffffu, row, 16 * s + 8 * x + n8);
+          seen[s][x] = rr >= 0;
+          const char* src = rr >= 0 ? kh + (uint64_t)(uint32_t)rr * p.token_stride : kZeros;
+#pragma unroll
+          for (int j = 0; j < KP; ++j) load_words<4>(kr[s][x][j], src + j * 64, pol);
+        }
+    };
+    auto load_v = [&](int row) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int rr = __shfl_sync(0xffffffffu, row, 16 * s + 8 * (x >> 1) + 2 * c4 + (x & 1));
+          const char* src = rr >= 0 ? vh + (uint64_t)(uint32_t)rr * p.token_stride : kZeros;
+#pragma unroll
+          for (int j = 0; j < VP; ++j) load_words<VW>(vr[s][x][j], src + j * 128, pol);
+        }
+    };
+
+    constexpr int kStride = kWarps * S::kTile;
+    int t0 = t_begin + warp * S::kTile;
+    int row = row_of(t0, entry(t0));
+    load_k(row);
+    load_v(row);
+    int id_next = entry(t0 + kStride);
+    for (; t0 < t_end; t0 += kStride) {
+      // ---- S^T = K Q^T
+      float x[NS][NT][4];
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) x[s][nt][0] = x[s][nt][1] = x[s][nt][2] = x[s][nt][3] = 0.f;
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int j = 0; j < KP; ++j) {
+          if constexpr (CT == kE4m3) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t lo = kr[s][0][j][i], hi = kr[s][1][j][i];
+              const uint32_t a0 = e4m3_to_f16(lo), a2 = e4m3_to_f16(lo >> 16);
+              const uint32_t a1 = e4m3_to_f16(hi), a3 = e4m3_to_f16(hi >> 16);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma<false>(x[s][nt], a0, a1, a2, a3, qf[nt][4 * j + i][0], qf[nt][4 * j + i][1]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma<kBf>(x[s][nt], kr[s][0][j][2 * i], kr[s][1][j][2 * i], kr[s][0][j][2 * i + 1],
+                         kr[s][1][j][2 * i + 1], qf[nt][2 * j + i][0], qf[nt][2 * j + i][1]);
+          }
+        }
+      // ---- scale, what is not seen, the reference
+      bool over = false;
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float y = seen[s][e >> 1] ? x[s][nt][e] * sc[nt][e & 1] : -INFINITY;
+            x[s][nt][e] = y;
+            over = over || y > m[nt][e & 1] + kSlack;
+          }
+      // the next tile's K (its page ids came with the tile before)
+      const int row_next = row_of(t0 + kStride, id_next);
+      load_k(row_next);
+      id_next = entry(t0 + 2 * kStride);
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int s = 0; s < NS; ++s) top = fmax3(top, x[s][nt][e], x[s][nt][e + 2]);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const float now = fmaxf(m[nt][e], top - kBelow);
+            const float a = m[nt][e] == -INFINITY ? 0.f : fast_exp2(m[nt][e] - now);
+            m[nt][e] = now;
+            l[nt][e] *= a;
+#pragma unroll
+            for (int i = 0; i < S::kSteps; ++i) {
+              o[nt][i][e] *= a;
+              o[nt][i][e + 2] *= a;
+            }
+          }
+      }
+      // ---- P^T fragments, then O^T += V^T P^T
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float ref = m[nt][e & 1];
+            y[e] = fast_exp2(x[s][nt][e] - (ref == -INFINITY ? 0.f : ref));
+          }
+          l[nt][0] += y[0] + y[2];
+          l[nt][1] += y[1] + y[3];
+#pragma unroll
+          for (int x2 = 0; x2 < 2; ++x2) {
+            const float y0 = y[2 * x2], y1 = y[2 * x2 + 1];
+            if constexpr (kBf) {
+              const uint32_t hi = pack_bf16(y0, y1);
+              ph[nt][x2] = transpose8x8(hi);
+              pl[nt][x2] = transpose8x8(pack_bf16(y0 - __uint_as_float(hi << 16),
+                                                  y1 - __uint_as_float(hi & 0xffff0000u)));
+            } else {
+              ph[nt][x2] = transpose8x8(pack_f16(y0, y1));
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < VP; ++j)
+#pragma unroll
+          for (int i = 0; i < VW; ++i) {
+            const uint32_t v0 = vr[s][0][j][i], v1 = vr[s][1][j][i];
+            const uint32_t v2 = vr[s][2][j][i], v3 = vr[s][3][j][i];
+            if constexpr (CT == kE4m3) {
+              const uint32_t a = __byte_perm(v0, v1, 0x5140), b2 = __byte_perm(v2, v3, 0x5140);
+              const uint32_t c = __byte_perm(v0, v1, 0x7362), d = __byte_perm(v2, v3, 0x7362);
+              const int t = 2 * (j * VW + i);
+              const uint32_t f[8] = {e4m3_to_f16(a), e4m3_to_f16(a >> 16), e4m3_to_f16(b2),
+                                     e4m3_to_f16(b2 >> 16), e4m3_to_f16(c), e4m3_to_f16(c >> 16),
+                                     e4m3_to_f16(d), e4m3_to_f16(d >> 16)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma<false>(o[nt][t], f[0], f[1], f[2], f[3], ph[nt][0], ph[nt][1]);
+                mma<false>(o[nt][t + 1], f[4], f[5], f[6], f[7], ph[nt][0], ph[nt][1]);
+              }
+            } else {
+              const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
+              const uint32_t a2 = __byte_perm(v2, v3, 0x5410), a3 = __byte_perm(v2, v3, 0x7632);
+              const int t = j * VW + i;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma<kBf>(o[nt][t], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
+                if constexpr (kBf) mma<kBf>(o[nt][t], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+              }
+            }
+          }
+      }
+      load_v(row_next);
+    }
+
+    // ---- the warps' parts meet in shared memory
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float y = l[nt][e];
+        y += __shfl_xor_sync(0xffffffffu, y, 4);
+        y += __shfl_xor_sync(0xffffffffu, y, 8);
+        y += __shfl_xor_sync(0xffffffffu, y, 16);
+        const int h = 8 * nt + 2 * c4 + e;
+        if (n8 == 0) {
+          sml[warp][h][0] = m[nt][e];
+          sml[warp][h][1] = y;
+        }
+        // tile t of the output: dimensions (piece, word) of this lane's V bytes
+#pragma unroll
+        for (int t = 0; t < S::kSteps; ++t) {
+          int d;
+          if constexpr (CT == kE4m3)
+            d = (t / (2 * VW)) * 128 + n8 * VW * 4 + (t % (2 * VW)) * 2;
+          else
+            d = (t / VW) * 64 + n8 * 8 + (t % VW) * 2;
+          *reinterpret_cast<float2*>(&so[warp][h][d]) = make_float2(o[nt][t][e], o[nt][t][e + 2]);
+        }
+      }
+    __syncthreads();
+
+    // parts of this sequence: ranges r_first .. r_last
+    const long long at = seg.at;
+    const int units = units_of(p, stored(p, b));
+    const int r_first = range_of(at, seg.W, seg.nr), r_last = range_of(at + units - 1, seg.W, seg.nr);
+    const bool whole = r_first == r_last;
+    const float vs = p.v_scale ? p.v_scale[kvh] : 1.f;
+    // slot 0: the segment a range begins with; slot 1: its last one, if another
+    const bool begins = seg.w == cut(seg.W, r, seg.nr);
+    const size_t part = ((size_t)r * 2 + (begins ? 0 : 1)) * HV + hv;
+#pragma unroll 1
+    for (int h = warp; h < nh; h += kWarps) {
+      float M = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) M = fmaxf(M, sml[i][h][0]);
+      float e[kWarps], L = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        e[i] = sml[i][h][0] == -INFINITY ? 0.f : fast_exp2(sml[i][h][0] - M);
+        L += e[i] * sml[i][h][1];
+      }
+      const float f = whole ? (L == 0.f ? 0.f : vs / L) : 1.f;
+      for (int d = 2 * lane; d < D; d += 64) {
+        float2 a = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+          const float2 y = *reinterpret_cast<const float2*>(&so[i][h][d]);
+          a.x += e[i] * y.x;
+          a.y += e[i] * y.y;
+        }
+        if (whole) {
+          const uint32_t y = p.q_bf16 ? pack_bf16(a.x * f, a.y * f) : pack_f16(a.x * f, a.y * f);
+          *reinterpret_cast<uint32_t*>(p.out + (((size_t)b * p.Hq + kvh * p.G + h0 + h) * D + d) * 2) = y;
+        } else {
+          *reinterpret_cast<float2*>(p.part_o + (part * p.hpg + h) * D + d) = a;
+        }
+      }
+      if (lane == 0) {
+        if (!whole)
+          *reinterpret_cast<float2*>(p.part_ml + (part * p.hpg + h) * 2) = make_float2(M, L);
+        else if (p.lse)
+          p.lse[(size_t)b * p.Hq + kvh * p.G + h0 + h] =
+              L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+      }
+    }
+    if (!whole) {
+      // ---- the last CTA of the sequence's parts joins them, in their order
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        int32_t* cnt = p.counters + (size_t)b * HV + hv;
+        s_last = atomicAdd(cnt, 1) == r_last - r_first;
+        if (s_last) *cnt = 0;  // ready for the next call
+        __threadfence();
+      }
+      __syncthreads();
+      if (s_last)
+        join<D>(p, b, r_first, r_last - r_first + 1, cut(seg.W, r_first, seg.nr) != at, hv, nh);
+    }
+    // ---- the next sequence that has units
+    __syncthreads();  // the shared parts and the control block are free
+    if (at + units >= seg.w1) return;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      int nb = b + 1;
+      while (units_of(p, stored(p, nb)) == 0) ++nb;  // there is one: units are left
+      seg.w = seg.at = at + units;
+      seg.b = nb;
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ host side
+int num_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 152;
+  return n;
+}
+
+struct DecodePlan {
+  int G, groups, hpg, nt, ranges;
+};
+
+constexpr int kMostPerSm = 4;  // CTAs of any instance on an SM
+
+// CTAs an SM holds at the instance's register bound
+constexpr int per_sm(bool e4m3, int D, int nt) {
+  return D == 256 || nt == 2 ? 2 : e4m3 && D == 64 ? 4 : 3;
+}
+
+bool make_plan(int B, int Hq, int Hkv, int D, int occ, DecodePlan* pl) {
+  if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv) return false;
+  pl->G = Hq / Hkv;
+  const int most = D == 256 ? 8 : 16;
+  pl->groups = (pl->G + most - 1) / most;
+  pl->hpg = (pl->G + pl->groups - 1) / pl->groups;
+  pl->groups = (pl->G + pl->hpg - 1) / pl->hpg;
+  pl->nt = pl->hpg > 8 ? 2 : 1;
+  pl->ranges = std::max(1, num_sms() * occ / (Hkv * pl->groups));
+  return true;
+}
+
+size_t ws_layout(const DecodePlan& pl, int Hkv, int D, size_t* off_o, size_t* off_ml) {
+  const size_t rows = (size_t)pl.ranges * 2 * Hkv * pl.groups * pl.hpg;
+  size_t off = sizeof(WsHeader) + (size_t)kMaxCounters * sizeof(int32_t);
+  *off_o = off;
+  off += (rows * D * sizeof(float) + 255) / 256 * 256;
+  *off_ml = off;
+  off += (rows * 2 * sizeof(float) + 255) / 256 * 256;
+  return off;
+}
+
+template <int CT, int D, int NT>
+spec_status launch(const DecodeParams& p, cudaStream_t st) {
+  constexpr int kOcc = per_sm(CT == kE4m3, D, NT);
+  decode_kernel<CT, D, NT, kOcc><<<p.ranges * p.Hkv * p.groups, kThreads, 0, st>>>(p);
+  return launch_status();
+}
+
+template <int CT>
+spec_status launch_d(const DecodeParams& p, int D, int nt, cudaStream_t st) {
+  if (D == 64) return nt == 1 ? launch<CT, 64, 1>(p, st) : launch<CT, 64, 2>(p, st);
+  if (D == 128) return nt == 1 ? launch<CT, 128, 1>(p, st) : launch<CT, 128, 2>(p, st);
+  return launch<CT, 256, 1>(p, st);
+}
+
+}  // namespace
+
+extern "C" size_t spec_decode_attn_workspace_size(int B, int Hq, int Hkv, int D) {
+  DecodePlan pl;
+  if ((D != 64 && D != 128 && D != 256) || !make_plan(B, Hq, Hkv, D, kMostPerSm, &pl)) return 0;
+  size_t a, c;
+  return ws_layout(pl, Hkv, D, &a, &c);
+}
+
+extern "C" spec_status spec_decode_attn(const void* q, int64_t q_stride_b, int64_t q_stride_h,
+                                        spec_dtype q_dtype, const void* k_cache,
+                                        const void* v_cache, spec_dtype cache_dtype,
+                                        const float* k_scale, const float* v_scale, int num_pages,
+                                        int page_size, int64_t page_stride, int64_t token_stride,
+                                        int64_t head_stride, const int32_t* block_table,
+                                        int max_pages, const int32_t* seq_len, int B, int Hq,
+                                        int Hkv, int D, int window, float scale, void* workspace,
+                                        size_t workspace_bytes, void* out, float* lse_out,
+                                        void* stream) {
+  if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || num_pages < 1 || page_size < 1 || max_pages < 1 ||
+      window < 0)
+    return SPEC_EINVAL;
+  if (q_dtype == SPEC_F32 || cache_dtype == SPEC_F32) return SPEC_EUNSUPPORTED;
+  if (q_dtype != SPEC_BF16 && q_dtype != SPEC_F16) return SPEC_EINVAL;
+  const bool e4m3 = cache_dtype == SPEC_E4M3;
+  if (!e4m3 && cache_dtype != q_dtype) return SPEC_EINVAL;
+  if (!e4m3 && (k_scale || v_scale)) return SPEC_EINVAL;
+  if (D != 64 && D != 128 && D != 256) return SPEC_EUNSUPPORTED;
+  if (B == 0) return SPEC_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !seq_len || !workspace || !out)
+    return SPEC_EINVAL;
+  const int es = e4m3 ? 1 : 2;
+  if (((uintptr_t)q | (uintptr_t)k_cache | (uintptr_t)v_cache | (uintptr_t)out) & 15)
+    return SPEC_EINVAL;
+  if ((uintptr_t)workspace & 255) return SPEC_EINVAL;
+  if (q_stride_b < 0 || q_stride_h < 0 || page_stride < 0 || token_stride < 1 || head_stride < 0)
+    return SPEC_EINVAL;
+  if (((q_stride_b | q_stride_h) * 2 | (page_stride | token_stride | head_stride) * es) & 15)
+    return SPEC_EINVAL;
+  // cache rows are numbered in token strides, in 31 bits
+  if (page_stride % token_stride || token_stride * es > UINT32_MAX) return SPEC_EUNSUPPORTED;
+  const int64_t page_rows = page_stride / token_stride;
+  if (page_rows > INT32_MAX || (page_rows * (num_pages - 1) + page_size) > INT32_MAX ||
+      (long long)max_pages * page_size > INT32_MAX)
+    return SPEC_EUNSUPPORTED;
+  DecodePlan pl;
+  if (!make_plan(B, Hq, Hkv, D, 1, &pl)) return SPEC_EINVAL;
+  make_plan(B, Hq, Hkv, D, per_sm(e4m3, D, pl.nt), &pl);
+  if ((long long)B * Hkv * pl.groups > kMaxCounters) return SPEC_EUNSUPPORTED;
+  size_t off_o, off_ml;
+  if (workspace_bytes < ws_layout(pl, Hkv, D, &off_o, &off_ml)) return SPEC_EINVAL;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  DecodeParams p{};
+  p.q = static_cast<const char*>(q);
+  p.k = static_cast<const char*>(k_cache);
+  p.v = static_cast<const char*>(v_cache);
+  p.table = block_table;
+  p.seq_len = seq_len;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.out = static_cast<char*>(out);
+  p.lse = lse_out;
+  p.counters = reinterpret_cast<int32_t*>(ws + sizeof(WsHeader));
+  p.part_o = reinterpret_cast<float*>(ws + off_o);
+  p.part_ml = reinterpret_cast<float*>(ws + off_ml);
+  p.q_stride_b = q_stride_b;
+  p.q_stride_h = q_stride_h;
+  p.head_stride = head_stride * es;
+  p.token_stride = (uint32_t)(token_stride * es);
+  p.page_rows = (uint32_t)page_rows;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = pl.G;
+  p.groups = pl.groups;
+  p.hpg = pl.hpg;
+  p.P = page_size;
+  p.num_pages = num_pages;
+  p.max_pages = max_pages;
+  p.window = window;
+  p.ranges = pl.ranges;
+  p.q_bf16 = q_dtype == SPEC_BF16;
+  p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * kLog2e;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (e4m3) return launch_d<kE4m3>(p, D, pl.nt, st);
+  return p.q_bf16 ? launch_d<kBf16>(p, D, pl.nt, st) : launch_d<kF16>(p, D, pl.nt, st);
+}

@@ -1,0 +1,325 @@
+// Pages, block tables and slots of a step, built on the GPU from lengths alone.
+//
+//  spec_extend_tables -- with have = ceil(ctx / P), want = ceil((ctx + add) / P),
+//    need = want - have and upto = the inclusive running sum of need over the
+//    sequences, sequence b is served iff its lengths are valid and (need = 0 or
+//    upto[b] <= free pages); its j-th new page is entry count - 1 -
+//    (upto[b] - need[b] + j) of the free list.  Token t of the packed rows
+//    belongs to the b with cu[b] <= t < cu[b + 1], sits at position
+//    ctx[b] + t - cu[b] and at slot page * P + position % P.
+//  spec_release_pages -- the same running sum over the pages behind the kept
+//    ones gives each sequence its place at the free list's end.
+//
+// What bounds them: latency.  A step moves a few KB to a few MB (12 bytes a
+// token, 8 a page), so the cost is the chain lengths -> running sums -> free
+// list -> store.  One launch each, no workspace and no grid-wide wait: every
+// CTA forms the running sums of ALL sequences again in its shared memory (at
+// most 8192 lengths, from L2) and then writes its share, so nothing passes
+// between CTAs.  A token's page comes from the old table entry or straight from
+// the free list, never from an entry that this launch writes.  The counts are
+// read from one word and written to another for the same reason.
+#include <climits>
+
+#include "common.cuh"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxSeqs = 8192;      // two running sums of 4 bytes: 64 KB of shared memory
+constexpr int kTokensPerThread = 4;
+constexpr int kWarpPages = 64;      // more pages than this: the whole CTA writes the row
+
+// Exclusive running sum over the block of one value per thread; *total: the sum.
+SPEC_DEV long long block_scan(long long v, long long* total) {
+  __shared__ long long part[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // `part` of an earlier call is read no more
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  long long before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += part[w];
+    sum += part[w];
+  }
+  *total = sum;
+  return before + x - v;
+}
+
+SPEC_DEV long long ceil_div(long long a, int b) { return (a + b - 1) / b; }
+
+SPEC_DEV int clamp_count(int c, int n) { return c < 0 ? 0 : c > n ? n : c; }
+
+struct ExtendParams {
+  const int32_t *ctx, *add, *free_list, *free_count;
+  int32_t *table, *positions, *cu, *new_len, *free_left, *status;
+  int64_t* slots;
+  int B, P, max_pages, num_pages, cap;
+};
+
+__global__ void __launch_bounds__(kThreads) extend_tables_kernel(const ExtendParams p) {
+  extern __shared__ int32_t sm[];
+  int32_t* tok = sm;             // [B + 1] first row of each sequence (at most cap + 1)
+  int32_t* pg = sm + p.B + 1;    // [B] pages of the step in front of it; < 0: refused (-1 - bit)
+  const int count = clamp_count(*p.free_count, p.num_pages);
+
+  // ---- running sums; a thread holds `per` consecutive sequences
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+  long long sum = 0, total;
+  for (int b = b0; b < b1; ++b) sum += max(p.add[b], 0);
+  long long at = block_scan(sum, &total);
+  long long need_sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const long long c = p.ctx[b], a = p.add[b];
+    tok[b] = (int32_t)min(at, (long long)p.cap + 1);
+    if (blockIdx.x == 0) p.cu[b] = (int32_t)min(at, (long long)INT_MAX);
+    at += max(a, 0ll);
+    const long long want = ceil_div(c + a, p.P);
+    const bool bad = c < 0 || a < 0 || want > p.max_pages || at > p.cap;
+    const int need = bad ? 0 : (int)(want - ceil_div(c, p.P));
+    pg[b] = bad ? INT_MIN : need;
+    need_sum += need;
+  }
+  if (threadIdx.x == 0) {
+    tok[p.B] = (int32_t)min(total, (long long)p.cap + 1);
+    if (blockIdx.x == 0) p.cu[p.B] = (int32_t)min(total, (long long)INT_MAX);
+  }
+  long long dummy;
+  long long pages = block_scan(need_sum, &dummy);
+  long long taken = 0;   // the largest running sum that fits: what the step takes
+  for (int b = b0; b < b1; ++b) {
+    const int need = pg[b];
+    if (need == INT_MIN) {
+      pg[b] = -1 - SPEC_SEQ_BAD_LEN;
+      continue;
+    }
+    const bool fits = need == 0 || pages + need <= count;
+    if (fits && need) taken = pages + need;
+    pg[b] = fits ? (int32_t)min(pages, (long long)INT_MAX) : -1 - SPEC_SEQ_NO_PAGES;
+    pages += need;
+  }
+  if (blockIdx.x == 0) {  // at most one thread's sequences end the served prefix
+    __shared__ int most;
+    if (threadIdx.x == 0) most = 0;
+    __syncthreads();
+    if (taken) atomicMax(&most, (int)taken);
+    __syncthreads();
+    if (threadIdx.x == 0) *p.free_left = count - most;
+  }
+  __syncthreads();
+
+  // ---- new pages into the table rows, lengths and statuses
+  auto row = [&](int b, int lane, int lanes) {
+    const int c = p.ctx[b], n = p.add[b];
+    const int have = (int)ceil_div(c, p.P), need = (int)(ceil_div((long long)c + n, p.P) - have);
+    int32_t* t = p.table + (size_t)b * p.max_pages;
+    bool bad = false;
+    if (lane == 0 && n > 0 && c % p.P) {  // the page the first new token falls into
+      const int id = t[have - 1];
+      bad = id < 0 || id >= p.num_pages;
+    }
+    for (int j = lane; j < need; j += lanes) {
+      const int id = p.free_list[count - 1 - (pg[b] + j)];
+      t[have + j] = id;
+      bad = bad || id < 0 || id >= p.num_pages;
+    }
+    return bad;
+  };
+  auto finish = [&](int b, bool bad) {
+    p.status[b] = bad ? SPEC_SEQ_BAD_PAGE : 0;
+    p.new_len[b] = bad ? p.ctx[b] : p.ctx[b] + p.add[b];
+  };
+  auto pages_of = [&](int b) {
+    const int c = p.ctx[b];
+    return ceil_div((long long)c + p.add[b], p.P) - ceil_div(c, p.P);
+  };
+  const int lane = threadIdx.x & 31;
+  for (int b = blockIdx.x * kWarps + (threadIdx.x >> 5); b < p.B; b += gridDim.x * kWarps) {
+    if (pg[b] < 0) {
+      if (lane == 0) {
+        p.status[b] = -1 - pg[b];
+        p.new_len[b] = p.ctx[b];
+      }
+    } else if (pages_of(b) <= kWarpPages) {
+      const bool bad = __any_sync(0xffffffffu, row(b, lane, 32));
+      if (lane == 0) finish(b, bad);
+    }
+  }
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (pg[b] < 0 || pages_of(b) <= kWarpPages) continue;
+    const bool bad = __syncthreads_or(row(b, threadIdx.x, kThreads));
+    if (threadIdx.x == 0) finish(b, bad);
+  }
+
+  // ---- slots and positions: consecutive rows per thread, one search each
+  for (long long t0 = ((long long)blockIdx.x * kThreads + threadIdx.x) * kTokensPerThread;
+       t0 < p.cap; t0 += (long long)gridDim.x * kThreads * kTokensPerThread) {
+    int lo = 0, hi = p.B;  // the last b with tok[b] <= t0 (rows behind the last: B)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (tok[mid] <= t0)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    int b = lo;
+#pragma unroll
+    for (int u = 0; u < kTokensPerThread; ++u) {
+      const int t = (int)t0 + u;
+      if (t >= p.cap) break;
+      while (b < p.B && tok[b + 1] <= t) ++b;
+      int64_t slot = -1;
+      int pos = -1;
+      if (b < p.B && pg[b] >= 0) {
+        const int c = p.ctx[b];
+        pos = c + (t - tok[b]);
+        const int idx = pos / p.P, have = (int)ceil_div(c, p.P);
+        const int id = idx < have ? p.table[(size_t)b * p.max_pages + idx]
+                                  : p.free_list[count - 1 - (pg[b] + idx - have)];
+        if (id >= 0 && id < p.num_pages)
+          slot = (int64_t)id * p.P + pos % p.P;
+        else
+          pos = -1;
+      }
+      p.slots[t] = slot;
+      p.positions[t] = pos;
+    }
+  }
+}
+
+struct ReleaseParams {
+  const int32_t *table, *len, *keep, *free_count;
+  int32_t *free_list, *free_total, *status;
+  int B, P, max_pages, num_pages;
+};
+
+__global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleaseParams p) {
+  extern __shared__ int32_t sm[];
+  int32_t* at = sm;  // [B] place of the sequence's first page on the list; < 0: refused
+  const int count = clamp_count(*p.free_count, p.num_pages);
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+  long long sum = 0, dummy;
+  for (int b = b0; b < b1; ++b) {
+    const long long n = p.len[b], k = p.keep[b], held = ceil_div(n, p.P);
+    const bool bad = n < 0 || k < 0 || k > held || held > p.max_pages;
+    at[b] = bad ? INT_MIN : (int)(held - k);
+    if (!bad) sum += held - k;
+  }
+  long long pages = count + block_scan(sum, &dummy);
+  long long end = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int n = at[b];
+    if (n == INT_MIN) {
+      at[b] = -1 - SPEC_SEQ_BAD_LEN;
+      continue;
+    }
+    const bool fits = n == 0 || pages + n <= p.num_pages;
+    if (fits && n) end = pages + n;
+    at[b] = fits ? (int32_t)min(pages, (long long)INT_MAX) : -1 - SPEC_SEQ_NO_PAGES;
+    pages += n;
+  }
+  if (blockIdx.x == 0) {
+    __shared__ int most;
+    if (threadIdx.x == 0) most = count;
+    __syncthreads();
+    if (end) atomicMax(&most, (int)end);
+    __syncthreads();
+    if (threadIdx.x == 0) *p.free_total = most;
+  }
+  __syncthreads();
+
+  auto row = [&](int b, int n, int lane, int lanes) {
+    const int32_t* t = p.table + (size_t)b * p.max_pages + p.keep[b];
+    bool bad = false;
+    for (int j = lane; j < n; j += lanes) {
+      const int id = t[j];
+      const bool ok = id >= 0 && id < p.num_pages;
+      p.free_list[at[b] + j] = ok ? id : -1;
+      bad = bad || !ok;
+    }
+    return bad;
+  };
+  auto pages_of = [&](int b) { return (int)(ceil_div(p.len[b], p.P) - p.keep[b]); };
+  const int lane = threadIdx.x & 31;
+  for (int b = blockIdx.x * kWarps + (threadIdx.x >> 5); b < p.B; b += gridDim.x * kWarps) {
+    int st = 0;
+    if (at[b] < 0) {
+      st = -1 - at[b];
+    } else {
+      const int n = pages_of(b);
+      if (n > kWarpPages) continue;
+      if (__any_sync(0xffffffffu, row(b, n, lane, 32))) st = SPEC_SEQ_BAD_PAGE;
+    }
+    if (lane == 0 && p.status) p.status[b] = st;
+  }
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (at[b] < 0) continue;
+    const int n = pages_of(b);
+    if (n <= kWarpPages) continue;
+    const bool bad = __syncthreads_or(row(b, n, threadIdx.x, kThreads));
+    if (threadIdx.x == 0 && p.status) p.status[b] = bad ? SPEC_SEQ_BAD_PAGE : 0;
+  }
+}
+
+// CTAs: a warp per sequence, four rows per thread, at most two per SM
+int grid_for(int B, long long tokens) {
+  const long long a = (B + kWarps - 1) / kWarps;
+  const long long t = (tokens + kThreads * kTokensPerThread - 1) / (kThreads * kTokensPerThread);
+  const long long g = a > t ? a : t;
+  return (int)(g < 1 ? 1 : g > 304 ? 304 : g);
+}
+
+}  // namespace
+
+extern "C" spec_status spec_extend_tables(const int32_t* ctx_len, const int32_t* add_len, int B,
+                                          int page_size, int32_t* block_table, int max_pages,
+                                          const int32_t* free_list, int num_pages,
+                                          const int32_t* free_count, int max_tokens,
+                                          int64_t* slot_map, int32_t* positions, int32_t* cu_len,
+                                          int32_t* new_len, int32_t* free_left,
+                                          int32_t* status_per_seq, void* stream) {
+  if (B < 0 || page_size < 1 || max_pages < 1 || num_pages < 1 || max_tokens < 0)
+    return SPEC_EINVAL;
+  if (!free_list || !free_count || !cu_len || !free_left || free_left == free_count)
+    return SPEC_EINVAL;
+  if (B && (!ctx_len || !add_len || !block_table || !new_len || !status_per_seq))
+    return SPEC_EINVAL;
+  if (max_tokens && (!slot_map || !positions)) return SPEC_EINVAL;
+  if (B > kMaxSeqs || (long long)max_pages * page_size > INT_MAX || max_tokens == INT_MAX)
+    return SPEC_EUNSUPPORTED;
+  const size_t smem = (2 * (size_t)B + 1) * sizeof(int32_t);
+  static PerDeviceOnce<int> smem_once;  // once per device, at the largest size
+  const spec_status ra = ensure_smem_limit(smem_once, (const void*)extend_tables_kernel,
+                                           (2 * kMaxSeqs + 1) * (int)sizeof(int32_t));
+  if (ra != SPEC_OK) return ra;
+  const ExtendParams p{ctx_len, add_len,   free_list, free_count, block_table, positions, cu_len,
+                       new_len, free_left, status_per_seq, slot_map, B, page_size, max_pages,
+                       num_pages, max_tokens};
+  extend_tables_kernel<<<grid_for(B, max_tokens), kThreads, smem, (cudaStream_t)stream>>>(p);
+  return launch_status();
+}
+
+extern "C" spec_status spec_release_pages(const int32_t* block_table, int max_pages,
+                                          const int32_t* len, const int32_t* keep_pages, int B,
+                                          int page_size, int32_t* free_list, int num_pages,
+                                          const int32_t* free_count, int32_t* free_total,
+                                          int32_t* status_per_seq, void* stream) {
+  if (B < 0 || page_size < 1 || max_pages < 1 || num_pages < 1) return SPEC_EINVAL;
+  if (!free_list || !free_count || !free_total || free_total == free_count) return SPEC_EINVAL;
+  if (B && (!block_table || !len || !keep_pages)) return SPEC_EINVAL;
+  if (B > kMaxSeqs || (long long)max_pages * page_size > INT_MAX) return SPEC_EUNSUPPORTED;
+  const ReleaseParams p{block_table, len, keep_pages, free_count, free_list, free_total,
+                        status_per_seq, B, page_size, max_pages, num_pages};
+  release_pages_kernel<<<grid_for(B, 0), kThreads, (size_t)B * sizeof(int32_t),
+                         (cudaStream_t)stream>>>(p);
+  return launch_status();
+}
