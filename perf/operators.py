@@ -336,15 +336,20 @@ def run(state):
         import speculative_decoding_verification_76_gb300 as sv
         c = state["case"]
         if op == "tables":
-            e = sv.extend_tables(state["ctx_len"], state["add_len"], state["block_table"],
-                                 state["free_list"], state["free_count"], c["page"],
-                                 state["max_tokens"])
-            count, released = sv.release_pages(state["block_table"], e["new_len"],
-                                               state["keep_pages"], state["free_list"],
-                                               e["free_count"], c["page"])
-            left = e.pop("free_count")
-            return dict(e, block_table=state["block_table"], left=left,
-                        free_list=state["free_list"], free_count=count, released=released)
+            if "out" not in state:  # what a serving loop keeps: outputs, the list to release into
+                state["out"], state["pool"] = None, state["free_list"].clone()
+                state["total"] = torch.empty_like(state["free_count"])
+                state["released"] = torch.empty_like(state["ctx_len"])
+            e = state["out"] = sv.extend_tables(
+                state["ctx_len"], state["add_len"], state["block_table"], state["free_list"],
+                state["free_count"], c["page"], state["max_tokens"], out=state["out"])
+            count, released = sv.release_pages(
+                state["block_table"], e["new_len"], state["keep_pages"], state["pool"],
+                e["free_count"], c["page"], total=state["total"], status=state["released"])
+            out = dict(e, block_table=state["block_table"], left=e["free_count"],
+                       free_list=state["pool"], released=released)
+            out["free_count"] = count
+            return out
         if op == "append":
             q, k, v = _split(state)
             sv.append_tokens(k, v, state["k_cache"], state["v_cache"], state["slot_map"],
