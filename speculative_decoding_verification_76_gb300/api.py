@@ -61,9 +61,11 @@ class SamplerConfig:
                         1 if self.greedy else 0, int(self.eos_id))
 
 
-# the current stream's handle without a Stream object (2 us of host time a call)
+# the current stream's handle without a Stream object, and the current device without
+# the check that CUDA is up (2 us of host time a call): both are asked for CUDA tensors
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 _lib = None
 _P = ctypes.c_void_p
@@ -211,8 +213,8 @@ def kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.T
     (optional) lets the kernel check that the path follows the tree.
     Returns (new_len, keep_pages, status)."""
     lib = load()
-    if k_cache.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("caches must be bf16 or fp32")
+    if k_cache.dtype not in _DTYPE:
+        raise ValueError("caches must be bf16, fp16, fp32 or float8_e4m3fn")
     npg, P, Hkv, D = k_cache.shape
     _need(k_cache, "k_cache", k_cache.dtype)
     _need(v_cache, "v_cache", k_cache.dtype, k_cache.shape)
@@ -475,11 +477,7 @@ _DTYPE = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPE
 
 def _elsewhere(dev, stream):
     """True when the call has to change the current device or stream first."""
-    return stream is not None or dev.index != torch.cuda.current_device()
-
-
-def _here(dev):
-    return _raw_stream(dev.index)
+    return stream is not None or dev.index != _current_device()
 
 
 def _tensor(t, name, dev, dtype, shape):
@@ -507,42 +505,39 @@ def _rows(t, name, dev, dtype, heads, D):
     """[T, heads, D] rows whose heads lie side by side; returns (pointer, row stride)."""
     if not isinstance(t, torch.Tensor) or t.device != dev:
         raise ValueError(f"{name} must be a tensor on {dev}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+    if t.dim() != 3 or t.shape[1:] != (heads, D):
         raise ValueError(f"{name} must be [tokens, {heads}, {D}], got {tuple(t.shape)}")
-    st = t.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != D):
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != D and heads > 1):
         raise ValueError(f"{name}: a row's heads must lie side by side")
-    return t.data_ptr(), st[0]
+    return t.data_ptr(), s0
 
 
 def _caches(k_cache, v_cache, dev, dtype):
-    """Checks the pair; returns its (page, token, head) strides."""
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor) or t.device != dev:
-            raise ValueError(f"{name} must be a tensor on {dev}")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    """Checks the pair; returns (k, v, shape, dtype code, page, token, head strides)."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.device != dev:
+        raise ValueError(f"k_cache must be a tensor on {dev}")
+    if not isinstance(v_cache, torch.Tensor) or v_cache.device != dev:
+        raise ValueError(f"v_cache must be a tensor on {dev}")
+    shape, kind, st = k_cache.shape, k_cache.dtype, k_cache.stride()
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("caches must be [pages, page_size, Hkv, D], both alike")
-    if v_cache.dtype != k_cache.dtype:
+    if v_cache.dtype is not kind:
         raise ValueError("k_cache and v_cache must have one dtype")
-    if k_cache.dtype != dtype and (k_cache.dtype != torch.float8_e4m3fn
-                                   or dtype == torch.float32):
-        raise ValueError(f"caches must be {dtype}" + ("" if dtype == torch.float32
+    if kind is not dtype and (kind is not torch.float8_e4m3fn or dtype is torch.float32):
+        raise ValueError(f"caches must be {dtype}" + ("" if dtype is torch.float32
                                                       else " or float8_e4m3fn"))
-    st = k_cache.stride()
     if st[3] != 1 or v_cache.stride() != st:
         raise ValueError("caches must have the same strides, 1 over D")
-    return st
+    return k_cache.data_ptr(), v_cache.data_ptr(), shape, _DTYPE[kind], st[0], st[1], st[2]
 
 
-def _scales(k_scale, v_scale, k_cache, dev):
-    if k_scale is None and v_scale is None:
-        return None, None
-    if k_cache.dtype != torch.float8_e4m3fn:
+def _scales(k_scale, v_scale, kind, Hkv, dev):
+    if kind != SPEC_E4M3:
         raise ValueError("scales belong to float8_e4m3fn caches")
-    shape = k_cache.shape[2:3]
-    return tuple(None if t is None else _tensor(t, name, dev, torch.float32, shape)
+    return tuple(None if t is None else _tensor(t, name, dev, torch.float32, (Hkv,))
                  for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")))
 
 
@@ -577,14 +572,14 @@ def extend_tables(ctx_len, add_len, block_table, free_list, free_count, page_siz
                    positions=torch.empty(max_tokens, dtype=i32, device=dev), cu_len=cu,
                    new_len=new_len, free_count=left, status=status)
     _check("spec_extend_tables",
-           load().spec_extend_tables(
+           (_lib or load()).spec_extend_tables(
                *ins, B, page_size, table, width, lst, n, cnt, max_tokens,
                _tensor(out["slot_map"], "slot_map", dev, torch.int64, (max_tokens,)),
                _tensor(out["positions"], "positions", dev, i32, (max_tokens,)),
                _tensor(out["cu_len"], "cu_len", dev, i32, (B + 1,)),
                _tensor(out["new_len"], "new_len", dev, i32, (B,)),
                _tensor(out["free_count"], "free_count", dev, i32, (1,)),
-               _tensor(out["status"], "status", dev, i32, (B,)), _here(dev)))
+               _tensor(out["status"], "status", dev, i32, (B,)), _raw_stream(dev.index)))
     return out
 
 
@@ -611,9 +606,9 @@ def release_pages(block_table, length, keep_pages, free_list, free_count, page_s
     total = torch.empty(1, dtype=i32, device=dev) if total is None else total
     status = torch.empty(B, dtype=i32, device=dev) if status is None else status
     _check("spec_release_pages",
-           load().spec_release_pages(table, width, held, keep, B, page_size, lst, n, cnt,
+           (_lib or load()).spec_release_pages(table, width, held, keep, B, page_size, lst, n, cnt,
                                      _tensor(total, "total", dev, i32, (1,)),
-                                     _tensor(status, "status", dev, i32, (B,)), _here(dev)))
+                                     _tensor(status, "status", dev, i32, (B,)), _raw_stream(dev.index)))
     return total, status
 
 
@@ -629,10 +624,9 @@ def append_tokens(k_new, v_new, k_cache, v_cache, slot_map, positions=None, q=No
             return append_tokens(k_new, v_new, k_cache, v_cache, slot_map, positions, q, q_out,
                                  rope_base, k_scale, v_scale)
     dt = k_new.dtype
-    if dt not in _DTYPE or dt == torch.float8_e4m3fn:
+    if dt not in _DTYPE or dt is torch.float8_e4m3fn:
         raise ValueError("k_new must be bf16, fp16 or fp32")
-    sp, st, sh, _ = _caches(k_cache, v_cache, dev, dt)
-    npg, P, Hkv, D = k_cache.shape
+    kc, vc, (npg, P, Hkv, D), kind, sp, st, sh = _caches(k_cache, v_cache, dev, dt)
     k, ks = _rows(k_new, "k_new", dev, dt, Hkv, D)
     v, vs = _rows(v_new, "v_new", dev, dt, Hkv, D)
     T = k_new.shape[0]
@@ -657,12 +651,14 @@ def append_tokens(k_new, v_new, k_cache, v_cache, slot_map, positions=None, q=No
             raise ValueError("q_out and q must have the same rows")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    sk, sv = _scales(k_scale, v_scale, k_cache, dev)
-    _check("spec_append_tokens",
-           load().spec_append_tokens(k, ks, v, vs, qp, qs, op, os_, _DTYPE[dt],
-                                     k_cache.data_ptr(), v_cache.data_ptr(),
-                                     _DTYPE[k_cache.dtype], sk, sv, npg, P, sp, st, sh, slots,
-                                     pos, T, Hq, Hkv, D, rope_base, _here(dev)))
+    sk = sv = None
+    if k_scale is not None or v_scale is not None:
+        sk, sv = _scales(k_scale, v_scale, kind, Hkv, dev)
+    rc = (_lib or load()).spec_append_tokens(k, ks, v, vs, qp, qs, op, os_, _DTYPE[dt], kc, vc,
+                                             kind, sk, sv, npg, P, sp, st, sh, slots, pos, T, Hq,
+                                             Hkv, D, rope_base, _raw_stream(dev.index))
+    if rc:
+        _check("spec_append_tokens", rc)
     return q_out
 
 
@@ -683,13 +679,12 @@ def decode_attn(q, k_cache, v_cache, block_table, seq_len, scale: float = 0.0, w
             return decode_attn(q, k_cache, v_cache, block_table, seq_len, scale, window, k_scale,
                                v_scale, workspace, out, lse)
     dt = q.dtype
-    if dt != torch.bfloat16 and dt != torch.float16:
+    if dt is not torch.bfloat16 and dt is not torch.float16:
         raise ValueError("q must be bf16 or fp16")
     if q.dim() != 3 or q.stride(2) != 1:
         raise ValueError("q must be [B, Hq, D], contiguous over D")
     B, Hq, D = q.shape
-    sp, st, sh, _ = _caches(k_cache, v_cache, dev, dt)
-    npg, P, Hkv, D2 = k_cache.shape
+    kc, vc, (npg, P, Hkv, D2), kind, sp, st, sh = _caches(k_cache, v_cache, dev, dt)
     if D2 != D:
         raise ValueError("head_dim mismatch")
     if block_table.dim() != 2:
@@ -697,22 +692,30 @@ def decode_attn(q, k_cache, v_cache, block_table, seq_len, scale: float = 0.0, w
     width = block_table.shape[1]
     table = _tensor(block_table, "block_table", dev, torch.int32, (B, width))
     lens = _tensor(seq_len, "seq_len", dev, torch.int32, (B,))
-    sk, sv = _scales(k_scale, v_scale, k_cache, dev)
-    lib = load()
+    sk = sv = None
+    if k_scale is not None or v_scale is not None:
+        sk, sv = _scales(k_scale, v_scale, kind, Hkv, dev)
+    lib = _lib or load()
     if workspace is None:
         workspace = new_workspace(lib.spec_decode_attn_workspace_size(B, Hq, Hkv, D), dev)
-    elif workspace.device != dev or workspace.dtype != torch.uint8 \
+    elif workspace.device != dev or workspace.dtype is not torch.uint8 \
             or not workspace.is_contiguous():
         raise ValueError("workspace must come from new_workspace on q's device")
     if out is None:
         out = torch.empty((B, Hq, D), dtype=dt, device=dev)
+        o = out.data_ptr()
+    else:
+        o = _tensor(out, "out", dev, dt, (B, Hq, D))
     if lse is None:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-    _check("spec_decode_attn",
-           lib.spec_decode_attn(q.data_ptr(), q.stride(0), q.stride(1), _DTYPE[dt],
-                                k_cache.data_ptr(), v_cache.data_ptr(), _DTYPE[k_cache.dtype], sk,
-                                sv, npg, P, sp, st, sh, table, width, lens, B, Hq, Hkv, D, window,
-                                scale, workspace.data_ptr(), workspace.numel(),
-                                _tensor(out, "out", dev, dt, (B, Hq, D)),
-                                _tensor(lse, "lse", dev, torch.float32, (B, Hq)), _here(dev)))
+        ls = lse.data_ptr()
+    else:
+        ls = _tensor(lse, "lse", dev, torch.float32, (B, Hq))
+    s0, s1, _ = q.stride()
+    rc = lib.spec_decode_attn(q.data_ptr(), s0, s1, _DTYPE[dt], kc, vc, kind, sk, sv, npg, P, sp,
+                              st, sh, table, width, lens, B, Hq, Hkv, D, window, scale,
+                              workspace.data_ptr(), workspace.numel(), o, ls,
+                              _raw_stream(dev.index))
+    if rc:
+        _check("spec_decode_attn", rc)
     return out, lse

@@ -38,7 +38,8 @@ struct AppendParams {
   const int32_t* pos;
   long long k_stride, v_stride, q_stride, q_out_stride;          // elements
   long long page_stride, token_stride, head_stride, num_slots;   // elements, slots
-  int P, T, Hq, Hkv, rotate;
+  FastDiv P;
+  int T, Hq, Hkv, rotate;
   uint64_t turn[kMaxD / 2];  // 2^64 x turns per position, of each pair
 };
 
@@ -101,7 +102,9 @@ __global__ void __launch_bounds__(kThreads) append_tokens_kernel(
     if (t < p.T) {
       const long long slot = p.slots[t];
       if (slot >= 0 && slot < p.num_slots && !(p.rotate && p.pos[t] < 0))
-        off = slot / p.P * p.page_stride + slot % p.P * p.token_stride;
+        off = p.num_slots <= 1u << 31 ? p.P.quot((int)slot) * p.page_stride +
+                                            ((int)slot - p.P.quot((int)slot) * p.P.d) * p.token_stride
+                                      : slot / p.P.d * p.page_stride + slot % p.P.d * p.token_stride;
     }
     dst[threadIdx.x] = off;
   }
@@ -221,7 +224,7 @@ extern "C" spec_status spec_append_tokens(
   p.token_stride = token_stride;
   p.head_stride = head_stride;
   p.num_slots = (long long)num_pages * page_size;
-  p.P = page_size;
+  p.P = FastDiv(page_size);
   p.T = T;
   p.Hq = q ? Hq : 0;
   p.Hkv = Hkv;

@@ -224,6 +224,28 @@ SPEC_DEV float fast_exp2(float x) {
   return y;
 }
 
+// x / d for 0 <= x < 2^31 and a divisor the host knows: with 2^s >= d the
+// multiplier m = ceil(2^(31+s) / d) errs by m d - 2^(31+s) < d <= 2^s, and
+// x times that error stays below 2^(31+s), so floor(x m / 2^(31+s)) is exact.
+// (The compiler's own division by a variable is some twenty instructions, and
+// short kernels pay for code they have to fetch.)
+struct FastDiv {
+  uint32_t mul, shift;
+  int d;
+  FastDiv() = default;
+  explicit FastDiv(int div) : d(div) {
+    uint32_t s = 0;
+    while (s < 31 && (1u << s) < (uint32_t)div) ++s;
+    shift = 31 + s;
+    mul = (uint32_t)(((1ull << shift) + div - 1) / div);
+  }
+  SPEC_DEV int quot(int x) const { return (int)(((uint64_t)(uint32_t)x * mul) >> shift); }
+  SPEC_DEV int ceil_quot(int x) const {
+    const int q = quot(x);
+    return q + (q * d != x);
+  }
+};
+
 SPEC_DEV float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));

@@ -35,6 +35,7 @@
 // output's own rounding.  The reference m of a row stays until a score exceeds
 // it by 15 (it is set 7 below the maximum: P stays in fp16's range).
 #include <algorithm>
+#include <atomic>
 
 #include <cuda_fp16.h>
 
@@ -62,13 +63,18 @@ struct DecodeParams {
   long long head_stride;                     // bytes
   uint32_t token_stride;                     // bytes
   uint32_t page_rows;                        // page stride in token strides
-  int B, Hq, Hkv, G, groups, hpg, P, num_pages, max_pages, window, ranges, q_bf16;
+  FastDiv P;                                 // page size
+  int B, Hq, Hkv, G, groups, hpg, num_pages, max_pages, window, ranges, q_bf16;
   float scale_log2;
 };
 
 // What is read in the place of positions that are not seen: an address instead of
-// a predicate on every load (a predicated load leaves its registers live).
-__device__ __align__(512) char kZeros[512];
+// a branch or a predicate around the loads, which made the compiler wait for them
+// there or keep their registers live (64 ragged sequences: 415 against 318 us).
+// One row per warp of a few hundred, so that the reads behind the last tiles do not
+// all ask one L2 slice (one row for all: 4 us at the end of each CTA).
+constexpr int kZeroRows = 512;
+__device__ __align__(512) char g_zeros[kZeroRows * 512];
 
 enum Cache { kBf16, kF16, kE4m3 };
 
@@ -130,7 +136,7 @@ SPEC_DEV int seen_from(const DecodeParams& p, int n) {
 // stored tokens of sequence b (never more than its table row can name)
 SPEC_DEV int stored(const DecodeParams& p, int b) {
   const int n = p.seq_len[b];
-  return n < 0 ? 0 : min(n, p.max_pages * p.P);
+  return n < 0 ? 0 : min(n, p.max_pages * p.P.d);
 }
 
 SPEC_DEV int units_of(const DecodeParams& p, int n) {
@@ -154,38 +160,17 @@ struct Row {  // a lane's N consecutive floats of a part's row
   }
 };
 
-// Block-wide sum of one value per thread (all threads get it).
-SPEC_DEV long long block_sum(long long v, long long* sh) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) v += sh[w];
-  __syncthreads();
-  return v;
-}
-
-SPEC_DEV long long warp_scan(long long v, int lane) {  // inclusive
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += y;
+// The nr ranges that W units are cut into: the first W % nr have one unit more.
+struct Cuts {
+  int q, rem;
+  SPEC_DEV Cuts(int W, int nr) : q((uint32_t)W / (uint32_t)nr), rem(W - q * nr) {}
+  SPEC_DEV int begin(int r) const { return r * q + min(r, rem); }
+  SPEC_DEV int range_of(int unit) const {
+    const int longer = rem * (q + 1);  // units of the longer ranges
+    return unit < longer ? (uint32_t)unit / (uint32_t)(q + 1)
+                         : rem + (uint32_t)(unit - longer) / (uint32_t)q;
   }
-  return v;
-}
-
-// floor(W r / nr): where range r of nr begins (32-bit division where it does)
-SPEC_DEV long long cut(long long W, int r, int nr) {
-  return W < 1 << 20 ? (long long)((uint32_t)W * (uint32_t)r / (uint32_t)nr) : W * r / nr;
-}
-
-// the range that holds unit x: the largest r with floor(W r / nr) <= x
-SPEC_DEV int range_of(long long x, long long W, int nr) {
-  return W < 1 << 20 ? (int)(((uint32_t)(x + 1) * (uint32_t)nr - 1) / (uint32_t)W)
-                     : (int)(((x + 1) * nr - 1) / W);
-}
+};
 
 template <int CT, int D, int NT>
 struct Shape {
@@ -198,14 +183,14 @@ struct Shape {
   static constexpr int kSteps = D / 16;
 };
 
-// The parts of sequence b's head group, joined by one CTA in the parts' order:
-// a warp per head; lanes hold the weights of 32 parts at a time, and kFlight
-// parts' rows are loaded together.  `late`: the first part is its range's last
-// segment (slot 1).  Out of line: its registers are not the loop's.
+// The parts of sequence b's head group, joined by one CTA in the parts' order: a
+// warp per head, kFlight parts' rows loaded together (a part's row is an L2 round
+// trip away, and one after another 57 parts took 12 us).  `late`: the first part is
+// its range's last segment (slot 1).
 template <int D>
 __device__ __forceinline__ void join(const DecodeParams& p, int b, int r_first, int np, bool late,
                                   int hv, int nh) {
-  constexpr int kPer = D / 32, kFlight = kPer > 4 ? 8 : 16;
+  constexpr int kPer = D / 32, kFlight = kPer > 4 ? 16 : 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, HV = p.Hkv * p.groups;
   const int kvh = hv / p.groups, h0 = hv % p.groups * p.hpg;
   const float vs = p.v_scale ? p.v_scale[kvh] : 1.f;
@@ -214,38 +199,44 @@ __device__ __forceinline__ void join(const DecodeParams& p, int b, int r_first, 
     // row of part 0 of head h (in slot 0), and the rows from part to part
     const size_t row0 = ((size_t)r_first * 2 * HV + hv) * p.hpg + h;
     const int step = 2 * HV * p.hpg, slot1 = late ? HV * p.hpg : 0;
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + row0;
+    auto ml_of = [&](int i) {
+      return i < np ? __ldcg(ml + (size_t)i * step + (i == 0 ? slot1 : 0))
+                    : make_float2(-INFINITY, 0.f);
+    };
     float M = -INFINITY, L = 0.f, acc[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
 #pragma unroll 1
-    for (int i0 = 0; i0 < np; i0 += 32) {
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (i0 + lane < np)
-        ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + row0 +
-                    (size_t)(i0 + lane) * step + (i0 + lane == 0 ? slot1 : 0));
-      const float now = fmaxf(M, warp_max(ml.x));
-      const float a = M == -INFINITY ? 0.f : fast_exp2(M - now);
-      const float e = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - now);
-      M = now;
-      L = L * a + warp_sum(e * ml.y);
+    for (int j0 = 0; j0 < np; j0 += kFlight) {
+      // (loads clamped, not skipped: a skipped load's registers stay live)
+      Row<kPer> y[kFlight];
+      const float* src = p.part_o + (row0 + (size_t)j0 * step) * D;
+      const size_t first = j0 == 0 ? (size_t)slot1 * D : 0;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] *= a;
-      const int cnt = min(32, np - i0);
+      for (int j = 0; j < kFlight; ++j)
+        y[j].load(src + (size_t)(min(j, np - 1 - j0) * step) * D + (j == 0 ? first : 0), lane);
+      const float2 mine = ml_of(j0 + min(lane, kFlight));
+      if (j0 == 0) {  // the references and sums of all parts, under the first rows' loads
+        const float2 x0 = ml_of(lane), x1 = ml_of(lane + 32);  // all there is, as a rule
+        M = fmaxf(x0.x, x1.x);
 #pragma unroll 1
-      for (int j0 = 0; j0 < cnt; j0 += kFlight) {
-        Row<kPer> y[kFlight];
-        const float* src = p.part_o + (row0 + (size_t)(i0 + j0) * step) * D;
-        const size_t first = i0 + j0 == 0 ? (size_t)slot1 * D : 0;
+        for (int i = lane + 64; i < np; i += 32) M = fmaxf(M, ml_of(i).x);
+        M = warp_max(M);
+        auto weigh = [&](float2 x) { L += (x.x == -INFINITY ? 0.f : fast_exp2(x.x - M)) * x.y; };
+        weigh(x0);
+        weigh(x1);
+#pragma unroll 1
+        for (int i = lane + 64; i < np; i += 32) weigh(ml_of(i));
+        L = warp_sum(L);
+      }
+      const float e = mine.x == -INFINITY ? 0.f : fast_exp2(mine.x - M);
 #pragma unroll
-        for (int j = 0; j < kFlight; ++j)
-          y[j].load(src + (size_t)(min(j, cnt - 1 - j0) * step) * D + (j == 0 ? first : 0), lane);
+      for (int j = 0; j < kFlight; ++j) {
+        const float ej = __shfl_sync(0xffffffffu, e, j);
+        if (j0 + j < np) {
 #pragma unroll
-        for (int j = 0; j < kFlight; ++j) {
-          const float ej = __shfl_sync(0xffffffffu, e, (j0 + j) & 31);
-          if (j0 + j < cnt) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) acc[i] += ej * y[j].x[i];
-          }
+          for (int i = 0; i < kPer; ++i) acc[i] += ej * y[j].x[i];
         }
       }
     }
@@ -270,14 +261,16 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
   constexpr bool kBf = CT == kBf16;
   constexpr int NS = S::kSub, KP = S::kKPieces, VW = S::kVWords, VP = S::kVPieces;
   constexpr int kHeads = 8 * NT;
-  __shared__ __align__(16) float so[kWarps][kHeads][D];
+  // row (h & 1) * 4 + (h >> 1 & 3) of each eight is head h, two words apart modulo the
+  // banks: a warp's float2 stores touch each bank once per half
+  __shared__ __align__(16) float so[kWarps][kHeads][D + 2];
   __shared__ float sml[kWarps][kHeads][2];
-  __shared__ long long ssum[kWarps];
+  __shared__ int ssum[kWarps];
   // the segment being worked on: in shared memory, read again behind the barriers,
   // so that it holds no registers while the positions stream through
   __shared__ struct {
-    long long W, w, w1, at;  // the batch's units; this CTA's next and end; in front of b
-    int nr, b;
+    int W, nr, w, w1;  // the batch's units and ranges; this CTA's next unit and its end
+    int b, at;         // the sequence, and the units in front of it
   } seg;
   __shared__ int s_last;
 
@@ -287,64 +280,59 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n8 = lane >> 2, c4 = lane & 3;
   const int HV = p.Hkv * p.groups;
 
-  // ---- this CTA's units [w0, w1) of the batch's W, and the sequence that holds w0
-  auto nothing_seen = [&](int b) {  // zeros and -inf for this CTA's heads
-    for (int i = threadIdx.x; i < nh * D; i += kThreads)
-      reinterpret_cast<uint16_t*>(p.out)[((size_t)b * p.Hq + kvh * p.G + h0) * D + i] = 0;
-    if (p.lse && threadIdx.x < nh)
-      p.lse[(size_t)b * p.Hq + kvh * p.G + h0 + threadIdx.x] = -INFINITY;
-  };
-  if (p.B <= kThreads) {  // one sequence per thread: one load of the lengths, one scan
-    const int tid = threadIdx.x;
-    const int u = tid < p.B ? units_of(p, stored(p, tid)) : 0;
-    const bool idle = tid < p.B && u == 0;
-    const long long x = warp_scan(u, lane);
+  // ---- this CTA's units of the batch's W, and the sequence that holds the first:
+  // every thread takes `per` consecutive sequences of one running sum
+  {
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+    int mine = 0;
+    bool idle = false;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      const int u = units_of(p, stored(p, b));
+      mine += u;
+      idle = idle || u == 0;
+    }
+    int x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
     if (lane == 31) ssum[warp] = x;
-    const int idles = __syncthreads_count(idle && tid % p.ranges == r);
-    long long before = 0, W = 0;
+    const bool idles = __syncthreads_or(idle);
+    int before = 0, W = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) before += ssum[w];
       W += ssum[w];
     }
-    if (idles)
-      for (int b = r; b < p.B; b += p.ranges)
-        if (units_of(p, stored(p, b)) == 0) nothing_seen(b);
-    const int nr = (int)min((long long)p.ranges, W);
-    if (r >= nr) return;
-    const long long w0 = cut(W, r, nr), pre = before + x - u;
-    if (u > 0 && pre <= w0 && w0 < pre + u)
-      seg = {W, w0, cut(W, r + 1, nr), pre, nr, tid};
-    __syncthreads();
-  } else {
-    for (int b = r; b < p.B; b += p.ranges)
-      if (units_of(p, stored(p, b)) == 0) nothing_seen(b);
-    long long mine = 0;
-    for (int b = threadIdx.x; b < p.B; b += kThreads) mine += units_of(p, stored(p, b));
-    const long long W = block_sum(mine, ssum);
-    const int nr = (int)min((long long)p.ranges, W);
-    if (r >= nr) return;
-    const long long w0 = cut(W, r, nr);
-    long long base = 0;  // units in front of these kThreads sequences
-    for (int b0 = 0; b0 < p.B && base <= w0; b0 += kThreads) {
-      const int b = b0 + threadIdx.x;
-      const int u = b < p.B ? units_of(p, stored(p, b)) : 0;
-      const long long x = warp_scan(u, lane);
-      if (lane == 31) ssum[warp] = x;
-      __syncthreads();
-      long long before = base;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += ssum[w];
-        base += ssum[w];
+    if (idles) {  // rows that see nothing: zeros and -inf for this CTA's heads
+#pragma unroll 1
+      for (int b = r; b < p.B; b += p.ranges) {
+        if (units_of(p, stored(p, b)) != 0) continue;
+        const size_t row = (size_t)b * p.Hq + kvh * p.G + h0;
+#pragma unroll 1
+        for (int i = threadIdx.x; i < nh * D; i += kThreads)
+          reinterpret_cast<uint16_t*>(p.out)[row * D + i] = 0;
+        if (p.lse && threadIdx.x < nh) p.lse[row + threadIdx.x] = -INFINITY;
       }
-      const long long pre = before + x - u;
-      if (u > 0 && pre <= w0 && w0 < pre + u)
-        seg = {W, w0, cut(W, r + 1, nr), pre, nr, b};
-      __syncthreads();
     }
+    const int nr = min(p.ranges, W);
+    if (r >= nr) return;
+    const Cuts cuts(W, nr);
+    const int w0 = cuts.begin(r);
+    int at = before + x - mine;
+    if (at <= w0 && w0 < at + mine) {
+      int b = b0, u;
+#pragma unroll 1
+      while (at + (u = units_of(p, stored(p, b))) <= w0) at += u, ++b;
+      seg = {W, nr, w0, cuts.begin(r + 1), b, at};
+    }
+    __syncthreads();
   }
 
+  const char* zeros = g_zeros + ((blockIdx.x * kWarps + warp) % kZeroRows) * 512;
   uint64_t pol;
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
   const char* kh = p.k + kvh * p.head_stride + c4 * 16;
@@ -355,8 +343,9 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
     int t_begin, t_end;
     {
       const int n = stored(p, b), first = seen_from(p, n);
-      t_begin = first + (int)(seg.w - seg.at) * kUnit;
-      t_end = (int)min((long long)n, first + (seg.w1 - seg.at) * kUnit);
+      t_begin = first + (seg.w - seg.at) * kUnit;
+      const int left = seg.w1 - seg.at;  // units of this sequence up to the range's end
+      t_end = left < units_of(p, n) ? first + left * kUnit : n;
     }
     const int32_t* bt = p.table + (size_t)b * p.max_pages;
 
@@ -429,34 +418,30 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
     const int tl = lane % S::kTile;
     auto entry = [&](int t0) {
       const int t = t0 + tl;
-      return t < t_end ? bt[t / p.P] : -1;
+      return t < t_end ? bt[p.P.quot(t)] : -1;
     };
     // cache row of that position, in token strides (-1: not seen)
     auto row_of = [&](int t0, int id) {
       const int t = t0 + tl;
-      return id >= 0 && id < p.num_pages ? (int)(id * p.page_rows + t % p.P) : -1;
+      return id >= 0 && id < p.num_pages ? (int)(id * p.page_rows + (t - p.P.quot(t) * p.P.d)) : -1;
     };
     uint32_t kr[NS][2][KP][4], vr[NS][4][VP][VW];
-    bool seen[NS][2];
-    auto load_k = [&](int row) {
-#pragma unroll
-      for (int s = 0; s < NS; ++s)
+    bool seen_next[NS][2];
+    auto load_k = [&](int row, int s) {  // subtile s of the tile whose rows the lanes hold
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int rr = __shfl_sync(0xffffffffu, row, 16 * s + 8 * x + n8);
-          seen[s][x] = rr >= 0;
-          const char* src = rr >= 0 ? kh + (uint64_t)(uint32_t)rr * p.token_stride : kZeros;
+          seen_next[s][x] = rr >= 0;
+          const char* src = rr >= 0 ? kh + (uint64_t)(uint32_t)rr * p.token_stride : zeros;
 #pragma unroll
           for (int j = 0; j < KP; ++j) load_words<4>(kr[s][x][j], src + j * 64, pol);
         }
     };
-    auto load_v = [&](int row) {
-#pragma unroll
-      for (int s = 0; s < NS; ++s)
+    auto load_v = [&](int row, int s) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int rr = __shfl_sync(0xffffffffu, row, 16 * s + 8 * (x >> 1) + 2 * c4 + (x & 1));
-          const char* src = rr >= 0 ? vh + (uint64_t)(uint32_t)rr * p.token_stride : kZeros;
+          const char* src = rr >= 0 ? vh + (uint64_t)(uint32_t)rr * p.token_stride : zeros;
 #pragma unroll
           for (int j = 0; j < VP; ++j) load_words<VW>(vr[s][x][j], src + j * 128, pol);
         }
@@ -465,18 +450,28 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
     constexpr int kStride = kWarps * S::kTile;
     int t0 = t_begin + warp * S::kTile;
     int row = row_of(t0, entry(t0));
-    load_k(row);
-    load_v(row);
-    int id_next = entry(t0 + kStride);
-    for (; t0 < t_end; t0 += kStride) {
-      // ---- S^T = K Q^T
-      float x[NS][NT][4];
 #pragma unroll
-      for (int s = 0; s < NS; ++s)
+    for (int s = 0; s < NS; ++s) load_k(row, s);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) load_v(row, s);
+    int id_next = entry(t0 + kStride);
+    bool more = t0 < t_end;
+#pragma unroll 1
+    while (more) {
+      // ---- S^T = K Q^T; a subtile's registers take the next tile's K at once (its
+      // page ids came with the tile before)
+      t0 += kStride;
+      more = t0 < t_end;
+      const int row_next = row_of(t0, id_next);
+      id_next = entry(t0 + kStride);
+      float x[NS][NT][4];
+      bool seen[NS][2];
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        seen[s][0] = seen_next[s][0];
+        seen[s][1] = seen_next[s][1];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) x[s][nt][0] = x[s][nt][1] = x[s][nt][2] = x[s][nt][3] = 0.f;
-#pragma unroll
-      for (int s = 0; s < NS; ++s)
 #pragma unroll
         for (int j = 0; j < KP; ++j) {
           if constexpr (CT == kE4m3) {
@@ -498,6 +493,8 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
                          kr[s][1][j][2 * i + 1], qf[nt][2 * j + i][0], qf[nt][2 * j + i][1]);
           }
         }
+        load_k(row_next, s);
+      }
       // ---- scale, what is not seen, the reference
       bool over = false;
 #pragma unroll
@@ -510,10 +507,6 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
             x[s][nt][e] = y;
             over = over || y > m[nt][e & 1] + kSlack;
           }
-      // the next tile's K (its page ids came with the tile before)
-      const int row_next = row_of(t0 + kStride, id_next);
-      load_k(row_next);
-      id_next = entry(t0 + 2 * kStride);
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -592,8 +585,8 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
               }
             }
           }
+        load_v(row_next, s);
       }
-      load_v(row_next);
     }
 
     // ---- the warps' parts meet in shared memory
@@ -618,19 +611,19 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
             d = (t / (2 * VW)) * 128 + n8 * VW * 4 + (t % (2 * VW)) * 2;
           else
             d = (t / VW) * 64 + n8 * 8 + (t % VW) * 2;
-          *reinterpret_cast<float2*>(&so[warp][h][d]) = make_float2(o[nt][t][e], o[nt][t][e + 2]);
+          *reinterpret_cast<float2*>(&so[warp][8 * nt + 4 * e + c4][d]) = make_float2(o[nt][t][e], o[nt][t][e + 2]);
         }
       }
     __syncthreads();
 
     // parts of this sequence: ranges r_first .. r_last
-    const long long at = seg.at;
-    const int units = units_of(p, stored(p, b));
-    const int r_first = range_of(at, seg.W, seg.nr), r_last = range_of(at + units - 1, seg.W, seg.nr);
+    const int at = seg.at, units = units_of(p, stored(p, b));
+    const Cuts cuts(seg.W, seg.nr);
+    const int r_first = cuts.range_of(at), r_last = cuts.range_of(at + units - 1);
     const bool whole = r_first == r_last;
     const float vs = p.v_scale ? p.v_scale[kvh] : 1.f;
     // slot 0: the segment a range begins with; slot 1: its last one, if another
-    const bool begins = seg.w == cut(seg.W, r, seg.nr);
+    const bool begins = seg.w == cuts.begin(r);
     const size_t part = ((size_t)r * 2 + (begins ? 0 : 1)) * HV + hv;
 #pragma unroll 1
     for (int h = warp; h < nh; h += kWarps) {
@@ -644,11 +637,12 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
         L += e[i] * sml[i][h][1];
       }
       const float f = whole ? (L == 0.f ? 0.f : vs / L) : 1.f;
+      const int hr = (h & ~7) + 4 * (h & 1) + (h >> 1 & 3);
       for (int d = 2 * lane; d < D; d += 64) {
         float2 a = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) {
-          const float2 y = *reinterpret_cast<const float2*>(&so[i][h][d]);
+          const float2 y = *reinterpret_cast<const float2*>(&so[i][hr][d]);
           a.x += e[i] * y.x;
           a.y += e[i] * y.y;
         }
@@ -668,18 +662,22 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
       }
     }
     if (!whole) {
-      // ---- the last CTA of the sequence's parts joins them, in their order
-      __threadfence();
+      // ---- the last CTA of the sequence's parts joins them, in their order (the
+      // barriers carry the CTA's stores to, and the others' from, one thread's atomic)
       __syncthreads();
       if (threadIdx.x == 0) {
         int32_t* cnt = p.counters + (size_t)b * HV + hv;
-        s_last = atomicAdd(cnt, 1) == r_last - r_first;
+        int before;
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                     : "=r"(before)
+                     : "l"(cnt)
+                     : "memory");
+        s_last = before == r_last - r_first;
         if (s_last) *cnt = 0;  // ready for the next call
-        __threadfence();
       }
       __syncthreads();
       if (s_last)
-        join<D>(p, b, r_first, r_last - r_first + 1, cut(seg.W, r_first, seg.nr) != at, hv, nh);
+        join<D>(p, b, r_first, r_last - r_first + 1, cuts.begin(r_first) != at, hv, nh);
     }
     // ---- the next sequence that has units
     __syncthreads();  // the shared parts and the control block are free
@@ -696,11 +694,15 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
 }
 
 // ------------------------------------------------------------------ host side
+// SMs of the current device, asked once per device (the query costs host time)
 int num_sms() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
     return 152;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -715,7 +717,8 @@ constexpr int per_sm(bool e4m3, int D, int nt) {
   return D == 256 || nt == 2 ? 2 : e4m3 && D == 64 ? 4 : 3;
 }
 
-bool make_plan(int B, int Hq, int Hkv, int D, int occ, DecodePlan* pl) {
+// occ: CTAs an SM holds (0: of the instance that the shape selects)
+bool make_plan(int B, int Hq, int Hkv, int D, bool e4m3, int occ, DecodePlan* pl) {
   if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv) return false;
   pl->G = Hq / Hkv;
   const int most = D == 256 ? 8 : 16;
@@ -723,6 +726,7 @@ bool make_plan(int B, int Hq, int Hkv, int D, int occ, DecodePlan* pl) {
   pl->hpg = (pl->G + pl->groups - 1) / pl->groups;
   pl->groups = (pl->G + pl->hpg - 1) / pl->hpg;
   pl->nt = pl->hpg > 8 ? 2 : 1;
+  if (occ == 0) occ = per_sm(e4m3, D, pl->nt);
   pl->ranges = std::max(1, num_sms() * occ / (Hkv * pl->groups));
   return true;
 }
@@ -755,7 +759,7 @@ spec_status launch_d(const DecodeParams& p, int D, int nt, cudaStream_t st) {
 
 extern "C" size_t spec_decode_attn_workspace_size(int B, int Hq, int Hkv, int D) {
   DecodePlan pl;
-  if ((D != 64 && D != 128 && D != 256) || !make_plan(B, Hq, Hkv, D, kMostPerSm, &pl)) return 0;
+  if ((D != 64 && D != 128 && D != 256) || !make_plan(B, Hq, Hkv, D, false, kMostPerSm, &pl)) return 0;
   size_t a, c;
   return ws_layout(pl, Hkv, D, &a, &c);
 }
@@ -796,9 +800,10 @@ extern "C" spec_status spec_decode_attn(const void* q, int64_t q_stride_b, int64
   if (page_rows > INT32_MAX || (page_rows * (num_pages - 1) + page_size) > INT32_MAX ||
       (long long)max_pages * page_size > INT32_MAX)
     return SPEC_EUNSUPPORTED;
+  // so are the batch's units
+  if (((long long)max_pages * page_size / kUnit + 1) * B > INT32_MAX) return SPEC_EUNSUPPORTED;
   DecodePlan pl;
-  if (!make_plan(B, Hq, Hkv, D, 1, &pl)) return SPEC_EINVAL;
-  make_plan(B, Hq, Hkv, D, per_sm(e4m3, D, pl.nt), &pl);
+  if (!make_plan(B, Hq, Hkv, D, e4m3, 0, &pl)) return SPEC_EINVAL;
   if ((long long)B * Hkv * pl.groups > kMaxCounters) return SPEC_EUNSUPPORTED;
   size_t off_o, off_ml;
   if (workspace_bytes < ws_layout(pl, Hkv, D, &off_o, &off_ml)) return SPEC_EINVAL;
@@ -827,7 +832,7 @@ extern "C" spec_status spec_decode_attn(const void* q, int64_t q_stride_b, int64
   p.G = pl.G;
   p.groups = pl.groups;
   p.hpg = pl.hpg;
-  p.P = page_size;
+  p.P = FastDiv(page_size);
   p.num_pages = num_pages;
   p.max_pages = max_pages;
   p.window = window;

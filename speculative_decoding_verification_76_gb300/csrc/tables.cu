@@ -30,30 +30,35 @@ constexpr int kMaxSeqs = 8192;      // two running sums of 4 bytes: 64 KB of sha
 constexpr int kTokensPerThread = 4;
 constexpr int kWarpPages = 64;      // more pages than this: the whole CTA writes the row
 
-// Exclusive running sum over the block of one value per thread; *total: the sum.
-SPEC_DEV long long block_scan(long long v, long long* total) {
-  __shared__ long long part[kWarps];
+// Sums of lengths and pages stop at 2^31 - 1 (nothing past the capacities matters).
+SPEC_DEV int sat_add(int a, int b) {
+  return (int)min((uint32_t)a + (uint32_t)b, (uint32_t)INT_MAX);
+}
+
+// Exclusive running sum over the block of one value >= 0 per thread; *total: the sum.
+SPEC_DEV int block_scan(int v, int* total) {
+  __shared__ int part[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
+  int x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x = sat_add(x, y);
   }
   __syncthreads();  // `part` of an earlier call is read no more
   if (lane == 31) part[warp] = x;
+  x = __shfl_up_sync(0xffffffffu, x, 1);
+  if (lane == 0) x = 0;
   __syncthreads();
-  long long before = 0, sum = 0;
+  int before = 0, sum = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += part[w];
-    sum += part[w];
+    if (w == warp) before = sum;
+    sum = sat_add(sum, part[w]);
   }
   *total = sum;
-  return before + x - v;
+  return sat_add(before, x);
 }
-
-SPEC_DEV long long ceil_div(long long a, int b) { return (a + b - 1) / b; }
 
 SPEC_DEV int clamp_count(int c, int n) { return c < 0 ? 0 : c > n ? n : c; }
 
@@ -61,7 +66,8 @@ struct ExtendParams {
   const int32_t *ctx, *add, *free_list, *free_count;
   int32_t *table, *positions, *cu, *new_len, *free_left, *status;
   int64_t* slots;
-  int B, P, max_pages, num_pages, cap;
+  FastDiv P;
+  int B, max_pages, num_pages, cap;
 };
 
 __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const ExtendParams p) {
@@ -73,61 +79,62 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const ExtendPar
   // ---- running sums; a thread holds `per` consecutive sequences
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
-  long long sum = 0, total;
-  for (int b = b0; b < b1; ++b) sum += max(p.add[b], 0);
-  long long at = block_scan(sum, &total);
-  long long need_sum = 0;
+  const uint32_t row_max = (uint32_t)p.max_pages * p.P.d;  // tokens a table row can name
+  int sum = 0, total;
+  for (int b = b0; b < b1; ++b) sum = sat_add(sum, max(p.add[b], 0));
+  int at = block_scan(sum, &total);
+  int need_sum = 0;
   for (int b = b0; b < b1; ++b) {
-    const long long c = p.ctx[b], a = p.add[b];
-    tok[b] = (int32_t)min(at, (long long)p.cap + 1);
-    if (blockIdx.x == 0) p.cu[b] = (int32_t)min(at, (long long)INT_MAX);
-    at += max(a, 0ll);
-    const long long want = ceil_div(c + a, p.P);
-    const bool bad = c < 0 || a < 0 || want > p.max_pages || at > p.cap;
-    const int need = bad ? 0 : (int)(want - ceil_div(c, p.P));
+    const int c = p.ctx[b], a = p.add[b];
+    tok[b] = min(at, p.cap + 1);
+    if (blockIdx.x == 0) p.cu[b] = at;
+    at = sat_add(at, max(a, 0));
+    const bool bad = c < 0 || a < 0 || (uint32_t)c + (uint32_t)a > row_max || at > p.cap;
+    const int need = bad ? 0 : p.P.ceil_quot(c + a) - p.P.ceil_quot(c);
     pg[b] = bad ? INT_MIN : need;
-    need_sum += need;
+    need_sum = sat_add(need_sum, need);
   }
   if (threadIdx.x == 0) {
-    tok[p.B] = (int32_t)min(total, (long long)p.cap + 1);
-    if (blockIdx.x == 0) p.cu[p.B] = (int32_t)min(total, (long long)INT_MAX);
+    tok[p.B] = min(total, p.cap + 1);
+    if (blockIdx.x == 0) p.cu[p.B] = total;
   }
-  long long dummy;
-  long long pages = block_scan(need_sum, &dummy);
-  long long taken = 0;   // the largest running sum that fits: what the step takes
+  int unused;
+  int pages = block_scan(need_sum, &unused);
+  int taken = 0;   // the largest running sum that fits: what the step takes
   for (int b = b0; b < b1; ++b) {
     const int need = pg[b];
     if (need == INT_MIN) {
       pg[b] = -1 - SPEC_SEQ_BAD_LEN;
       continue;
     }
-    const bool fits = need == 0 || pages + need <= count;
-    if (fits && need) taken = pages + need;
-    pg[b] = fits ? (int32_t)min(pages, (long long)INT_MAX) : -1 - SPEC_SEQ_NO_PAGES;
-    pages += need;
+    const int upto = sat_add(pages, need);
+    const bool fits = need == 0 || upto <= count;
+    if (fits && need) taken = upto;
+    pg[b] = fits ? pages : -1 - SPEC_SEQ_NO_PAGES;
+    pages = upto;
   }
-  if (blockIdx.x == 0) {  // at most one thread's sequences end the served prefix
+  if (blockIdx.x == 0) {  // the served sequences that take pages come first
     __shared__ int most;
     if (threadIdx.x == 0) most = 0;
     __syncthreads();
-    if (taken) atomicMax(&most, (int)taken);
+    if (taken) atomicMax(&most, taken);
     __syncthreads();
     if (threadIdx.x == 0) *p.free_left = count - most;
   }
   __syncthreads();
 
   // ---- new pages into the table rows, lengths and statuses
-  auto row = [&](int b, int lane, int lanes) {
-    const int c = p.ctx[b], n = p.add[b];
-    const int have = (int)ceil_div(c, p.P), need = (int)(ceil_div((long long)c + n, p.P) - have);
+  auto row = [&](int b, int have, int need, int lane, int lanes) {
     int32_t* t = p.table + (size_t)b * p.max_pages;
     bool bad = false;
-    if (lane == 0 && n > 0 && c % p.P) {  // the page the first new token falls into
+    if (lane == 0 && have * p.P.d != p.ctx[b] && p.add[b] > 0) {  // the first token's old page
       const int id = t[have - 1];
       bad = id < 0 || id >= p.num_pages;
     }
+    const int32_t* from = p.free_list + (count - 1 - pg[b]);
+#pragma unroll 4
     for (int j = lane; j < need; j += lanes) {
-      const int id = p.free_list[count - 1 - (pg[b] + j)];
+      const int id = from[-j];
       t[have + j] = id;
       bad = bad || id < 0 || id >= p.num_pages;
     }
@@ -137,10 +144,6 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const ExtendPar
     p.status[b] = bad ? SPEC_SEQ_BAD_PAGE : 0;
     p.new_len[b] = bad ? p.ctx[b] : p.ctx[b] + p.add[b];
   };
-  auto pages_of = [&](int b) {
-    const int c = p.ctx[b];
-    return ceil_div((long long)c + p.add[b], p.P) - ceil_div(c, p.P);
-  };
   const int lane = threadIdx.x & 31;
   for (int b = blockIdx.x * kWarps + (threadIdx.x >> 5); b < p.B; b += gridDim.x * kWarps) {
     if (pg[b] < 0) {
@@ -148,14 +151,18 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const ExtendPar
         p.status[b] = -1 - pg[b];
         p.new_len[b] = p.ctx[b];
       }
-    } else if (pages_of(b) <= kWarpPages) {
-      const bool bad = __any_sync(0xffffffffu, row(b, lane, 32));
-      if (lane == 0) finish(b, bad);
+      continue;
     }
+    const int have = p.P.ceil_quot(p.ctx[b]), need = p.P.ceil_quot(p.ctx[b] + p.add[b]) - have;
+    if (need > kWarpPages) continue;
+    const bool bad = __any_sync(0xffffffffu, row(b, have, need, lane, 32));
+    if (lane == 0) finish(b, bad);
   }
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (pg[b] < 0 || pages_of(b) <= kWarpPages) continue;
-    const bool bad = __syncthreads_or(row(b, threadIdx.x, kThreads));
+    if (pg[b] < 0) continue;
+    const int have = p.P.ceil_quot(p.ctx[b]), need = p.P.ceil_quot(p.ctx[b] + p.add[b]) - have;
+    if (need <= kWarpPages) continue;
+    const bool bad = __syncthreads_or(row(b, have, need, threadIdx.x, kThreads));
     if (threadIdx.x == 0) finish(b, bad);
   }
 
@@ -181,11 +188,11 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const ExtendPar
       if (b < p.B && pg[b] >= 0) {
         const int c = p.ctx[b];
         pos = c + (t - tok[b]);
-        const int idx = pos / p.P, have = (int)ceil_div(c, p.P);
+        const int idx = p.P.quot(pos), have = p.P.ceil_quot(c);
         const int id = idx < have ? p.table[(size_t)b * p.max_pages + idx]
                                   : p.free_list[count - 1 - (pg[b] + idx - have)];
         if (id >= 0 && id < p.num_pages)
-          slot = (int64_t)id * p.P + pos % p.P;
+          slot = (int64_t)id * p.P.d + (pos - idx * p.P.d);
         else
           pos = -1;
       }
@@ -198,7 +205,8 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const ExtendPar
 struct ReleaseParams {
   const int32_t *table, *len, *keep, *free_count;
   int32_t *free_list, *free_total, *status;
-  int B, P, max_pages, num_pages;
+  FastDiv P;
+  int B, max_pages, num_pages;
 };
 
 __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleaseParams p) {
@@ -207,31 +215,32 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleasePa
   const int count = clamp_count(*p.free_count, p.num_pages);
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
-  long long sum = 0, dummy;
+  int sum = 0, unused;
   for (int b = b0; b < b1; ++b) {
-    const long long n = p.len[b], k = p.keep[b], held = ceil_div(n, p.P);
+    const int n = p.len[b], k = p.keep[b], held = n < 0 ? 0 : p.P.ceil_quot(n);
     const bool bad = n < 0 || k < 0 || k > held || held > p.max_pages;
-    at[b] = bad ? INT_MIN : (int)(held - k);
-    if (!bad) sum += held - k;
+    at[b] = bad ? INT_MIN : held - k;
+    if (!bad) sum = sat_add(sum, held - k);
   }
-  long long pages = count + block_scan(sum, &dummy);
-  long long end = 0;
+  int pages = sat_add(count, block_scan(sum, &unused));
+  int end = 0;
   for (int b = b0; b < b1; ++b) {
     const int n = at[b];
     if (n == INT_MIN) {
       at[b] = -1 - SPEC_SEQ_BAD_LEN;
       continue;
     }
-    const bool fits = n == 0 || pages + n <= p.num_pages;
-    if (fits && n) end = pages + n;
-    at[b] = fits ? (int32_t)min(pages, (long long)INT_MAX) : -1 - SPEC_SEQ_NO_PAGES;
-    pages += n;
+    const int upto = sat_add(pages, n);
+    const bool fits = n == 0 || upto <= p.num_pages;
+    if (fits && n) end = upto;
+    at[b] = fits ? pages : -1 - SPEC_SEQ_NO_PAGES;
+    pages = upto;
   }
   if (blockIdx.x == 0) {
     __shared__ int most;
     if (threadIdx.x == 0) most = count;
     __syncthreads();
-    if (end) atomicMax(&most, (int)end);
+    if (end) atomicMax(&most, end);
     __syncthreads();
     if (threadIdx.x == 0) *p.free_total = most;
   }
@@ -240,6 +249,7 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleasePa
   auto row = [&](int b, int n, int lane, int lanes) {
     const int32_t* t = p.table + (size_t)b * p.max_pages + p.keep[b];
     bool bad = false;
+#pragma unroll 4
     for (int j = lane; j < n; j += lanes) {
       const int id = t[j];
       const bool ok = id >= 0 && id < p.num_pages;
@@ -248,7 +258,7 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleasePa
     }
     return bad;
   };
-  auto pages_of = [&](int b) { return (int)(ceil_div(p.len[b], p.P) - p.keep[b]); };
+  auto pages_of = [&](int b) { return p.P.ceil_quot(p.len[b]) - p.keep[b]; };
   const int lane = threadIdx.x & 31;
   for (int b = blockIdx.x * kWarps + (threadIdx.x >> 5); b < p.B; b += gridDim.x * kWarps) {
     int st = 0;
@@ -294,16 +304,19 @@ extern "C" spec_status spec_extend_tables(const int32_t* ctx_len, const int32_t*
   if (B && (!ctx_len || !add_len || !block_table || !new_len || !status_per_seq))
     return SPEC_EINVAL;
   if (max_tokens && (!slot_map || !positions)) return SPEC_EINVAL;
-  if (B > kMaxSeqs || (long long)max_pages * page_size > INT_MAX || max_tokens == INT_MAX)
+  if (B > kMaxSeqs || (long long)max_pages * page_size > INT_MAX || max_tokens == INT_MAX ||
+      num_pages == INT_MAX)
     return SPEC_EUNSUPPORTED;
   const size_t smem = (2 * (size_t)B + 1) * sizeof(int32_t);
-  static PerDeviceOnce<int> smem_once;  // once per device, at the largest size
-  const spec_status ra = ensure_smem_limit(smem_once, (const void*)extend_tables_kernel,
-                                           (2 * kMaxSeqs + 1) * (int)sizeof(int32_t));
-  if (ra != SPEC_OK) return ra;
+  if (smem > 48 * 1024) {
+    static PerDeviceOnce<int> smem_once;  // once per device, at the largest size
+    const spec_status ra = ensure_smem_limit(smem_once, (const void*)extend_tables_kernel,
+                                             (2 * kMaxSeqs + 1) * (int)sizeof(int32_t));
+    if (ra != SPEC_OK) return ra;
+  }
   const ExtendParams p{ctx_len, add_len,   free_list, free_count, block_table, positions, cu_len,
-                       new_len, free_left, status_per_seq, slot_map, B, page_size, max_pages,
-                       num_pages, max_tokens};
+                       new_len, free_left, status_per_seq, slot_map, FastDiv(page_size), B,
+                       max_pages, num_pages, max_tokens};
   extend_tables_kernel<<<grid_for(B, max_tokens), kThreads, smem, (cudaStream_t)stream>>>(p);
   return launch_status();
 }
@@ -316,9 +329,10 @@ extern "C" spec_status spec_release_pages(const int32_t* block_table, int max_pa
   if (B < 0 || page_size < 1 || max_pages < 1 || num_pages < 1) return SPEC_EINVAL;
   if (!free_list || !free_count || !free_total || free_total == free_count) return SPEC_EINVAL;
   if (B && (!block_table || !len || !keep_pages)) return SPEC_EINVAL;
-  if (B > kMaxSeqs || (long long)max_pages * page_size > INT_MAX) return SPEC_EUNSUPPORTED;
+  if (B > kMaxSeqs || (long long)max_pages * page_size > INT_MAX || num_pages == INT_MAX)
+    return SPEC_EUNSUPPORTED;
   const ReleaseParams p{block_table, len, keep_pages, free_count, free_list, free_total,
-                        status_per_seq, B, page_size, max_pages, num_pages};
+                        status_per_seq, FastDiv(page_size), B, max_pages, num_pages};
   release_pages_kernel<<<grid_for(B, 0), kThreads, (size_t)B * sizeof(int32_t),
                          (cudaStream_t)stream>>>(p);
   return launch_status();
