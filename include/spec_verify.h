@@ -336,8 +336,9 @@ spec_status spec_workspace_error(const void* workspace, int32_t* host_err, void*
  * trees and visibility": a tree's accepted path is compacted into the next
  * logical prefix so branch states are no longer addressable.
  *
- *   k_cache, v_cache [num_pages, page_size, Hkv, D], elem_bytes 2 (bf16) or
- *            4 (fp32), 16-byte aligned, updated in place (trees only).
+ *   k_cache, v_cache [num_pages, page_size, Hkv, D], elem_bytes 1 (e4m3), 2
+ *            (bf16, fp16) or 4 (fp32), 16-byte aligned, updated in place (trees
+ *            only).
  *   block_table [B, max_pages] int32; ctx_len [B] int32: block row j was
  *            written at cache position ctx_len[b] + j.
  *   accepted_len [B] int32: drafts accepted (0 .. R-1).
@@ -363,7 +364,8 @@ spec_status spec_workspace_error(const void* workspace, int32_t* host_err, void*
  *            accepted_len, the path or a page index it touches is out of
  *            range, or the path breaks the rules above; that sequence is left
  *            untouched and new_len = ctx_len.
- *   1 <= R <= 64, D in {64, 128}.  Device pointers, async on the stream.
+ *   1 <= R <= 64, D in {64, 128}, or 256 in at most 2 bytes.  Device pointers,
+ *   async on the stream.
  * ---------------------------------------------------------------------- */
 spec_status spec_kv_commit(void* k_cache, void* v_cache, int elem_bytes, int num_pages,
                            int page_size, int Hkv, int D, const int32_t* block_table,

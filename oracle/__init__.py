@@ -31,9 +31,13 @@ by eye, with no blocking, fusion or reordering beyond the definitions:
   append.py     the block's K/V rows written into the paged cache, keys
                 rotated for their depth position ("Speculative Decoding"
                 (atlas), "Chains, trees and visibility": position ids follow
-                depth; the rotation itself is a reading, see the module).
+                depth; the rotation itself is a reading, see the module), and
+                packed rows at their slots, with the e4m3 grid.
+  tables.py     block tables, slots, positions and the free list of a step.
+  decode.py     attention of one new token per sequence over the paged cache
+                (full softmax over the seen positions).
 
 Every function is pinned by a test in tests/test_oracle_*.py against worked
 examples printed on the pages, closed forms or brute force.
 """
-from . import append, attention, commit, sampler, tree  # noqa: F401
+from . import append, attention, commit, decode, sampler, tables, tree  # noqa: F401

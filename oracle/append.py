@@ -53,3 +53,30 @@ def append_block(k_cache, v_cache, block_table, ctx_len, k_new, v_new, pos_ids, 
             kc[page, off] = rope(np.asarray(k_new)[b, j], int(pos_ids[b][j]), base)
             vc[page, off] = np.asarray(v_new)[b, j]
     return kc, vc
+
+
+def e4m3(x):
+    """x rounded to the nearest e4m3 value (ties to even, limited to +-448): 3 fraction
+    bits, exponents -6 .. 8, steps of 2^-9 below 2^-6."""
+    x = np.asarray(x, dtype=np.float64)
+    mag = np.minimum(np.abs(x), 448.0)
+    e = np.clip(np.floor(np.log2(np.maximum(mag, 2.0 ** -6))), -6, 8)
+    step = 2.0 ** (e - 3)
+    return np.copysign(np.minimum(np.rint(mag / step) * step, 448.0), x)
+
+
+def append_tokens(k_cache, v_cache, k_new, v_new, slots, positions, page_size: int, base=10000.0,
+                  k_scale=None, v_scale=None):
+    """Copies of the caches with packed rows [T, Hkv, D] at their slots, before any
+    rounding (divided by the heads' scales where those are given); base 0: no rotation.
+    Rows whose slot is outside the cache are skipped."""
+    kc = np.array(k_cache, dtype=np.float64, copy=True)
+    vc = np.array(v_cache, dtype=np.float64, copy=True)
+    for t, slot in enumerate(np.asarray(slots).tolist()):
+        if not 0 <= slot < kc.shape[0] * page_size or (base and positions[t] < 0):
+            continue
+        at = (slot // page_size, slot % page_size)
+        k = rope(np.asarray(k_new)[t], int(positions[t]), base) if base else np.asarray(k_new)[t]
+        kc[at] = k if k_scale is None else k / np.asarray(k_scale)[:, None]
+        vc[at] = v_new[t] if v_scale is None else v_new[t] / np.asarray(v_scale)[:, None]
+    return kc, vc

@@ -88,7 +88,9 @@ extern "C" spec_status spec_kv_commit(void* k_cache, void* v_cache, int elem_byt
   if (parent && !path) return SPEC_EINVAL;
   if (!k_cache || !v_cache || num_pages < 1 || page_size < 1 || Hkv < 1 || max_pages < 1)
     return SPEC_EINVAL;
-  if ((elem_bytes != 2 && elem_bytes != 4) || (D != 64 && D != 128)) return SPEC_EUNSUPPORTED;
+  if ((elem_bytes != 1 && elem_bytes != 2 && elem_bytes != 4) ||
+      (D != 64 && D != 128 && (D != 256 || elem_bytes == 4)))
+    return SPEC_EUNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache)) & 15)
     return SPEC_EINVAL;
   if (B == 0) return SPEC_OK;
