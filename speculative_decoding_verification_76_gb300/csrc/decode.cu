@@ -46,7 +46,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnit = 64;             // positions: the granularity of the ranges
-constexpr int kMaxCounters = 65536;   // sequences x KV heads x head groups
+constexpr int kMaxHeadGroups = 4096;  // KV heads x head groups
+constexpr int kMaxCounters = 2 * kMaxHeadGroups;  // two per CTA
+constexpr int kMaxJoin = 64;          // parts that the last CTA joins; more: join_kernel
 constexpr float kBelow = 7.f;         // the reference sits this far under the maximum
 constexpr float kSlack = 15.f;        // a score may exceed the reference by this much
 constexpr float kLog2e = 1.4426950408889634f;
@@ -58,7 +60,7 @@ struct DecodeParams {
   const float *k_scale, *v_scale;
   char* out;
   float *lse, *part_o, *part_ml;
-  int32_t* counters;
+  int32_t* counters;                         // by a sequence's first part: zero between calls
   long long q_stride_b, q_stride_h;          // elements
   long long head_stride;                     // bytes
   uint32_t token_stride;                     // bytes
@@ -279,6 +281,8 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
   const int nh = min(p.hpg, p.G - h0);                         // query heads of this CTA
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n8 = lane >> 2, c4 = lane & 3;
   const int HV = p.Hkv * p.groups;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // join_kernel waits for our end
 
   // ---- this CTA's units of the batch's W, and the sequence that holds the first:
   // every thread takes `per` consecutive sequences of one running sum
@@ -619,7 +623,9 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
     // parts of this sequence: ranges r_first .. r_last
     const int at = seg.at, units = units_of(p, stored(p, b));
     const Cuts cuts(seg.W, seg.nr);
-    const int r_first = cuts.range_of(at), r_last = cuts.range_of(at + units - 1);
+    int r_first = r, r_last = r;
+    if (at < cuts.begin(r)) r_first = cuts.range_of(at);
+    if (at + units > seg.w1) r_last = cuts.range_of(at + units - 1);
     const bool whole = r_first == r_last;
     const float vs = p.v_scale ? p.v_scale[kvh] : 1.f;
     // slot 0: the segment a range begins with; slot 1: its last one, if another
@@ -666,14 +672,18 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
       // barriers carry the CTA's stores to, and the others' from, one thread's atomic)
       __syncthreads();
       if (threadIdx.x == 0) {
-        int32_t* cnt = p.counters + (size_t)b * HV + hv;
-        int before;
-        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
-                     : "=r"(before)
-                     : "l"(cnt)
-                     : "memory");
-        s_last = before == r_last - r_first;
-        if (s_last) *cnt = 0;  // ready for the next call
+        s_last = 0;
+        if (r_last - r_first < kMaxJoin) {  // (more parts: join_kernel's)
+          int32_t* cnt =
+              p.counters + ((size_t)r_first * 2 + (cuts.begin(r_first) != at)) * HV + hv;
+          int before;
+          asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                       : "=r"(before)
+                       : "l"(cnt)
+                       : "memory");
+          s_last = before == r_last - r_first;
+          if (s_last) *cnt = 0;  // ready for the next call
+        }
       }
       __syncthreads();
       if (s_last)
@@ -691,6 +701,147 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
     }
     __syncthreads();
   }
+}
+
+// The sequences cut into more than kMaxJoin parts (one of a few KV heads over all the
+// GPU: joining 304 parts of 16 heads in one CTA took 50 us): a CTA per head of the k-th
+// such sequence.  Launched as a programmatic dependent of decode_kernel, and only where
+// the batch may have one: their number is below ranges / (kMaxJoin - 1).
+constexpr int kJoinWarps = 16;
+
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr int kPer = D / 32, kFlight = 8;
+  __shared__ float e[1024];  // parts' weights (ranges <= 1024)
+  __shared__ __align__(16) float so[kJoinWarps][D];
+  __shared__ int part[kJoinWarps];
+  __shared__ float fpart[kJoinWarps];
+  __shared__ int s_b, s_at, s_u;
+  const int k = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq, HV = p.Hkv * p.groups;
+  const int kvh = hq / p.G, hv = kvh * p.groups + hq % p.G / p.hpg, h = hq % p.G % p.hpg;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // exclusive running sum over the block; *all: the sum
+  auto scan = [&](int v, int* all) {
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    int before = 0;
+    *all = 0;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      if (w < warp) before += part[w];
+      *all += part[w];
+    }
+    return before + x - v;
+  };
+  auto reduce = [&](float v, auto op) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+    __syncthreads();
+    if (lane == 0) fpart[warp] = v;
+    __syncthreads();
+    v = fpart[0];
+#pragma unroll
+    for (int w = 1; w < kJoinWarps; ++w) v = op(v, fpart[w]);
+    return v;
+  };
+  const int per = (p.B + 32 * kJoinWarps - 1) / (32 * kJoinWarps);
+  const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+  int mine = 0, W, many, deep = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) mine += units_of(p, stored(p, b));
+  const int pre = scan(mine, &W), nr = min(p.ranges, W);
+  if (nr <= kMaxJoin) return;
+  const Cuts cuts(W, nr);
+  auto is_deep = [&](int at, int u) {
+    return u >= kMaxJoin && cuts.range_of(at + u - 1) - cuts.range_of(at) >= kMaxJoin;
+  };
+  int at = pre;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const int u = units_of(p, stored(p, b));
+    deep += is_deep(at, u);
+    at += u;
+  }
+  int nth = scan(deep, &many);
+  if (k >= many) return;
+  at = pre;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) {
+    const int u = units_of(p, stored(p, b));
+    if (is_deep(at, u) && nth++ == k) {
+      s_b = b;
+      s_at = at;
+      s_u = u;
+    }
+    at += u;
+  }
+  __syncthreads();
+  const int b = s_b, r_first = cuts.range_of(s_at);
+  const int np = cuts.range_of(s_at + s_u - 1) - r_first + 1;
+  const bool late = cuts.begin(r_first) != s_at;
+  auto row_of = [&](int i) {  // part i of head h
+    return (((size_t)(r_first + i) * 2 + (i == 0 && late)) * HV + hv) * p.hpg + h;
+  };
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  float2 x[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int i = threadIdx.x + u * 32 * kJoinWarps;
+    x[u] = i < np ? __ldcg(ml + row_of(i)) : make_float2(-INFINITY, 0.f);
+  }
+  const float M = reduce(fmaxf(x[0].x, x[1].x), [](float a, float c) { return fmaxf(a, c); });
+  float l = 0.f;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const float w = x[u].x == -INFINITY ? 0.f : fast_exp2(x[u].x - M);
+    l += w * x[u].y;
+    e[threadIdx.x + u * 32 * kJoinWarps] = w;
+  }
+  const float L = reduce(l, [](float a, float c) { return a + c; });  // (and e is written)
+  float acc[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+#pragma unroll 1
+  for (int i0 = warp; i0 < np; i0 += kJoinWarps * kFlight) {
+    Row<kPer> y[kFlight];
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j)
+      y[j].load(p.part_o + row_of(min(i0 + j * kJoinWarps, np - 1)) * D, lane);
+#pragma unroll
+    for (int j = 0; j < kFlight; ++j) {
+      const int i = i0 + j * kJoinWarps;
+      if (i < np) {
+#pragma unroll
+        for (int d = 0; d < kPer; ++d) acc[d] += e[i] * y[j].x[d];
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < kPer; d += 2)
+    *reinterpret_cast<float2*>(&so[warp][kPer * lane + d]) = make_float2(acc[d], acc[d + 1]);
+  __syncthreads();
+  const size_t o = (size_t)b * p.Hq + hq;
+  const float f = L == 0.f ? 0.f : (p.v_scale ? p.v_scale[kvh] : 1.f) / L;
+  if (2 * threadIdx.x < D) {
+    float2 a = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float2 y = *reinterpret_cast<const float2*>(&so[w][2 * threadIdx.x]);
+      a.x += y.x;
+      a.y += y.y;
+    }
+    *reinterpret_cast<uint32_t*>(p.out + (o * D + 2 * threadIdx.x) * 2) =
+        p.q_bf16 ? pack_bf16(a.x * f, a.y * f) : pack_f16(a.x * f, a.y * f);
+  }
+  if (threadIdx.x == 0 && p.lse) p.lse[o] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host side
@@ -727,7 +878,7 @@ bool make_plan(int B, int Hq, int Hkv, int D, bool e4m3, int occ, DecodePlan* pl
   pl->groups = (pl->G + pl->hpg - 1) / pl->hpg;
   pl->nt = pl->hpg > 8 ? 2 : 1;
   if (occ == 0) occ = per_sm(e4m3, D, pl->nt);
-  pl->ranges = std::max(1, num_sms() * occ / (Hkv * pl->groups));
+  pl->ranges = std::max(1, std::min(1024, num_sms() * occ / (Hkv * pl->groups)));
   return true;
 }
 
@@ -745,6 +896,22 @@ template <int CT, int D, int NT>
 spec_status launch(const DecodeParams& p, cudaStream_t st) {
   constexpr int kOcc = per_sm(CT == kE4m3, D, NT);
   decode_kernel<CT, D, NT, kOcc><<<p.ranges * p.Hkv * p.groups, kThreads, 0, st>>>(p);
+  spec_status rc = launch_status();
+  // may a sequence be cut into more parts than its last CTA joins?  (Each holds a unit at
+  // least, and the window or the table's width bounds its units.)
+  const int row = p.max_pages * p.P.d, longest = p.window > 0 ? std::min(p.window, row) : row;
+  const bool deep = p.ranges > kMaxJoin && longest / kUnit + 1 > kMaxJoin;
+  if (rc != SPEC_OK || !deep) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.ranges / kMaxJoin * p.Hq, 1, 1);
+  cfg.blockDim = dim3(32 * kJoinWarps, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, join_kernel<D>, p) != cudaSuccess) return SPEC_ECUDA;
   return launch_status();
 }
 
@@ -804,7 +971,7 @@ extern "C" spec_status spec_decode_attn(const void* q, int64_t q_stride_b, int64
   if (((long long)max_pages * page_size / kUnit + 1) * B > INT32_MAX) return SPEC_EUNSUPPORTED;
   DecodePlan pl;
   if (!make_plan(B, Hq, Hkv, D, e4m3, 0, &pl)) return SPEC_EINVAL;
-  if ((long long)B * Hkv * pl.groups > kMaxCounters) return SPEC_EUNSUPPORTED;
+  if ((long long)Hkv * pl.groups > kMaxHeadGroups) return SPEC_EUNSUPPORTED;
   size_t off_o, off_ml;
   if (workspace_bytes < ws_layout(pl, Hkv, D, &off_o, &off_ml)) return SPEC_EINVAL;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

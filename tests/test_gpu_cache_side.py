@@ -311,6 +311,16 @@ def test_decode_attn_splits(qt, cache, B, n):
     check_decode(q, k, v, table, lens, sc, cache, qt, sm_scale=0.2)
 
 
+@pytest.mark.parametrize("D,G,lens", [(64, 3, [40000, 0, 100, 39000, 5]), (256, 8, [30001]),
+                                      (128, 16, [9000, 20000, 64]), (128, 40, [50000])])
+def test_decode_attn_one_kv_head_over_the_whole_gpu(D, G, lens):
+    """Sequences cut into more parts than one CTA joins, beside short and idle ones."""
+    k, v, table, sc = make_cache(lens, 1, D, 32, "bf16", D + G)
+    q = torch.randn((len(lens), G, D), generator=torch.Generator().manual_seed(D)).bfloat16()
+    check_decode(q, k, v, table, lens, sc, "bf16", "bf16")
+    check_decode(q, k, v, table, lens, sc, "bf16", "bf16", window=8000)
+
+
 def test_decode_attn_large_scores_and_masked_garbage():
     """Scores that grow along the sequence (the reference moves again and again), queries at
     the ends of bf16's range beside an 8-bit cache, Inf and NaN behind the sequences."""

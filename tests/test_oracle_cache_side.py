@@ -177,15 +177,15 @@ DECODE = dict(q=_p(), qb=4096, qh=128, qt=api.SPEC_BF16, kc=_p(), vc=_p(), ct=ap
     (dict(ws=_p(4096 + 128)), 1), (dict(wsb=1000), 1), (dict(qb=4097), 1), (dict(st=0), 1),
     (dict(kc=_p(4100)), 1), (dict(qt=api.SPEC_F32, ct=api.SPEC_F32), 2), (dict(D=96), 2),
     (dict(sp=1000 * 1024 + 512), 2), (dict(pages=1 << 28), 2), (dict(maxp=1 << 28), 2),
-    (dict(B=8193), 2), (dict(maxp=1 << 26, B=8192), 2), (dict(B=0), 0)])
+    (dict(Hq=4097, Hkv=4097), 2), (dict(maxp=1 << 26, B=8192), 2), (dict(B=0), 0)])
 def test_decode_attn_refuses_on_the_host(lib, change, code):
     assert lib.spec_decode_attn(*dict(DECODE, **change).values()) == code
 
 
 def test_decode_workspace(lib):
     one = sv.decode_attn_workspace_size(1, 32, 8, 128)
-    # header, 65536 counters, partial rows of fp32: no dependence on the batch
-    assert one == sv.decode_attn_workspace_size(4096, 32, 8, 128) > 256 + 65536 * 4
+    # header, 8192 counters, partial rows of fp32: no dependence on the batch
+    assert one == sv.decode_attn_workspace_size(4096, 32, 8, 128) > 256 + 8192 * 4
     assert sv.decode_attn_workspace_size(1, 33, 8, 128) == 0
     assert sv.decode_attn_workspace_size(1, 32, 8, 96) == 0
     ws = sv.decode_attn_workspace_size(2, 32, 8, 128)
