@@ -505,14 +505,16 @@ def _rows(t, name, dev, dtype, heads, D):
     """[T, heads, D] rows whose heads lie side by side; returns (pointer, row stride)."""
     if not isinstance(t, torch.Tensor) or t.device != dev:
         raise ValueError(f"{name} must be a tensor on {dev}")
+    if t.dtype is dtype and t.dim() == 3:
+        _, h, d = t.shape
+        s0, s1, s2 = t.stride()
+        if h == heads and d == D:
+            if s2 == 1 and (s1 == D or heads == 1):
+                return t.data_ptr(), s0
+            raise ValueError(f"{name}: a row's heads must lie side by side")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1:] != (heads, D):
-        raise ValueError(f"{name} must be [tokens, {heads}, {D}], got {tuple(t.shape)}")
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != D and heads > 1):
-        raise ValueError(f"{name}: a row's heads must lie side by side")
-    return t.data_ptr(), s0
+    raise ValueError(f"{name} must be [tokens, {heads}, {D}], got {tuple(t.shape)}")
 
 
 def _caches(k_cache, v_cache, dev, dtype):

@@ -11,12 +11,15 @@
 // whose rate on this GPU is a small part of fp32's.  Sine and cosine are fp32 of
 // that fraction; a row rotates in fp32 and is rounded once.
 //
-// What bounds it: each row is read once and written once (200 MB read and 167 MB
-// written for 16384 tokens of 32 / 8 heads of 128 into an e4m3 cache), so HBM,
-// and for a verify block (a few hundred rows) the launch.  One thread takes 8 + 8
-// elements of one head, i and i + D/2 on: two 16-byte loads, the rotation in
-// registers, two stores; consecutive threads take consecutive 16 bytes.  A
-// token's D/2 sines and cosines serve all its heads from shared memory.
+// What bounds it: each row is read once and written once, so HBM, and for a verify
+// block (a few hundred rows) the launch.  One thread takes 8 + 8 elements of one head,
+// i and i + D/2 on: two 16-byte loads, the rotation in registers, two stores;
+// consecutive threads take consecutive 16 bytes, and a thread has three such items'
+// loads in flight.  A token's D/2 sines and cosines serve all its heads from shared
+// memory.  A CTA of 128 threads takes two tokens, or one where there are few.
+// Measured (32 / 8 heads of 128, bf16 rows): 16384 tokens into an e4m3 cache 59 us =
+// 6.3 TB/s, into a bf16 one 64 us = 6.3 TB/s (one token a CTA 63 and 65; one item in
+// flight 69 and 71); 320 tokens 3.2 us (two tokens a CTA 4.0).
 #include <algorithm>
 #include <cmath>
 
@@ -27,7 +30,9 @@
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kFlight = 3;        // work items of a thread in flight
+constexpr int kFewTokens = 1216;  // up to eight per SM: a CTA per token
 constexpr int kMaxD = 256;
 
 struct AppendParams {
@@ -38,7 +43,7 @@ struct AppendParams {
   const int32_t* pos;
   long long k_stride, v_stride, q_stride, q_out_stride;          // elements
   long long page_stride, token_stride, head_stride, num_slots;   // elements, slots
-  FastDiv P;
+  FastDiv P, per;  // page size; work items of a token
   int T, Hq, Hkv, rotate;
   uint64_t turn[kMaxD / 2];  // 2^64 x turns per position, of each pair
 };
@@ -121,49 +126,64 @@ __global__ void __launch_bounds__(kThreads) append_tokens_kernel(
     }
   __syncthreads();
 
-  const int per = (p.Hq + 2 * p.Hkv) * kChunks;  // work items of one token
-  for (int i = threadIdx.x; i < TB * per; i += kThreads) {
-    const int u = i / per, r = i % per, h = r / kChunks, e = r % kChunks * 8;
-    const int t = t0 + u;
-    if (dst[u] < 0) continue;
-    const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
-    const int hh = is_q ? h : is_k ? h - p.Hq : h - p.Hq - p.Hkv;
-    const char* src = is_q   ? p.q + (t * p.q_stride) * (long long)sizeof(T)
-                      : is_k ? p.k + (t * p.k_stride) * (long long)sizeof(T)
-                             : p.v + (t * p.v_stride) * (long long)sizeof(T);
-    src += ((long long)hh * D + e) * (long long)sizeof(T);
-    const Vec8<T> lo = *reinterpret_cast<const Vec8<T>*>(src);
-    const Vec8<T> hi = *reinterpret_cast<const Vec8<T>*>(src + kHalf * sizeof(T));
-    float a[8], b[8];
-    unpack8(lo, a);
-    unpack8(hi, b);
-    if (p.rotate && (is_q || is_k)) {
+  // kFlight work items a thread at a time, their loads together (items behind the last
+  // and of skipped tokens load what is there and store nothing)
+  const int per = (p.Hq + 2 * p.Hkv) * kChunks, n = TB * per;  // work items of a token, of all
+  for (int i0 = threadIdx.x; i0 < n; i0 += kFlight * kThreads) {
+    Vec8<T> lo[kFlight], hi[kFlight];
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const float c = cs[u][e + x], s = sn[u][e + x], y = a[x];
-        a[x] = y * c - b[x] * s;
-        b[x] = y * s + b[x] * c;
-      }
+    for (int f = 0; f < kFlight; ++f) {
+      const int i = min(i0 + f * kThreads, n - 1), u = p.per.quot(i), r = i - u * per;
+      const int h = r / kChunks, e = r % kChunks * 8, t = min(t0 + u, p.T - 1);
+      const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
+      const char* src = is_q ? p.q : is_k ? p.k : p.v;
+      const long long stride = is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride;
+      const int hh = is_q ? h : is_k ? h - p.Hq : h - p.Hq - p.Hkv;
+      src += (t * stride + (hh * D + e)) * (long long)sizeof(T);
+      lo[f] = *reinterpret_cast<const Vec8<T>*>(src);
+      hi[f] = *reinterpret_cast<const Vec8<T>*>(src + kHalf * sizeof(T));
     }
-    if (is_q) {
-      char* o = p.q_out + (t * p.q_out_stride + (long long)hh * D + e) * (long long)sizeof(T);
-      store8<T>(o, a, 1.f);
-      store8<T>(o + kHalf * sizeof(T), b, 1.f);
-    } else {
-      const float* sc = is_k ? p.k_scale : p.v_scale;
-      const float inv = sizeof(C) == 1 && sc ? 1.f / sc[hh] : 1.f;
-      char* o = (is_k ? p.kc : p.vc) +
-                (dst[u] + hh * p.head_stride + e) * (long long)sizeof(C);
-      store8<C>(o, a, inv);
-      store8<C>(o + kHalf * sizeof(C), b, inv);
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int i = i0 + f * kThreads;
+      if (i >= n) break;
+      const int u = p.per.quot(i), r = i - u * per, h = r / kChunks, e = r % kChunks * 8;
+      if (dst[u] < 0) continue;
+      const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
+      float a[8], b[8];
+      unpack8(lo[f], a);
+      unpack8(hi[f], b);
+      if (p.rotate && (is_q || is_k)) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const float c = cs[u][e + x], s = sn[u][e + x], y = a[x];
+          a[x] = y * c - b[x] * s;
+          b[x] = y * s + b[x] * c;
+        }
+      }
+      if (is_q) {
+        char* o = p.q_out + ((t0 + u) * p.q_out_stride + (h * D + e)) * (long long)sizeof(T);
+        store8<T>(o, a, 1.f);
+        store8<T>(o + kHalf * sizeof(T), b, 1.f);
+      } else {
+        const int hh = is_k ? h - p.Hq : h - p.Hq - p.Hkv;
+        const float* sc = is_k ? p.k_scale : p.v_scale;
+        const float inv = sizeof(C) == 1 && sc ? 1.f / sc[hh] : 1.f;
+        char* o = (is_k ? p.kc : p.vc) +
+                  (dst[u] + hh * p.head_stride + e) * (long long)sizeof(C);
+        store8<C>(o, a, inv);
+        store8<C>(o + kHalf * sizeof(C), b, inv);
+      }
     }
   }
 }
 
 template <typename T, typename C, int D>
 spec_status launch(const AppendParams& p, cudaStream_t st) {
-  constexpr int TB = 2;
-  append_tokens_kernel<T, C, D, TB><<<(p.T + TB - 1) / TB, kThreads, 0, st>>>(p);
+  if (p.T <= kFewTokens)
+    append_tokens_kernel<T, C, D, 1><<<p.T, kThreads, 0, st>>>(p);
+  else
+    append_tokens_kernel<T, C, D, 2><<<(p.T + 1) / 2, kThreads, 0, st>>>(p);
   return launch_status();
 }
 
@@ -183,6 +203,7 @@ extern "C" spec_status spec_append_tokens(
     const int64_t* slot_map, const int32_t* positions, int T, int Hq, int Hkv, int D,
     double rope_base, void* stream) {
   if (T < 0 || Hq < 0 || Hkv < 1 || num_pages < 1 || page_size < 1) return SPEC_EINVAL;
+  if (Hq > 4096 || Hkv > 4096) return SPEC_EUNSUPPORTED;
   if (new_dtype != SPEC_F32 && new_dtype != SPEC_BF16 && new_dtype != SPEC_F16) return SPEC_EINVAL;
   const bool e4m3 = cache_dtype == SPEC_E4M3;
   if (!e4m3 && cache_dtype != new_dtype) return SPEC_EINVAL;
@@ -229,6 +250,7 @@ extern "C" spec_status spec_append_tokens(
   p.Hq = q ? Hq : 0;
   p.Hkv = Hkv;
   p.rotate = rope_base != 0.0;
+  p.per = FastDiv((p.Hq + 2 * Hkv) * (D / 16));
   if (p.rotate) {
     // turns per position as a 64-bit fraction (1 / 2 pi of a turn at i = 0); the
     // last base's frequencies are kept per host thread: D / 2 powers cost more

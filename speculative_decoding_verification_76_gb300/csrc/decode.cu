@@ -30,9 +30,9 @@
 //   P^T's fragments are S^T's accumulators, packed and transposed by movmatrix.
 // K's loads for the next tile go out when this tile's S is done, V's when its
 // product is; the page lookups are two tiles ahead.
-// P is fp16 beside fp16 and e4m3 caches (e4m3 converts to fp16 exactly) and a
-// sum of two bf16 parts beside bf16 ones, so that rounding P adds nothing to the
-// output's own rounding.  The reference m of a row stays until a score exceeds
+// P is a sum of two parts of the cache's 16-bit type, so that rounding P adds
+// nothing to the output's own rounding, and one fp16 number beside e4m3 caches (which
+// convert to fp16 exactly): 2^-11 where V itself holds 2^-4.  The reference m of a row stays until a score exceeds
 // it by 15 (it is set 7 below the maximum: P stays in fp16's range).
 #include <algorithm>
 #include <atomic>
@@ -260,7 +260,7 @@ template <int CT, int D, int NT, int MINB>
 __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
     const __grid_constant__ DecodeParams p) {
   using S = Shape<CT, D, NT>;
-  constexpr bool kBf = CT == kBf16;
+  constexpr bool kBf = CT == kBf16, kTwo = CT != kE4m3;  // (P as two parts)
   constexpr int NS = S::kSub, KP = S::kKPieces, VW = S::kVWords, VP = S::kVPieces;
   constexpr int kHeads = 8 * NT;
   // row (h & 1) * 4 + (h >> 1 & 3) of each eight is head h, two words apart modulo the
@@ -556,7 +556,12 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
               pl[nt][x2] = transpose8x8(pack_bf16(y0 - __uint_as_float(hi << 16),
                                                   y1 - __uint_as_float(hi & 0xffff0000u)));
             } else {
-              ph[nt][x2] = transpose8x8(pack_f16(y0, y1));
+              const uint32_t hi = pack_f16(y0, y1);
+              ph[nt][x2] = transpose8x8(hi);
+              if constexpr (kTwo) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                pl[nt][x2] = transpose8x8(pack_f16(y0 - f.x, y1 - f.y));
+              }
             }
           }
         }
@@ -585,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 mma<kBf>(o[nt][t], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-                if constexpr (kBf) mma<kBf>(o[nt][t], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                if constexpr (kTwo) mma<kBf>(o[nt][t], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
               }
             }
           }

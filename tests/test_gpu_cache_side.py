@@ -123,8 +123,17 @@ def test_tables_largest_batch_and_many_tokens():
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("layout", ["dense", "pairs", "heads first"])
 def test_append_tokens_matches_oracle(new, cache, D, layout):
+    check_append(new, cache, D, layout, 37, 11)
+
+
+@pytest.mark.parametrize("new,cache,D", [("bf16", "e4m3", 128), ("f16", "f16", 64)])
+def test_append_tokens_many_tokens(new, cache, D):
+    check_append(new, cache, D, "dense", 1301, 300)    # an odd number, two to a block
+
+
+def check_append(new, cache, D, layout, T, pages):
     rng = np.random.default_rng(D + len(new) + len(layout))
-    T, Hq, Hkv, P, pages = 37, 6, 2, 5, 11
+    Hq, Hkv, P = 6, 2, 5
     g = torch.Generator().manual_seed(D)
     qkv = torch.randn((T, (Hq + 2 * Hkv) * D), generator=g).to(TYPES[new])
     scale = [torch.rand(Hkv, generator=g) * 0.01 + 0.01 for _ in range(2)] \
