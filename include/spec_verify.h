@@ -551,7 +551,8 @@ spec_status spec_append_tokens(const void* k_new, int64_t k_stride, const void* 
  *   block_table [B,max_pages] int32; seq_len [B] int32: stored tokens, the new
  *            one included (append it first).  The token sees positions
  *            max(0, seq_len - window) .. seq_len - 1 (window 0: all of them).
- *            Positions past the table or whose page id is not in
+ *            Both stay as they are until the call has run.  Positions past the
+ *            table or whose page id is not in
  *            [0, num_pages) are not seen.  Nothing behind seq_len is read as a
  *            number: unwritten slots may hold anything.
  *   scale    softmax scale; <= 0 selects 1/sqrt(D).
@@ -563,7 +564,8 @@ spec_status spec_append_tokens(const void* k_new, int64_t k_stride, const void* 
  *
  * The result of a sequence does not depend on atomics' order; it may depend on
  * the rest of the batch (by where the cache is split) within rounding.
- * B * Hkv * ceil(Hq / Hkv / 16) <= 65536 (/ 8 instead of / 16 for D = 256).
+ * Hkv * ceil(Hq / Hkv / 16) <= 4096 (/ 8 instead of / 16 for D = 256); B *
+ * max_pages * page_size / 64 < 2^31.
  * ---------------------------------------------------------------------- */
 size_t spec_decode_attn_workspace_size(int B, int Hq, int Hkv, int D);
 

@@ -558,6 +558,8 @@ def extend_tables(ctx_len, add_len, block_table, free_list, free_count, page_siz
             return extend_tables(ctx_len, add_len, block_table, free_list, free_count, page_size,
                                  max_tokens, out)
     i32 = torch.int32
+    if not (0 < page_size < 2 ** 31 and 0 <= max_tokens < 2 ** 31):
+        raise ValueError("page_size and max_tokens must be below 2^31")
     if ctx_len.dim() != 1 or block_table.dim() != 2 or free_list.dim() != 1:
         raise ValueError("ctx_len [B], block_table [B, max_pages], free_list [num_pages]")
     B, width = ctx_len.shape[0], block_table.shape[1]
@@ -597,6 +599,8 @@ def release_pages(block_table, length, keep_pages, free_list, free_count, page_s
             return release_pages(block_table, length, keep_pages, free_list, free_count,
                                  page_size, total, status)
     i32 = torch.int32
+    if not 0 < page_size < 2 ** 31:
+        raise ValueError("page_size must be below 2^31")
     if length.dim() != 1 or block_table.dim() != 2 or free_list.dim() != 1:
         raise ValueError("length [B], block_table [B, max_pages], free_list [num_pages]")
     B, width, n = length.shape[0], block_table.shape[1], free_list.shape[0]
@@ -689,6 +693,8 @@ def decode_attn(q, k_cache, v_cache, block_table, seq_len, scale: float = 0.0, w
     kc, vc, (npg, P, Hkv, D2), kind, sp, st, sh = _caches(k_cache, v_cache, dev, dt)
     if D2 != D:
         raise ValueError("head_dim mismatch")
+    if not 0 <= window < 2 ** 31:
+        raise ValueError("window must be 0 or a number of positions below 2^31")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_pages]")
     width = block_table.shape[1]

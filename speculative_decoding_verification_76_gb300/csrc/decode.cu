@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
     if (at <= w0 && w0 < at + mine) {
       int b = b0, u;
 #pragma unroll 1
-      while (at + (u = units_of(p, stored(p, b))) <= w0) at += u, ++b;
+      while (b + 1 < b1 && at + (u = units_of(p, stored(p, b))) <= w0) at += u, ++b;
       seg = {W, nr, w0, cuts.begin(r + 1), b, at};
     }
     __syncthreads();
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
     const Cuts cuts(seg.W, seg.nr);
     int r_first = r, r_last = r;
     if (at < cuts.begin(r)) r_first = cuts.range_of(at);
-    if (at + units > seg.w1) r_last = cuts.range_of(at + units - 1);
+    if (at + units > seg.w1) r_last = min(cuts.range_of(at + units - 1), p.ranges - 1);
     const bool whole = r_first == r_last;
     const float vs = p.v_scale ? p.v_scale[kvh] : 1.f;
     // slot 0: the segment a range begins with; slot 1: its last one, if another
@@ -696,11 +696,11 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
     }
     // ---- the next sequence that has units
     __syncthreads();  // the shared parts and the control block are free
-    if (at + units >= seg.w1) return;
+    if (at + units >= seg.w1 || b + 1 >= p.B) return;
     __syncthreads();
     if (threadIdx.x == 0) {
-      int nb = b + 1;
-      while (units_of(p, stored(p, nb)) == 0) ++nb;  // there is one: units are left
+      int nb = b + 1;  // (there is one: units are left)
+      while (nb + 1 < p.B && units_of(p, stored(p, nb)) == 0) ++nb;
       seg.w = seg.at = at + units;
       seg.b = nb;
     }

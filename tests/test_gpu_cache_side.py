@@ -407,6 +407,38 @@ def test_decode_attn_offsets_past_32_bits():
     assert torch.equal(k[-1, -1], new[0]) and torch.equal(v[-1, -1], new[0])
 
 
+@pytest.mark.parametrize("B,Hkv,G", [(2, 700, 1), (5000, 1, 2), (3, 5, 7)])
+def test_decode_attn_many_heads_and_sequences(B, Hkv, G):
+    """More KV heads than blocks fit the GPU, thousands of sequences, odd head counts."""
+    lens = np.random.default_rng(B).integers(0, 40, B)
+    k, v, table, sc = make_cache(lens, Hkv, 64, 16, "f16", B)
+    q = torch.randn((B, Hkv * G, 64), generator=torch.Generator().manual_seed(B)).half()
+    check_decode(q, k, v, table, lens, sc, "f16", "f16")
+
+
+def test_calls_on_a_stream_of_their_own():
+    """stream=: work and outputs belong to that stream; the current one is left alone."""
+    s = torch.cuda.Stream()
+    ctx, add = [5, 0, 30], [3, 20, 1]
+    table, lst = random_pool(np.random.default_rng(1), ctx, 8, 6, 9)
+    ins = [dev(x) for x in (ctx, add, table, lst, [9])]
+    kc, vc = (torch.zeros((15, 8, 2, 64), dtype=torch.float16, device=DEV) for _ in range(2))
+    x = torch.randn((24, 2, 64), device=DEV).half()
+    keep = dev([0, 0, 0])
+    torch.cuda.synchronize()
+    e = sv.extend_tables(*ins, 8, 24, stream=s)
+    sv.append_tokens(x, x, kc, vc, e["slot_map"], e["positions"], stream=s)
+    out, _ = sv.decode_attn(x[:3], kc, vc, ins[2], e["new_len"], stream=s)
+    n, st = sv.release_pages(ins[2], e["new_len"], keep, ins[3], e["free_count"], 8,
+                             stream=s)
+    s.synchronize()
+    ref = otab.extend(ctx, add, table, lst, 9, 8, 24)
+    np.testing.assert_array_equal(num(e["slot_map"]), ref["slot_map"])
+    assert n.tolist() == [ref["free_count"] + 1 + 3 + 4]
+    want, _, _, _ = odec.decode_attention(num(x[:3]), num(kc), num(vc), num(ins[2]), [8, 20, 31])
+    assert np.abs(num(out) - want).max() < 2e-3
+
+
 def test_decode_attn_one_workspace_for_all_shapes_and_streams():
     """Calls of other shapes on one workspace, one after the other; the same call again gives
     the same bits; a call on a stream of its own."""
@@ -467,7 +499,15 @@ def test_bindings_refuse():
     refuses("add_len", e, n, n[:1], t, lst, cnt, 16, 4)
     refuses("block_table", e, n, n, t[:1], lst, cnt, 16, 4)
     refuses("free_count", e, n, n, t, lst, z(2, dtype=i32), 16, 4)
-    refuses("SPEC_EINVAL", e, n, n, t, lst, cnt, 0, 4)
+    refuses("page_size", e, n, n, t, lst, cnt, 0, 4)
+    refuses("page_size", e, n, n, t, lst, cnt, 2 ** 32 + 16, 4)
+    refuses("max_tokens", e, n, n, t, lst, cnt, 16, -1)
+    refuses("window", d, q, k, k, t, n, window=2 ** 32)
+    refuses("window", d, q, k, k, t, n, window=-1)
+    left = e(n, n, t, lst, cnt, 16, 4)
+    refuses("SPEC_EINVAL", e, n, n, t, lst, left["free_count"], 16, 4, out=left)
+    refuses("slot_map has shape", e, n, n, t, lst, cnt, 16, 5, out=left)
+    refuses("page_size", sv.release_pages, t, n, n, lst, cnt, 0)
     refuses("SPEC_EINVAL", sv.release_pages, t, n, n, lst, cnt, 16, total=cnt)
 
 
