@@ -112,10 +112,11 @@ SPEC_DEV uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-SPEC_DEV uint32_t e4m3_to_f16(uint32_t pair) {  // low two bytes
-  uint32_t r;
-  asm("{\n .reg .b16 x;\n cvt.u16.u32 x, %1;\n cvt.rn.f16x2.e4m3x2 %0, x;\n}\n" : "=r"(r) : "r"(pair));
-  return r;
+SPEC_DEV void e4m3_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {  // bytes 0, 1 and 2, 3
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
 // N words of the cache, read once: not kept in L1, first out of L2
@@ -481,9 +482,9 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
           if constexpr (CT == kE4m3) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint32_t lo = kr[s][0][j][i], hi = kr[s][1][j][i];
-              const uint32_t a0 = e4m3_to_f16(lo), a2 = e4m3_to_f16(lo >> 16);
-              const uint32_t a1 = e4m3_to_f16(hi), a3 = e4m3_to_f16(hi >> 16);
+              uint32_t a0, a1, a2, a3;
+              e4m3_to_f16(kr[s][0][j][i], a0, a2);
+              e4m3_to_f16(kr[s][1][j][i], a1, a3);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 mma<false>(x[s][nt], a0, a1, a2, a3, qf[nt][4 * j + i][0], qf[nt][4 * j + i][1]);
@@ -575,9 +576,11 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
               const uint32_t a = __byte_perm(v0, v1, 0x5140), b2 = __byte_perm(v2, v3, 0x5140);
               const uint32_t c = __byte_perm(v0, v1, 0x7362), d = __byte_perm(v2, v3, 0x7362);
               const int t = 2 * (j * VW + i);
-              const uint32_t f[8] = {e4m3_to_f16(a), e4m3_to_f16(a >> 16), e4m3_to_f16(b2),
-                                     e4m3_to_f16(b2 >> 16), e4m3_to_f16(c), e4m3_to_f16(c >> 16),
-                                     e4m3_to_f16(d), e4m3_to_f16(d >> 16)};
+              uint32_t f[8];
+              e4m3_to_f16(a, f[0], f[1]);
+              e4m3_to_f16(b2, f[2], f[3]);
+              e4m3_to_f16(c, f[4], f[5]);
+              e4m3_to_f16(d, f[6], f[7]);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 mma<false>(o[nt][t], f[0], f[1], f[2], f[3], ph[nt][0], ph[nt][1]);
