@@ -547,7 +547,7 @@ spec_status spec_append_tokens(const void* k_new, int64_t k_stride, const void* 
  *            + h * q_stride_h + d.
  *   k_cache, v_cache cache_dtype (q's type, or SPEC_E4M3 with k_scale / v_scale
  *            as in spec_append_tokens), strides as there; page_stride is a
- *            multiple of token_stride.
+ *            multiple of token_stride, caches and strides 32-byte aligned.
  *   block_table [B,max_pages] int32; seq_len [B] int32: stored tokens, the new
  *            one included (append it first).  The token sees positions
  *            max(0, seq_len - window) .. seq_len - 1 (window 0: all of them).

@@ -14,7 +14,7 @@
 // Design.  A CTA (4 warps) takes one KV head (up to 8 or 16 of its query heads)
 // and one contiguous range of the batch's positions; all CTAs of a launch are
 // resident at once and the ranges are cut evenly over the whole batch (units of
-// 64 positions, counted from seq_len on the device), so ragged batches, one long
+// 64 or 128 positions, counted from seq_len on the device), so ragged batches, one long
 // sequence and the launch of a captured graph whose lengths change all fill the
 // GPU alike.  The CTAs of a range's heads are neighbours in the grid and walk the
 // same token rows together.
@@ -45,7 +45,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kUnit = 64;             // positions: the granularity of the ranges
+// Ranges are cut in units of the positions that a CTA's warps take at once: 64 or 128.
+constexpr int kMinUnit = 16 * kWarps;
 constexpr int kMaxHeadGroups = 4096;  // KV heads x head groups
 constexpr int kMaxCounters = 2 * kMaxHeadGroups;  // two per CTA
 constexpr int kMaxJoin = 64;          // parts that the last CTA joins; more: join_kernel
@@ -122,7 +123,13 @@ SPEC_DEV void e4m3_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {  // bytes 0,
 // N words of the cache, read once: not kept in L1, first out of L2
 template <int N>
 SPEC_DEV void load_words(uint32_t* w, const char* p, uint64_t pol) {
-  if constexpr (N == 4)
+  if constexpr (N == 8)
+    asm volatile(
+        "ld.global.nc.L1::no_allocate.L2::cache_hint.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], %9;"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
+          "=r"(w[7])
+        : "l"(p), "l"(pol));
+  else if constexpr (N == 4)
     asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.b32 {%0,%1,%2,%3}, [%4], %5;"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                  : "l"(p), "l"(pol));
@@ -142,8 +149,9 @@ SPEC_DEV int stored(const DecodeParams& p, int b) {
   return n < 0 ? 0 : min(n, p.max_pages * p.P.d);
 }
 
+template <int U>
 SPEC_DEV int units_of(const DecodeParams& p, int n) {
-  return (n - seen_from(p, n) + kUnit - 1) / kUnit;
+  return (n - seen_from(p, n) + U - 1) / U;
 }
 
 template <int N>
@@ -180,10 +188,17 @@ struct Shape {
   static constexpr int kBytes = D * elem_bytes<CT>();           // of a row
   static constexpr int kTile = 16 * kBytes <= 2048 ? 32 : 16;   // positions of a warp's tile
   static constexpr int kSub = kTile / 16;
+  static constexpr int kUnit = kTile * kWarps;
   static constexpr int kKPieces = kBytes / 64;                  // 16-byte pieces per lane and row
   static constexpr int kVWords = kBytes >= 128 ? 4 : kBytes / 32;  // words of a lane's V piece
   static constexpr int kVPieces = kBytes >= 128 ? kBytes / 128 : 1;
   static constexpr int kSteps = D / 16;
+  // A lane's 16-byte pieces of a row, in pairs where the row is long enough (one 32-byte
+  // load): byte of piece j of lane c of 4 (K) and of lane n of 8 (V).
+  static constexpr bool kPairK = kBytes >= 128, kPairV = kBytes >= 256;
+  SPEC_DEV static constexpr int k_byte(int j) { return kPairK ? (j >> 1) * 128 + (j & 1) * 16 : j * 64; }
+  SPEC_DEV static constexpr int v_byte(int j) { return kPairV ? (j >> 1) * 256 + (j & 1) * 16 : j * 128; }
+  static constexpr int kLaneK = kPairK ? 32 : 16, kLaneV = kPairV ? 32 : kVWords * 4;
 };
 
 // The parts of sequence b's head group, joined by one CTA in the parts' order: a
@@ -261,6 +276,7 @@ template <int CT, int D, int NT, int MINB>
 __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
     const __grid_constant__ DecodeParams p) {
   using S = Shape<CT, D, NT>;
+  constexpr int kUnit = S::kUnit;
   constexpr bool kBf = CT == kBf16, kTwo = CT != kE4m3;  // (P as two parts)
   constexpr int NS = S::kSub, KP = S::kKPieces, VW = S::kVWords, VP = S::kVPieces;
   constexpr int kHeads = 8 * NT;
@@ -294,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
     bool idle = false;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-      const int u = units_of(p, stored(p, b));
+      const int u = units_of<kUnit>(p, stored(p, b));
       mine += u;
       idle = idle || u == 0;
     }
@@ -315,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
     if (idles) {  // rows that see nothing: zeros and -inf for this CTA's heads
 #pragma unroll 1
       for (int b = r; b < p.B; b += p.ranges) {
-        if (units_of(p, stored(p, b)) != 0) continue;
+        if (units_of<kUnit>(p, stored(p, b)) != 0) continue;
         const size_t row = (size_t)b * p.Hq + kvh * p.G + h0;
 #pragma unroll 1
         for (int i = threadIdx.x; i < nh * D; i += kThreads)
@@ -331,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
     if (at <= w0 && w0 < at + mine) {
       int b = b0, u;
 #pragma unroll 1
-      while (b + 1 < b1 && at + (u = units_of(p, stored(p, b))) <= w0) at += u, ++b;
+      while (b + 1 < b1 && at + (u = units_of<kUnit>(p, stored(p, b))) <= w0) at += u, ++b;
       seg = {W, nr, w0, cuts.begin(r + 1), b, at};
     }
     __syncthreads();
@@ -340,8 +356,8 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
   const char* zeros = g_zeros + ((blockIdx.x * kWarps + warp) % kZeroRows) * 512;
   uint64_t pol;
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
-  const char* kh = p.k + kvh * p.head_stride + c4 * 16;
-  const char* vh = p.v + kvh * p.head_stride + n8 * VW * 4;
+  const char* kh = p.k + kvh * p.head_stride + c4 * S::kLaneK;
+  const char* vh = p.v + kvh * p.head_stride + n8 * S::kLaneV;
 
   while (true) {
     const int b = seg.b;
@@ -350,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
       const int n = stored(p, b), first = seen_from(p, n);
       t_begin = first + (seg.w - seg.at) * kUnit;
       const int left = seg.w1 - seg.at;  // units of this sequence up to the range's end
-      t_end = left < units_of(p, n) ? first + left * kUnit : n;
+      t_end = left < units_of<kUnit>(p, n) ? first + left * kUnit : n;
     }
     const int32_t* bt = p.table + (size_t)b * p.max_pages;
 
@@ -366,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
       if constexpr (CT == kE4m3) {  // 16 dimensions per lane and piece
 #pragma unroll
         for (int j = 0; j < KP; ++j) {
-          const uint4* s4 = reinterpret_cast<const uint4*>(src + (j * 4 + c4) * 16);
+          const uint4* s4 = reinterpret_cast<const uint4*>(src + c4 * S::kLaneK + S::k_byte(j));
           const uint4 x = s4[0], y = s4[1];
           raw[8 * j] = x.x, raw[8 * j + 1] = x.y, raw[8 * j + 2] = x.z, raw[8 * j + 3] = x.w;
           raw[8 * j + 4] = y.x, raw[8 * j + 5] = y.y, raw[8 * j + 6] = y.z, raw[8 * j + 7] = y.w;
@@ -374,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
       } else {
 #pragma unroll
         for (int j = 0; j < KP; ++j) {
-          const uint4 x = *reinterpret_cast<const uint4*>(src + (j * 4 + c4) * 8);
+          const uint4 x = *reinterpret_cast<const uint4*>(src + (c4 * S::kLaneK + S::k_byte(j)) / 2);
           raw[4 * j] = x.x, raw[4 * j + 1] = x.y, raw[4 * j + 2] = x.z, raw[4 * j + 3] = x.w;
         }
       }
@@ -439,7 +455,8 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
           seen_next[s][x] = rr >= 0;
           const char* src = rr >= 0 ? kh + (uint64_t)(uint32_t)rr * p.token_stride : zeros;
 #pragma unroll
-          for (int j = 0; j < KP; ++j) load_words<4>(kr[s][x][j], src + j * 64, pol);
+          for (int j = 0; j < KP; j += S::kPairK ? 2 : 1)
+            load_words<S::kPairK ? 8 : 4>(kr[s][x][j], src + S::k_byte(j), pol);
         }
     };
     auto load_v = [&](int row, int s) {
@@ -448,7 +465,8 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
           const int rr = __shfl_sync(0xffffffffu, row, 16 * s + 8 * (x >> 1) + 2 * c4 + (x & 1));
           const char* src = rr >= 0 ? vh + (uint64_t)(uint32_t)rr * p.token_stride : zeros;
 #pragma unroll
-          for (int j = 0; j < VP; ++j) load_words<VW>(vr[s][x][j], src + j * 128, pol);
+          for (int j = 0; j < VP; j += S::kPairV ? 2 : 1)
+            load_words<S::kPairV ? 8 : VW>(vr[s][x][j], src + S::v_byte(j), pol);
         }
     };
 
@@ -620,16 +638,16 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
         for (int t = 0; t < S::kSteps; ++t) {
           int d;
           if constexpr (CT == kE4m3)
-            d = (t / (2 * VW)) * 128 + n8 * VW * 4 + (t % (2 * VW)) * 2;
+            d = S::v_byte(t / (2 * VW)) + n8 * S::kLaneV + (t % (2 * VW)) * 2;
           else
-            d = (t / VW) * 64 + n8 * 8 + (t % VW) * 2;
+            d = (S::v_byte(t / VW) + n8 * S::kLaneV) / 2 + (t % VW) * 2;
           *reinterpret_cast<float2*>(&so[warp][8 * nt + 4 * e + c4][d]) = make_float2(o[nt][t][e], o[nt][t][e + 2]);
         }
       }
     __syncthreads();
 
     // parts of this sequence: ranges r_first .. r_last
-    const int at = seg.at, units = units_of(p, stored(p, b));
+    const int at = seg.at, units = units_of<kUnit>(p, stored(p, b));
     const Cuts cuts(seg.W, seg.nr);
     int r_first = r, r_last = r;
     if (at < cuts.begin(r)) r_first = cuts.range_of(at);
@@ -703,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
     __syncthreads();
     if (threadIdx.x == 0) {
       int nb = b + 1;  // (there is one: units are left)
-      while (nb + 1 < p.B && units_of(p, stored(p, nb)) == 0) ++nb;
+      while (nb + 1 < p.B && units_of<kUnit>(p, stored(p, nb)) == 0) ++nb;
       seg.w = seg.at = at + units;
       seg.b = nb;
     }
@@ -717,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
 // the batch may have one: their number is below ranges / (kMaxJoin - 1).
 constexpr int kJoinWarps = 16;
 
-template <int D>
+template <int D, int kUnit>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int kPer = D / 32, kFlight = 8;
   __shared__ float e[1024];  // parts' weights (ranges <= 1024)
@@ -763,7 +781,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
   int mine = 0, W, many, deep = 0;
 #pragma unroll 1
-  for (int b = b0; b < b1; ++b) mine += units_of(p, stored(p, b));
+  for (int b = b0; b < b1; ++b) mine += units_of<kUnit>(p, stored(p, b));
   const int pre = scan(mine, &W), nr = min(p.ranges, W);
   if (nr <= kMaxJoin) return;
   const Cuts cuts(W, nr);
@@ -773,7 +791,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   int at = pre;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    const int u = units_of(p, stored(p, b));
+    const int u = units_of<kUnit>(p, stored(p, b));
     deep += is_deep(at, u);
     at += u;
   }
@@ -782,7 +800,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   at = pre;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    const int u = units_of(p, stored(p, b));
+    const int u = units_of<kUnit>(p, stored(p, b));
     if (is_deep(at, u) && nth++ == k) {
       s_b = b;
       s_at = at;
@@ -908,7 +926,7 @@ spec_status launch(const DecodeParams& p, cudaStream_t st) {
   // may a sequence be cut into more parts than its last CTA joins?  (Each holds a unit at
   // least, and the window or the table's width bounds its units.)
   const int row = p.max_pages * p.P.d, longest = p.window > 0 ? std::min(p.window, row) : row;
-  const bool deep = p.ranges > kMaxJoin && longest / kUnit + 1 > kMaxJoin;
+  const bool deep = p.ranges > kMaxJoin && longest / kMinUnit + 1 > kMaxJoin;
   if (rc != SPEC_OK || !deep) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.ranges / kMaxJoin * p.Hq, 1, 1);
@@ -919,7 +937,7 @@ spec_status launch(const DecodeParams& p, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, join_kernel<D>, p) != cudaSuccess) return SPEC_ECUDA;
+  if (cudaLaunchKernelEx(&cfg, join_kernel<D, Shape<CT, D, NT>::kUnit>, p) != cudaSuccess) return SPEC_ECUDA;
   return launch_status();
 }
 
@@ -962,12 +980,13 @@ extern "C" spec_status spec_decode_attn(const void* q, int64_t q_stride_b, int64
   if (!q || !k_cache || !v_cache || !block_table || !seq_len || !workspace || !out)
     return SPEC_EINVAL;
   const int es = e4m3 ? 1 : 2;
-  if (((uintptr_t)q | (uintptr_t)k_cache | (uintptr_t)v_cache | (uintptr_t)out) & 15)
+  if ((((uintptr_t)q | (uintptr_t)out) & 15) || (((uintptr_t)k_cache | (uintptr_t)v_cache) & 31))
     return SPEC_EINVAL;
   if ((uintptr_t)workspace & 255) return SPEC_EINVAL;
   if (q_stride_b < 0 || q_stride_h < 0 || page_stride < 0 || token_stride < 1 || head_stride < 0)
     return SPEC_EINVAL;
-  if (((q_stride_b | q_stride_h) * 2 | (page_stride | token_stride | head_stride) * es) & 15)
+  if ((((q_stride_b | q_stride_h) * 2) & 15) ||
+      (((page_stride | token_stride | head_stride) * es) & 31))
     return SPEC_EINVAL;
   // cache rows are numbered in token strides, in 31 bits
   if (page_stride % token_stride || token_stride * es > UINT32_MAX) return SPEC_EUNSUPPORTED;
@@ -976,7 +995,7 @@ extern "C" spec_status spec_decode_attn(const void* q, int64_t q_stride_b, int64
       (long long)max_pages * page_size > INT32_MAX)
     return SPEC_EUNSUPPORTED;
   // so are the batch's units
-  if (((long long)max_pages * page_size / kUnit + 1) * B > INT32_MAX) return SPEC_EUNSUPPORTED;
+  if (((long long)max_pages * page_size / kMinUnit + 1) * B > INT32_MAX) return SPEC_EUNSUPPORTED;
   DecodePlan pl;
   if (!make_plan(B, Hq, Hkv, D, e4m3, 0, &pl)) return SPEC_EINVAL;
   if ((long long)Hkv * pl.groups > kMaxHeadGroups) return SPEC_EUNSUPPORTED;

@@ -175,7 +175,8 @@ DECODE = dict(q=_p(), qb=4096, qh=128, qt=api.SPEC_BF16, kc=_p(), vc=_p(), ct=ap
     (dict(Hq=33), 1), (dict(Hkv=0), 1), (dict(window=-1), 1), (dict(P=0), 1), (dict(maxp=0), 1),
     (dict(ct=api.SPEC_F16), 1), (dict(sk=_p()), 1), (dict(qt=api.SPEC_E4M3), 1),
     (dict(ws=_p(4096 + 128)), 1), (dict(wsb=1000), 1), (dict(qb=4097), 1), (dict(st=0), 1),
-    (dict(kc=_p(4100)), 1), (dict(qt=api.SPEC_F32, ct=api.SPEC_F32), 2), (dict(D=96), 2),
+    (dict(kc=_p(4112)), 1), (dict(vc=_p(4112)), 1), (dict(sh=136), 1), (dict(out=_p(4104)), 1),
+    (dict(q=_p(4104)), 1), (dict(qt=api.SPEC_F32, ct=api.SPEC_F32), 2), (dict(D=96), 2),
     (dict(sp=1000 * 1024 + 512), 2), (dict(pages=1 << 28), 2), (dict(maxp=1 << 28), 2),
     (dict(Hq=4097, Hkv=4097), 2), (dict(maxp=1 << 26, B=8192), 2), (dict(B=0), 0)])
 def test_decode_attn_refuses_on_the_host(lib, change, code):
