@@ -2,7 +2,8 @@
 
 Every function here checks tensor placement, dtype and shape, allocates the
 outputs and workspaces with PyTorch, and calls the C ABI declared in
-include/spec_verify.h on the current CUDA stream.  All arithmetic of the
+include/spec_verify.h on the current CUDA stream (with ctypes, or from
+csrc/binding.cpp for the calls of a drafter's own steps).  All arithmetic of the
 verify step runs in the library's kernels; there is no fallback: if the
 library is missing or a call fails, an exception is raised.
 """
@@ -60,12 +61,6 @@ class SamplerConfig:
         return _Sampler(float(self.temperature), int(self.top_k), float(self.top_p),
                         1 if self.greedy else 0, int(self.eos_id))
 
-
-# the current stream's handle without a Stream object, and the current device without
-# the check that CUDA is up (2 us of host time a call): both are asked for CUDA tensors
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 _lib = None
 _P = ctypes.c_void_p
@@ -213,7 +208,7 @@ def kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.T
     (optional) lets the kernel check that the path follows the tree.
     Returns (new_len, keep_pages, status)."""
     lib = load()
-    if k_cache.dtype not in _DTYPE:
+    if k_cache.dtype not in (torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn):
         raise ValueError("caches must be bf16, fp16, fp32 or float8_e4m3fn")
     npg, P, Hkv, D = k_cache.shape
     _need(k_cache, "k_cache", k_cache.dtype)
@@ -471,76 +466,24 @@ def accept_sample_tree(logits, draft_probs, node_tokens, parent, uniforms, cfg: 
 
 
 # ------------------------------------------------------------------ the cache's side
-_DTYPE = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16,
-          torch.float8_e4m3fn: SPEC_E4M3}
+# These calls run once per drafted token: their checks, allocations and launches are
+# native (csrc/binding.cpp), on the tensors' device and its current stream.
+_native = None
 
 
-def _elsewhere(dev, stream):
-    """True when the call has to change the current device or stream first."""
-    return stream is not None or dev.index != _current_device()
-
-
-def _tensor(t, name, dev, dtype, shape):
-    """The address of a contiguous tensor of this type and shape on `dev`."""
-    if not isinstance(t, torch.Tensor):
-        raise ValueError(f"{name} must be a tensor on {dev}")
-    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
-        return t.data_ptr()
-    if t.device != dev:
-        raise ValueError(f"{name} must be a tensor on {dev}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _cuda_device(t, name):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
-
-
-def _rows(t, name, dev, dtype, heads, D):
-    """[T, heads, D] rows whose heads lie side by side; returns (pointer, row stride)."""
-    if not isinstance(t, torch.Tensor) or t.device != dev:
-        raise ValueError(f"{name} must be a tensor on {dev}")
-    if t.dtype is dtype and t.dim() == 3:
-        _, h, d = t.shape
-        s0, s1, s2 = t.stride()
-        if h == heads and d == D:
-            if s2 == 1 and (s1 == D or heads == 1):
-                return t.data_ptr(), s0
-            raise ValueError(f"{name}: a row's heads must lie side by side")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    raise ValueError(f"{name} must be [tokens, {heads}, {D}], got {tuple(t.shape)}")
-
-
-def _caches(k_cache, v_cache, dev, dtype):
-    """Checks the pair; returns (k, v, shape, dtype code, page, token, head strides)."""
-    if not isinstance(k_cache, torch.Tensor) or k_cache.device != dev:
-        raise ValueError(f"k_cache must be a tensor on {dev}")
-    if not isinstance(v_cache, torch.Tensor) or v_cache.device != dev:
-        raise ValueError(f"v_cache must be a tensor on {dev}")
-    shape, kind, st = k_cache.shape, k_cache.dtype, k_cache.stride()
-    if len(shape) != 4 or v_cache.shape != shape:
-        raise ValueError("caches must be [pages, page_size, Hkv, D], both alike")
-    if v_cache.dtype is not kind:
-        raise ValueError("k_cache and v_cache must have one dtype")
-    if kind is not dtype and (kind is not torch.float8_e4m3fn or dtype is torch.float32):
-        raise ValueError(f"caches must be {dtype}" + ("" if dtype is torch.float32
-                                                      else " or float8_e4m3fn"))
-    if st[3] != 1 or v_cache.stride() != st:
-        raise ValueError("caches must have the same strides, 1 over D")
-    return k_cache.data_ptr(), v_cache.data_ptr(), shape, _DTYPE[kind], st[0], st[1], st[2]
-
-
-def _scales(k_scale, v_scale, kind, Hkv, dev):
-    if kind != SPEC_E4M3:
-        raise ValueError("scales belong to float8_e4m3fn caches")
-    return tuple(None if t is None else _tensor(t, name, dev, torch.float32, (Hkv,))
-                 for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")))
+def _calls():
+    """The native binding (once).  Raises if it has not been built."""
+    global _native
+    if _native is None:
+        load()
+        path = os.path.join(_HERE, "_native.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with __graft_entry__.build(); "
+                               "there is no fallback")
+        from . import _native as m
+        m.set_error(SpecError)
+        _native = m
+    return _native
 
 
 def extend_tables(ctx_len, add_len, block_table, free_list, free_count, page_size: int,
@@ -552,39 +495,12 @@ def extend_tables(ctx_len, add_len, block_table, free_list, free_count, page_siz
     [max_tokens], cu_len [B+1], new_len [B], free_count [1], status [B]); free_count is
     what is left of the list, for the next call.  out: an earlier call's dict of these
     shapes, written again (its free_count is not this call's)."""
-    dev = _cuda_device(ctx_len, "ctx_len")
-    if _elsewhere(dev, stream):
-        with torch.cuda.device(dev), torch.cuda.stream(stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
             return extend_tables(ctx_len, add_len, block_table, free_list, free_count, page_size,
                                  max_tokens, out)
-    i32 = torch.int32
-    if not (0 < page_size < 2 ** 31 and 0 <= max_tokens < 2 ** 31):
-        raise ValueError("page_size and max_tokens must be below 2^31")
-    if ctx_len.dim() != 1 or block_table.dim() != 2 or free_list.dim() != 1:
-        raise ValueError("ctx_len [B], block_table [B, max_pages], free_list [num_pages]")
-    B, width = ctx_len.shape[0], block_table.shape[1]
-    ins = (_tensor(ctx_len, "ctx_len", dev, i32, (B,)),
-           _tensor(add_len, "add_len", dev, i32, (B,)))
-    table = _tensor(block_table, "block_table", dev, i32, (B, width))
-    n = free_list.shape[0]
-    lst = _tensor(free_list, "free_list", dev, i32, (n,))
-    cnt = _tensor(free_count, "free_count", dev, i32, (1,))
-    if out is None:
-        cu, new_len, left, status = torch.empty(3 * B + 2, dtype=i32, device=dev).split(
-            (B + 1, B, 1, B))
-        out = dict(slot_map=torch.empty(max_tokens, dtype=torch.int64, device=dev),
-                   positions=torch.empty(max_tokens, dtype=i32, device=dev), cu_len=cu,
-                   new_len=new_len, free_count=left, status=status)
-    _check("spec_extend_tables",
-           (_lib or load()).spec_extend_tables(
-               *ins, B, page_size, table, width, lst, n, cnt, max_tokens,
-               _tensor(out["slot_map"], "slot_map", dev, torch.int64, (max_tokens,)),
-               _tensor(out["positions"], "positions", dev, i32, (max_tokens,)),
-               _tensor(out["cu_len"], "cu_len", dev, i32, (B + 1,)),
-               _tensor(out["new_len"], "new_len", dev, i32, (B,)),
-               _tensor(out["free_count"], "free_count", dev, i32, (1,)),
-               _tensor(out["status"], "status", dev, i32, (B,)), _raw_stream(dev.index)))
-    return out
+    return (_native or _calls()).extend_tables(ctx_len, add_len, block_table, free_list,
+                                               free_count, page_size, max_tokens, out)
 
 
 def release_pages(block_table, length, keep_pages, free_list, free_count, page_size: int,
@@ -593,29 +509,12 @@ def release_pages(block_table, length, keep_pages, free_list, free_count, page_s
 
     length [B]: tokens the rows were extended for; keep_pages [B]: kv_commit's, or 0
     for a finished request.  Returns (free_count [1], status [B])."""
-    dev = _cuda_device(length, "length")
-    if _elsewhere(dev, stream):
-        with torch.cuda.device(dev), torch.cuda.stream(stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
             return release_pages(block_table, length, keep_pages, free_list, free_count,
                                  page_size, total, status)
-    i32 = torch.int32
-    if not 0 < page_size < 2 ** 31:
-        raise ValueError("page_size must be below 2^31")
-    if length.dim() != 1 or block_table.dim() != 2 or free_list.dim() != 1:
-        raise ValueError("length [B], block_table [B, max_pages], free_list [num_pages]")
-    B, width, n = length.shape[0], block_table.shape[1], free_list.shape[0]
-    table = _tensor(block_table, "block_table", dev, i32, (B, width))
-    held = _tensor(length, "length", dev, i32, (B,))
-    keep = _tensor(keep_pages, "keep_pages", dev, i32, (B,))
-    lst = _tensor(free_list, "free_list", dev, i32, (n,))
-    cnt = _tensor(free_count, "free_count", dev, i32, (1,))
-    total = torch.empty(1, dtype=i32, device=dev) if total is None else total
-    status = torch.empty(B, dtype=i32, device=dev) if status is None else status
-    _check("spec_release_pages",
-           (_lib or load()).spec_release_pages(table, width, held, keep, B, page_size, lst, n, cnt,
-                                     _tensor(total, "total", dev, i32, (1,)),
-                                     _tensor(status, "status", dev, i32, (B,)), _raw_stream(dev.index)))
-    return total, status
+    return (_native or _calls()).release_pages(block_table, length, keep_pages, free_list,
+                                               free_count, page_size, total, status)
 
 
 def append_tokens(k_new, v_new, k_cache, v_cache, slot_map, positions=None, q=None, q_out=None,
@@ -624,48 +523,12 @@ def append_tokens(k_new, v_new, k_cache, v_cache, slot_map, positions=None, q=No
     `positions` (rope_base 0: not); with q [T, Hq, D] the rotated queries go to q_out
     (allocated if not given; q itself rotates in place).  Rows with a slot outside the
     cache are skipped.  Returns q_out (None without q)."""
-    dev = _cuda_device(k_new, "k_new")
-    if _elsewhere(dev, stream):
-        with torch.cuda.device(dev), torch.cuda.stream(stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
             return append_tokens(k_new, v_new, k_cache, v_cache, slot_map, positions, q, q_out,
                                  rope_base, k_scale, v_scale)
-    dt = k_new.dtype
-    if dt not in _DTYPE or dt is torch.float8_e4m3fn:
-        raise ValueError("k_new must be bf16, fp16 or fp32")
-    kc, vc, (npg, P, Hkv, D), kind, sp, st, sh = _caches(k_cache, v_cache, dev, dt)
-    k, ks = _rows(k_new, "k_new", dev, dt, Hkv, D)
-    v, vs = _rows(v_new, "v_new", dev, dt, Hkv, D)
-    T = k_new.shape[0]
-    slots = _tensor(slot_map, "slot_map", dev, torch.int64, (T,))
-    if v_new.shape[0] != T:
-        raise ValueError("v_new and k_new must have the same rows")
-    pos = None
-    if positions is not None:
-        pos = _tensor(positions, "positions", dev, torch.int32, (T,))
-    elif rope_base:
-        raise ValueError("positions are needed to rotate (rope_base 0: no rotation)")
-    Hq, qp, qs, op, os_ = 0, None, 0, None, 0
-    if q is not None:
-        if q.dim() != 3 or q.shape[0] != T:
-            raise ValueError("q must be [tokens, Hq, D]")
-        Hq = q.shape[1]
-        qp, qs = _rows(q, "q", dev, dt, Hq, D)
-        if q_out is None:
-            q_out = torch.zeros((T, Hq, D), dtype=dt, device=dev)
-        op, os_ = _rows(q_out, "q_out", dev, dt, Hq, D)
-        if q_out.shape[0] != T:
-            raise ValueError("q_out and q must have the same rows")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    sk = sv = None
-    if k_scale is not None or v_scale is not None:
-        sk, sv = _scales(k_scale, v_scale, kind, Hkv, dev)
-    rc = (_lib or load()).spec_append_tokens(k, ks, v, vs, qp, qs, op, os_, _DTYPE[dt], kc, vc,
-                                             kind, sk, sv, npg, P, sp, st, sh, slots, pos, T, Hq,
-                                             Hkv, D, rope_base, _raw_stream(dev.index))
-    if rc:
-        _check("spec_append_tokens", rc)
-    return q_out
+    return (_native or _calls()).append_tokens(k_new, v_new, k_cache, v_cache, slot_map,
+                                               positions, q, q_out, rope_base, k_scale, v_scale)
 
 
 def decode_attn_workspace_size(B, Hq, Hkv, D) -> int:
@@ -679,51 +542,9 @@ def decode_attn(q, k_cache, v_cache, block_table, seq_len, scale: float = 0.0, w
     q [B, Hq, D] bf16 or fp16 (strided over B and Hq as it comes); caches [pages, P,
     Hkv, D] of q's dtype or float8_e4m3fn with scales [Hkv]; seq_len [B] counts the
     stored tokens, the new one included.  Returns (out [B, Hq, D], lse [B, Hq])."""
-    dev = _cuda_device(q, "q")
-    if _elsewhere(dev, stream):
-        with torch.cuda.device(dev), torch.cuda.stream(stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
             return decode_attn(q, k_cache, v_cache, block_table, seq_len, scale, window, k_scale,
                                v_scale, workspace, out, lse)
-    dt = q.dtype
-    if dt is not torch.bfloat16 and dt is not torch.float16:
-        raise ValueError("q must be bf16 or fp16")
-    if q.dim() != 3 or q.stride(2) != 1:
-        raise ValueError("q must be [B, Hq, D], contiguous over D")
-    B, Hq, D = q.shape
-    kc, vc, (npg, P, Hkv, D2), kind, sp, st, sh = _caches(k_cache, v_cache, dev, dt)
-    if D2 != D:
-        raise ValueError("head_dim mismatch")
-    if not 0 <= window < 2 ** 31:
-        raise ValueError("window must be 0 or a number of positions below 2^31")
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    width = block_table.shape[1]
-    table = _tensor(block_table, "block_table", dev, torch.int32, (B, width))
-    lens = _tensor(seq_len, "seq_len", dev, torch.int32, (B,))
-    sk = sv = None
-    if k_scale is not None or v_scale is not None:
-        sk, sv = _scales(k_scale, v_scale, kind, Hkv, dev)
-    lib = _lib or load()
-    if workspace is None:
-        workspace = new_workspace(lib.spec_decode_attn_workspace_size(B, Hq, Hkv, D), dev)
-    elif workspace.device != dev or workspace.dtype is not torch.uint8 \
-            or not workspace.is_contiguous():
-        raise ValueError("workspace must come from new_workspace on q's device")
-    if out is None:
-        out = torch.empty((B, Hq, D), dtype=dt, device=dev)
-        o = out.data_ptr()
-    else:
-        o = _tensor(out, "out", dev, dt, (B, Hq, D))
-    if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-        ls = lse.data_ptr()
-    else:
-        ls = _tensor(lse, "lse", dev, torch.float32, (B, Hq))
-    s0, s1, _ = q.stride()
-    rc = lib.spec_decode_attn(q.data_ptr(), s0, s1, _DTYPE[dt], kc, vc, kind, sk, sv, npg, P, sp,
-                              st, sh, table, width, lens, B, Hq, Hkv, D, window, scale,
-                              workspace.data_ptr(), workspace.numel(), o, ls,
-                              _raw_stream(dev.index))
-    if rc:
-        _check("spec_decode_attn", rc)
-    return out, lse
+    return (_native or _calls()).decode_attn(q, k_cache, v_cache, block_table, seq_len, scale,
+                                             window, k_scale, v_scale, workspace, out, lse)

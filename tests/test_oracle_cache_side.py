@@ -193,7 +193,7 @@ def test_decode_workspace(lib):
     assert lib.spec_decode_attn(*dict(DECODE, wsb=ws // 2).values()) == api.SPEC_EINVAL
 
 
-def test_bindings_refuse_host_tensors():
+def test_bindings_refuse_host_tensors(lib):
     z = torch.zeros
     i = torch.int32
     with pytest.raises(ValueError, match="CUDA tensor"):
