@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(kThreads) append_tokens_kernel(
   __shared__ __align__(16) float cs[TB][kHalf], sn[TB][kHalf];
   __shared__ long long dst[TB];  // element offset of the token's cache row; < 0: skipped
   const int t0 = blockIdx.x * TB;
+  chain_wait();
   if (threadIdx.x < TB) {
     const int t = t0 + threadIdx.x;
     long long off = -1;
@@ -180,11 +181,9 @@ __global__ void __launch_bounds__(kThreads) append_tokens_kernel(
 
 template <typename T, typename C, int D>
 spec_status launch(const AppendParams& p, cudaStream_t st) {
-  if (p.T <= kFewTokens)
-    append_tokens_kernel<T, C, D, 1><<<p.T, kThreads, 0, st>>>(p);
-  else
-    append_tokens_kernel<T, C, D, 2><<<(p.T + 1) / 2, kThreads, 0, st>>>(p);
-  return launch_status();
+  return p.T <= kFewTokens
+             ? launch_chained(append_tokens_kernel<T, C, D, 1>, p.T, kThreads, 0, st, p)
+             : launch_chained(append_tokens_kernel<T, C, D, 2>, (p.T + 1) / 2, kThreads, 0, st, p);
 }
 
 template <typename T, typename C>

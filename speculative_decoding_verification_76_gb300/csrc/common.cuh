@@ -269,6 +269,32 @@ static inline spec_status launch_status() {
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
 }
 
+// Programmatic dependent launch: a kernel started by launch_chained is set up while the
+// kernel in front of it on the stream still runs, and chain_wait() holds it until that
+// kernel is complete and its stores are visible; every global access comes after it.
+// chain_next() lets the next such kernel start early.  It is worth having only where that
+// one has work to do before its wait: blocks that merely wait slowed the ones they waited
+// for (extend + release 8.4 against 9.7 us, one-token attention 13.1 against 14.1).
+SPEC_DEV void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+SPEC_DEV void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename P>
+static inline spec_status launch_chained(void (*kernel)(P), int grid, int block, size_t smem,
+                                         cudaStream_t st, const P& params) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, params) != cudaSuccess) return SPEC_ECUDA;
+  return launch_status();
+}
+
 // Raise `func`'s dynamic shared-memory limit to `bytes` on the current device,
 // once per device and thread-safely (`once` is the launch site's record).
 // Device ordinals beyond the record's range set the attribute on every call.

@@ -68,6 +68,7 @@ struct DecodeParams {
   uint32_t page_rows;                        // page stride in token strides
   FastDiv P;                                 // page size
   int B, Hq, Hkv, G, groups, hpg, num_pages, max_pages, window, ranges, q_bf16;
+  int deep;                                  // join_kernel follows
   float scale_log2;
 };
 
@@ -299,7 +300,8 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n8 = lane >> 2, c4 = lane & 3;
   const int HV = p.Hkv * p.groups;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // join_kernel waits for our end
+  chain_wait();
+  if (p.deep) chain_next();  // join_kernel: it finds its sequence meanwhile
 
   // ---- this CTA's units of the batch's W, and the sequence that holds the first:
   // every thread takes `per` consecutive sequences of one running sum
@@ -815,7 +817,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   auto row_of = [&](int i) {  // part i of head h
     return (((size_t)(r_first + i) * 2 + (i == 0 && late)) * HV + hv) * p.hpg + h;
   };
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  chain_wait();
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
   float2 x[2];
 #pragma unroll
@@ -919,26 +921,17 @@ size_t ws_layout(const DecodePlan& pl, int Hkv, int D, size_t* off_o, size_t* of
 }
 
 template <int CT, int D, int NT>
-spec_status launch(const DecodeParams& p, cudaStream_t st) {
+spec_status launch(DecodeParams p, cudaStream_t st) {
   constexpr int kOcc = per_sm(CT == kE4m3, D, NT);
-  decode_kernel<CT, D, NT, kOcc><<<p.ranges * p.Hkv * p.groups, kThreads, 0, st>>>(p);
-  spec_status rc = launch_status();
   // may a sequence be cut into more parts than its last CTA joins?  (Each holds a unit at
   // least, and the window or the table's width bounds its units.)
   const int row = p.max_pages * p.P.d, longest = p.window > 0 ? std::min(p.window, row) : row;
-  const bool deep = p.ranges > kMaxJoin && longest / kMinUnit + 1 > kMaxJoin;
-  if (rc != SPEC_OK || !deep) return rc;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.ranges / kMaxJoin * p.Hq, 1, 1);
-  cfg.blockDim = dim3(32 * kJoinWarps, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, join_kernel<D, Shape<CT, D, NT>::kUnit>, p) != cudaSuccess) return SPEC_ECUDA;
-  return launch_status();
+  p.deep = p.ranges > kMaxJoin && longest / kMinUnit + 1 > kMaxJoin;
+  const spec_status rc = launch_chained(decode_kernel<CT, D, NT, kOcc>,
+                                        p.ranges * p.Hkv * p.groups, kThreads, 0, st, p);
+  if (rc != SPEC_OK || !p.deep) return rc;
+  return launch_chained(join_kernel<D, Shape<CT, D, NT>::kUnit>, p.ranges / kMaxJoin * p.Hq,
+                        32 * kJoinWarps, 0, st, p);
 }
 
 template <int CT>

@@ -24,8 +24,7 @@
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kFewSeqs = 256;       // up to here blocks of 128 threads, else of 256
 constexpr int kMaxSeqs = 8192;      // two running sums of 4 bytes: 64 KB of shared memory
 constexpr int kTokensPerThread = 4;
 constexpr int kWarpPages = 64;      // more pages than this: the whole CTA writes the row
@@ -36,7 +35,9 @@ SPEC_DEV int sat_add(int a, int b) {
 }
 
 // Exclusive running sum over the block of one value >= 0 per thread; *total: the sum.
+template <int kThreads>
 SPEC_DEV int block_scan(int v, int* total) {
+  constexpr int kWarps = kThreads / 32;
   __shared__ int part[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
@@ -70,10 +71,13 @@ struct ExtendParams {
   int B, max_pages, num_pages, cap;
 };
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const ExtendParams p) {
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ int32_t sm[];
   int32_t* tok = sm;             // [B + 1] first row of each sequence (at most cap + 1)
   int32_t* pg = sm + p.B + 1;    // [B] pages of the step in front of it; < 0: refused (-1 - bit)
+  chain_wait();
   const int count = clamp_count(*p.free_count, p.num_pages);
 
   // ---- running sums; a thread holds `per` consecutive sequences
@@ -82,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const ExtendPar
   const uint32_t row_max = (uint32_t)p.max_pages * p.P.d;  // tokens a table row can name
   int sum = 0, total;
   for (int b = b0; b < b1; ++b) sum = sat_add(sum, max(p.add[b], 0));
-  int at = block_scan(sum, &total);
+  int at = block_scan<kThreads>(sum, &total);
   int need_sum = 0;
   for (int b = b0; b < b1; ++b) {
     const int c = p.ctx[b], a = p.add[b];
@@ -99,7 +103,7 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const ExtendPar
     if (blockIdx.x == 0) p.cu[p.B] = total;
   }
   int unused;
-  int pages = block_scan(need_sum, &unused);
+  int pages = block_scan<kThreads>(need_sum, &unused);
   int taken = 0;   // the largest running sum that fits: what the step takes
   for (int b = b0; b < b1; ++b) {
     const int need = pg[b];
@@ -209,9 +213,12 @@ struct ReleaseParams {
   int B, max_pages, num_pages;
 };
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleaseParams p) {
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ int32_t sm[];
   int32_t* at = sm;  // [B] place of the sequence's first page on the list; < 0: refused
+  chain_wait();
   const int count = clamp_count(*p.free_count, p.num_pages);
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
@@ -222,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleasePa
     at[b] = bad ? INT_MIN : held - k;
     if (!bad) sum = sat_add(sum, held - k);
   }
-  int pages = sat_add(count, block_scan(sum, &unused));
+  int pages = sat_add(count, block_scan<kThreads>(sum, &unused));
   int end = 0;
   for (int b = b0; b < b1; ++b) {
     const int n = at[b];
@@ -280,10 +287,11 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleasePa
   }
 }
 
-// CTAs: a warp per sequence, four rows per thread, at most two per SM
-int grid_for(int B, long long tokens) {
-  const long long a = (B + kWarps - 1) / kWarps;
-  const long long t = (tokens + kThreads * kTokensPerThread - 1) / (kThreads * kTokensPerThread);
+// CTAs of `threads`: a warp per sequence, four rows per thread, at most two per SM
+int grid_for(int B, long long tokens, int threads) {
+  const int warps = threads / 32;
+  const long long a = (B + warps - 1) / warps;
+  const long long t = (tokens + threads * kTokensPerThread - 1) / (threads * kTokensPerThread);
   const long long g = a > t ? a : t;
   return (int)(g < 1 ? 1 : g > 304 ? 304 : g);
 }
@@ -310,15 +318,16 @@ extern "C" spec_status spec_extend_tables(const int32_t* ctx_len, const int32_t*
   const size_t smem = (2 * (size_t)B + 1) * sizeof(int32_t);
   if (smem > 48 * 1024) {
     static PerDeviceOnce<int> smem_once;  // once per device, at the largest size
-    const spec_status ra = ensure_smem_limit(smem_once, (const void*)extend_tables_kernel,
+    const spec_status ra = ensure_smem_limit(smem_once, (const void*)extend_tables_kernel<256>,
                                              (2 * kMaxSeqs + 1) * (int)sizeof(int32_t));
     if (ra != SPEC_OK) return ra;
   }
   const ExtendParams p{ctx_len, add_len,   free_list, free_count, block_table, positions, cu_len,
                        new_len, free_left, status_per_seq, slot_map, FastDiv(page_size), B,
                        max_pages, num_pages, max_tokens};
-  extend_tables_kernel<<<grid_for(B, max_tokens), kThreads, smem, (cudaStream_t)stream>>>(p);
-  return launch_status();
+  const int threads = B <= kFewSeqs ? 128 : 256;
+  return launch_chained(B <= kFewSeqs ? extend_tables_kernel<128> : extend_tables_kernel<256>,
+                        grid_for(B, max_tokens, threads), threads, smem, (cudaStream_t)stream, p);
 }
 
 extern "C" spec_status spec_release_pages(const int32_t* block_table, int max_pages,
@@ -333,7 +342,8 @@ extern "C" spec_status spec_release_pages(const int32_t* block_table, int max_pa
     return SPEC_EUNSUPPORTED;
   const ReleaseParams p{block_table, len, keep_pages, free_count, free_list, free_total,
                         status_per_seq, FastDiv(page_size), B, max_pages, num_pages};
-  release_pages_kernel<<<grid_for(B, 0), kThreads, (size_t)B * sizeof(int32_t),
-                         (cudaStream_t)stream>>>(p);
-  return launch_status();
+  const int threads = B <= kFewSeqs ? 128 : 256;
+  return launch_chained(B <= kFewSeqs ? release_pages_kernel<128> : release_pages_kernel<256>,
+                        grid_for(B, 0, threads), threads, (size_t)B * sizeof(int32_t),
+                        (cudaStream_t)stream, p);
 }
