@@ -18,12 +18,14 @@
 // between CTAs.  A token's page comes from the old table entry or straight from
 // the free list, never from an entry that this launch writes.  The counts are
 // read from one word and written to another for the same reason.
+#include <algorithm>
 #include <climits>
 
 #include "common.cuh"
 
 namespace {
 
+constexpr int kMostCtas = 304;      // two per SM
 constexpr int kFewSeqs = 256;       // up to here blocks of 128 threads, else of 256
 constexpr int kMaxSeqs = 8192;      // two running sums of 4 bytes: 64 KB of shared memory
 constexpr int kTokensPerThread = 4;
@@ -59,6 +61,22 @@ SPEC_DEV int block_scan(int v, int* total) {
   }
   *total = sum;
   return sat_add(before, x);
+}
+
+// dst[j] = f(src[step j]) for j < n, a lane's ids loaded eight at a time (the compiler
+// cannot move a load over a store here: 30000 ids of one request took 80 us one by one).
+template <typename F>
+SPEC_DEV void copy_ids(const int32_t* src, int step, int32_t* dst, int n, int lane, int lanes,
+                       F f) {
+#pragma unroll 1
+  for (int j0 = lane; j0 < n; j0 += 8 * lanes) {
+    int id[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) id[u] = j0 + u * lanes < n ? src[step * (j0 + u * lanes)] : 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (j0 + u * lanes < n) dst[j0 + u * lanes] = f(id[u]);
+  }
 }
 
 SPEC_DEV int clamp_count(int c, int n) { return c < 0 ? 0 : c > n ? n : c; }
@@ -136,12 +154,10 @@ __global__ void __launch_bounds__(kThreads) extend_tables_kernel(const ExtendPar
       bad = id < 0 || id >= p.num_pages;
     }
     const int32_t* from = p.free_list + (count - 1 - pg[b]);
-#pragma unroll 4
-    for (int j = lane; j < need; j += lanes) {
-      const int id = from[-j];
-      t[have + j] = id;
+    copy_ids(from, -1, t + have, need, lane, lanes, [&](int id) {
       bad = bad || id < 0 || id >= p.num_pages;
-    }
+      return id;
+    });
     return bad;
   };
   auto finish = [&](int b, bool bad) {
@@ -256,13 +272,11 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleasePa
   auto row = [&](int b, int n, int lane, int lanes) {
     const int32_t* t = p.table + (size_t)b * p.max_pages + p.keep[b];
     bool bad = false;
-#pragma unroll 4
-    for (int j = lane; j < n; j += lanes) {
-      const int id = t[j];
+    copy_ids(t, 1, p.free_list + at[b], n, lane, lanes, [&](int id) {
       const bool ok = id >= 0 && id < p.num_pages;
-      p.free_list[at[b] + j] = ok ? id : -1;
       bad = bad || !ok;
-    }
+      return ok ? id : -1;
+    });
     return bad;
   };
   auto pages_of = [&](int b) { return p.P.ceil_quot(p.len[b]) - p.keep[b]; };
@@ -293,7 +307,7 @@ int grid_for(int B, long long tokens, int threads) {
   const long long a = (B + warps - 1) / warps;
   const long long t = (tokens + threads * kTokensPerThread - 1) / (threads * kTokensPerThread);
   const long long g = a > t ? a : t;
-  return (int)(g < 1 ? 1 : g > 304 ? 304 : g);
+  return (int)(g < 1 ? 1 : g > kMostCtas ? kMostCtas : g);
 }
 
 }  // namespace
@@ -343,7 +357,9 @@ extern "C" spec_status spec_release_pages(const int32_t* block_table, int max_pa
   const ReleaseParams p{block_table, len, keep_pages, free_count, free_list, free_total,
                         status_per_seq, FastDiv(page_size), B, max_pages, num_pages};
   const int threads = B <= kFewSeqs ? 128 : 256;
+  // a CTA per sequence where rows may be long (a finished request gives all its pages)
   return launch_chained(B <= kFewSeqs ? release_pages_kernel<128> : release_pages_kernel<256>,
-                        grid_for(B, 0, threads), threads, (size_t)B * sizeof(int32_t),
-                        (cudaStream_t)stream, p);
+                        max_pages > kWarpPages ? std::max(1, std::min(B, kMostCtas))
+                                               : grid_for(B, 0, threads),
+                        threads, (size_t)B * sizeof(int32_t), (cudaStream_t)stream, p);
 }
