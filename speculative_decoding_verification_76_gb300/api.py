@@ -494,7 +494,7 @@ def extend_tables(ctx_len, add_len, block_table, free_list, free_count, page_siz
     [1] (int32) are only read.  Returns dict(slot_map [max_tokens] int64, positions
     [max_tokens], cu_len [B+1], new_len [B], free_count [1], status [B]); free_count is
     what is left of the list, for the next call.  out: an earlier call's dict of these
-    shapes, written again (its free_count is not this call's)."""
+    shapes, written again (its free_count and new_len are not this call's inputs)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return extend_tables(ctx_len, add_len, block_table, free_list, free_count, page_size,

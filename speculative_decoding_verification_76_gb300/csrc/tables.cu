@@ -20,6 +20,7 @@
 // read from one word and written to another for the same reason.
 #include <algorithm>
 #include <climits>
+#include <initializer_list>
 
 #include "common.cuh"
 
@@ -301,6 +302,14 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleasePa
   }
 }
 
+// Outputs that are an input's memory: some blocks would read what others have written.
+bool share(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+  for (const void* o : outs)
+    for (const void* i : ins)
+      if (o && o == i) return true;
+  return false;
+}
+
 // CTAs of `threads`: a warp per sequence, four rows per thread, at most two per SM
 int grid_for(int B, long long tokens, int threads) {
   const int warps = threads / 32;
@@ -321,7 +330,9 @@ extern "C" spec_status spec_extend_tables(const int32_t* ctx_len, const int32_t*
                                           int32_t* status_per_seq, void* stream) {
   if (B < 0 || page_size < 1 || max_pages < 1 || num_pages < 1 || max_tokens < 0)
     return SPEC_EINVAL;
-  if (!free_list || !free_count || !cu_len || !free_left || free_left == free_count)
+  if (!free_list || !free_count || !cu_len || !free_left) return SPEC_EINVAL;
+  if (share({block_table, slot_map, positions, cu_len, new_len, free_left, status_per_seq},
+            {ctx_len, add_len, free_list, free_count}))
     return SPEC_EINVAL;
   if (B && (!ctx_len || !add_len || !block_table || !new_len || !status_per_seq))
     return SPEC_EINVAL;
@@ -350,7 +361,9 @@ extern "C" spec_status spec_release_pages(const int32_t* block_table, int max_pa
                                           const int32_t* free_count, int32_t* free_total,
                                           int32_t* status_per_seq, void* stream) {
   if (B < 0 || page_size < 1 || max_pages < 1 || num_pages < 1) return SPEC_EINVAL;
-  if (!free_list || !free_count || !free_total || free_total == free_count) return SPEC_EINVAL;
+  if (!free_list || !free_count || !free_total) return SPEC_EINVAL;
+  if (share({free_list, free_total, status_per_seq}, {block_table, len, keep_pages, free_count}))
+    return SPEC_EINVAL;
   if (B && (!block_table || !len || !keep_pages)) return SPEC_EINVAL;
   if (B > kMaxSeqs || (long long)max_pages * page_size > INT_MAX || num_pages == INT_MAX)
     return SPEC_EUNSUPPORTED;

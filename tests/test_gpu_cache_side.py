@@ -212,6 +212,19 @@ def test_append_tokens_in_place_far_positions_saturation_and_nan():
     sv.append_tokens(big[:0], big[:0], *c8, dev([], torch.int64), rope_base=0)   # no rows
 
 
+def test_append_tokens_slots_past_32_bits():
+    """More slots than 2^32, on pages that share one page's memory."""
+    base = [torch.zeros((1, 4096, 1, 64), dtype=torch.float8_e4m3fn, device=DEV) for _ in range(2)]
+    kc, vc = (b.expand(1 << 20, 4096, 1, 64) for b in base)
+    x = torch.randn((3, 1, 64), generator=torch.Generator().manual_seed(1)).half().to(DEV)
+    slots = [2 ** 32 - 5, 2 ** 31 + 7, 2 ** 32]          # the last is past the cache
+    sv.append_tokens(x, x, kc, vc, dev(slots, torch.int64), rope_base=0)
+    want = np.zeros((4096, 64))
+    want[4091], want[7] = oapp.e4m3(num(x[0, 0])), oapp.e4m3(num(x[1, 0]))
+    for b in base:
+        np.testing.assert_array_equal(num(b)[0, :, 0], want)
+
+
 # ------------------------------------------------------------------ one-token attention
 def attention_bound(ref, big, mass, lse, n, D, q_half, cache):
     """What rounding can do.  A score is a sum of D exact products in fp32 (D 2^-23 of the
@@ -506,6 +519,7 @@ def test_bindings_refuse():
     refuses("window", d, q, k, k, t, n, window=-1)
     left = e(n, n, t, lst, cnt, 16, 4)
     refuses("SPEC_EINVAL", e, n, n, t, lst, left["free_count"], 16, 4, out=left)
+    refuses("SPEC_EINVAL", e, left["new_len"], n, t, lst, cnt, 16, 4, out=left)
     refuses("slot_map has shape", e, n, n, t, lst, cnt, 16, 5, out=left)
     refuses("page_size", sv.release_pages, t, n, n, lst, cnt, 0)
     refuses("SPEC_EINVAL", sv.release_pages, t, n, n, lst, cnt, 16, total=cnt)

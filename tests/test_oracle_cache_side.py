@@ -126,7 +126,9 @@ def test_extend_and_release_refuse_on_the_host(lib):
     for name in "ctx add table lst cnt slots pos cu new left status".split():
         assert extend(**{name: None}) == api.SPEC_EINVAL, name
     for kw in (dict(B=-1), dict(P=0), dict(maxp=0), dict(pool=0), dict(cap=-1),
-               dict(left=_p(7 * 4096), cnt=_p(7 * 4096))):
+               dict(left=_p(7 * 4096), cnt=_p(7 * 4096)), dict(new=_p(9000), ctx=_p(9000)),
+               dict(new=_p(9000), add=_p(9000)), dict(cu=_p(9000), ctx=_p(9000)),
+               dict(status=_p(9000), add=_p(9000)), dict(table=_p(9000), lst=_p(9000))):
         assert extend(**kw) == api.SPEC_EINVAL, kw
     for kw in (dict(B=8193), dict(maxp=1 << 28), dict(cap=2 ** 31 - 1), dict(pool=2 ** 31 - 1)):
         assert extend(**kw) == api.SPEC_EUNSUPPORTED, kw
@@ -140,6 +142,8 @@ def test_extend_and_release_refuse_on_the_host(lib):
     for name in "table len keep lst cnt total".split():
         assert release(**{name: None}) == api.SPEC_EINVAL, name
     assert release(total=_p(5), cnt=_p(5)) == api.SPEC_EINVAL
+    assert release(status=_p(5), keep=_p(5)) == api.SPEC_EINVAL
+    assert release(lst=_p(5), table=_p(5)) == api.SPEC_EINVAL
     assert release(P=0) == api.SPEC_EINVAL
     assert release(B=8193) == api.SPEC_EUNSUPPORTED
 
