@@ -28,12 +28,12 @@
 //     fragment columns want, and byte permutes pair the rows; the rows of the
 //     output tile are whatever dimensions those pieces hold.
 //   P^T's fragments are S^T's accumulators, packed and transposed by movmatrix.
-// K's loads for the next tile go out when this tile's S is done, V's when its
-// product is; the page lookups are two tiles ahead.
-// P is a sum of two parts of the cache's 16-bit type, so that rounding P adds
-// nothing to the output's own rounding, and one fp16 number beside e4m3 caches (which
-// convert to fp16 exactly): 2^-11 where V itself holds 2^-4.  The reference m of a row stays until a score exceeds
-// it by 15 (it is set 7 below the maximum: P stays in fp16's range).
+// K's loads for the next tile go out as soon as a subtile's S has taken its registers,
+// V's when its product has; the page lookups are two tiles ahead.
+// P is a sum of two parts of the cache's 16-bit type, so that rounding P adds nothing to
+// the output's own rounding, and one fp16 number beside e4m3 caches (which convert to
+// fp16 exactly): 2^-11 where V itself holds 2^-4.  The reference m of a row stays until
+// a score exceeds it by 15 (it is set 7 below the maximum: P stays in fp16's range).
 //
 // Measured: 64 ragged sequences (540 K positions, 32 / 8 heads of 128) in bf16 318 us =
 // 6.95 TB/s, in e4m3 174 us = 6.4; one request of 8192 13 us, of 131072 in e4m3 with 64
@@ -896,7 +896,10 @@ struct DecodePlan {
 
 constexpr int kMostPerSm = 4;  // CTAs of any instance on an SM
 
-// CTAs an SM holds at the instance's register bound
+// CTAs an SM holds at the instance's register bound.  Three of 168 registers take tiles of
+// 8 KB a warp (four of 128 with smaller tiles or fewer loads in flight: e4m3 at D = 128
+// 187 against 180 us on 64 ragged sequences, 16 bits at D = 64 178 against 172); D = 256
+// and 16 heads a CTA need 255.
 constexpr int per_sm(bool e4m3, int D, int nt) {
   return D == 256 || nt == 2 ? 2 : e4m3 && D == 64 ? 4 : 3;
 }
@@ -905,6 +908,8 @@ constexpr int per_sm(bool e4m3, int D, int nt) {
 bool make_plan(int B, int Hq, int Hkv, int D, bool e4m3, int occ, DecodePlan* pl) {
   if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv) return false;
   pl->G = Hq / Hkv;
+  // query heads of a CTA: up to 16 share one read of K and V (8 where D = 256 fills the
+  // registers; the other groups read the same rows from L2 at the same time)
   const int most = D == 256 ? 8 : 16;
   pl->groups = (pl->G + most - 1) / most;
   pl->hpg = (pl->G + pl->groups - 1) / pl->groups;

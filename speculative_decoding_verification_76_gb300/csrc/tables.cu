@@ -27,7 +27,9 @@
 namespace {
 
 constexpr int kMostCtas = 304;      // two per SM
-constexpr int kFewSeqs = 256;       // up to here blocks of 128 threads, else of 256
+// up to here blocks of 128 threads, else of 256 (extend + release of 64 sequences 7.4
+// against 8.5 us, of 1000 11.5 against 10.5)
+constexpr int kFewSeqs = 256;
 constexpr int kMaxSeqs = 8192;      // two running sums of 4 bytes: 64 KB of shared memory
 constexpr int kTokensPerThread = 4;
 constexpr int kWarpPages = 64;      // more pages than this: the whole CTA writes the row

@@ -452,6 +452,28 @@ def test_calls_on_a_stream_of_their_own():
     assert np.abs(num(out) - want).max() < 2e-3
 
 
+def test_decode_attn_on_two_streams_at_once():
+    """Calls that run side by side, each stream with a workspace of its own, give what they
+    give alone."""
+    cases = []
+    for i, (Hkv, lens) in enumerate([(2, [9000, 300, 4000]), (1, [20000, 64])]):
+        k, v, table, _ = make_cache(lens, Hkv, 128, 16, "f16", 60 + i)
+        q = torch.randn((len(lens), 8, 128), generator=torch.Generator().manual_seed(i)).half()
+        cases.append([x.to(DEV) for x in (q, k, v)] + [dev(table), dev(lens)])
+    alone = [sv.decode_attn(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    ws = [sv.new_workspace(sv.decode_attn_workspace_size(3, 8, h, 128), DEV) for h in (2, 1)]
+    torch.cuda.synchronize()
+    outs = [[] for _ in cases]
+    for _ in range(20):
+        for c, st, w, o in zip(cases, streams, ws, outs):
+            o.append(sv.decode_attn(*c, workspace=w, stream=st))
+    torch.cuda.synchronize()
+    for (a, la), got in zip(alone, outs):
+        for b, lb in got:
+            assert torch.equal(a, b) and torch.equal(la, lb)
+
+
 def test_decode_attn_one_workspace_for_all_shapes_and_streams():
     """Calls of other shapes on one workspace, one after the other; the same call again gives
     the same bits; a call on a stream of its own."""
