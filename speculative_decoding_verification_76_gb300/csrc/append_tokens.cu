@@ -26,7 +26,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include "common.cuh"
+#include "serving.cuh"
 
 namespace {
 

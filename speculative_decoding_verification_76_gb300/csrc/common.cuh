@@ -224,28 +224,6 @@ SPEC_DEV float fast_exp2(float x) {
   return y;
 }
 
-// x / d for 0 <= x < 2^31 and a divisor the host knows: with 2^s >= d the
-// multiplier m = ceil(2^(31+s) / d) errs by m d - 2^(31+s) < d <= 2^s, and
-// x times that error stays below 2^(31+s), so floor(x m / 2^(31+s)) is exact.
-// (The compiler's own division by a variable is some twenty instructions, and
-// short kernels pay for code they have to fetch.)
-struct FastDiv {
-  uint32_t mul, shift;
-  int d;
-  FastDiv() = default;
-  explicit FastDiv(int div) : d(div) {
-    uint32_t s = 0;
-    while (s < 31 && (1u << s) < (uint32_t)div) ++s;
-    shift = 31 + s;
-    mul = (uint32_t)(((1ull << shift) + div - 1) / div);
-  }
-  SPEC_DEV int quot(int x) const { return (int)(((uint64_t)(uint32_t)x * mul) >> shift); }
-  SPEC_DEV int ceil_quot(int x) const {
-    const int q = quot(x);
-    return q + (q * d != x);
-  }
-};
-
 SPEC_DEV float warp_max(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -267,32 +245,6 @@ SPEC_DEV float warp_sum(float v) {
 
 static inline spec_status launch_status() {
   return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ECUDA;
-}
-
-// Programmatic dependent launch: a kernel started by launch_chained is set up while the
-// kernel in front of it on the stream still runs, and chain_wait() holds it until that
-// kernel is complete and its stores are visible; every global access comes after it.
-// chain_next() lets the next such kernel start early.  It is worth having only where that
-// one has work to do before its wait: blocks that merely wait slowed the ones they waited
-// for (extend + release 8.4 against 9.7 us, one-token attention 13.1 against 14.1).
-SPEC_DEV void chain_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-SPEC_DEV void chain_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-template <typename P>
-static inline spec_status launch_chained(void (*kernel)(P), int grid, int block, size_t smem,
-                                         cudaStream_t st, const P& params) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(block, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, params) != cudaSuccess) return SPEC_ECUDA;
-  return launch_status();
 }
 
 // Raise `func`'s dynamic shared-memory limit to `bytes` on the current device,

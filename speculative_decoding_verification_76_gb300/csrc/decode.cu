@@ -44,7 +44,7 @@
 
 #include <cuda_fp16.h>
 
-#include "common.cuh"
+#include "serving.cuh"
 
 namespace {
 

@@ -22,7 +22,7 @@
 #include <climits>
 #include <initializer_list>
 
-#include "common.cuh"
+#include "serving.cuh"
 
 namespace {
 

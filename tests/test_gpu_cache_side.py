@@ -543,6 +543,14 @@ def test_bindings_refuse():
     refuses("SPEC_EINVAL", e, n, n, t, lst, left["free_count"], 16, 4, out=left)
     refuses("SPEC_EINVAL", e, left["new_len"], n, t, lst, cnt, 16, 4, out=left)
     refuses("slot_map has shape", e, n, n, t, lst, cnt, 16, 5, out=left)
+    refuses("out must be the dict", e, n, n, t, lst, cnt, 16, 4, out=[])
+    refuses("out has no slot_map", e, n, n, t, lst, cnt, 16, 4, out={})
+    refuses("must be a tensor on", e, n, [1, 2], t, lst, cnt, 16, 4)
+    for bad in ("x", None, 1.5):
+        with pytest.raises(TypeError):
+            e(n, n, t, lst, cnt, bad, 4)
+    with pytest.raises(OverflowError):
+        e(n, n, t, lst, cnt, 2 ** 70, 4)
     refuses("page_size", sv.release_pages, t, n, n, lst, cnt, 0)
     refuses("SPEC_EINVAL", sv.release_pages, t, n, n, lst, cnt, 16, total=cnt)
 
