@@ -790,7 +790,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) mine += units_of<kUnit>(p, stored(p, b));
   const int pre = scan(mine, &W), nr = min(p.ranges, W);
-  if (nr <= kMaxJoin) return;
+  // No block ends without the wait: decode_kernel released this grid early, and what
+  // follows on the stream is ordered behind this grid alone.
+  if (nr <= kMaxJoin) return chain_wait();
   const Cuts cuts(W, nr);
   auto is_deep = [&](int at, int u) {
     return u >= kMaxJoin && cuts.range_of(at + u - 1) - cuts.range_of(at) >= kMaxJoin;
@@ -803,7 +805,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
     at += u;
   }
   int nth = scan(deep, &many);
-  if (k >= many) return;
+  if (k >= many) return chain_wait();
   at = pre;
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {

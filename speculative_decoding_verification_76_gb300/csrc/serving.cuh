@@ -27,7 +27,11 @@ struct FastDiv {
 
 // Programmatic dependent launch: a kernel started by launch_chained is set up while the
 // kernel in front of it on the stream still runs, and chain_wait() holds it until that
-// kernel is complete and its stores are visible; every global access comes after it.
+// kernel is complete and its stores are visible.  EVERY thread runs it before it ends:
+// the next operation on the stream waits for this kernel alone, so a grid that ends early
+// would let it pass the kernel in front.  Every global access comes after it, but for
+// join_kernel's (decode.cu) reads of the lengths: decode_kernel, which releases it, has
+// itself waited for whatever wrote them.
 // chain_next() lets the next such kernel start early.  It is worth having only where that
 // one has work to do before its wait: blocks that merely wait slowed the ones they waited
 // for (extend + release 8.4 against 9.7 us, one-token attention 13.1 against 14.1).

@@ -1,0 +1,40 @@
+"""Faults of the cache-side calls that show without a GPU: read from the sources, or from
+what the host entry points answer before anything is launched."""
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "speculative_decoding_verification_76_gb300", "csrc")
+
+
+def kernels(name):
+    """(name, body) of every kernel of a source file, comments taken out."""
+    with open(os.path.join(CSRC, name)) as f:
+        src = re.sub(r"//[^\n]*", "", f.read())
+    for m in re.finditer(r"__global__ void __launch_bounds__\([^{;]*?\)\s*(\w+)\s*\(", src):
+        at = src.index("{", m.end())
+        end, depth = at, 0
+        while True:
+            depth += {"{": 1, "}": -1}.get(src[end], 0)
+            end += 1
+            if depth == 0:
+                break
+        yield m.group(1), src[at:end]
+
+
+@pytest.mark.parametrize("name,count", [("tables.cu", 2), ("append_tokens.cu", 1),
+                                        ("decode.cu", 2)])
+def test_no_chained_kernel_ends_without_waiting(name, count):
+    """These kernels are programmatic dependents.  The next operation on the stream is ordered
+    behind them alone, so a block that returns before the wait lets it overtake the kernel in
+    front."""
+    found = list(kernels(name))
+    assert len(found) == count
+    for kernel, body in found:
+        waits = [m.start() for m in re.finditer(r"(?<!return )chain_wait\(\);", body)]
+        assert len(waits) == 1, kernel
+        # a bare return in front of the wait (a lambda's returns carry a value; an exit that
+        # waits reads `return chain_wait();`)
+        assert not re.search(r"\breturn;", body[:waits[0]]), kernel
