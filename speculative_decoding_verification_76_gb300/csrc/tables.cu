@@ -343,7 +343,7 @@ extern "C" spec_status spec_extend_tables(const int32_t* ctx_len, const int32_t*
       num_pages == INT_MAX)
     return SPEC_EUNSUPPORTED;
   const size_t smem = (2 * (size_t)B + 1) * sizeof(int32_t);
-  if (smem > 48 * 1024) {
+  if (B > kFewSeqs) {  // (the default limit counts the kernel's static shared memory too)
     static PerDeviceOnce<int> smem_once;  // once per device, at the largest size
     const spec_status ra = ensure_smem_limit(smem_once, (const void*)extend_tables_kernel<256>,
                                              (2 * kMaxSeqs + 1) * (int)sizeof(int32_t));
