@@ -521,7 +521,7 @@ spec_status spec_release_pages(const int32_t* block_table, int max_pages, const 
  *   k_cache, v_cache: element (page, token, head, d) is at page * page_stride +
  *            token * token_stride + head * head_stride + d (elements), the same
  *            for both.  cache_dtype is new_dtype, or SPEC_E4M3 with 16-bit rows:
- *            then x / scale is stored, rounded to nearest even and limited to
+ *            then x / scale (in fp32) is stored, rounded to nearest even and limited to
  *            +-448 (a NaN stays NaN).
  *   k_scale, v_scale [Hkv] fp32, > 0 (NULL: 1; only with SPEC_E4M3): what a
  *            stored 1.0 stands for.
