@@ -567,7 +567,8 @@ spec_status spec_append_tokens(const void* k_new, int64_t k_stride, const void* 
  * The result of a sequence does not depend on atomics' order; it may depend on
  * the rest of the batch (by where the cache is split) within rounding.
  * Hkv * ceil(Hq / Hkv / 16) <= 4096 (/ 8 instead of / 16 for D = 256); B *
- * max_pages * page_size / 64 < 2^31.
+ * max_pages * page_size / 64 < 2^31; max_pages * page_size and B at most
+ * 2^31 - 513.
  * ---------------------------------------------------------------------- */
 size_t spec_decode_attn_workspace_size(int B, int Hq, int Hkv, int D);
 

@@ -52,6 +52,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 // Ranges are cut in units of the positions that a CTA's warps take at once: 64 or 128.
 constexpr int kMinUnit = 16 * kWarps;
+// How far past a sequence's end positions are counted (the next two tiles of a warp, the last
+// unit's rest), or past the batch's (a thread's share of the sequences).
+constexpr int kPast = 512;
 constexpr int kMaxHeadGroups = 4096;  // KV heads x head groups
 constexpr int kMaxCounters = 2 * kMaxHeadGroups;  // two per CTA
 constexpr int kMaxJoin = 64;          // parts that the last CTA joins; more: join_kernel
@@ -478,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
     };
 
     constexpr int kStride = kWarps * S::kTile;
+    static_assert(2 * kStride + 32 + kUnit <= kPast, "32-bit positions");
     int t0 = t_begin + warp * S::kTile;
     int row = row_of(t0, entry(t0));
 #pragma unroll
@@ -997,7 +1001,7 @@ extern "C" spec_status spec_decode_attn(const void* q, int64_t q_stride_b, int64
   if (page_stride % token_stride || token_stride * es > UINT32_MAX) return SPEC_EUNSUPPORTED;
   const int64_t page_rows = page_stride / token_stride;
   if (page_rows > INT32_MAX || (page_rows * (num_pages - 1) + page_size) > INT32_MAX ||
-      (long long)max_pages * page_size > INT32_MAX)
+      (long long)max_pages * page_size > INT32_MAX - kPast || B > INT32_MAX - kPast)
     return SPEC_EUNSUPPORTED;
   // so are the batch's units
   if (((long long)max_pages * page_size / kMinUnit + 1) * B > INT32_MAX) return SPEC_EUNSUPPORTED;

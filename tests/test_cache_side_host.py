@@ -38,3 +38,27 @@ def test_no_chained_kernel_ends_without_waiting(name, count):
         # a bare return in front of the wait (a lambda's returns carry a value; an exit that
         # waits reads `return chain_wait();`)
         assert not re.search(r"\breturn;", body[:waits[0]]), kernel
+
+
+# ------------------------------------------------------------------ sizes near 2^31
+@pytest.fixture(scope="module")
+def lib():
+    import speculative_decoding_verification_76_gb300 as sv
+    from speculative_decoding_verification_76_gb300 import build
+    build.build()
+    return sv.load()
+
+
+def test_decode_attn_refuses_rows_and_batches_near_two_to_the_31(lib):
+    """The position loop looks up to two rounds of a block's warps past a sequence's end, in
+    32 bits.  (The workspace is refused behind the sizes: nothing is ever launched here.)"""
+    from tests.test_oracle_cache_side import DECODE
+
+    def call(**change):
+        return lib.spec_decode_attn(*dict(DECODE, pages=1, maxp=1, wsb=0, **change).values())
+    top = 2 ** 31 - 1
+    for n in (top, top - 1, top - 127, top - 511):
+        assert call(B=1, P=n) == 2, n
+        assert call(B=n, P=1) == 2, n
+    assert call(B=1, P=top - 512) == 1
+    assert call(B=top - 512, P=1) == 1
