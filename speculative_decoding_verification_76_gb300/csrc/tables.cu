@@ -33,6 +33,7 @@ constexpr int kFewSeqs = 256;
 constexpr int kMaxSeqs = 8192;      // two running sums of 4 bytes: 64 KB of shared memory
 constexpr int kTokensPerThread = 4;
 constexpr int kWarpPages = 64;      // more pages than this: the whole CTA writes the row
+constexpr int kPast = 4096;         // how far past a row's end its entries are counted
 
 // Sums of lengths and pages stop at 2^31 - 1 (nothing past the capacities matters).
 SPEC_DEV int sat_add(int a, int b) {
@@ -339,8 +340,8 @@ extern "C" spec_status spec_extend_tables(const int32_t* ctx_len, const int32_t*
   if (B && (!ctx_len || !add_len || !block_table || !new_len || !status_per_seq))
     return SPEC_EINVAL;
   if (max_tokens && (!slot_map || !positions)) return SPEC_EINVAL;
-  if (B > kMaxSeqs || (long long)max_pages * page_size > INT_MAX || max_tokens == INT_MAX ||
-      num_pages == INT_MAX)
+  if (B > kMaxSeqs || (long long)max_pages * page_size > INT_MAX || max_pages > INT_MAX - kPast ||
+      max_tokens == INT_MAX || num_pages == INT_MAX)
     return SPEC_EUNSUPPORTED;
   const size_t smem = (2 * (size_t)B + 1) * sizeof(int32_t);
   if (B > kFewSeqs) {  // (the default limit counts the kernel's static shared memory too)
@@ -367,7 +368,8 @@ extern "C" spec_status spec_release_pages(const int32_t* block_table, int max_pa
   if (share({free_list, free_total, status_per_seq}, {block_table, len, keep_pages, free_count}))
     return SPEC_EINVAL;
   if (B && (!block_table || !len || !keep_pages)) return SPEC_EINVAL;
-  if (B > kMaxSeqs || (long long)max_pages * page_size > INT_MAX || num_pages == INT_MAX)
+  if (B > kMaxSeqs || (long long)max_pages * page_size > INT_MAX || max_pages > INT_MAX - kPast ||
+      num_pages == INT_MAX)
     return SPEC_EUNSUPPORTED;
   const ReleaseParams p{block_table, len, keep_pages, free_count, free_list, free_total,
                         status_per_seq, FastDiv(page_size), B, max_pages, num_pages};

@@ -62,3 +62,15 @@ def test_decode_attn_refuses_rows_and_batches_near_two_to_the_31(lib):
         assert call(B=n, P=1) == 2, n
     assert call(B=1, P=top - 512) == 1
     assert call(B=top - 512, P=1) == 1
+
+
+def test_tables_refuse_rows_near_two_to_the_31(lib):
+    """Rows of page ids are walked eight blocks' widths at a time, in 32 bits."""
+    import ctypes
+    top = 2 ** 31 - 1
+    p = [ctypes.c_void_p(1 << (33 + i)) for i in range(11)]   # apart by more than the sizes
+    for maxp in (top, top - 1, top - 4095):
+        assert lib.spec_extend_tables(p[0], p[1], 1, 1, p[10], maxp, p[2], 8, p[3], 0, p[4], p[5],
+                                      p[6], p[7], p[8], p[9], None) == 2
+        assert lib.spec_release_pages(p[10], maxp, p[1], p[2], 1, 1, p[3], 8, p[4], p[5], p[6],
+                                      None) == 2
