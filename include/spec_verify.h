@@ -527,7 +527,8 @@ spec_status spec_release_pages(const int32_t* block_table, int max_pages, const 
  *            stored 1.0 stands for.
  *   rope_base 0: no rotation, else > 1: as in spec_append_block (split-half
  *            form; angles in 64 bits, rotation in fp32, one rounding).
- *   D in {64,128,256}.  Rows, strides and caches are 16-byte aligned.
+ *   T < 2^31 - 1, D in {64,128,256}.  Rows, strides and caches are 16-byte
+ *   aligned.
  * ---------------------------------------------------------------------- */
 spec_status spec_append_tokens(const void* k_new, int64_t k_stride, const void* v_new,
                                int64_t v_stride, const void* q, int64_t q_stride, void* q_out,

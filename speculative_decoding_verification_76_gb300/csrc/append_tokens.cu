@@ -226,7 +226,7 @@ extern "C" spec_status spec_append_tokens(
     const int64_t* slot_map, const int32_t* positions, int T, int Hq, int Hkv, int D,
     double rope_base, void* stream) {
   if (T < 0 || Hq < 0 || Hkv < 1 || num_pages < 1 || page_size < 1) return SPEC_EINVAL;
-  if (Hq > 4096 || Hkv > 4096) return SPEC_EUNSUPPORTED;
+  if (Hq > 4096 || Hkv > 4096 || T == INT32_MAX) return SPEC_EUNSUPPORTED;
   if (new_dtype != SPEC_F32 && new_dtype != SPEC_BF16 && new_dtype != SPEC_F16) return SPEC_EINVAL;
   const bool e4m3 = cache_dtype == SPEC_E4M3;
   if (!e4m3 && cache_dtype != new_dtype) return SPEC_EINVAL;

@@ -74,3 +74,11 @@ def test_tables_refuse_rows_near_two_to_the_31(lib):
                                       p[6], p[7], p[8], p[9], None) == 2
         assert lib.spec_release_pages(p[10], maxp, p[1], p[2], 1, 1, p[3], 8, p[4], p[5], p[6],
                                       None) == 2
+
+
+def test_append_refuses_tokens_that_no_grid_counts(lib):
+    """Two rows to a block: T + 1 is counted in 32 bits."""
+    from tests.test_oracle_cache_side import APPEND
+    top = 2 ** 31 - 1
+    assert lib.spec_append_tokens(*dict(APPEND, T=top, slots=None).values()) == 2
+    assert lib.spec_append_tokens(*dict(APPEND, T=top - 1, slots=None).values()) == 1
