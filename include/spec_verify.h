@@ -467,9 +467,10 @@ spec_status spec_logits_penalize(float* logits, int B, int R, int V, const int32
  *            SPEC_SEQ_BAD_PAGE: a table or free-list entry the new tokens fall
  *            on is not a page id; those tokens' slots are -1, new_len is
  *            ctx_len, and the pages taken stay in the table row.
- *   No output is an input's memory (new_len is not the next call's ctx_len and
- *   out again at once).  B <= 8192; max_pages * page_size below 2^31, max_pages
- *   below 2^31 - 4096, num_pages and max_tokens below 2^31 - 1.
+ *   No output shares memory with an input or another output (new_len is not the
+ *   next call's ctx_len and out again at once).  B <= 8192; max_pages * page_size
+ *   below 2^31, max_pages below 2^31 - 4096, num_pages and max_tokens below
+ *   2^31 - 1.
  * ---------------------------------------------------------------------- */
 spec_status spec_extend_tables(const int32_t* ctx_len, const int32_t* add_len, int B,
                                int page_size, int32_t* block_table, int max_pages,
@@ -496,7 +497,7 @@ spec_status spec_extend_tables(const int32_t* ctx_len, const int32_t* add_len, i
  *            sequence and every later one with pages to give release nothing),
  *            SPEC_SEQ_BAD_PAGE (an entry is not a page id: -1 goes on the list
  *            in its place, which spec_extend_tables reports when it draws it).
- *   No output is another argument's memory.  Sizes as in spec_extend_tables.
+ *   No output shares memory with another argument.  Sizes as in spec_extend_tables.
  * ---------------------------------------------------------------------- */
 spec_status spec_release_pages(const int32_t* block_table, int max_pages, const int32_t* len,
                                const int32_t* keep_pages, int B, int page_size,

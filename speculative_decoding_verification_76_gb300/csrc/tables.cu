@@ -305,11 +305,23 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleasePa
   }
 }
 
-// Outputs that are an input's memory: some blocks would read what others have written.
-bool share(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
-  for (const void* o : outs)
-    for (const void* i : ins)
-      if (o && o == i) return true;
+// Outputs that share memory with an input or with one another, in part or in whole: some
+// blocks would read what others have written.
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+bool meet(const Span& a, const Span& b) {
+  const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
+  return a.at && b.at && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+bool share(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span& o : outs) {
+    for (const Span& i : ins)
+      if (meet(o, i)) return true;
+    for (const Span& other : outs)
+      if (&other != &o && meet(o, other)) return true;
+  }
   return false;
 }
 
@@ -334,15 +346,17 @@ extern "C" spec_status spec_extend_tables(const int32_t* ctx_len, const int32_t*
   if (B < 0 || page_size < 1 || max_pages < 1 || num_pages < 1 || max_tokens < 0)
     return SPEC_EINVAL;
   if (!free_list || !free_count || !cu_len || !free_left) return SPEC_EINVAL;
-  if (share({block_table, slot_map, positions, cu_len, new_len, free_left, status_per_seq},
-            {ctx_len, add_len, free_list, free_count}))
-    return SPEC_EINVAL;
   if (B && (!ctx_len || !add_len || !block_table || !new_len || !status_per_seq))
     return SPEC_EINVAL;
   if (max_tokens && (!slot_map || !positions)) return SPEC_EINVAL;
   if (B > kMaxSeqs || (long long)max_pages * page_size > INT_MAX || max_pages > INT_MAX - kPast ||
       max_tokens == INT_MAX || num_pages == INT_MAX)
     return SPEC_EUNSUPPORTED;
+  const size_t seqs = (size_t)B * 4, rows = (size_t)max_tokens;
+  if (share({{block_table, seqs * max_pages}, {slot_map, rows * 8}, {positions, rows * 4},
+             {cu_len, seqs + 4}, {new_len, seqs}, {free_left, 4}, {status_per_seq, seqs}},
+            {{ctx_len, seqs}, {add_len, seqs}, {free_list, (size_t)num_pages * 4}, {free_count, 4}}))
+    return SPEC_EINVAL;
   const size_t smem = (2 * (size_t)B + 1) * sizeof(int32_t);
   if (B > kFewSeqs) {  // (the default limit counts the kernel's static shared memory too)
     static PerDeviceOnce<int> smem_once;  // once per device, at the largest size
@@ -365,12 +379,14 @@ extern "C" spec_status spec_release_pages(const int32_t* block_table, int max_pa
                                           int32_t* status_per_seq, void* stream) {
   if (B < 0 || page_size < 1 || max_pages < 1 || num_pages < 1) return SPEC_EINVAL;
   if (!free_list || !free_count || !free_total) return SPEC_EINVAL;
-  if (share({free_list, free_total, status_per_seq}, {block_table, len, keep_pages, free_count}))
-    return SPEC_EINVAL;
   if (B && (!block_table || !len || !keep_pages)) return SPEC_EINVAL;
   if (B > kMaxSeqs || (long long)max_pages * page_size > INT_MAX || max_pages > INT_MAX - kPast ||
       num_pages == INT_MAX)
     return SPEC_EUNSUPPORTED;
+  const size_t seqs = (size_t)B * 4;
+  if (share({{free_list, (size_t)num_pages * 4}, {free_total, 4}, {status_per_seq, seqs}},
+            {{block_table, seqs * max_pages}, {len, seqs}, {keep_pages, seqs}, {free_count, 4}}))
+    return SPEC_EINVAL;
   const ReleaseParams p{block_table, len, keep_pages, free_count, free_list, free_total,
                         status_per_seq, FastDiv(page_size), B, max_pages, num_pages};
   const int threads = B <= kFewSeqs ? 128 : 256;

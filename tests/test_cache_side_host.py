@@ -82,3 +82,37 @@ def test_append_refuses_tokens_that_no_grid_counts(lib):
     top = 2 ** 31 - 1
     assert lib.spec_append_tokens(*dict(APPEND, T=top, slots=None).values()) == 2
     assert lib.spec_append_tokens(*dict(APPEND, T=top - 1, slots=None).values()) == 1
+
+
+def test_tables_refuse_outputs_that_overlap(lib):
+    """No output may share memory with an input or with another output, in part either: some
+    blocks would read what others have written.  (B 2, four pages a row, a pool of 8, 64 rows.)"""
+    import ctypes
+    at = {k: 1 << (20 + i) for i, k in enumerate(
+        "ctx add table lst cnt slots pos cu new left status".split())}
+    size = dict(ctx=8, add=8, table=32, lst=32, cnt=4, slots=512, pos=256, cu=12, new=8, left=4,
+                status=8)
+    outs = "table slots pos cu new left status".split()
+
+    def extend(**move):
+        a = {k: ctypes.c_void_p(v) for k, v in dict(at, **move).items()}
+        return lib.spec_extend_tables(a["ctx"], a["add"], 2, 16, a["table"], 4, a["lst"], 8,
+                                      a["cnt"], 64, a["slots"], a["pos"], a["cu"], a["new"],
+                                      a["left"], a["status"], None)
+    for o in outs:
+        for other in at:
+            if other != o:
+                for by in (size[other] - 4, 4 - size[o]):   # the last word, the first word
+                    assert extend(**{o: at[other] + by}) == 1, (o, other, by)
+    rel = {k: 1 << (20 + i) for i, k in enumerate("table len keep lst cnt total status".split())}
+    rsize = dict(table=32, len=8, keep=8, lst=32, cnt=4, total=4, status=8)
+
+    def release(**move):
+        a = {k: ctypes.c_void_p(v) for k, v in dict(rel, **move).items()}
+        return lib.spec_release_pages(a["table"], 4, a["len"], a["keep"], 2, 16, a["lst"], 8,
+                                      a["cnt"], a["total"], a["status"], None)
+    for o in ("lst", "total", "status"):
+        for other in rel:
+            if other != o:
+                for by in (rsize[other] - 4, 4 - rsize[o]):
+                    assert release(**{o: rel[other] + by}) == 1, (o, other, by)
