@@ -561,7 +561,10 @@ spec_status spec_append_tokens(const void* k_new, int64_t k_stride, const void* 
  *            number: unwritten slots may hold anything.
  *   scale    softmax scale; <= 0 selects 1/sqrt(D).
  *   out      [B,Hq,D] q_dtype; lse_out [B,Hq] fp32 natural log (nullable).  A
- *            sequence that sees nothing (seq_len <= 0) has zeros and -inf.
+ *            sequence that sees nothing (seq_len <= 0) has zeros and -inf.  A NaN
+ *            that is seen makes NaN, an infinite value an infinity of its sign,
+ *            both signs NaN.  (A weight below 2^-32 of the largest may count as 0
+ *            beside fp16 caches, and 0 times infinity is NaN.)
  *   workspace >= spec_decode_attn_workspace_size(...) bytes, 256-byte aligned,
  *            used for spec_decode_attn only; one workspace serves calls of any
  *            shape whose own size fits in it.

@@ -30,9 +30,12 @@
 //   P^T's fragments are S^T's accumulators, packed and transposed by movmatrix.
 // K's loads for the next tile go out as soon as a subtile's S has taken its registers,
 // V's when its product has; the page lookups are two tiles ahead.
-// P is a sum of two parts of the cache's 16-bit type, so that rounding P adds nothing to
-// the output's own rounding, and one fp16 number beside e4m3 caches (which convert to
-// fp16 exactly): 2^-11 where V itself holds 2^-4.  The reference m of a row stays until
+// P is a sum hi + lo of two parts of the cache's 16-bit type, so that rounding P adds nothing
+// to the output's own rounding, and one fp16 number beside e4m3 caches (which convert to
+// fp16 exactly): 2^-11 where V itself holds 2^-4.  An infinite V must come out infinite, and
+// lo V alone would be an infinity of the other sign or 0 Inf: in bf16 hi is the number next
+// below P, so that lo is positive too (lo < 2^-7 P, rounded to 2^-16 P); in fp16, where such a
+// lo may fall below the smallest number, lo multiplies V with its infinities made finite.  The reference m of a row stays until
 // a score exceeds it by 15 (it is set 7 below the maximum: P stays in fp16's range).
 //
 // Measured: 64 ragged sequences (540 K positions, 32 / 8 heads of 128) in bf16 318 us =
@@ -120,6 +123,13 @@ SPEC_DEV uint32_t transpose8x8(uint32_t x) {
 SPEC_DEV uint32_t pack_f16(float lo, float hi) {
   __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// Two halves, infinities (and NaN) replaced by the largest finite number of their sign
+SPEC_DEV uint32_t finite_f16(uint32_t x) {
+  uint32_t r;
+  asm("min.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x7bff7bffu));
+  return r;
 }
 
 SPEC_DEV void e4m3_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {  // bytes 0, 1 and 2, 3
@@ -580,11 +590,11 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
 #pragma unroll
           for (int x2 = 0; x2 < 2; ++x2) {
             const float y0 = y[2 * x2], y1 = y[2 * x2 + 1];
-            if constexpr (kBf) {
-              const uint32_t hi = pack_bf16(y0, y1);
-              ph[nt][x2] = transpose8x8(hi);
-              pl[nt][x2] = transpose8x8(pack_bf16(y0 - __uint_as_float(hi << 16),
-                                                  y1 - __uint_as_float(hi & 0xffff0000u)));
+            if constexpr (kBf) {  // hi: the bf16 number next below, so that lo > 0
+              const uint32_t u0 = max(__float_as_uint(y0), 1u) - 1, u1 = max(__float_as_uint(y1), 1u) - 1;
+              ph[nt][x2] = transpose8x8(__byte_perm(u0, u1, 0x7632));
+              pl[nt][x2] = transpose8x8(pack_bf16(y0 - __uint_as_float(u0 & 0xffff0000u),
+                                                  y1 - __uint_as_float(u1 & 0xffff0000u)));
             } else {
               const uint32_t hi = pack_f16(y0, y1);
               ph[nt][x2] = transpose8x8(hi);
@@ -622,7 +632,11 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 mma<kBf>(o[nt][t], a0, a1, a2, a3, ph[nt][0], ph[nt][1]);
-                if constexpr (kTwo) mma<kBf>(o[nt][t], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                if constexpr (kBf)
+                  mma<kBf>(o[nt][t], a0, a1, a2, a3, pl[nt][0], pl[nt][1]);
+                else
+                  mma<kBf>(o[nt][t], finite_f16(a0), finite_f16(a1), finite_f16(a2),
+                           finite_f16(a3), pl[nt][0], pl[nt][1]);
               }
             }
           }
