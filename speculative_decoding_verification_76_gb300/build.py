@@ -1,15 +1,18 @@
 """Build libspecverify.so in-tree with nvcc for sm_103a (no cmake).
 
 Each CUDA source is compiled in parallel to an object file, then linked into
-one shared library beside this file; _native.so, the native part of the Python
+one shared library beside this file.  _native.so, the native part of the Python
 binding (csrc/binding.cpp, host code against the installed PyTorch), is linked to
-it.  Rebuilds only when a source or header is newer than the two.
+it; the library does not need it, and where PyTorch is not installed the library
+alone is built.  Each is built again when one of its sources or headers is newer,
+the binding also for another PyTorch or Python.
 """
 import concurrent.futures as cf
 import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -35,17 +38,48 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
+def _headers():
+    return glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
+
+
+def _older(path, deps) -> bool:
+    return not os.path.exists(path) or \
+        any(os.path.getmtime(d) > os.path.getmtime(path) for d in deps)
+
+
+def _lib_stale() -> bool:
+    return _older(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + _headers())
+
+
+def _torch():
+    """The installed PyTorch, or None."""
+    try:
+        import torch
+        return torch
+    except ImportError:
+        return None
+
+
+def _built_for(torch) -> str:
+    return f"torch {torch.__version__}, python {sys.version}"
+
+
+def _record():
+    return os.path.join(BUILD, "native.txt")  # what _native.so was built for
+
+
+def _native_stale(torch) -> bool:
+    if _older(NATIVE, [BINDING] + _headers()) or not os.path.exists(_record()):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
-    deps = sources() + [BINDING] + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
-    return any(os.path.getmtime(d) > t for d in deps)
+    with open(_record()) as f:
+        return f.read() != _built_for(torch)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
+    torch = _torch()
+    lib = force or _lib_stale()
+    native = torch is not None and (force or _native_stale(torch))
+    if not lib and not native:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -63,7 +97,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     def compile_binding():
-        import torch
         root = os.path.dirname(torch.__file__)
         obj = os.path.join(BUILD, "binding.cpp.o")
         cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")
@@ -77,23 +110,26 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj, os.path.join(root, "lib")
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        native = ex.submit(compile_binding)
-        objs = list(ex.map(compile_one, sources()))
-        native = native.result()
-    tmp = LIB + ".tmp"
-    r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, "-Xlinker", "-soname=libspecverify.so",
-                        *objs], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, LIB)
-    obj, torch_lib = native
-    tmp = NATIVE + ".tmp"
-    r = subprocess.run(["g++", "-shared", "-o", tmp, obj, LIB, "-L" + torch_lib, "-ltorch_python",
-                        "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"],
-                       capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, NATIVE)
+        binding = ex.submit(compile_binding) if native else None
+        if lib:
+            objs = list(ex.map(compile_one, sources()))
+            tmp = LIB + ".tmp"
+            r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, "-Xlinker",
+                                "-soname=libspecverify.so", *objs], capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stderr}")
+            os.replace(tmp, LIB)
+    if native:
+        obj, torch_lib = binding.result()   # (a failure leaves the library in place)
+        tmp = NATIVE + ".tmp"
+        r = subprocess.run(["g++", "-shared", "-o", tmp, obj, LIB, "-L" + torch_lib,
+                            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+                            "-Wl,-rpath,$ORIGIN"], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stderr}")
+        os.replace(tmp, NATIVE)
+        with open(_record(), "w") as f:
+            f.write(_built_for(torch))
     return LIB
 
 
