@@ -220,7 +220,7 @@ struct Shape {
   static constexpr int kLaneK = kPairK ? 32 : 16, kLaneV = kPairV ? 32 : kVWords * 4;
 };
 
-// The parts of sequence b's head group, joined by one CTA in the parts' order: a
+// The np <= kMaxJoin parts of sequence b's head group, joined by one CTA in their order: a
 // warp per head, kFlight parts' rows loaded together (a part's row is an L2 round
 // trip away, and one after another 57 parts took 12 us).  `late`: the first part is
 // its range's last segment (slot 1).
@@ -255,16 +255,12 @@ __device__ __forceinline__ void join(const DecodeParams& p, int b, int r_first, 
         y[j].load(src + (size_t)(min(j, np - 1 - j0) * step) * D + (j == 0 ? first : 0), lane);
       const float2 mine = ml_of(j0 + min(lane, kFlight));
       if (j0 == 0) {  // the references and sums of all parts, under the first rows' loads
-        const float2 x0 = ml_of(lane), x1 = ml_of(lane + 32);  // all there is, as a rule
-        M = fmaxf(x0.x, x1.x);
-#pragma unroll 1
-        for (int i = lane + 64; i < np; i += 32) M = fmaxf(M, ml_of(i).x);
-        M = warp_max(M);
+        static_assert(kMaxJoin <= 64, "two parts a lane");
+        const float2 x0 = ml_of(lane), x1 = ml_of(lane + 32);
+        M = warp_max(fmaxf(x0.x, x1.x));
         auto weigh = [&](float2 x) { L += (x.x == -INFINITY ? 0.f : fast_exp2(x.x - M)) * x.y; };
         weigh(x0);
         weigh(x1);
-#pragma unroll 1
-        for (int i = lane + 64; i < np; i += 32) weigh(ml_of(i));
         L = warp_sum(L);
       }
       const float e = mine.x == -INFINITY ? 0.f : fast_exp2(mine.x - M);
@@ -757,7 +753,8 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
 // The sequences cut into more than kMaxJoin parts (one of a few KV heads over all the
 // GPU: joining 304 parts of 16 heads in one CTA took 50 us): a CTA per head of the k-th
 // such sequence.  Launched as a programmatic dependent of decode_kernel, and only where
-// the batch may have one: their number is below ranges / (kMaxJoin - 1).
+// the batch may have one.  Neighbours share a range at most, so k such sequences span
+// 64 k + 1 ranges or more: there are at most (ranges - 1) / kMaxJoin.
 constexpr int kJoinWarps = 16;
 
 template <int D, int kUnit>
