@@ -30,13 +30,18 @@
 //   P^T's fragments are S^T's accumulators, packed and transposed by movmatrix.
 // K's loads for the next tile go out as soon as a subtile's S has taken its registers,
 // V's when its product has; the page lookups are two tiles ahead.
-// P is a sum hi + lo of two parts of the cache's 16-bit type, so that rounding P adds nothing
-// to the output's own rounding, and one fp16 number beside e4m3 caches (which convert to
-// fp16 exactly): 2^-11 where V itself holds 2^-4.  An infinite V must come out infinite, and
-// lo V alone would be an infinity of the other sign or 0 Inf: in bf16 hi is the number next
-// below P, so that lo is positive too (lo < 2^-7 P, rounded to 2^-16 P); in fp16, where such a
-// lo may fall below the smallest number, lo multiplies V with its infinities made finite.  The reference m of a row stays until
-// a score exceeds it by 15 (it is set 7 below the maximum: P stays in fp16's range).
+// P is a sum hi + lo of two parts of the cache's 16-bit type, or of fp16 beside e4m3 caches
+// (which convert to fp16 exactly), so that rounding P adds nothing to the output's own
+// rounding.  Beside bf16 queries an e4m3 cache takes one fp16 part: its 2^-11 is an eighth of
+// what the bf16 output is rounded by.  (Two parts: 64 ragged sequences with 16 heads a CTA 118
+// against 115 us, with 4 heads 176 both; fp16 outputs, whose error one part would double, pay
+// it.)
+// An infinite V must come out infinite, and lo V alone would be an infinity of the other sign
+// or 0 Inf: in bf16 hi is the number next below P, so that lo is positive too (lo < 2^-7 P,
+// rounded to 2^-16 P); in fp16, where such a lo may fall below the smallest number, lo
+// multiplies V with its infinities made finite.
+// The reference m of a row stays until a score exceeds it by 15 (it is set 7 below the
+// maximum: P stays in fp16's range).
 //
 // Measured: 64 ragged sequences (540 K positions, 32 / 8 heads of 128) in bf16 318 us =
 // 6.95 TB/s, in e4m3 174 us = 6.4; one request of 8192 13 us, of 131072 in e4m3 with 64
@@ -91,10 +96,12 @@ struct DecodeParams {
 constexpr int kZeroRows = 512;
 __device__ __align__(512) char g_zeros[kZeroRows * 512];
 
-enum Cache { kBf16, kF16, kE4m3 };
+enum Cache { kBf16, kF16, kE4m3, kE4m3F16 };  // (e4m3 beside bf16 and beside fp16 queries)
 
 template <int CT>
-constexpr int elem_bytes() { return CT == kE4m3 ? 1 : 2; }
+constexpr bool is_e4m3() { return CT == kE4m3 || CT == kE4m3F16; }
+template <int CT>
+constexpr int elem_bytes() { return is_e4m3<CT>() ? 1 : 2; }
 
 // D = A(16x16, row) * B(16x8, col) + D (fp32), f16 or bf16 operands
 template <bool BF>
@@ -292,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
     const __grid_constant__ DecodeParams p) {
   using S = Shape<CT, D, NT>;
   constexpr int kUnit = S::kUnit;
-  constexpr bool kBf = CT == kBf16, kTwo = CT != kE4m3;  // (P as two parts)
+  constexpr bool kBf = CT == kBf16, k8 = is_e4m3<CT>(), kTwo = CT != kE4m3;  // (P as two parts)
   constexpr int NS = S::kSub, KP = S::kKPieces, VW = S::kVWords, VP = S::kVPieces;
   constexpr int kHeads = 8 * NT;
   // row (h & 1) * 4 + (h >> 1 & 3) of each eight is head h, two words apart modulo the
@@ -395,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
       const uint16_t* src = reinterpret_cast<const uint16_t*>(p.q) + b * p.q_stride_b +
                             (kvh * p.G + h0 + min(g, nh - 1)) * p.q_stride_h;
       uint32_t raw[S::kSteps * 2];
-      if constexpr (CT == kE4m3) {  // 16 dimensions per lane and piece
+      if constexpr (k8) {  // 16 dimensions per lane and piece
 #pragma unroll
         for (int j = 0; j < KP; ++j) {
           const uint4* s4 = reinterpret_cast<const uint4*>(src + c4 * S::kLaneK + S::k_byte(j));
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
         }
       }
       float up = 1.f;
-      if (CT == kE4m3 && p.q_bf16) {
+      if constexpr (CT == kE4m3) {
         // bf16 q beside fp16 operands: scaled by a power of two that puts the
         // head's largest element at 2^14, so that nothing overflows and what
         // becomes subnormal is 2^-28 of the largest
@@ -514,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
         for (int nt = 0; nt < NT; ++nt) x[s][nt][0] = x[s][nt][1] = x[s][nt][2] = x[s][nt][3] = 0.f;
 #pragma unroll
         for (int j = 0; j < KP; ++j) {
-          if constexpr (CT == kE4m3) {
+          if constexpr (k8) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t a0, a1, a2, a3;
@@ -607,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
           for (int i = 0; i < VW; ++i) {
             const uint32_t v0 = vr[s][0][j][i], v1 = vr[s][1][j][i];
             const uint32_t v2 = vr[s][2][j][i], v3 = vr[s][3][j][i];
-            if constexpr (CT == kE4m3) {
+            if constexpr (k8) {
               const uint32_t a = __byte_perm(v0, v1, 0x5140), b2 = __byte_perm(v2, v3, 0x5140);
               const uint32_t c = __byte_perm(v0, v1, 0x7362), d = __byte_perm(v2, v3, 0x7362);
               const int t = 2 * (j * VW + i);
@@ -620,6 +627,10 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
               for (int nt = 0; nt < NT; ++nt) {
                 mma<false>(o[nt][t], f[0], f[1], f[2], f[3], ph[nt][0], ph[nt][1]);
                 mma<false>(o[nt][t + 1], f[4], f[5], f[6], f[7], ph[nt][0], ph[nt][1]);
+                if constexpr (kTwo) {
+                  mma<false>(o[nt][t], f[0], f[1], f[2], f[3], pl[nt][0], pl[nt][1]);
+                  mma<false>(o[nt][t + 1], f[4], f[5], f[6], f[7], pl[nt][0], pl[nt][1]);
+                }
               }
             } else {
               const uint32_t a0 = __byte_perm(v0, v1, 0x5410), a1 = __byte_perm(v0, v1, 0x7632);
@@ -658,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, MINB) decode_kernel(
 #pragma unroll
         for (int t = 0; t < S::kSteps; ++t) {
           int d;
-          if constexpr (CT == kE4m3)
+          if constexpr (k8)
             d = S::v_byte(t / (2 * VW)) + n8 * S::kLaneV + (t % (2 * VW)) * 2;
           else
             d = (S::v_byte(t / VW) + n8 * S::kLaneV) / 2 + (t % VW) * 2;
@@ -949,7 +960,7 @@ size_t ws_layout(const DecodePlan& pl, int Hkv, int D, size_t* off_o, size_t* of
 
 template <int CT, int D, int NT>
 spec_status launch(DecodeParams p, cudaStream_t st) {
-  constexpr int kOcc = per_sm(CT == kE4m3, D, NT);
+  constexpr int kOcc = per_sm(is_e4m3<CT>(), D, NT);
   // may a sequence be cut into more parts than its last CTA joins?  (Each holds a unit at
   // least, and the window or the table's width bounds its units.)
   const int row = p.max_pages * p.P.d, longest = p.window > 0 ? std::min(p.window, row) : row;
@@ -1054,6 +1065,7 @@ extern "C" spec_status spec_decode_attn(const void* q, int64_t q_stride_b, int64
   p.q_bf16 = q_dtype == SPEC_BF16;
   p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * kLog2e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (e4m3) return launch_d<kE4m3>(p, D, pl.nt, st);
+  if (e4m3)
+    return p.q_bf16 ? launch_d<kE4m3>(p, D, pl.nt, st) : launch_d<kE4m3F16>(p, D, pl.nt, st);
   return p.q_bf16 ? launch_d<kBf16>(p, D, pl.nt, st) : launch_d<kF16>(p, D, pl.nt, st);
 }
