@@ -512,7 +512,8 @@ spec_status spec_release_pages(const int32_t* block_table, int max_pages, const 
  *   k_new, v_new rows of Hkv*D new_dtype elements, k_stride / v_stride elements
  *            apart (slices of a fused projection are taken as they are).
  *   q, q_out rows of Hq*D (nullable, both): q rotated into q_out; the same
- *            memory with the same stride rotates in place.
+ *            memory with the same stride rotates in place.  Otherwise q_out and
+ *            the caches share no memory with the rows read.
  *   slot_map [T] int64 (spec_extend_tables): row t goes to offset slot % P of
  *            page slot / P.  Rows whose slot is outside 0 .. num_pages * P - 1
  *            are skipped whole (their q_out row stays as it was).  Slots are
@@ -565,6 +566,7 @@ spec_status spec_append_tokens(const void* k_new, int64_t k_stride, const void* 
  *            that is seen makes NaN, an infinite value an infinity of its sign,
  *            both signs NaN.  (A weight below 2^-32 of the largest may count as 0
  *            beside fp16 caches, and 0 times infinity is NaN.)
+ *            Neither shares memory with an input.
  *   workspace >= spec_decode_attn_workspace_size(...) bytes, 256-byte aligned,
  *            used for spec_decode_attn only; one workspace serves calls of any
  *            shape whose own size fits in it.

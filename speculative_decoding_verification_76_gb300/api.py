@@ -522,7 +522,10 @@ def append_tokens(k_new, v_new, k_cache, v_cache, slot_map, positions=None, q=No
     """Packed rows [T, Hkv, D] into the paged cache at their slots, keys rotated at
     `positions` (rope_base 0: not); with q [T, Hq, D] the rotated queries go to q_out
     (allocated if not given; q itself rotates in place).  Rows with a slot outside the
-    cache are skipped.  Returns q_out (None without q)."""
+    cache are skipped.  Returns q_out (None without q).
+
+    append_block does the same from block tables for bf16 and fp32 blocks; with slots at
+    hand this call is the faster one."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return append_tokens(k_new, v_new, k_cache, v_cache, slot_map, positions, q, q_out,
@@ -541,7 +544,10 @@ def decode_attn(q, k_cache, v_cache, block_table, seq_len, scale: float = 0.0, w
 
     q [B, Hq, D] bf16 or fp16 (strided over B and Hq as it comes); caches [pages, P,
     Hkv, D] of q's dtype or float8_e4m3fn with scales [Hkv]; seq_len [B] counts the
-    stored tokens, the new one included.  Returns (out [B, Hq, D], lse [B, Hq])."""
+    stored tokens, the new one included.  Returns (out [B, Hq, D], lse [B, Hq]).
+
+    verify_attn with one row does the same for bf16 caches of D = 128 (or fp32); on a
+    batch this call is the faster one."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return decode_attn(q, k_cache, v_cache, block_table, seq_len, scale, window, k_scale,

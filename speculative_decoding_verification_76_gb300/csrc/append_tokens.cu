@@ -17,8 +17,8 @@
 // consecutive threads take consecutive 16 bytes, and a thread has three such items'
 // loads in flight.  A token's D/2 sines and cosines serve all its heads from shared
 // memory.  A CTA of 128 threads takes two tokens, or one where there are few.
-// Measured (32 / 8 heads of 128, bf16 rows): 16384 tokens into an e4m3 cache 59 us =
-// 6.3 TB/s, into a bf16 one 64 us = 6.3 TB/s (one token a CTA 63 and 65; one item in
+// Measured (32 / 8 heads of 128, bf16 rows): 16384 tokens into an e4m3 cache 58 us =
+// 6.3 TB/s, into a bf16 one 63 us = 6.4 TB/s (one token a CTA 63 and 65; one item in
 // flight 69 and 71); 320 tokens 3.2 us (two tokens a CTA 4.0).
 #include <algorithm>
 #include <cmath>

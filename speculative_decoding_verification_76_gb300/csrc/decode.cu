@@ -43,9 +43,9 @@
 // The reference m of a row stays until a score exceeds it by 15 (it is set 7 below the
 // maximum: P stays in fp16's range).
 //
-// Measured: 64 ragged sequences (540 K positions, 32 / 8 heads of 128) in bf16 318 us =
-// 6.95 TB/s, in e4m3 174 us = 6.4; one request of 8192 13 us, of 131072 in e4m3 with 64
-// query heads 52 us.  A short call is a chain of round trips (lengths, page ids, K and V,
+// Measured: 64 ragged sequences (540 K positions, 32 / 8 heads of 128) in bf16 320 us =
+// 6.93 TB/s, in e4m3 176 us = 6.3; one request of 8192 13 us, of 131072 in e4m3 with 64
+// query heads 53 us.  A short call is a chain of round trips (lengths, page ids, K and V,
 // merge, join: 2, 1, 5, 1.5 and 3 us).
 #include <algorithm>
 #include <atomic>
