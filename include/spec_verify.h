@@ -589,6 +589,211 @@ spec_status spec_decode_attn(const void* q, int64_t q_stride_b, int64_t q_stride
                              void* workspace, size_t workspace_bytes, void* out, float* lse_out,
                              void* stream);
 
+/* ------------------------------------------------------------------------
+ * spec_rope -- how a head turns for its position.  "Speculative Decoding"
+ * (atlas), "Chains, trees and visibility": position ids follow depth; the
+ * pages do not print the rotation, so every common form of it can be named.
+ *
+ *   dim         the head's first `dim` elements turn, in dim/2 pairs; the others
+ *               stay.  Even, at most D; a multiple of 16 for pairs of halves.
+ *   interleaved 0: pair i is (x_i, x_{i + dim/2}); 1: (x_2i, x_{2i+1}).
+ *   Pair i at position t becomes magnitude * (a cos u - b sin u, a sin u +
+ *   b cos u), u = t f_i, where f_i = base^(-2i/dim), changed by `scaling`:
+ *     SPEC_ROPE_NONE    as it is
+ *     SPEC_ROPE_LINEAR  f_i / factor (positions within `factor` times the
+ *                       original context keep to its angles)
+ *     SPEC_ROPE_NTK     from the base base * factor^(dim / (dim - 2)): the
+ *                       slowest pair is divided by factor, the fastest stays
+ *     SPEC_ROPE_PARTS   g f_i + (1 - g) f_i / factor, g = (turns - low) /
+ *                       (high - low) limited to 0 .. 1, turns = original_len
+ *                       f_i / 2 pi: what turns often within the original context
+ *                       stays, what turns less than `low` times is stretched
+ *   freqs       dim/2 angles per position in radians, in HOST memory, instead of
+ *               all of that (NULL: base, scaling and its numbers).
+ *   base > 1; factor >= 1; low < high and original_len > 0 (PARTS); dim > 2 (NTK);
+ *   freqs finite; magnitude finite.
+ * Angles are kept as 64-bit fractions of a turn, so that they are as exact at
+ * position 2^31 - 1 as at 1; sine, cosine and the rotation are in fp32.
+ * ---------------------------------------------------------------------- */
+enum { SPEC_ROPE_NONE = 0, SPEC_ROPE_LINEAR = 1, SPEC_ROPE_NTK = 2, SPEC_ROPE_PARTS = 3 };
+
+typedef struct {
+  int32_t dim, interleaved, scaling, reserved; /* reserved: 0 */
+  double base, factor, original_len, low, high, magnitude;
+  const double* freqs;
+} spec_rope;
+
+/* ------------------------------------------------------------------------
+ * spec_rotate -- rows of queries and keys turned for their positions: what
+ * spec_append_tokens and spec_append_block do for pairs of halves over the whole
+ * head, for every form that spec_rope names (store the turned keys with
+ * rope_base 0).
+ *
+ *   q, q_out rows of Hq*D dtype elements, strides apart; k, k_out rows of Hkv*D
+ *            (k and k_out NULL, Hkv 0: queries alone).  Out may be the input with the
+ *            same stride (in place); otherwise an output shares no memory with what is read.
+ *   positions [T] int32: a row with a negative one is skipped (its output rows
+ *            stay as they were).
+ *   dtype    SPEC_BF16, SPEC_F16 or SPEC_F32; each element is rounded once.
+ *   D a multiple of 16, at most 512; T < 2^31 - 1; Hq, Hkv at most 4096; rows and
+ *   strides 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+spec_status spec_rotate(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                        const void* k, int64_t k_stride, void* k_out, int64_t k_out_stride,
+                        spec_dtype dtype, const int32_t* positions, int T, int Hq, int Hkv, int D,
+                        const spec_rope* rope, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Scaled caches: e4m3 caches with one scale for each block of tokens and KV head.
+ *
+ *   k_cache, v_cache as in spec_append_tokens (SPEC_E4M3): element (page, token,
+ *            head, d) at page * page_stride + token * token_stride + head *
+ *            head_stride + d.
+ *   k_scale, v_scale [num_pages, page_size / block, Hkv] fp32: token j of a page
+ *            belongs to its block j / block.  A code c stands for c * scale.
+ *   block    1 .. 64, divides page_size.
+ *
+ * spec_append_scaled -- packed rows stored at their slots, as spec_append_tokens
+ * does, with scales that come from what is stored.
+ *
+ *   k_new, v_new, q, q_out, slot_map, positions, T: as in spec_append_tokens
+ *            (16-bit rows).  rope NULL: no rotation (positions are not read).
+ *   Rows of one block stand next to each other (spec_extend_tables' slot_map
+ *   does that); of rows that do not, and of rows with the same slot, what is
+ *   stored is unspecified.  Rows whose slot is outside 0 .. num_pages *
+ *   page_size - 1, or whose position is negative, are skipped whole.
+ *   Scales are powers of two.  What a block needs is the smallest 2^k >= 2^-64
+ *   with |x| <= 448 * 2^k for all finite x that the call stores to it (keys after
+ *   their rotation, in fp32).  A block whose first token is among the rows begins
+ *   anew with what it needs; otherwise it takes the larger of that and its scale
+ *   (one that is not positive and finite does not count, one that is no power of
+ *   two counts as the next), and where that is larger than the scale was, the
+ *   block's other codes are re-expressed: exact, but that what falls below the
+ *   type's normal numbers is rounded.  x / scale is rounded to nearest even;
+ *   infinities become +-448 * scale, NaN stays NaN.
+ *   D in {64,128,256}; Hq, Hkv at most 4096; num_pages * page_size and T below
+ *   2^31 - 64; rows, strides and caches 16-byte aligned.  The caches share no memory
+ *   with the rows.
+ * ---------------------------------------------------------------------- */
+spec_status spec_append_scaled(const void* k_new, int64_t k_stride, const void* v_new,
+                               int64_t v_stride, const void* q, int64_t q_stride, void* q_out,
+                               int64_t q_out_stride, spec_dtype new_dtype, void* k_cache,
+                               void* v_cache, float* k_scale, float* v_scale, int num_pages,
+                               int page_size, int block, int64_t page_stride,
+                               int64_t token_stride, int64_t head_stride,
+                               const int64_t* slot_map, const int32_t* positions, int T, int Hq,
+                               int Hkv, int D, const spec_rope* rope, void* stream);
+
+/* spec_read_scaled -- rows of a scaled cache as the values they stand for:
+ * code * scale, in fp32, rounded once to out_dtype (bf16, fp16 or fp32; bf16 is
+ * exact where scales are powers of two).
+ *   k_out, v_out [T] rows of Hkv*D, strides apart (v_out may be NULL with v_cache
+ *   and v_scale); a row whose slot is outside the cache stays as it was.  Slots may
+ *   repeat.  Sizes and alignment as in spec_append_scaled. */
+spec_status spec_read_scaled(const void* k_cache, const void* v_cache, const float* k_scale,
+                             const float* v_scale, int num_pages, int page_size, int block,
+                             int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                             const int64_t* slot_map, int T, int Hkv, int D, void* k_out,
+                             int64_t k_out_stride, void* v_out, int64_t v_out_stride,
+                             spec_dtype out_dtype, void* stream);
+
+/* spec_commit_scaled -- spec_kv_commit on a scaled cache: the accepted rows of a
+ * tree move to the next logical prefix, into blocks of other scales, as if
+ * spec_append_scaled stored the values they stand for (a block whose first token
+ * is among the moved rows begins anew).  Arguments as there; contiguous caches
+ * and scales as above.  Pages of one sequence are not another's. */
+spec_status spec_commit_scaled(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                               int num_pages, int page_size, int block, int Hkv, int D,
+                               const int32_t* block_table, int max_pages, const int32_t* ctx_len,
+                               const int32_t* accepted_len, const int32_t* path,
+                               const int32_t* parent, int B, int R, int32_t* new_len,
+                               int32_t* keep_pages, int32_t* status_per_seq, void* stream);
+
+/* ------------------------------------------------------------------------
+ * spec_verify_attn_scaled -- spec_verify_attn over a scaled cache: the block of a
+ * chain or a draft tree against the committed prefix and itself, and with R = 1
+ * the attention of single tokens.
+ *
+ *   q        [B,R,Hq,D] q_dtype (bf16 or fp16); element (b,i,h,d) at b * q_stride_b
+ *            + i * q_stride_r + h * q_stride_h + d.
+ *   k_cache, v_cache, k_scale, v_scale: a scaled cache as above (any positive
+ *            finite scales); block row j of sequence b is stored at position
+ *            ctx_len[b] + j (append it first).
+ *   block_table [B,max_pages] int32; ctx_len [B] int32: tokens stored in front of
+ *            the block (R = 1: one less than a decoded sequence's length).  A
+ *            negative one is an idle row of the batch.  Both stay as they are
+ *            until the call has run.
+ *   anc_mask [B,R] uint64: as in spec_verify_attn; NULL: a chain.
+ *   window   0: row i sees every committed position.  Otherwise (>= R) only those
+ *            from ctx_len + n_i - window on, n_i being the number of block rows it
+ *            sees: the last `window` tokens of its own text.
+ *   Positions past the table, or whose page id is not in [0, num_pages), are not
+ *   seen.  What a row does not see does not reach its output, whatever it
+ *   holds (NaN codes or scales included).  A row that sees nothing has zeros and
+ *   -inf.  A NaN that is seen, or a q that is not finite, makes NaN.
+ *   scale    softmax scale; <= 0 selects 1/sqrt(D).
+ *   out      [B,R,Hq,D] q_dtype; lse_out [B,R,Hq] fp32 natural log (nullable).
+ *            Neither shares memory with an input.
+ *   workspace >= spec_verify_attn_scaled_workspace_size(...) bytes, 256-byte
+ *            aligned; it keeps nothing from call to call.
+ *
+ * The result of a sequence may depend on the rest of the batch (by where the
+ * cache is split) within rounding, and never on timing.
+ * 1 <= R <= 64, D in {64,128,256}, Hkv * ceil(R * Hq / Hkv / 64) <= 4096; caches,
+ * strides and q 16-byte aligned; max_pages * page_size and B at most 2^31 - 513;
+ * B * Hkv * (max_pages * page_size / 128 + 1) < 2^31.
+ * ---------------------------------------------------------------------- */
+size_t spec_verify_attn_scaled_workspace_size(int B, int R, int Hq, int Hkv, int D);
+
+spec_status spec_verify_attn_scaled(const void* q, int64_t q_stride_b, int64_t q_stride_r,
+                                    int64_t q_stride_h, spec_dtype q_dtype, const void* k_cache,
+                                    const void* v_cache, const float* k_scale,
+                                    const float* v_scale, int num_pages, int page_size, int block,
+                                    int64_t page_stride, int64_t token_stride,
+                                    int64_t head_stride, const int32_t* block_table,
+                                    int max_pages, const int32_t* ctx_len,
+                                    const uint64_t* anc_mask, int B, int R, int Hq, int Hkv,
+                                    int D, int window, float scale, void* workspace,
+                                    size_t workspace_bytes, void* out, float* lse_out,
+                                    void* stream);
+
+/* ------------------------------------------------------------------------
+ * spec_logits_process -- the target logits as served, in front of
+ * spec_accept_sample(_tree), with every request's own settings: what
+ * spec_logits_penalize does for one penalty and one list of bans, and the rest.
+ *
+ *   logits   [B,R,V] dtype (bf16, fp16 or fp32), rows logits_stride elements apart;
+ *   out      [B,R,V] fp32, contiguous: may be `logits` itself (fp32, contiguous), and
+ *            shares no memory with any input otherwise.
+ *   In this order, each step in fp32 and only where its array is given:
+ *   repetition [B] fp32 > 0: an id of the row's prompt or text has l -> l / r if
+ *            l > 0, else l * r.
+ *   frequency, presence [B] fp32: an id that stands n > 0 times in the row's text
+ *            has l -> l - frequency * n, then l - presence.
+ *     history [B,H] int32: the sequence's tokens (pending anchor included; ids
+ *            outside [0,V), such as -1, are skipped); the first prompt_len[b] of
+ *            its entries (NULL: 0) are the prompt, the others text.  A row's text
+ *            goes on with the block tokens in front of it: block_tokens and parent
+ *            as in spec_logits_penalize (a chain's drafts 0 .. i-1, a tree node's
+ *            ancestors below the anchor and the node).
+ *   bias_ids, bias [B,n_bias]: l -> l + (the biases listed for its id, summed from
+ *            first to last).  Ids outside [0,V) are skipped.
+ *   mask     [n_masks, ceil(V/32)] int32: bit v % 32 of word v / 32 set: id v is
+ *            allowed; any other becomes -inf, whatever it was.  mask_row [B,R] int32:
+ *            the mask of each row, outside 0 .. n_masks - 1: none (NULL: row i of
+ *            sequence b has mask b * R + i).
+ *   1 <= R <= 64; V < 2^31 - 4096; a parent row that is no tree in storage order
+ *   (0 <= parent[i] < i) ends the walk there.
+ * ---------------------------------------------------------------------- */
+spec_status spec_logits_process(const void* logits, int64_t logits_stride, spec_dtype dtype,
+                                float* out, int B, int R, int V, const int32_t* history, int H,
+                                const int32_t* prompt_len, const int32_t* block_tokens,
+                                const int32_t* parent, const float* repetition,
+                                const float* frequency, const float* presence,
+                                const int32_t* bias_ids, const float* bias, int n_bias,
+                                const int32_t* mask, int n_masks, const int32_t* mask_row,
+                                void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -36,8 +36,13 @@ by eye, with no blocking, fusion or reordering beyond the definitions:
   tables.py     block tables, slots, positions and the free list of a step.
   decode.py     attention of one new token per sequence over the paged cache
                 (full softmax over the seen positions).
+  rope.py       rotary positions in every served form.
+  scaled.py     e4m3 caches with a scale for each block and head: what an
+                append stores, a tree's commit, the verify attention.
+  logits.py     penalties, biases and grammar masks on the target logits.
 
 Every function is pinned by a test in tests/test_oracle_*.py against worked
 examples printed on the pages, closed forms or brute force.
 """
-from . import append, attention, commit, decode, sampler, tables, tree  # noqa: F401
+from . import (append, attention, commit, decode, logits, rope, sampler, scaled,  # noqa: F401
+               tables, tree)

@@ -34,6 +34,8 @@ EXPORTS = (
     "spec_append_block", "spec_logits_penalize", "spec_debug_attn_fault",
     "spec_extend_tables", "spec_release_pages", "spec_append_tokens",
     "spec_decode_attn_workspace_size", "spec_decode_attn",
+    "spec_rotate", "spec_append_scaled", "spec_read_scaled", "spec_commit_scaled",
+    "spec_verify_attn_scaled_workspace_size", "spec_verify_attn_scaled", "spec_logits_process",
 )
 
 
@@ -60,6 +62,54 @@ class SamplerConfig:
     def c(self) -> _Sampler:
         return _Sampler(float(self.temperature), int(self.top_k), float(self.top_p),
                         1 if self.greedy else 0, int(self.eos_id))
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("magnitude", ctypes.c_double),
+                ("freqs", ctypes.c_void_p)]
+
+
+_SCALING = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
+
+
+@dataclass(frozen=True)
+class Rope:
+    """How a head turns for its position: its first `dim` elements, in dim/2 pairs
+    (x_i, x_{i + dim/2}) or, interleaved, (x_2i, x_{2i+1}), by t * f_i with f_i =
+    base^(-2i/dim), changed for long contexts by `scaling`:
+
+      "none"    as it is
+      "linear"  f_i / factor
+      "ntk"     from the base base * factor^(dim / (dim - 2))
+      "parts"   what turns more than `high` times within original_len positions stays,
+                what turns less than `low` times is divided by factor, a ramp between
+
+    magnitude multiplies the turned elements; freqs (dim/2 radians per position) stands
+    in for base and scaling."""
+    dim: int
+    base: float = 10000.0
+    interleaved: bool = False
+    scaling: str = "none"
+    factor: float = 1.0
+    original_len: float = 0.0
+    low: float = 1.0
+    high: float = 4.0
+    magnitude: float = 1.0
+    freqs: tuple | None = None
+
+    def __post_init__(self):
+        if self.scaling not in _SCALING:
+            raise ValueError(f"scaling must be one of {sorted(_SCALING)}, got {self.scaling!r}")
+        freqs = None if self.freqs is None else tuple(float(f) for f in self.freqs)
+        # what the native binding reads, in spec_rope's order
+        object.__setattr__(self, "_c", (
+            int(self.dim), int(bool(self.interleaved)), _SCALING[self.scaling], float(self.base),
+            float(self.factor), float(self.original_len), float(self.low), float(self.high),
+            float(self.magnitude), freqs))
 
 
 _lib = None
@@ -138,6 +188,27 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.spec_decode_attn.argtypes = [_P, _L, _L, _I, _P, _P, _I, _P, _P, _I, _I, _L, _L, _L, _P,
                                      _I, _P, _I, _I, _I, _I, _I, ctypes.c_float, _P, _SZ, _P, _P,
                                      _P]
+    _R = ctypes.POINTER(_Rope)
+    lib.spec_rotate.restype = _I
+    lib.spec_rotate.argtypes = [_P, _L, _P, _L, _P, _L, _P, _L, _I, _P, _I, _I, _I, _I, _R, _P]
+    lib.spec_append_scaled.restype = _I
+    lib.spec_append_scaled.argtypes = [_P, _L, _P, _L, _P, _L, _P, _L, _I, _P, _P, _P, _P, _I, _I,
+                                       _I, _L, _L, _L, _P, _P, _I, _I, _I, _I, _R, _P]
+    lib.spec_read_scaled.restype = _I
+    lib.spec_read_scaled.argtypes = [_P, _P, _P, _P, _I, _I, _I, _L, _L, _L, _P, _I, _I, _I, _P,
+                                     _L, _P, _L, _I, _P]
+    lib.spec_commit_scaled.restype = _I
+    lib.spec_commit_scaled.argtypes = [_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _I, _P, _P, _P, _P,
+                                       _I, _I, _P, _P, _P, _P]
+    lib.spec_verify_attn_scaled_workspace_size.restype = _SZ
+    lib.spec_verify_attn_scaled_workspace_size.argtypes = [_I] * 5
+    lib.spec_verify_attn_scaled.restype = _I
+    lib.spec_verify_attn_scaled.argtypes = [_P, _L, _L, _L, _I, _P, _P, _P, _P, _I, _I, _I, _L, _L,
+                                            _L, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I,
+                                            ctypes.c_float, _P, _SZ, _P, _P, _P]
+    lib.spec_logits_process.restype = _I
+    lib.spec_logits_process.argtypes = [_P, _L, _I, _P, _I, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P,
+                                        _P, _P, _I, _P, _I, _P, _P]
     _lib = lib
     return lib
 
@@ -201,12 +272,14 @@ def tree_prepare(parent: torch.Tensor | None, ctx_len: torch.Tensor, R: int | No
 
 def kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
               ctx_len: torch.Tensor, accepted_len: torch.Tensor, path=None, parent=None,
-              R: int | None = None, new_len=None, keep_pages=None, status=None, stream=None):
+              R: int | None = None, new_len=None, keep_pages=None, status=None, stream=None,
+              k_scale=None, v_scale=None):
     """Processed lengths after acceptance.  For a tree, path [B,R] int32 holds the
     accepted nodes (node 0 implied), as accept_sample_tree returns them; their K/V
     rows move in place to positions ctx + 1 .. ctx + accepted_len.  parent [B,R]
-    (optional) lets the kernel check that the path follows the tree.
-    Returns (new_len, keep_pages, status)."""
+    (optional) lets the kernel check that the path follows the tree.  For a scaled cache
+    (append_scaled) k_scale and v_scale are its scales: rows move between blocks of
+    different ones.  Returns (new_len, keep_pages, status)."""
     lib = load()
     if k_cache.dtype not in (torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn):
         raise ValueError("caches must be bf16, fp16, fp32 or float8_e4m3fn")
@@ -229,6 +302,25 @@ def kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.T
     keep_pages = (torch.empty((B,), dtype=torch.int32, device=dev) if keep_pages is None
                   else keep_pages)
     status = torch.empty((B,), dtype=torch.int32, device=dev) if status is None else status
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale come together")
+    if k_scale is not None:
+        if k_cache.dtype != torch.float8_e4m3fn:
+            raise ValueError("scales belong to float8_e4m3fn caches")
+        _need(k_scale, "k_scale", torch.float32)
+        if k_scale.dim() != 3 or k_scale.shape[1] < 1 or P % k_scale.shape[1]:
+            raise ValueError("k_scale must be [pages, page_size / block, Hkv]")
+        nb = k_scale.shape[1]
+        _need(k_scale, "k_scale", torch.float32, (npg, nb, Hkv))
+        _need(v_scale, "v_scale", torch.float32, (npg, nb, Hkv))
+    if k_scale is not None and path is not None:
+        _check("spec_commit_scaled",
+               lib.spec_commit_scaled(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                      npg, P, P // nb, Hkv, D, _ptr(block_table),
+                                      block_table.shape[1], _ptr(ctx_len), _ptr(accepted_len),
+                                      _ptr(path), _ptr(parent), B, R, _ptr(new_len),
+                                      _ptr(keep_pages), _ptr(status), _stream(stream)))
+        return new_len, keep_pages, status
     _check("spec_kv_commit",
            lib.spec_kv_commit(_ptr(k_cache), _ptr(v_cache), k_cache.element_size(), npg, P, Hkv,
                               D, _ptr(block_table), block_table.shape[1], _ptr(ctx_len),
@@ -554,3 +646,90 @@ def decode_attn(q, k_cache, v_cache, block_table, seq_len, scale: float = 0.0, w
                                v_scale, workspace, out, lse)
     return (_native or _calls()).decode_attn(q, k_cache, v_cache, block_table, seq_len, scale,
                                              window, k_scale, v_scale, workspace, out, lse)
+
+
+# ------------------------------------------------------------------ a scaled cache's step
+def rotate(q, positions, rope: Rope, k=None, q_out=None, k_out=None, stream=None):
+    """Rows q [T, Hq, D] (and k [T, Hkv, D]) turned for `positions` [T] as `rope` says.
+
+    Outputs are allocated unless given; q_out may be q and k_out k (in place).  A row
+    with a negative position is skipped.  D is a multiple of 16, at most 512.  Returns
+    (q_out, k_out).  append_tokens and append_block turn pairs of halves over the whole
+    head by themselves; rows turned here are stored with rope_base 0."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rotate(q, positions, rope, k, q_out, k_out)
+    return (_native or _calls()).rotate(q, positions, rope, k, q_out, k_out)
+
+
+def append_scaled(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_map, positions=None,
+                  q=None, q_out=None, rope: Rope | None = None, stream=None):
+    """Packed rows [T, Hkv, D] into a scaled cache at their slots: float8_e4m3fn caches
+    [pages, P, Hkv, D] whose scales k_scale, v_scale [pages, P / block, Hkv] are made
+    from what is stored (powers of two; a block whose first token is among the rows
+    begins anew, another's scale only grows).  Keys, and q [T, Hq, D] into q_out, turn
+    for `positions` as `rope` says (None: not).  A block's rows stand next to each other
+    in the call, as extend_tables' slot_map has them; rows with a slot outside the cache
+    are skipped.  Returns q_out (None without q)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return append_scaled(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_map,
+                                 positions, q, q_out, rope)
+    return (_native or _calls()).append_scaled(k_new, v_new, k_cache, v_cache, k_scale, v_scale,
+                                               slot_map, positions, q, q_out, rope)
+
+
+def read_scaled(k_cache, v_cache, k_scale, v_scale, slot_map, k_out=None, v_out=None,
+                stream=None):
+    """Rows of a scaled cache as the values they stand for, [T, Hkv, D] of the outputs'
+    dtype (bf16 if none is given, in which a power-of-two scale makes them exact).
+    Rows with a slot outside the cache stay as they were (zeros where allocated here).
+    Returns (k_out, v_out)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return read_scaled(k_cache, v_cache, k_scale, v_scale, slot_map, k_out, v_out)
+    return (_native or _calls()).read_scaled(k_cache, v_cache, k_scale, v_scale, slot_map, k_out,
+                                             v_out)
+
+
+def verify_attn_scaled_workspace_size(B, R, Hq, Hkv, D) -> int:
+    return int(load().spec_verify_attn_scaled_workspace_size(B, R, Hq, Hkv, D))
+
+
+def verify_attn_scaled(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_len, anc_mask=None,
+                       scale: float = 0.0, window: int = 0, workspace=None, out=None, lse=None,
+                       stream=None):
+    """verify_attn over a scaled cache: q [B, R, Hq, D] bf16 or fp16 (strided over B, R and
+    Hq as it comes), block row j of sequence b stored at position ctx_len[b] + j; anc_mask
+    [B, R] (tree_prepare's) or None for a chain.  With R = 1 it is the attention of single
+    tokens (ctx_len: what is stored in front of them; negative: an idle row).  window:
+    each row sees the last `window` tokens of its own text.  Returns (out, lse)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return verify_attn_scaled(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_len,
+                                      anc_mask, scale, window, workspace, out, lse)
+    return (_native or _calls()).verify_attn_scaled(q, k_cache, v_cache, k_scale, v_scale,
+                                                    block_table, ctx_len, anc_mask, scale, window,
+                                                    workspace, out, lse)
+
+
+def logits_process(logits, out=None, history=None, prompt_len=None, block_tokens=None, parent=None,
+                   repetition=None, frequency=None, presence=None, bias_ids=None, bias=None,
+                   mask=None, mask_row=None, stream=None):
+    """The target logits as served: logits [B, R, V] (bf16, fp16 or fp32) -> out [B, R, V]
+    fp32, which accept_sample takes (out may be logits itself, fp32: in place).
+
+    repetition, frequency, presence [B]: each request's penalties over its history [B, H]
+    (the first prompt_len[b] entries are the prompt, which only repetition counts) and
+    the block tokens in front of each row (a chain's drafts [B, R-1], or a tree's
+    node tokens [B, R] with parent).  bias_ids, bias [B, n]: added.  mask [n_masks,
+    ceil(V/32)] int32: ids whose bit is clear become -inf; mask_row [B, R]: each row's
+    mask (-1: none).  logits_penalize is the in-place form of one penalty and one list
+    of bans for the whole batch."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return logits_process(logits, out, history, prompt_len, block_tokens, parent,
+                                  repetition, frequency, presence, bias_ids, bias, mask, mask_row)
+    return (_native or _calls()).logits_process(logits, out, history, prompt_len, block_tokens,
+                                                parent, repetition, frequency, presence, bias_ids,
+                                                bias, mask, mask_row)

@@ -1,0 +1,566 @@
+// spec_append_scaled, spec_read_scaled, spec_commit_scaled -- an e4m3 cache whose scales, one for
+// each block of tokens and KV head, come from what is stored.
+//
+// Mathematics: a block needs the smallest power of two s with max |x| <= 448 s over the rows
+// that a call stores to it; x is stored as x / s rounded to the nearest e4m3 number.  A block
+// whose first token is stored begins anew; one that is only added to keeps the larger scale, and
+// its other codes c become c s_old / s (scaled.cuh has why powers of two).  Keys turn for their
+// positions first (rope.cuh).
+//
+// What bounds it: the rows are read once and the codes written once, so HBM, and for a verify
+// block (a few hundred rows) a chain of round trips: slots, rows and scale, store.
+//
+// Design: the rows of a block stand next to each other in the call, so a block's rows are a run of
+// at most `block` rows, and the run's first row tells who handles it.  A CTA takes the runs that
+// begin among its W rows (and turns those rows' queries): a warp takes one run of one head's keys
+// or values, whole -- maximum over the run's rows by shuffles, no atomics, no second launch -- so
+// every block has one writer and results do not depend on timing.  Rows that fit a warp's registers
+// (4 x 4 rows at D = 128) are read once, longer runs twice, the second time from L1 / L2.
+#include "rope.cuh"
+#include "scaled.cuh"
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTile = 16;        // rows of a CTA where there are many
+constexpr int kFewRows = 2432;   // up to sixteen per SM: a CTA per row
+constexpr int kPasses = 4;       // row groups that a warp keeps in registers
+
+struct AppendParams {
+  const char *k, *v, *q;
+  char *q_out, *kc, *vc;
+  float *ks, *vs;
+  const int64_t* slots;
+  const int32_t* pos;                                        // null: no rotation
+  long long k_stride, v_stride, q_stride, q_out_stride;      // elements
+  long long page_stride, token_stride, head_stride;          // bytes
+  FastDiv P, block;
+  int T, Hq, Hkv, W, num_slots;
+  RopeTable<128> rope;
+};
+
+SPEC_DEV long long slot_offset(const FastDiv& P, long long page_stride, long long token_stride,
+                               int slot) {
+  const int page = P.quot(slot);
+  return page * page_stride + (slot - page * P.d) * token_stride;
+}
+
+// The codes of a block's rows that are not in `written`, under a new scale: a warp's work.
+template <int D>
+SPEC_DEV void move_others(char* cache, long long token_stride, int block, uint64_t written,
+                          float ratio, int lane) {
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+  for (int o = lane / kLanes; o < block; o += kRows)
+    if (!(written >> o & 1)) {
+      uint4* p = reinterpret_cast<uint4*>(cache + o * token_stride + lane % kLanes * 16);
+      *p = moved_codes(*p, ratio);
+    }
+}
+
+// T: type of the rows
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) append_scaled_kernel(
+    const __grid_constant__ AppendParams p) {
+  constexpr int kItems = D / 16;             // of a row
+  constexpr int kRows = 32 / kItems;         // rows of a warp's pass
+  constexpr int kMost = kTile + kMaxBlock;   // rows looked at
+  extern __shared__ __align__(16) float table[];  // [rows][2][D/2]: cosines, sines
+  __shared__ int slot_s[kMost + 1];               // of row t0 - 1 + i; -1: none
+  __shared__ int pos_s[kMost + 1];
+  __shared__ int run_at[kTile], run_n[kTile];     // the runs that begin here
+  __shared__ int runs, rows_end;
+  const int t0 = blockIdx.x * p.W, t1 = min(t0 + p.W, p.T);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  chain_wait();
+  const int look = min(t1 - 1 + p.block.d, p.T);  // past the last row a run from here may have
+  if (threadIdx.x <= look - t0) {
+    const int t = t0 - 1 + (int)threadIdx.x;
+    int s = -1, at = 0;
+    if (t >= 0) {
+      const int64_t slot = p.slots[t];
+      at = p.pos ? p.pos[t] : 0;
+      if (slot >= 0 && slot < p.num_slots && at >= 0) s = (int)slot;
+    }
+    slot_s[threadIdx.x] = s;
+    pos_s[threadIdx.x] = at;
+  }
+  if (threadIdx.x == 0) runs = 0, rows_end = t1;
+  __syncthreads();
+  // ---- the runs that begin in t0 .. t1 - 1, in order
+  if (warp == 0) {
+    const int t = t0 + lane;
+    bool first = false;
+    int n = 0;
+    if (t < t1 && slot_s[lane + 1] >= 0) {
+      const int b = p.block.quot(slot_s[lane + 1]), before = slot_s[lane];
+      first = before < 0 || p.block.quot(before) != b;
+      if (first) {
+        n = 1;
+        while (n < p.block.d && t + n < look && slot_s[lane + 1 + n] >= 0 &&
+               p.block.quot(slot_s[lane + 1 + n]) == b)
+          ++n;
+      }
+    }
+    const uint32_t who = __ballot_sync(0xffffffffu, first);
+    if (first) {
+      const int i = __popc(who & ((1u << lane) - 1));
+      run_at[i] = t;
+      run_n[i] = n;
+      atomicMax(&rows_end, t + n);
+    }
+    if (lane == 0) runs = __popc(who);
+  }
+  __syncthreads();
+  if (p.rope.pairs > 0) {
+    const int n = (rows_end - t0) * (D / 2);
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const int u = i / (D / 2), j = i % (D / 2);
+      const float2 e = rope_entry(p.rope, pos_s[u + 1], j);
+      table[u * D + j] = e.x;
+      table[u * D + D / 2 + j] = e.y;
+    }
+    __syncthreads();
+  }
+
+  // ---- keys and values: a warp takes a run of one head
+  const int items = runs * p.Hkv * 2;
+  const int j = lane % kItems, sub = lane / kItems;   // item of a row, row of a pass
+  for (int i = warp; i < items; i += kWarps) {
+    const int r = i / (2 * p.Hkv), w = i - r * 2 * p.Hkv;
+    const bool is_k = w < p.Hkv;
+    const int h = is_k ? w : w - p.Hkv;
+    const int at = run_at[r], n = run_n[r], s0 = slot_s[at - t0 + 1];
+    const int b = p.block.quot(s0);
+    const T* src = reinterpret_cast<const T*>(is_k ? p.k : p.v) + h * D;
+    const long long stride = is_k ? p.k_stride : p.v_stride;
+    float* scale = (is_k ? p.ks : p.vs) + (long long)b * p.Hkv + h;
+    const float stored = *scale;
+    const bool turn = is_k && p.rope.pairs > 0;
+    const int2 c = is_k ? rope_chunks(p.rope, j) : make_int2(j, j + kItems);
+    uint4 raw[kPasses][2];
+    // rows base .. of the run, kPasses groups of kRows (rows behind the last: the last again)
+    auto load = [&](int base) {
+#pragma unroll
+      for (int x = 0; x < kPasses; ++x) {
+        if (base + x * kRows >= n) break;
+        const int t = at + min(base + x * kRows + sub, n - 1);
+        const uint4* row = reinterpret_cast<const uint4*>(src + t * stride);
+        raw[x][0] = row[c.x];
+        raw[x][1] = row[c.y];
+      }
+    };
+    auto values = [&](int x, int base, float* a, float* e) {
+      unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&raw[x][0]), a);
+      unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&raw[x][1]), e);
+      if (turn) {
+        const float* cs = table + (at - t0 + min(base + x * kRows + sub, n - 1)) * D + 8 * j;
+        rope_turn(p.rope.interleaved, a, e, cs, cs + D / 2);
+      }
+    };
+    float big = 0.f;
+    uint32_t lo = 0, hi = 0;  // written places of the block
+    for (int u = lane; u < n; u += 32) {
+      const int o = slot_s[at - t0 + 1 + u] - b * p.block.d;
+      if (o < 32) lo |= 1u << o; else hi |= 1u << (o - 32);
+    }
+    const uint64_t written = (uint64_t)__reduce_or_sync(0xffffffffu, hi) << 32 |
+                             __reduce_or_sync(0xffffffffu, lo);
+    for (int base = 0; base < n; base += kPasses * kRows) {
+      load(base);
+#pragma unroll
+      for (int x = 0; x < kPasses; ++x) {
+        if (base + x * kRows >= n) break;
+        float a[8], e[8];
+        values(x, base, a, e);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) big = fmaxf(big, fmaxf(finite_abs(a[y]), finite_abs(e[y])));
+      }
+    }
+    big = warp_max(big);
+    const bool fresh = written & 1;
+    const float held = fresh ? 0.f : held_scale(stored);
+    const float s = fmaxf(held, needed_scale(big));
+    char* cache = (is_k ? p.kc : p.vc) + h * p.head_stride;
+    if (held > 0.f && s != stored)
+      move_others<D>(cache + slot_offset(p.P, p.page_stride, p.token_stride, b * p.block.d),
+                     p.token_stride, p.block.d, written, stored / s, lane);
+    if (lane == 0 && s != stored) *scale = s;
+    const float by = 1.f / s;  // (a power of two)
+    const bool once = n <= kPasses * kRows;
+    for (int base = 0; base < n; base += kPasses * kRows) {
+      if (!once) load(base);
+#pragma unroll
+      for (int x = 0; x < kPasses; ++x) {
+        const int u = base + x * kRows + sub;
+        if (base + x * kRows >= n) break;
+        float a[8], e[8];
+        values(x, base, a, e);
+        if (u < n) {
+          char* to = cache + slot_offset(p.P, p.page_stride, p.token_stride,
+                                         slot_s[at - t0 + 1 + u]);
+#pragma unroll
+          for (int y = 0; y < 8; ++y) a[y] *= by, e[y] *= by;
+          *reinterpret_cast<uint2*>(to + c.x * 8) =
+              make_uint2(e4m3_word(a[0], a[1], a[2], a[3]), e4m3_word(a[4], a[5], a[6], a[7]));
+          *reinterpret_cast<uint2*>(to + c.y * 8) =
+              make_uint2(e4m3_word(e[0], e[1], e[2], e[3]), e4m3_word(e[4], e[5], e[6], e[7]));
+        }
+      }
+    }
+  }
+
+  // ---- this tile's queries
+  if (p.Hq == 0) return;
+  const int per = p.Hq * kItems, n = (t1 - t0) * per;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int u = i / per, y = i - u * per, h = y / kItems, x = y % kItems;
+    if (slot_s[u + 1] < 0) continue;
+    const int2 c = rope_chunks(p.rope, x);
+    const uint4* row = reinterpret_cast<const uint4*>(
+        reinterpret_cast<const T*>(p.q) + (t0 + u) * p.q_stride + h * D);
+    uint4* to = reinterpret_cast<uint4*>(
+        reinterpret_cast<T*>(p.q_out) + (t0 + u) * p.q_out_stride + h * D);
+    float a[8], e[8];
+    const uint4 ra = row[c.x], re = row[c.y];
+    unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&ra), a);
+    unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&re), e);
+    if (p.rope.pairs > 0)
+      rope_turn(p.rope.interleaved, a, e, table + u * D + 8 * x, table + u * D + D / 2 + 8 * x);
+    to[c.x] = pack_chunk<T>(a).w[0];
+    to[c.y] = pack_chunk<T>(e).w[0];
+  }
+}
+
+// ------------------------------------------------------------------ reading back
+struct ReadParams {
+  const char *kc, *vc;
+  const float *ks, *vs;
+  const int64_t* slots;
+  char *k_out, *v_out;
+  long long page_stride, token_stride, head_stride;  // bytes
+  long long k_stride, v_stride;                      // elements
+  FastDiv P, block, chunks, heads;                   // 16-byte chunks of a row's head; heads
+  long long n;                                       // chunks in all
+  int num_slots;
+};
+
+template <typename O>
+__global__ void __launch_bounds__(kThreads) read_scaled_kernel(const __grid_constant__ ReadParams p) {
+  chain_wait();
+  const int per = p.chunks.d * p.heads.d;
+  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < p.n;
+       i += (long long)gridDim.x * kThreads) {
+    const long long row = i / per;
+    const int y = (int)(i - row * per), h = p.chunks.quot(y), x = y - h * p.chunks.d;
+    const int64_t slot = p.slots[row];
+    if (slot < 0 || slot >= p.num_slots) continue;
+    const long long from = slot_offset(p.P, p.page_stride, p.token_stride, (int)slot) +
+                           h * p.head_stride + x * 16;
+    const long long sc = (long long)p.block.quot((int)slot) * p.heads.d + h;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      if (kv && !p.vc) break;
+      const uint4 w = *reinterpret_cast<const uint4*>((kv ? p.vc : p.kc) + from);
+      const float s = (kv ? p.vs : p.ks)[sc];
+      float v[16];
+      e4m3_values(w.x, v);
+      e4m3_values(w.y, v + 4);
+      e4m3_values(w.z, v + 8);
+      e4m3_values(w.w, v + 12);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] *= s;
+      Chunk8<O>* to = reinterpret_cast<Chunk8<O>*>(
+          reinterpret_cast<O*>(kv ? p.v_out : p.k_out) + row * (kv ? p.v_stride : p.k_stride) +
+          (h * p.chunks.d + x) * 16);
+      to[0] = pack_chunk<O>(v);
+      to[1] = pack_chunk<O>(v + 8);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ commit
+struct CommitParams {
+  char *kc, *vc;
+  float *ks, *vs;
+  const int32_t *table, *ctx, *accepted, *path, *parent;
+  int32_t *new_len, *keep, *status;
+  FastDiv P, block;
+  int num_pages, Hkv, max_pages, R;
+};
+
+// A CTA per sequence and KV head: every moving row is read into shared memory before any is
+// written, then a warp takes each block that rows move to, of the keys and of the values.
+template <int D>
+__global__ void __launch_bounds__(kThreads) commit_scaled_kernel(
+    const __grid_constant__ CommitParams p) {
+  constexpr int kChunks = D / 16;
+  __shared__ uint4 rows[2][64][kChunks];
+  __shared__ float row_scale[2][64];
+  __shared__ int ok;
+  const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  chain_wait();
+  const int c = p.ctx[b], a = p.accepted[b], P = p.P.d;
+  const int32_t* bt = p.table + (size_t)b * p.max_pages;
+  const int32_t* pth = p.path + (size_t)b * p.R;
+  const int32_t* par = p.parent ? p.parent + (size_t)b * p.R : nullptr;
+  if (threadIdx.x == 0) {
+    bool good = c >= 0 && a >= 0 && a < p.R && (long long)c + p.R <= (long long)p.max_pages * P;
+    int prev = 0;  // the anchor
+    for (int i = 0; i < a && good; ++i) {
+      const int v = pth[i];
+      good = v > prev && v < p.R && (!par || par[v] == prev);
+      prev = v;
+      if (good) {
+        const int ps = bt[(c + v) / P], pd = bt[(c + i + 1) / P];
+        good = ps >= 0 && ps < p.num_pages && pd >= 0 && pd < p.num_pages;
+      }
+    }
+    ok = good;
+    if (h == 0) {
+      const int n = good ? c + 1 + a : c;
+      p.new_len[b] = n;
+      if (p.keep) p.keep[b] = (int)(((long long)n + P - 1) / P);
+      if (p.status) p.status[b] = good ? 0 : SPEC_SEQ_BAD_TREE;
+    }
+  }
+  __syncthreads();
+  if (!ok || a == 0) return;
+  auto slot_of = [&](int t) { return (long long)bt[p.P.quot(t)] * P + (t - p.P.quot(t) * P); };
+  auto code_at = [&](int kv, long long slot) {
+    return (kv ? p.vc : p.kc) + (slot * p.Hkv + h) * D;
+  };
+  const int nb = P / p.block.d;
+  auto scale_at = [&](int kv, int t) {
+    const int page = p.P.quot(t);
+    return (kv ? p.vs : p.ks) +
+           ((long long)bt[page] * nb + p.block.quot(t - page * P)) * p.Hkv + h;
+  };
+  for (int i = threadIdx.x; i < 2 * a * kChunks; i += kThreads) {
+    const int kv = i / (a * kChunks), r = i - kv * a * kChunks, k = r / kChunks, x = r % kChunks;
+    rows[kv][k][x] = reinterpret_cast<const uint4*>(code_at(kv, slot_of(c + pth[k])))[x];
+    if (x == 0) row_scale[kv][k] = *scale_at(kv, c + pth[k]);
+  }
+  __syncthreads();
+  // blocks of positions c + 1 .. c + a (a page holds whole blocks)
+  const int first = p.block.quot(c + 1), last = p.block.quot(c + a);
+  for (int i = warp; i < 2 * (last - first + 1); i += kWarps) {
+    const int kv = i & 1, blk = first + (i >> 1);
+    const int begin = blk * p.block.d;
+    const int lo = max(begin, c + 1), hi = min(begin + p.block.d, c + a + 1);  // written positions
+    float big = 0.f;
+    for (int u = lane; u < (hi - lo) * kChunks; u += 32) {
+      const int k = lo - c - 1 + u / kChunks;
+      const uint4 w = rows[kv][k][u % kChunks];
+      const uint32_t* ww = reinterpret_cast<const uint32_t*>(&w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x[4];
+        e4m3_values(ww[e], x);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) big = fmaxf(big, finite_abs(x[y] * row_scale[kv][k]));
+      }
+    }
+    big = warp_max(big);
+    float* scale = scale_at(kv, begin);
+    const float stored = *scale, held = lo == begin ? 0.f : held_scale(stored);
+    const float s = fmaxf(held, needed_scale(big));
+    if (held > 0.f && s != stored) {
+      const uint64_t written =
+          (hi - lo == 64 ? ~0ull : (1ull << (hi - lo)) - 1) << (lo - begin);
+      move_others<D>(code_at(kv, slot_of(begin)), (long long)p.Hkv * D, p.block.d, written,
+                     stored / s, lane);
+    }
+    __syncwarp();
+    if (lane == 0 && s != stored) *scale = s;
+    for (int u = lane; u < (hi - lo) * kChunks; u += 32) {
+      const int k = lo - c - 1 + u / kChunks;
+      reinterpret_cast<uint4*>(code_at(kv, slot_of(c + 1 + k)))[u % kChunks] =
+          moved_codes(rows[kv][k][u % kChunks], row_scale[kv][k] / s);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host side
+template <typename T, int D>
+spec_status launch_append(const AppendParams& p, cudaStream_t st) {
+  const size_t smem =
+      p.rope.pairs ? (size_t)(p.W - 1 + p.block.d) * D * sizeof(float) : 0;
+  static PerDeviceOnce<int> once;
+  const spec_status rc = ensure_smem_limit(once, (const void*)append_scaled_kernel<T, D>,
+                                           (kTile - 1 + kMaxBlock) * D * (int)sizeof(float));
+  if (rc != SPEC_OK) return rc;
+  return launch_chained(append_scaled_kernel<T, D>, (p.T + p.W - 1) / p.W, kThreads, smem, st, p);
+}
+
+template <typename T>
+spec_status launch_append_d(const AppendParams& p, int D, cudaStream_t st) {
+  return D == 64 ? launch_append<T, 64>(p, st)
+                 : D == 128 ? launch_append<T, 128>(p, st) : launch_append<T, 256>(p, st);
+}
+
+// What the calls ask of a scaled cache.
+spec_status check_cache(const void* k_cache, const void* v_cache, int num_pages, int page_size,
+                        int block, int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                        int Hkv, int D) {
+  if (num_pages < 1 || page_size < 1 || Hkv < 1 || block < 1 || page_size % block)
+    return SPEC_EINVAL;
+  if (block > kMaxBlock || Hkv > 4096 || (D != 64 && D != 128 && D != 256))
+    return SPEC_EUNSUPPORTED;
+  if ((long long)num_pages * page_size > INT32_MAX - kMaxBlock) return SPEC_EUNSUPPORTED;
+  if (page_stride < 0 || token_stride < 0 || head_stride < 0) return SPEC_EINVAL;
+  if ((((uintptr_t)k_cache | (uintptr_t)v_cache) & 15) ||
+      ((page_stride | token_stride | head_stride) & 15))
+    return SPEC_EINVAL;
+  return SPEC_OK;
+}
+
+}  // namespace
+
+extern "C" spec_status spec_append_scaled(
+    const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride, const void* q,
+    int64_t q_stride, void* q_out, int64_t q_out_stride, spec_dtype new_dtype, void* k_cache,
+    void* v_cache, float* k_scale, float* v_scale, int num_pages, int page_size, int block,
+    int64_t page_stride, int64_t token_stride, int64_t head_stride, const int64_t* slot_map,
+    const int32_t* positions, int T, int Hq, int Hkv, int D, const spec_rope* rope, void* stream) {
+  if (T < 0 || Hq < 0) return SPEC_EINVAL;
+  spec_status rc = check_cache(k_cache, v_cache, num_pages, page_size, block, page_stride,
+                               token_stride, head_stride, Hkv, D);
+  if (rc != SPEC_OK) return rc;
+  if (new_dtype == SPEC_F32) return SPEC_EUNSUPPORTED;
+  if (new_dtype != SPEC_BF16 && new_dtype != SPEC_F16) return SPEC_EINVAL;
+  if (Hq > 4096 || T > INT32_MAX - kMaxBlock) return SPEC_EUNSUPPORTED;
+  if ((q == nullptr) != (q_out == nullptr) || (q && Hq < 1)) return SPEC_EINVAL;
+  AppendParams p{};
+  rc = rope_table(rope, D, &p.rope);
+  if (rc != SPEC_OK) return rc;
+  if (T == 0) return SPEC_OK;
+  if (!k_new || !v_new || !k_cache || !v_cache || !k_scale || !v_scale || !slot_map ||
+      (rope && !positions))
+    return SPEC_EINVAL;
+  if (((uintptr_t)k_new | (uintptr_t)v_new | (uintptr_t)q | (uintptr_t)q_out) & 15)
+    return SPEC_EINVAL;
+  if (k_stride < 0 || v_stride < 0 || q_stride < 0 || q_out_stride < 0) return SPEC_EINVAL;
+  if (((k_stride | v_stride | (q ? q_stride | q_out_stride : 0)) * 2) & 15) return SPEC_EINVAL;
+  if (q && q == q_out && q_stride != q_out_stride) return SPEC_EINVAL;
+  p.k = static_cast<const char*>(k_new);
+  p.v = static_cast<const char*>(v_new);
+  p.q = static_cast<const char*>(q);
+  p.q_out = static_cast<char*>(q_out);
+  p.kc = static_cast<char*>(k_cache);
+  p.vc = static_cast<char*>(v_cache);
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.slots = slot_map;
+  p.pos = rope ? positions : nullptr;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_stride = q_stride;
+  p.q_out_stride = q_out_stride;
+  p.page_stride = page_stride;
+  p.token_stride = token_stride;
+  p.head_stride = head_stride;
+  p.P = FastDiv(page_size);
+  p.block = FastDiv(block);
+  p.T = T;
+  p.Hq = q ? Hq : 0;
+  p.Hkv = Hkv;
+  p.W = T <= kFewRows ? 1 : kTile;
+  p.num_slots = num_pages * page_size;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return new_dtype == SPEC_BF16 ? launch_append_d<__nv_bfloat16>(p, D, st)
+                                : launch_append_d<__half>(p, D, st);
+}
+
+extern "C" spec_status spec_read_scaled(const void* k_cache, const void* v_cache,
+                                        const float* k_scale, const float* v_scale, int num_pages,
+                                        int page_size, int block, int64_t page_stride,
+                                        int64_t token_stride, int64_t head_stride,
+                                        const int64_t* slot_map, int T, int Hkv, int D,
+                                        void* k_out, int64_t k_out_stride, void* v_out,
+                                        int64_t v_out_stride, spec_dtype out_dtype, void* stream) {
+  if (T < 0) return SPEC_EINVAL;
+  const spec_status rc = check_cache(k_cache, v_cache, num_pages, page_size, block, page_stride,
+                                     token_stride, head_stride, Hkv, D);
+  if (rc != SPEC_OK) return rc;
+  if (out_dtype != SPEC_BF16 && out_dtype != SPEC_F16 && out_dtype != SPEC_F32) return SPEC_EINVAL;
+  if ((v_out == nullptr) != (v_cache == nullptr) || (v_out == nullptr) != (v_scale == nullptr))
+    return SPEC_EINVAL;
+  if (T > INT32_MAX - kMaxBlock) return SPEC_EUNSUPPORTED;
+  if (T == 0) return SPEC_OK;
+  if (!k_cache || !k_scale || !slot_map || !k_out) return SPEC_EINVAL;
+  if (((uintptr_t)k_out | (uintptr_t)v_out) & 15) return SPEC_EINVAL;
+  const int es = out_dtype == SPEC_F32 ? 4 : 2;
+  if (k_out_stride < 0 || v_out_stride < 0 ||
+      (((k_out_stride | (v_out ? v_out_stride : 0)) * es) & 15))
+    return SPEC_EINVAL;
+  ReadParams p{};
+  p.kc = static_cast<const char*>(k_cache);
+  p.vc = static_cast<const char*>(v_cache);
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.slots = slot_map;
+  p.k_out = static_cast<char*>(k_out);
+  p.v_out = static_cast<char*>(v_out);
+  p.page_stride = page_stride;
+  p.token_stride = token_stride;
+  p.head_stride = head_stride;
+  p.k_stride = k_out_stride;
+  p.v_stride = v_out_stride;
+  p.P = FastDiv(page_size);
+  p.block = FastDiv(block);
+  p.chunks = FastDiv(D / 16);
+  p.heads = FastDiv(Hkv);
+  p.n = (long long)T * Hkv * (D / 16);
+  p.num_slots = num_pages * page_size;
+  const int grid = (int)std::min<long long>((p.n + kThreads - 1) / kThreads, 1 << 20);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (out_dtype == SPEC_F32) return launch_chained(read_scaled_kernel<float>, grid, kThreads, 0, st, p);
+  if (out_dtype == SPEC_BF16)
+    return launch_chained(read_scaled_kernel<__nv_bfloat16>, grid, kThreads, 0, st, p);
+  return launch_chained(read_scaled_kernel<__half>, grid, kThreads, 0, st, p);
+}
+
+extern "C" spec_status spec_commit_scaled(void* k_cache, void* v_cache, float* k_scale,
+                                          float* v_scale, int num_pages, int page_size, int block,
+                                          int Hkv, int D, const int32_t* block_table,
+                                          int max_pages, const int32_t* ctx_len,
+                                          const int32_t* accepted_len, const int32_t* path,
+                                          const int32_t* parent, int B, int R, int32_t* new_len,
+                                          int32_t* keep_pages, int32_t* status_per_seq,
+                                          void* stream) {
+  if (B < 0 || R < 1 || R > 64 || max_pages < 1) return SPEC_EINVAL;
+  const spec_status rc = check_cache(k_cache, v_cache, num_pages, page_size, block, 0, 0, 0, Hkv, D);
+  if (rc != SPEC_OK) return rc;
+  if ((long long)max_pages * page_size > INT32_MAX - kMaxBlock || (long long)B * Hkv > INT32_MAX)
+    return SPEC_EUNSUPPORTED;
+  if (B == 0) return SPEC_OK;
+  if (!k_cache || !v_cache || !k_scale || !v_scale || !block_table || !ctx_len || !accepted_len ||
+      !path || !new_len)
+    return SPEC_EINVAL;
+  CommitParams p{};
+  p.kc = static_cast<char*>(k_cache);
+  p.vc = static_cast<char*>(v_cache);
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.table = block_table;
+  p.ctx = ctx_len;
+  p.accepted = accepted_len;
+  p.path = path;
+  p.parent = parent;
+  p.new_len = new_len;
+  p.keep = keep_pages;
+  p.status = status_per_seq;
+  p.P = FastDiv(page_size);
+  p.block = FastDiv(block);
+  p.num_pages = num_pages;
+  p.Hkv = Hkv;
+  p.max_pages = max_pages;
+  p.R = R;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int grid = B * Hkv;
+  if (D == 64) return launch_chained(commit_scaled_kernel<64>, grid, kThreads, 0, st, p);
+  if (D == 128) return launch_chained(commit_scaled_kernel<128>, grid, kThreads, 0, st, p);
+  return launch_chained(commit_scaled_kernel<256>, grid, kThreads, 0, st, p);
+}

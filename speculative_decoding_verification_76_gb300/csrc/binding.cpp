@@ -1,4 +1,5 @@
-// The host side of extend_tables, release_pages, append_tokens and decode_attn: checks
+// The host side of the calls of a serving step (tables, appends, rotation, scaled caches,
+// one-token and scaled-cache attention, served logits): checks
 // the tensors, allocates the outputs and calls the C ABI on the tensors' device and its
 // current stream.  These calls run once per drafted token, where a few microseconds of
 // kernels sit behind a dozen tensor arguments: checked in Python and marshalled with
@@ -18,6 +19,7 @@
 
 #include <climits>
 #include <sstream>
+#include <vector>
 
 #include "../../include/spec_verify.h"
 
@@ -321,6 +323,362 @@ PyObject* decode_attn(PyObject* const* a) {
   return PyTuple_Pack(2, out[0], out[1]);
 }
 
+// ------------------------------------------------------------------ scaled caches and their step
+struct Rope {  // a Python Rope as the C struct, and its own frequencies
+  spec_rope c{};
+  std::vector<double> freqs;
+};
+
+const spec_rope* rope_of(PyObject* o, Rope* r) {
+  if (!given(o)) return nullptr;
+  // Rope keeps its numbers as one tuple, in spec_rope's order (attributes one by one cost 1 us)
+  THPObjectPtr t(PyObject_GetAttrString(o, "_c"));
+  if (!t || !PyTuple_Check(t.get()) || PyTuple_GET_SIZE(t.get()) != 10) {
+    PyErr_Clear();
+    refuse("rope must be a Rope");
+  }
+  auto item = [&](int i) { return PyTuple_GET_ITEM(t.get(), i); };
+  r->c.dim = (int32_t)whole(item(0), "rope.dim", 0);
+  r->c.interleaved = (int32_t)whole(item(1), "rope.interleaved", 0);
+  r->c.scaling = (int32_t)whole(item(2), "rope.scaling", 0);
+  double* to[6] = {&r->c.base, &r->c.factor, &r->c.original_len,
+                   &r->c.low,  &r->c.high,   &r->c.magnitude};
+  for (int i = 0; i < 6; ++i) *to[i] = number(item(3 + i));
+  if (given(item(9))) {
+    PyObject* f = item(9);
+    if (!PyTuple_Check(f) || PyTuple_GET_SIZE(f) != r->c.dim / 2)
+      refuse("rope.freqs must hold dim / 2 numbers");
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(f); ++i)
+      r->freqs.push_back(number(PyTuple_GET_ITEM(f, i)));
+    r->c.freqs = r->freqs.data();
+  }
+  return &r->c;
+}
+
+// Bytes that a tensor spans, for outputs that must not lie over inputs.
+struct Span {
+  uintptr_t from, to;
+  explicit Span(const Tensor& t) : from((uintptr_t)t.data_ptr()), to(from) {
+    if (t.numel() == 0) return;
+    int64_t last = 0;
+    for (int64_t i = 0; i < t.dim(); ++i) last += (t.size(i) - 1) * t.stride(i);
+    to = from + (last + 1) * t.element_size();
+  }
+  bool meets(const Span& o) const { return from < o.to && o.from < to; }
+};
+
+void apart(PyObject* out, const char* name, std::initializer_list<PyObject*> ins) {
+  const Span a(THPVariable_Unpack(out));
+  for (PyObject* o : ins)
+    if (given(o) && THPVariable_Check(o) && a.meets(Span(THPVariable_Unpack(o))))
+      refuse(name, " must not share memory with an input");
+}
+
+// Out may be the input itself; otherwise the two are apart (rows may interleave: slices of one
+// projection lie between one another, which the spans of a single row settle).
+bool rows_meet(const Tensor& a, const Tensor& b) {
+  if (!Span(a).meets(Span(b))) return false;
+  if (a.dim() != 3 || b.dim() != 3 || a.size(0) < 2 || b.size(0) < 2) return true;
+  const int64_t s = a.stride(0) * (int64_t)a.element_size();
+  if (s <= 0 || s != b.stride(0) * (int64_t)b.element_size()) return true;
+  // rows of both repeat every s bytes: compare one period
+  const int64_t na = a.size(1) * a.size(2) * (int64_t)a.element_size();
+  const int64_t nb = b.size(1) * b.size(2) * (int64_t)b.element_size();
+  int64_t d = ((int64_t)((uintptr_t)b.data_ptr() - (uintptr_t)a.data_ptr()) % s + s) % s;
+  return d < na || d + nb > s;
+}
+
+void out_apart(PyObject* out, const char* name, PyObject* same, std::initializer_list<PyObject*> ins) {
+  const Tensor& t = THPVariable_Unpack(out);
+  for (PyObject* o : ins) {
+    if (!given(o) || !THPVariable_Check(o)) continue;
+    const Tensor& u = THPVariable_Unpack(o);
+    if (o == same && u.data_ptr() == t.data_ptr() && u.strides() == t.strides()) continue;  // in place
+    if (rows_meet(t, u)) refuse(name, " must not share memory with another argument");
+  }
+}
+
+PyObject* rotate(PyObject* const* a) {  // q, positions, rope, k, q_out, k_out
+  const Tensor& q = cuda_tensor(a[0], "q");
+  const auto dev = q.device();
+  const c10::cuda::CUDAGuard guard(dev);
+  const auto type = q.scalar_type();
+  if (type != at::kFloat && type != at::kBFloat16 && type != at::kHalf)
+    refuse("q must be bf16, fp16 or fp32");
+  if (q.dim() != 3) refuse("q must be [tokens, Hq, D]");
+  const int64_t T = q.size(0), Hq = q.size(1), D = q.size(2);
+  if (T > INT_MAX || Hq > INT_MAX || D > INT_MAX) refuse("sizes must be below 2^31");
+  int64_t qs, ks = 0, qos, kos = 0, Hkv = 0;
+  const void* qp = rows(a[0], "q", dev, type, T, Hq, D, &qs);
+  const int32_t* pos = plain(a[1], "positions", dev, at::kInt, {T});
+  Rope rope;
+  if (!given(a[2])) refuse("rope is needed");
+  const spec_rope* rp = rope_of(a[2], &rope);
+  const void* kp = nullptr;
+  if (given(a[3])) {
+    const Tensor& k = tensor_on(a[3], "k", dev);
+    if (k.dim() != 3) refuse("k must be [tokens, Hkv, D]");
+    Hkv = k.size(1);
+    if (Hkv < 1 || Hkv > INT_MAX) refuse("k must have heads");
+    kp = rows(a[3], "k", dev, type, T, Hkv, D, &ks);
+  } else if (given(a[5])) {
+    refuse("k_out without k");
+  }
+  THPObjectPtr made[2];
+  PyObject* out[2] = {a[4], a[5]};
+  for (int i = 0; i < 2; ++i)
+    if (!given(out[i]) && (i == 0 || kp)) {
+      made[i] = THPVariable_Wrap(at::zeros({T, i ? Hkv : Hq, D},
+                                           at::TensorOptions().dtype(type).device(dev)));
+      if (!made[i]) throw python_error();
+      out[i] = made[i].get();
+    }
+  void* qo = rows(out[0], "q_out", dev, type, T, Hq, D, &qos);
+  void* ko = kp ? rows(out[1], "k_out", dev, type, T, Hkv, D, &kos) : nullptr;
+  if (!made[0]) out_apart(out[0], "q_out", a[0], {a[0], a[1], a[3], made[1] || !kp ? Py_None : out[1]});
+  if (kp && !made[1]) out_apart(out[1], "k_out", a[3], {a[0], a[1], a[3]});
+  check("spec_rotate", spec_rotate(qp, qs, qo, qos, kp, ks, ko, kos, code_of(type), pos, (int)T,
+                                   (int)Hq, (int)Hkv, (int)D, rp, stream_of(dev)));
+  return PyTuple_Pack(2, out[0], out[1]);
+}
+
+struct Scaled : Caches {
+  float *ks, *vs;
+  int block;
+};
+
+Scaled scaled_cache(PyObject* const* a, c10::Device dev) {  // k_cache, v_cache, k_scale, v_scale
+  const Tensor& k = tensor_on(a[0], "k_cache", dev);
+  if (k.scalar_type() != at::kFloat8_e4m3fn) refuse("a scaled cache is Float8_e4m3fn");
+  Scaled c{caches(a[0], a[1], dev, at::kHalf), nullptr, nullptr, 0};
+  const Tensor& s = tensor_on(a[2], "k_scale", dev);
+  if (s.dim() != 3 || s.size(1) < 1 || c.P % s.size(1))
+    refuse("k_scale must be [pages, page_size / block, Hkv]");
+  c.block = (int)(c.P / s.size(1));
+  c.ks = plain<float>(a[2], "k_scale", dev, at::kFloat, {c.pages, s.size(1), c.Hkv});
+  c.vs = plain<float>(a[3], "v_scale", dev, at::kFloat, {c.pages, s.size(1), c.Hkv});
+  return c;
+}
+
+// k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_map, positions, q, q_out, rope
+PyObject* append_scaled(PyObject* const* a) {
+  const Tensor& kn = cuda_tensor(a[0], "k_new");
+  const auto dev = kn.device();
+  const c10::cuda::CUDAGuard guard(dev);
+  const auto type = kn.scalar_type();
+  if (type != at::kBFloat16 && type != at::kHalf) refuse("k_new must be bf16 or fp16");
+  const Scaled c = scaled_cache(a + 2, dev);
+  if (kn.dim() != 3) refuse("k_new must be [tokens, ", c.Hkv, ", ", c.D, "]");
+  const int64_t T = kn.size(0);
+  if (T > INT_MAX) refuse("tokens must be below 2^31");
+  int64_t ks, vs, qs = 0, os = 0, Hq = 0;
+  const void* k = rows(a[0], "k_new", dev, type, T, c.Hkv, c.D, &ks);
+  const void* v = rows(a[1], "v_new", dev, type, T, c.Hkv, c.D, &vs);
+  const int64_t* slots = plain<int64_t>(a[6], "slot_map", dev, at::kLong, {T});
+  Rope rope;
+  const spec_rope* rp = rope_of(a[10], &rope);
+  const int32_t* pos = nullptr;
+  if (given(a[7]))
+    pos = plain(a[7], "positions", dev, at::kInt, {T});
+  else if (rp)
+    refuse("positions are needed to rotate");
+  const void* q = nullptr;
+  void* qo = nullptr;
+  PyObject* out = a[9];
+  THPObjectPtr made;
+  if (given(a[8])) {
+    const Tensor& qt = tensor_on(a[8], "q", dev);
+    if (qt.dim() != 3 || qt.size(0) != T) refuse("q must be [tokens, Hq, D]");
+    Hq = qt.size(1);
+    if (Hq > INT_MAX) refuse("heads must be below 2^31");
+    q = rows(a[8], "q", dev, type, T, Hq, c.D, &qs);
+    if (!given(out)) {
+      made = THPVariable_Wrap(
+          at::zeros({T, Hq, c.D}, at::TensorOptions().dtype(type).device(dev)));
+      if (!made) throw python_error();
+      out = made.get();
+    }
+    qo = rows(out, "q_out", dev, type, T, Hq, c.D, &os);
+    if (!made) out_apart(out, "q_out", a[8], {a[8], a[0], a[1]});
+  } else if (given(out)) {
+    refuse("q_out without q");
+  }
+  check("spec_append_scaled",
+        spec_append_scaled(k, ks, v, vs, q, qs, qo, os, code_of(type), c.k, c.v, c.ks, c.vs,
+                           c.pages, c.P, c.block, c.page, c.token, c.head, slots, pos, (int)T,
+                           (int)Hq, c.Hkv, c.D, rp, stream_of(dev)));
+  Py_INCREF(out);
+  return out;
+}
+
+// k_cache, v_cache, k_scale, v_scale, slot_map, k_out, v_out
+PyObject* read_scaled(PyObject* const* a) {
+  const Tensor& kc = cuda_tensor(a[0], "k_cache");
+  const auto dev = kc.device();
+  const c10::cuda::CUDAGuard guard(dev);
+  const Scaled c = scaled_cache(a, dev);
+  const Tensor& sl = tensor_on(a[4], "slot_map", dev);
+  if (sl.dim() != 1 || sl.size(0) > INT_MAX) refuse("slot_map must be [tokens]");
+  const int64_t T = sl.size(0);
+  const int64_t* slots = plain<int64_t>(a[4], "slot_map", dev, at::kLong, {T});
+  auto type = at::kBFloat16;
+  for (int i = 5; i < 7; ++i)
+    if (given(a[i])) type = tensor_on(a[i], "an output", dev).scalar_type();
+  if (type != at::kFloat && type != at::kBFloat16 && type != at::kHalf)
+    refuse("outputs must be bf16, fp16 or fp32");
+  THPObjectPtr made[2];
+  PyObject* out[2] = {a[5], a[6]};
+  int64_t st[2];
+  void* p[2];
+  for (int i = 0; i < 2; ++i) {
+    if (!given(out[i])) {
+      made[i] = THPVariable_Wrap(
+          at::zeros({T, c.Hkv, c.D}, at::TensorOptions().dtype(type).device(dev)));
+      if (!made[i]) throw python_error();
+      out[i] = made[i].get();
+    }
+    p[i] = rows(out[i], i ? "v_out" : "k_out", dev, type, T, c.Hkv, c.D, &st[i]);
+  }
+  if (!made[0]) out_apart(out[0], "k_out", nullptr, {a[0], a[1], a[2], a[3], a[4], out[1]});
+  if (!made[1]) out_apart(out[1], "v_out", nullptr, {a[0], a[1], a[2], a[3], a[4], out[0]});
+  check("spec_read_scaled",
+        spec_read_scaled(c.k, c.v, c.ks, c.vs, c.pages, c.P, c.block, c.page, c.token, c.head,
+                         slots, (int)T, c.Hkv, c.D, p[0], st[0], p[1], st[1], code_of(type),
+                         stream_of(dev)));
+  return PyTuple_Pack(2, out[0], out[1]);
+}
+
+// q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_len, anc_mask, scale, window, workspace,
+// out, lse
+PyObject* verify_attn_scaled(PyObject* const* a) {
+  const Tensor& q = cuda_tensor(a[0], "q");
+  const auto dev = q.device();
+  const c10::cuda::CUDAGuard guard(dev);
+  const auto type = q.scalar_type();
+  if (type != at::kBFloat16 && type != at::kHalf) refuse("q must be bf16 or fp16");
+  if (q.dim() != 4 || q.stride(3) != 1) refuse("q must be [B, R, Hq, D], contiguous over D");
+  const Scaled c = scaled_cache(a + 1, dev);
+  const int64_t B = q.size(0), R = q.size(1), Hq = q.size(2), D = q.size(3);
+  if (D != c.D) refuse("head_dim mismatch");
+  const Tensor& tab = tensor_on(a[5], "block_table", dev);
+  if (tab.dim() != 2) refuse("block_table must be [B, max_pages]");
+  const int64_t width = tab.size(1);
+  if (B > INT_MAX || R > INT_MAX || Hq > INT_MAX || width > INT_MAX)
+    refuse("sizes must be below 2^31");
+  const int32_t* table = plain(a[5], "block_table", dev, at::kInt, {B, width});
+  const int32_t* ctx = plain(a[6], "ctx_len", dev, at::kInt, {B});
+  const uint64_t* mask = nullptr;
+  if (given(a[7])) mask = plain<uint64_t>(a[7], "anc_mask", dev, at::kLong, {B, R});
+  const double sm_scale = number(a[8]);
+  const int64_t window = whole(a[9], "window", 0);
+  Tensor ws;
+  if (given(a[10])) {
+    if (!THPVariable_Check(a[10]) || THPVariable_Unpack(a[10]).device() != dev ||
+        THPVariable_Unpack(a[10]).scalar_type() != at::kByte ||
+        !THPVariable_Unpack(a[10]).is_contiguous())
+      refuse("workspace must come from new_workspace on q's device");
+    ws = THPVariable_Unpack(a[10]);
+  } else {
+    const size_t need = spec_verify_attn_scaled_workspace_size((int)B, (int)R, (int)Hq, c.Hkv, (int)D);
+    ws = at::zeros({(int64_t)(need < 256 ? 256 : need)},
+                   at::TensorOptions().dtype(at::kByte).device(dev));
+  }
+  THPObjectPtr made[2];
+  PyObject* out[2] = {a[11], a[12]};
+  for (int i = 0; i < 2; ++i)
+    if (!given(out[i])) {
+      made[i] = THPVariable_Wrap(i ? empty({B, R, Hq}, at::kFloat, dev)
+                                   : empty({B, R, Hq, D}, type, dev));
+      if (!made[i]) throw python_error();
+      out[i] = made[i].get();
+    }
+  void* o = plain<void>(out[0], "out", dev, type, {B, R, Hq, D});
+  float* lse = plain<float>(out[1], "lse", dev, at::kFloat, {B, R, Hq});
+  for (int i = 0; i < 2; ++i)
+    if (!made[i])
+      apart(out[i], i ? "lse" : "out",
+            {a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[10], i ? out[0] : Py_None});
+  check("spec_verify_attn_scaled",
+        spec_verify_attn_scaled(q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), code_of(type),
+                                c.k, c.v, c.ks, c.vs, c.pages, c.P, c.block, c.page, c.token,
+                                c.head, table, (int)width, ctx, mask, (int)B, (int)R, (int)Hq,
+                                c.Hkv, (int)D, (int)window, (float)sm_scale, ws.data_ptr(),
+                                (size_t)ws.numel(), o, lse, stream_of(dev)));
+  return PyTuple_Pack(2, out[0], out[1]);
+}
+
+// logits, out, history, prompt_len, block_tokens, parent, repetition, frequency, presence,
+// bias_ids, bias, mask, mask_row
+PyObject* logits_process(PyObject* const* a) {
+  const Tensor& x = cuda_tensor(a[0], "logits");
+  const auto dev = x.device();
+  const c10::cuda::CUDAGuard guard(dev);
+  const auto type = x.scalar_type();
+  if (type != at::kFloat && type != at::kBFloat16 && type != at::kHalf)
+    refuse("logits must be bf16, fp16 or fp32");
+  if (x.dim() != 3) refuse("logits must be [B, R, V]");
+  const int64_t B = x.size(0), R = x.size(1), V = x.size(2);
+  if (B > INT_MAX || R > INT_MAX || V > INT_MAX) refuse("sizes must be below 2^31");
+  if (x.stride(2) != 1 || (B > 1 && R > 0 && x.stride(0) != R * x.stride(1)))
+    refuse("logits: rows must be equally far apart, contiguous over V");
+  const int64_t stride = R > 1 ? x.stride(1) : B > 1 ? x.stride(0) : V;
+  auto width = [&](int i, const char* name) -> int64_t {  // of a [B, n] array; 0: not given
+    if (!given(a[i])) return 0;
+    const Tensor& t = tensor_on(a[i], name, dev);
+    if (t.dim() != 2 || t.size(1) > INT_MAX) refuse(name, " must have two dimensions");
+    return t.size(1);
+  };
+  auto ints = [&](int i, const char* name, at::IntArrayRef shape) -> const int32_t* {
+    return given(a[i]) ? plain(a[i], name, dev, at::kInt, shape) : nullptr;
+  };
+  auto floats = [&](int i, const char* name, at::IntArrayRef shape) -> const float* {
+    return given(a[i]) ? plain<float>(a[i], name, dev, at::kFloat, shape) : nullptr;
+  };
+  const int64_t H = width(2, "history"), n = width(9, "bias_ids");
+  const int32_t* history = ints(2, "history", {B, H});
+  const int32_t* prompt = ints(3, "prompt_len", {B});
+  if (prompt && !history) refuse("prompt_len without history");
+  const int32_t* parent = ints(5, "parent", {B, R});
+  if (parent && !given(a[4])) refuse("parent without block_tokens");
+  const int32_t* tokens = ints(4, "block_tokens", {B, parent ? R : R - 1});
+  const float* rep = floats(6, "repetition", {B});
+  const float* fr = floats(7, "frequency", {B});
+  const float* pr = floats(8, "presence", {B});
+  if (given(a[9]) != given(a[10])) refuse("bias_ids and bias come together");
+  const int32_t* ids = ints(9, "bias_ids", {B, n});
+  const float* bias = floats(10, "bias", {B, n});
+  int64_t masks = 0;
+  const int32_t* mask = nullptr;
+  if (given(a[11])) {
+    width(11, "mask");
+    masks = THPVariable_Unpack(a[11]).size(0);
+    if (masks > INT_MAX) refuse("masks must be below 2^31");
+    mask = ints(11, "mask", {masks, (V + 31) / 32});
+    if (!given(a[12]) && masks != B * R) refuse("mask must have B * R rows without mask_row");
+  } else if (given(a[12])) {
+    refuse("mask_row without mask");
+  }
+  const int32_t* row = ints(12, "mask_row", {B, R});
+  THPObjectPtr made;
+  PyObject* out = a[1];
+  if (!given(out)) {
+    made = THPVariable_Wrap(empty({B, R, V}, at::kFloat, dev));
+    if (!made) throw python_error();
+    out = made.get();
+  }
+  float* o = plain<float>(out, "out", dev, at::kFloat, {B, R, V});
+  if (!made) {
+    if (o != x.data_ptr() || type != at::kFloat || !x.is_contiguous()) apart(out, "out", {a[0]});
+    apart(out, "out", {a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10], a[11], a[12]});
+  }
+  check("spec_logits_process",
+        spec_logits_process(x.data_ptr(), stride, code_of(type), o, (int)B, (int)R, (int)V,
+                            history, (int)H, prompt, tokens, parent, rep, fr, pr, ids, bias,
+                            (int)n, mask, (int)masks, row, stream_of(dev)));
+  Py_INCREF(out);
+  return out;
+}
+
 // ------------------------------------------------------------------ the module
 PyObject* g_spec_error = nullptr;  // the package's SpecError
 
@@ -368,6 +726,11 @@ PyModuleDef* module_def() {
                                   method<release_pages, 8>("release_pages"),
                                   method<append_tokens, 11>("append_tokens"),
                                   method<decode_attn, 12>("decode_attn"),
+                                  method<rotate, 6>("rotate"),
+                                  method<append_scaled, 11>("append_scaled"),
+                                  method<read_scaled, 7>("read_scaled"),
+                                  method<verify_attn_scaled, 13>("verify_attn_scaled"),
+                                  method<logits_process, 13>("logits_process"),
                                   {"set_error", set_error, METH_O, nullptr},
                                   {nullptr, nullptr, 0, nullptr}};
   static PyModuleDef def = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1,     methods,

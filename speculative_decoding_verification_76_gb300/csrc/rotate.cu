@@ -1,0 +1,102 @@
+// spec_rotate -- packed rows of queries and keys turned for their positions.
+//
+// Mathematics: pair (a, b) at position t becomes magnitude * (a cos u - b sin u, a sin u +
+// b cos u), u = t f_i (rope.cuh), in fp32 with one rounding.
+//
+// What bounds it: every row is read once and written once, so HBM, and for the rows of a verify
+// block the launch.  A thread takes 8 + 8 elements whose pairs lie within them (two 16-byte loads
+// and stores); a token's sines and cosines serve all its heads from shared memory.
+#include "rope.cuh"
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kMaxPairs = kMaxRopePairs;
+
+struct RotateParams {
+  const char *q, *k;
+  char *q_out, *k_out;
+  const int32_t* pos;
+  long long q_stride, k_stride, q_out_stride, k_out_stride;  // elements
+  FastDiv per, items;  // work items of a token; of a head
+  int T, Hq, Hkv, D;
+  RopeTable<> rope;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ RotateParams p) {
+  __shared__ __align__(16) float cs[kMaxPairs], sn[kMaxPairs];
+  const int t = blockIdx.x;
+  chain_wait();
+  const int at = p.pos[t];
+  if (at < 0) return;
+  for (int i = threadIdx.x; i < p.D / 2; i += kThreads) {
+    const float2 e = rope_entry(p.rope, at, i);
+    cs[i] = e.x;
+    sn[i] = e.y;
+  }
+  __syncthreads();
+  const int n = (p.Hq + p.Hkv) * p.items.d;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int h = p.items.quot(i), j = i - h * p.items.d;
+    const bool is_q = h < p.Hq;
+    const int2 c = rope_chunks(p.rope, j);
+    const long long from = is_q ? t * p.q_stride + (long long)h * p.D
+                                : t * p.k_stride + (long long)(h - p.Hq) * p.D;
+    const long long to = is_q ? t * p.q_out_stride + (long long)h * p.D
+                              : t * p.k_out_stride + (long long)(h - p.Hq) * p.D;
+    const char* src = (is_q ? p.q : p.k) + from * (long long)sizeof(T);
+    char* dst = (is_q ? p.q_out : p.k_out) + to * (long long)sizeof(T);
+    float a[8], b[8];
+    unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(src + c.x * 8 * sizeof(T)), a);
+    unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(src + c.y * 8 * sizeof(T)), b);
+    rope_turn(p.rope.interleaved, a, b, cs + 8 * j, sn + 8 * j);
+    *reinterpret_cast<Chunk8<T>*>(dst + c.x * 8 * sizeof(T)) = pack_chunk<T>(a);
+    *reinterpret_cast<Chunk8<T>*>(dst + c.y * 8 * sizeof(T)) = pack_chunk<T>(b);
+  }
+}
+
+}  // namespace
+
+extern "C" spec_status spec_rotate(const void* q, int64_t q_stride, void* q_out,
+                                   int64_t q_out_stride, const void* k, int64_t k_stride,
+                                   void* k_out, int64_t k_out_stride, spec_dtype dtype,
+                                   const int32_t* positions, int T, int Hq, int Hkv, int D,
+                                   const spec_rope* rope, void* stream) {
+  if (T < 0 || Hq < 1 || Hkv < 0 || D < 1 || !rope) return SPEC_EINVAL;
+  if (dtype != SPEC_BF16 && dtype != SPEC_F16 && dtype != SPEC_F32) return SPEC_EINVAL;
+  if ((k == nullptr) != (k_out == nullptr) || (k == nullptr) != (Hkv == 0)) return SPEC_EINVAL;
+  if (D % 16 || D > 2 * kMaxPairs || Hq > 4096 || Hkv > 4096 || T == INT32_MAX)
+    return SPEC_EUNSUPPORTED;
+  RotateParams p{};
+  const spec_status rc = rope_table(rope, D, &p.rope);
+  if (rc != SPEC_OK) return rc;
+  if (T == 0) return SPEC_OK;
+  if (!q || !q_out || !positions) return SPEC_EINVAL;
+  if (((uintptr_t)q | (uintptr_t)q_out | (uintptr_t)k | (uintptr_t)k_out) & 15) return SPEC_EINVAL;
+  if (q_stride < 0 || q_out_stride < 0 || k_stride < 0 || k_out_stride < 0) return SPEC_EINVAL;
+  const int es = dtype == SPEC_F32 ? 4 : 2;
+  if (((q_stride | q_out_stride | (k ? k_stride | k_out_stride : 0)) * es) & 15) return SPEC_EINVAL;
+  if ((q == q_out && q_stride != q_out_stride) || (k && k == k_out && k_stride != k_out_stride))
+    return SPEC_EINVAL;
+  p.q = static_cast<const char*>(q);
+  p.k = static_cast<const char*>(k);
+  p.q_out = static_cast<char*>(q_out);
+  p.k_out = static_cast<char*>(k_out);
+  p.pos = positions;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.q_out_stride = q_out_stride;
+  p.k_out_stride = k_out_stride;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.items = FastDiv(D / 16);
+  p.per = FastDiv((Hq + Hkv) * (D / 16));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == SPEC_F32) return launch_chained(rotate_kernel<float>, T, kThreads, 0, st, p);
+  if (dtype == SPEC_BF16)
+    return launch_chained(rotate_kernel<__nv_bfloat16>, T, kThreads, 0, st, p);
+  return launch_chained(rotate_kernel<__half>, T, kThreads, 0, st, p);
+}
