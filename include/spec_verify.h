@@ -739,7 +739,7 @@ spec_status spec_commit_scaled(void* k_cache, void* v_cache, float* k_scale, flo
  *
  * The result of a sequence may depend on the rest of the batch (by where the
  * cache is split) within rounding, and never on timing.
- * 1 <= R <= 64, D in {64,128,256}, Hkv * ceil(R * Hq / Hkv / 64) <= 4096; caches,
+ * 1 <= R <= 64, D in {64,128,256}, Hkv * ceil(R * Hq / Hkv / 64) <= 4096 (/ 32 for D = 256); caches,
  * strides and q 16-byte aligned; max_pages * page_size and B at most 2^31 - 513;
  * B * Hkv * (max_pages * page_size / 128 + 1) < 2^31.
  * ---------------------------------------------------------------------- */

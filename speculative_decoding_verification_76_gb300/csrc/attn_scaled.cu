@@ -32,7 +32,8 @@ bool make_plan(int B, int R, int Hq, int Hkv, int D, Plan* pl) {
     return false;
   const long long rows = (long long)R * (Hq / Hkv);
   if (rows > 64ll * 65535) return false;
-  pl->tiles = (int)((rows + 63) / 64);
+  const int most = scaled_attn::most_rows(D);
+  pl->tiles = (int)((rows + most - 1) / most);
   pl->rows_per_tile = (int)((rows + pl->tiles - 1) / pl->tiles);
   pl->rt = pl->rows_per_tile <= 16 ? 16 : pl->rows_per_tile <= 32 ? 32 : 64;
   pl->teams = std::max(1, num_sms() / pl->tiles);

@@ -43,12 +43,12 @@
 namespace scaled_attn {
 
 constexpr int kUnit = 128;                       // positions of a tile
-constexpr int kSoftWarps = 8, kSoft = 32 * kSoftWarps;
-constexpr int kMmaWarp = kSoftWarps, kCopyWarp0 = kMmaWarp + 1, kCopyWarps = 4;
+constexpr int kGroup = 128;                      // threads of a soft group: one per position
+constexpr int kSoftWarps = 8, kSoft = 2 * kGroup;
+constexpr int kScoreWarp = kSoftWarps, kSumWarp = kScoreWarp + 1;  // one thread each issues MMAs
+constexpr int kCopyWarp0 = kSumWarp + 1, kCopyWarps = 2;
 constexpr int kCopy = 32 * kCopyWarps;
 constexpr int kThreads = 32 * (kCopyWarp0 + kCopyWarps);
-constexpr float kTop = 8.f;                      // weights stay at or below 2^8 ...
-constexpr float kBelow = 2.f;                    // ... and begin at 2^2
 constexpr float kNone = -1e30f;                  // the reference of a row that has seen nothing
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -117,11 +117,11 @@ struct Walk {
 };
 
 // ---------------------------------------------------------------- tensor-core pieces
-// Shared-memory matrix descriptor with a layout type (0: none, 2: 128-byte, 4: 64-byte swizzle).
-SPEC_DEV uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint32_t layout) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
-         (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46 | (uint64_t)layout << 61;
-}
+// Shared-memory matrix descriptors as two words: the lower has the address / 16 (a step of n bytes adds
+// n / 16) and the leading byte offset / 16, the upper the stride byte offset / 16, the version and the
+// layout type (0: none, 2: 128-byte, 4: 64-byte swizzle).
+SPEC_DEV uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return saddr >> 4 | (lbo >> 4) << 16; }
+constexpr uint32_t desc_hi(uint32_t sbo, uint32_t layout) { return sbo >> 4 | 1u << 14 | layout << 29; }
 
 // kind::f8f6f4 with an e4m3 A and an fp32 accumulator; B e4m3 (0) or e5m2 (1).
 constexpr uint32_t idesc_f8(int M, int N, bool b_e5m2, bool mn_major) {
@@ -129,11 +129,26 @@ constexpr uint32_t idesc_f8(int M, int N, bool b_e5m2, bool mn_major) {
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-SPEC_DEV void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+SPEC_DEV void mma_f8(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                     uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " setp.ne.b32 p, %6, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// kind::f16 with fp16 operands, both with M / N contiguous, and an fp32 accumulator.
+constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (3u << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+SPEC_DEV void mma_f16(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                      uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " setp.ne.b32 p, %6, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -163,18 +178,20 @@ SPEC_DEV void tmem_st8(uint32_t addr, const uint32_t* r) {
                : "memory");
 }
 
-// A barrier of the soft warps that ORs a predicate.
-SPEC_DEV bool soft_any(bool x) {
+// Barrier `id` of n threads that ORs a predicate; the soft groups have 1 and 2, both together 3.
+SPEC_DEV bool any_of(int id, int n, bool x) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n"
       " selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"((uint32_t)x), "n"(kSoft)
+      : "r"((uint32_t)x), "r"(id), "r"(n)
       : "memory");
   return r != 0;
 }
-SPEC_DEV void soft_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kSoft) : "memory"); }
+SPEC_DEV void sync_of(int id, int n) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
 
 // Columns combined over a warp's lanes in about N shuffles: lane holds column (lane * N / 32 ...)
 // of the result, N = 8, 16 or 32; returns the column that this lane's result belongs to.
@@ -232,23 +249,33 @@ SPEC_DEV uint32_t nan_bytes(uint32_t w) {  // bit 7 of every byte that is a NaN 
 template <int D, int RT, bool F16>
 struct Shape {
   static constexpr int kRowBytes = D <= 128 ? D : 128;          // of a swizzled row
-  static constexpr int kHalves = D / kRowBytes;                 // column halves of a tile
   static constexpr uint32_t kLayout = D == 64 ? 4 : 2;
-  static constexpr uint32_t kGroup = 8 * kRowBytes;             // bytes of 8 rows
+  static constexpr uint32_t kRows8 = 8 * kRowBytes;             // bytes of 8 rows
   static constexpr int kTileBytes = kUnit * D;
   static constexpr int kParts = F16 ? 3 : 2;                    // of Q
+  // V as fp16, converted in shared memory, and the weights with it; else (no room at D = 256) V as it
+  // lies, and the weights as three 8-bit parts
+  static constexpr bool kHalfV = D <= 128;
+  static constexpr int kSums = kHalfV ? 1 : 3;                  // columns of O per row and 128 dimensions
+  static constexpr int kHalves = D == 256 ? 2 : 1;
+  static constexpr int kOCols = kSums * RT * kHalves;
+  // weights stay at or below 2^kTop and begin at 2^kBelow
+  static constexpr float kTop = kHalfV ? 15.f : 8.f, kBelow = kHalfV ? 8.f : 2.f;
+  // Q's parts as columns side by side, added up by the readers, where tensor memory has room: an
+  // MMA of 128 x N x 32 takes 61 cycles up to N = 96, and N / 2 above that
+  static constexpr bool kStack = 2 * kParts * RT + 2 * kOCols <= 512;
+  static constexpr int kSCols = kStack ? kParts * RT : RT;      // of a score buffer
   static constexpr int kStageBytes = 2 * kTileBytes + 1024;     // V, K, scales
   static constexpr int kQBytes = kParts * RT * D;
-  static constexpr int kPBytes = 3 * RT * kUnit;
-  static constexpr int kPBufs = D == 256 && RT == 64 ? 1 : 2;
-  static constexpr int kFixed = kQBytes + kPBufs * kPBytes + 1024;
+  static constexpr int kPBytes = kHalfV ? RT * kUnit * 2 : 3 * RT * kUnit;
+  static constexpr int kVBytes = kHalfV ? 2 * kTileBytes : 0;
+  static constexpr int kFixed = kQBytes + 2 * kPBytes + 2 * kVBytes + 1024;
   static constexpr int kRoom = 225 * 1024 - 8 * 1024 - kFixed;  // (static shared memory: < 8 KB)
   static constexpr int kStages = kRoom / kStageBytes < 8 ? kRoom / kStageBytes : 8;
   static_assert(kStages >= 2, "a ring needs two stages");
   static constexpr int kSmem = kFixed + kStages * kStageBytes;
-  static constexpr int kHalfCols = 3 * RT;                      // of O, per 128 dimensions
-  static constexpr int kColS = 0, kColO = 2 * RT;
-  static constexpr int kCols = kColO + kHalfCols * (D == 256 ? 2 : 1);
+  // tensor memory: a score buffer and an O for each soft group
+  static constexpr int kColO = 2 * kSCols, kCols = kColO + 2 * kOCols;
   static constexpr int kAlloc = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static_assert(kCols <= 512, "tensor memory");
 };
@@ -264,12 +291,14 @@ template <int D, int RT, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
     const __grid_constant__ Params p) {
   using S = Shape<D, RT, F16>;
-  constexpr int NC = RT / 2;  // columns of a soft warp
   constexpr int NS = S::kStages;
+  constexpr int kC = 16;  // columns that a soft thread works on at a time
   extern __shared__ uint8_t dyn[];
-  __shared__ __align__(8) uint64_t full[NS], empty[NS], s_full[2], p_full[2], pv_done[2], q_full, fin;
-  __shared__ __align__(16) float sc_s[RT], neg_m[RT], fac_s[RT], red[kSoftWarps][NC];
+  __shared__ __align__(8) uint64_t full[NS], empty[NS], s_full[2], p_full[2], pv_done[2], q_full, o_full, fin;
+  __shared__ __align__(16) float sc_s[RT], neg_m[2][RT], fac_s[2][RT], red[kSoftWarps][RT];
+  __shared__ __align__(16) float inv_s[RT];
   __shared__ uint64_t see_s[RT];
+  __shared__ long long out_s[RT];  // element of the row's output, or of its part's
   __shared__ int from_s[RT];
   __shared__ uint32_t nan_s[RT][D / 32];
   __shared__ Walk start;
@@ -278,9 +307,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int team = blockIdx.x / p.tiles, tile = blockIdx.x % p.tiles;
-  const uint32_t base = (smem_u32(dyn) + 1023u) & ~1023u;  // stages first: whole swizzle atoms
-  const uint32_t q_at = base + NS * S::kStageBytes;
-  uint8_t* const dyn0 = dyn + (base - smem_u32(dyn));
+  // fp16 V, the stages, Q, the weights: whole swizzle atoms
+  const uint32_t v16_at = (smem_u32(dyn) + 1023u) & ~1023u, base = v16_at + 2 * S::kVBytes;
+  const uint32_t q_at = base + NS * S::kStageBytes, p_at = q_at + S::kQBytes;
+  uint8_t* const v16_0 = dyn + (v16_at - smem_u32(dyn));
+  uint8_t* const dyn0 = v16_0 + 2 * S::kVBytes;
 
   chain_wait();
   // ---- this CTA's range, and the sequence it begins in: each thread sums consecutive sequences
@@ -318,18 +349,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
     if (threadIdx.x == 0) {
       for (int i = 0; i < NS; ++i) {
         mbar_init(&full[i], kCopy);
-        mbar_init(&empty[i], 1);
+        mbar_init(&empty[i], S::kHalfV ? kGroup : 1);
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&s_full[i], 1);
-        mbar_init(&p_full[i], kSoft);
+        mbar_init(&p_full[i], kGroup);
         mbar_init(&pv_done[i], 1);
       }
       mbar_init(&q_full, kSoft);
-      mbar_init(&fin, 1);
+      mbar_init(&o_full, 1);
+      mbar_init(&fin, 2);
       fence_mbar_init();
     }
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
       tmem_alloc(&tmem_base, S::kAlloc);
       tmem_relinquish();
     }
@@ -338,12 +370,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
     tc_fence_after();
   }
   const uint32_t tmem = tmem_base;
-  const uint32_t p_at = q_at + S::kQBytes;
 
   if (warp >= kCopyWarp0) {
     // ================================================================ copy warps
-    constexpr int L = D / 16, kRows = 32 / L;  // lanes of a row; rows of one instruction
-    const int pt = threadIdx.x - 32 * kCopyWarp0, w = pt >> 5;
+    // a lane copies chunks c and c + L of a row (L lanes of a row, 32 / L rows an instruction)
+    constexpr int L = D / 32, kRows = 32 / L;
+    constexpr int kMine = kUnit / kCopy;       // positions of a lane: 32 apart
+    const int w = warp - kCopyWarp0, first = w * 32 * kMine;
     const int sub = lane / L, chunk = lane % L;
     uint64_t pol;
     if (p.tiles == 1)  // the only reader of these rows
@@ -355,47 +388,63 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
     bool ok = true;
     for (Walk walk = start; walk.more() && ok; walk.next(p)) {
       const int n = walk.count();
-      int t = walk.seq.first + walk.first_unit() * kUnit + pt;
+      int t = walk.seq.first + walk.first_unit() * kUnit + first + lane;
       const int32_t* bt = p.table + (size_t)walk.b * p.max_pages;
       const char* kh = p.k + walk.kvh * p.head_stride;
       const char* vh = p.v + walk.kvh * p.head_stride;
-      int id = t < walk.seq.end ? bt[p.P.quot(t)] : -1;
+      int id[kMine];
+#pragma unroll
+      for (int m = 0; m < kMine; ++m)
+        id[m] = t + 32 * m < walk.seq.end ? bt[p.P.quot(t + 32 * m)] : -1;
 #pragma unroll 1
       for (int j = 0; j < n; ++j, ++g, t += kUnit) {
         const int stage = g % NS;
-        const int off = t - p.P.quot(t) * p.P.d;
-        const bool here = id >= 0 && id < p.num_pages;
-        const long long row = here ? id * p.page_stride + off * p.token_stride : -1;
-        const long long sc = here ? ((long long)id * nb + p.block.quot(off)) * p.Hkv + walk.kvh : 0;
-        const int tn = t + kUnit;
-        id = j + 1 < n && tn < walk.seq.end ? bt[p.P.quot(tn)] : -1;
+        long long row[kMine], sc[kMine];
+        uint32_t here[kMine];
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+          const int tm = t + 32 * m, off = tm - p.P.quot(tm) * p.P.d;
+          const bool ok_id = id[m] >= 0 && id[m] < p.num_pages;
+          here[m] = __ballot_sync(0xffffffffu, ok_id);
+          row[m] = ok_id ? id[m] * p.page_stride + off * p.token_stride : 0;
+          sc[m] = ((long long)id[m] * nb + p.block.quot(off)) * p.Hkv + walk.kvh;
+          const int tn = tm + kUnit;
+          id[m] = j + 1 < n && tn < walk.seq.end ? bt[p.P.quot(tn)] : -1;
+        }
         // (the warp as one: the shuffles below need every lane)
         if (g >= NS)
           ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], ((g / NS) - 1) & 1, p.err, p.wait_ns));
         if (!ok) break;
         const uint32_t v_at = base + stage * S::kStageBytes, k_at = v_at + S::kTileBytes;
 #pragma unroll
-        for (int i = 0; i < L; ++i) {
-          const int r = i * kRows + sub;
-          const long long from = __shfl_sync(0xffffffffu, row, r);
-          const uint32_t to = swizzled<D>(kUnit, w * 32 + r, chunk), bytes = from >= 0 ? 16u : 0u;
-          const long long at = (from >= 0 ? from : 0) + chunk * 16;
-          asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(
-                           k_at + to),
-                       "l"(kh + at), "r"(bytes), "l"(pol)
+        for (int m = 0; m < kMine; ++m) {
+#pragma unroll
+          for (int i = 0; i < L; ++i) {
+            const int r = i * kRows + sub;
+            const long long from = __shfl_sync(0xffffffffu, row[m], r) + chunk * 16;
+            const uint32_t bytes = here[m] >> r & 1 ? 16u : 0u;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t to = swizzled<D>(kUnit, first + 32 * m + r, chunk + x * L);
+              asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(
+                               k_at + to),
+                           "l"(kh + from + x * L * 16), "r"(bytes), "l"(pol)
+                           : "memory");
+              asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(
+                               v_at + to),
+                           "l"(vh + from + x * L * 16), "r"(bytes), "l"(pol)
+                           : "memory");
+            }
+          }
+          const uint32_t s_at = v_at + 2 * S::kTileBytes + (first + 32 * m + lane) * 4;
+          const bool mine = here[m] >> lane & 1;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_at),
+                       "l"(mine ? p.ks + sc[m] : &g_unseen)
                        : "memory");
-          asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(
-                           v_at + to),
-                       "l"(vh + at), "r"(bytes), "l"(pol)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_at + 512),
+                       "l"(mine ? p.vs + sc[m] : &g_unseen)
                        : "memory");
         }
-        const uint32_t s_at = v_at + 2 * S::kTileBytes + pt * 4;
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_at),
-                     "l"(here ? p.ks + sc : &g_unseen)
-                     : "memory");
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_at + 512),
-                     "l"(here ? p.vs + sc : &g_unseen)
-                     : "memory");
         if (g != p.withhold_stage)  // (a test can withhold one: its waiters time out)
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                            smem_u32(&full[stage]))
@@ -403,77 +452,111 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == kMmaWarp) {
-    // ================================================================ the MMA thread
+  } else if (warp == kScoreWarp) {
+    // ================================================================ the scores' MMA thread
     if (lane == 0) {
-      constexpr uint32_t kIdS = idesc_f8(128, RT, false, false);
-      constexpr uint32_t kIdP = idesc_f8(128, 2 * RT, false, true);
-      constexpr uint32_t kIdL = idesc_f8(128, RT, true, true);
+      constexpr uint32_t kId = idesc_f8(128, S::kSCols, false, false);
+      constexpr uint32_t kHi = desc_hi(S::kRows8, S::kLayout);
+      // (a part is RT rows: stacked parts are kParts * RT rows of one operand)
+      constexpr int kQRows = S::kStack ? S::kParts * RT : RT;
+      const uint32_t q_lo = desc_lo(q_at, 16);
       int g = 0, seg = 0;
       bool ok = true;
-      // O^T (+)= V^T W^T of unit u
-      auto pv = [&](int u, bool first) {
-        if (!mbar_wait(&p_full[u & 1], u >> 1 & 1, p.err, p.wait_ns)) return false;
-        tc_fence_after();
-        const uint32_t v_at = base + u % NS * S::kStageBytes;
-        const uint32_t w_at = p_at + (S::kPBufs == 2 ? u & 1 : 0) * S::kPBytes;
-#pragma unroll
-        for (int half = 0; half < (D == 256 ? 2 : 1); ++half)
-#pragma unroll
-          for (int k = 0; k < kUnit / 32; ++k) {
-            // (D = 64: the rows behind the tile's 64 are the K tile's, and are not used)
-            const uint64_t a = smem_desc(v_at + half * (kUnit * 128) + k * 4 * S::kGroup,
-                                         D == 64 ? S::kTileBytes : 16384, S::kGroup, S::kLayout);
-            const uint32_t d = tmem + S::kColO + half * S::kHalfCols;
-            const uint32_t acc = !first || k > 0;
-            mma_f8(d, a, smem_desc(w_at + k * 512, 128, 2048, 0), kIdP, acc);
-            mma_f8(d + 2 * RT, a, smem_desc(w_at + 2 * RT * kUnit + k * 512, 128, 2048, 0), kIdL, acc);
-          }
-        tc_commit(&empty[u % NS]);
-        tc_commit(&pv_done[u & 1]);
-        return true;
-      };
       for (Walk walk = start; walk.more() && ok; walk.next(p), ++seg) {
         const int n = walk.count();
         if (!mbar_wait(&q_full, seg & 1, p.err, p.wait_ns)) break;
 #pragma unroll 1
-        for (int j = 0; j < n && ok; ++j, ++g) {
+        for (int j = 0; j < n; ++j, ++g) {
           const int stage = g % NS;
+          // the score buffer's last tile has been read, this tile has landed
+          if (g >= 2 && !(ok = mbar_wait(&p_full[g & 1], (g - 2) >> 1 & 1, p.err, p.wait_ns))) break;
           if (!(ok = mbar_wait(&full[stage], (g / NS) & 1, p.err, p.wait_ns))) break;
           fence_proxy_async();  // the copies' writes, for the tensor cores
           tc_fence_after();
-          const uint32_t k_at = base + stage * S::kStageBytes + S::kTileBytes;
+          const uint32_t k_lo = desc_lo(base + stage * S::kStageBytes + S::kTileBytes, 16);
+          const uint32_t d = tmem + (g & 1) * S::kSCols;
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) {
-            const uint32_t in = D == 64 ? k * 32 : (k & 3) * 32;
-            const uint64_t a = smem_desc(k_at + (k >> 2) * (kUnit * 128) + in, 16, S::kGroup, S::kLayout);
+            constexpr int kIn = D == 64 ? 2 : 4;  // steps within a swizzled row
 #pragma unroll
-            for (int part = 0; part < S::kParts; ++part)
-              mma_f8(tmem + S::kColS + (g & 1) * RT, a,
-                     smem_desc(q_at + part * RT * D + (k >> 2) * (RT * 128) + in, 16, S::kGroup,
-                               S::kLayout),
-                     kIdS, k > 0 || part > 0);
+            for (int part = 0; part < (S::kStack ? 1 : S::kParts); ++part)
+              mma_f8(d, k_lo + ((k / kIn) * (kUnit * 128) + k % kIn * 32) / 16, kHi,
+                     q_lo + (part * RT * D + (k / kIn) * (kQRows * 128) + k % kIn * 32) / 16, kHi, kId,
+                     k > 0 || part > 0);
           }
           tc_commit(&s_full[g & 1]);
-          if (j > 0) ok = pv(g - 1, j == 1);
         }
-        if (ok) ok = pv(g - 1, n == 1);
       }
       // nothing of this thread's is in flight when the tensor memory goes
       tc_commit(&fin);
       mbar_wait(&fin, 0, nullptr);
     }
     __syncwarp();
+  } else if (warp == kSumWarp) {
+    // ================================================================ O^T += V^T W^T
+    if (lane == 0) {
+      constexpr uint32_t kHi = desc_hi(S::kRows8, S::kLayout), kHiW = desc_hi(2048, 0);
+      int g = 0;
+      bool ok = true;
+      for (Walk walk = start; walk.more() && ok; walk.next(p)) {
+        const int n = walk.count();
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++g) {
+          const int stage = g % NS;
+          if constexpr (!S::kHalfV) ok = mbar_wait(&full[stage], (g / NS) & 1, p.err, p.wait_ns);
+          ok = ok && mbar_wait(&p_full[g & 1], g >> 1 & 1, p.err, p.wait_ns);
+          if (!ok) break;
+          if constexpr (!S::kHalfV) fence_proxy_async();
+          tc_fence_after();
+          const uint32_t w_lo = desc_lo(p_at + (g & 1) * S::kPBytes, 128);
+          const uint32_t o = tmem + S::kColO + (g & 1) * S::kOCols;
+          const uint32_t later = j >= 2;  // this group's O holds something
+          if constexpr (S::kHalfV) {
+            // (D = 64: rows 64 .. 127 are what lies behind the tile, and are not used)
+            constexpr uint32_t kId = idesc_f16(128, RT), kHiV = desc_hi(1024, 2);
+            const uint32_t v_lo = desc_lo(v16_at + (g & 1) * S::kVBytes, kUnit * 128);
+#pragma unroll
+            for (int k = 0; k < kUnit / 16; ++k)
+              mma_f16(o, v_lo + k * 2048 / 16, kHiV, w_lo + k * 256 / 16, kHiW, kId, k > 0 ? 1u : later);
+          } else {
+            constexpr uint32_t kIdP = idesc_f8(128, 2 * RT, false, true);
+            constexpr uint32_t kIdL = idesc_f8(128, RT, true, true);
+            const uint32_t v_lo = desc_lo(base + stage * S::kStageBytes, 16384);
+#pragma unroll
+            for (int half = 0; half < S::kHalves; ++half)
+#pragma unroll
+              for (int k = 0; k < kUnit / 32; ++k) {
+                const uint32_t a = v_lo + (half * (kUnit * 128) + k * 4 * S::kRows8) / 16;
+                const uint32_t d = o + half * 3 * RT;
+                mma_f8(d, a, kHi, w_lo + k * 512 / 16, kHiW, kIdP, k > 0 ? 1u : later);
+                mma_f8(d + 2 * RT, a, kHi, w_lo + (2 * RT * kUnit + k * 512) / 16, kHiW, kIdL,
+                       k > 0 ? 1u : later);
+              }
+            tc_commit(&empty[stage]);
+          }
+          tc_commit(&pv_done[g & 1]);
+        }
+        if (ok) tc_commit(&o_full);
+      }
+      tc_commit(&fin);
+      mbar_wait(&fin, 0, nullptr);
+    }
+    __syncwarp();
   } else {
     // ================================================================ scores into weights
-    const int side = warp >> 2, c0 = side * NC;  // this warp's columns c0 .. c0 + NC - 1
+    // Two groups of four warps take the tiles in turn, each with references, sums and an O of its
+    // own: one tile's chain of waits lies under the other's work.
+    const int group = warp >> 2, bar = 1 + group;
     const int tok = (warp & 3) * 32 + lane;      // a position of the tile, a dimension of O
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
     const int rows = min(p.rows_per_tile, p.R * p.G - tile * p.rows_per_tile);
+    const int range0 = start.s;
     int g = 0, seg = 0;
     bool ok = true;
     for (Walk walk = start; walk.more(); walk.next(p), ++seg) {
       const int b = walk.b, n_units = walk.count(), ctx = walk.seq.ctx;
+      const bool whole = n_units == walk.seq.units;
+      const int part = (team * 2 + (walk.s == range0 ? 0 : 1)) * p.tiles + tile;
       // ---- Q as sums of e4m3 parts under a power of two per row
       {
         constexpr int kPer = kSoft / RT;  // threads of a row
@@ -483,9 +566,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         const uint4* src = reinterpret_cast<const uint4*>(
             p.q + (b * p.q_stride_b + (real ? i : 0) * p.q_stride_r +
                    (walk.kvh * p.G + (real ? row - i * p.G : 0)) * p.q_stride_h) * 2);
-        auto values = [&](int c, float* x) {
-          const uint4 w = real ? src[c] : make_uint4(0, 0, 0, 0);
-          const uint32_t* u = reinterpret_cast<const uint32_t*>(&w);
+        constexpr int kMine = D / 8 / kPer > 0 ? D / 8 / kPer : 1;  // 16-byte chunks of a thread
+        uint4 raw[kMine];
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+          const int c = x0 + m * kPer;
+          raw[m] = real && c < D / 8 ? src[c] : make_uint4(0, 0, 0, 0);
+        }
+        auto values = [&](int m, float* x) {
+          const uint32_t* u = reinterpret_cast<const uint32_t*>(&raw[m]);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if constexpr (F16) {
@@ -499,10 +588,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         };
         float big = 0.f;
         bool bad = false;
-#pragma unroll 1
-        for (int c = x0; c < D / 8; c += kPer) {
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
           float x[8];
-          values(c, x);
+          values(m, x);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             big = fmaxf(big, finite_abs(x[e]));
@@ -515,18 +604,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
           bad = __shfl_xor_sync(0xffffffffu, (int)bad, o) || bad;
         }
         const float s = needed_scale(big), down = 1.f / s;
-#pragma unroll 1
-        for (int c = x0; c < D / 8; c += kPer) {
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+          const int c = x0 + m * kPer;
+          if (c >= D / 8) break;
           float x[8];
-          values(c, x);
+          values(m, x);
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] *= down;
-          const uint32_t to = q_at - base + swizzled<D>(RT, n, c >> 1) + (c & 1) * 8;
 #pragma unroll
           for (int part = 0; part < S::kParts; ++part) {
+            const uint32_t to =
+                S::kStack ? swizzled<D>(S::kParts * RT, part * RT + n, c >> 1)
+                          : part * RT * D + swizzled<D>(RT, n, c >> 1);
             const uint2 w = make_uint2(e4m3_word(x[0], x[1], x[2], x[3]),
                                        e4m3_word(x[4], x[5], x[6], x[7]));
-            *reinterpret_cast<uint2*>(dyn0 + to + part * RT * D) = w;
+            *reinterpret_cast<uint2*>(dyn0 + (q_at - base) + to + (c & 1) * 8) = w;
             float y[8];
             e4m3_values(w.x, y);
             e4m3_values(w.y, y + 4);
@@ -536,13 +629,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         }
         if (x0 == 0) {
           sc_s[n] = bad ? NAN : real ? p.scale_log2 * s : 0.f;
-          neg_m[n] = -kNone;
+          neg_m[0][n] = neg_m[1][n] = -kNone;
           uint64_t m = 0;
           if (real) {
             m = p.mask ? p.mask[(size_t)b * p.R + i] : i >= 63 ? ~0ull : (2ull << i) - 1;
             if (p.R < 64) m &= (1ull << p.R) - 1;
           }
           see_s[n] = m;
+          out_s[n] = whole ? ((long long)b * p.R + i) * p.Hq + walk.kvh * p.G + row - i * p.G
+                           : (long long)part * RT + n;
           from_s[n] = p.window > 0 ? ctx + __popcll(m) - p.window : 0;
 #pragma unroll
           for (int e = 0; e < D / 32; ++e) nan_s[n][e] = 0;
@@ -551,236 +646,291 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         fence_proxy_async();
         mbar_arrive(&q_full);
       }
-      soft_sync();
+      sync_of(3, kSoft);
 
-      uint64_t l2[NC / 2];
+      uint64_t l2[RT / 2];
 #pragma unroll
-      for (int i = 0; i < NC / 2; ++i) l2[i] = 0ull;
-      int t0 = walk.seq.first + walk.first_unit() * kUnit;
+      for (int i = 0; i < RT / 2; ++i) l2[i] = 0ull;
+      bool begun = false;  // this group's O holds something
+      const int t_seg = walk.seq.first + walk.first_unit() * kUnit;
 #pragma unroll 1
-      for (int j = 0; j < n_units; ++j, ++g, t0 += kUnit) {
-        const int stage = g % NS;
-        ok = ok && mbar_wait(&full[stage], (g / NS) & 1, p.err, p.wait_ns) &&
-             mbar_wait(&s_full[g & 1], g >> 1 & 1, p.err, p.wait_ns);
-        tc_fence_after();
-        uint32_t s[NC];
-        tmem_ld<NC>(lanes + S::kColS + (g & 1) * RT + c0, s);
+      for (int j = (g ^ group) & 1; j < n_units; j += 2) {
+        const int u = g + j, stage = u % NS, t0 = t_seg + j * kUnit;
+        ok = ok && mbar_wait(&full[stage], (u / NS) & 1, p.err, p.wait_ns);
         const float* scales =
             reinterpret_cast<const float*>(dyn0 + stage * S::kStageBytes + 2 * S::kTileBytes);
         float ks = scales[tok], vs = scales[kUnit + tok];
         const bool here = ks != -INFINITY;
         vs = !here ? 1.f : vs < 0x1p-100f ? 0x1p-100f : vs;
         ks = here ? ks : 0.f;
-        const float lvs = here ? log2f(vs) : -INFINITY, rvs = here ? 1.f / vs : 0.f;
+        const float lvs = here ? __log2f(vs) : -INFINITY, rvs = here ? __fdividef(1.f, vs) : 0.f;
         // positions that some rows see and others do not
         const bool mixed = (t0 + kUnit > ctx && (p.R > 1 || p.mask)) ||
                            (p.window > 0 && t0 < ctx + p.R - p.window);
-        uint32_t see = 0xffffffffu;  // columns that see this thread's position
+        uint64_t see = ~0ull;  // columns that see this thread's position
         if (mixed) {
           const int t = t0 + tok, jb = t - ctx;
           see = 0;
 #pragma unroll 1
-          for (int c = 0; c < NC; ++c)
-            if (jb < 0 ? t >= from_s[c0 + c] : jb < 64 && (see_s[c0 + c] >> jb & 1)) see |= 1u << c;
-          // NaN codes of V: noted for the rows that see them, then zeroed
-          uint8_t* vrow = dyn0 + stage * S::kStageBytes;
-          bool nan = false;
+          for (int c = 0; c < RT; ++c)
+            if (jb < 0 ? t >= from_s[c] : jb < 64 && (see_s[c] >> jb & 1)) see |= 1ull << c;
+        }
+        // the group's last product is complete: its O and its operands' buffers are free
+        if (u >= 2) ok = ok && mbar_wait(&pv_done[group], (u - 2) >> 1 & 1, p.err, p.wait_ns);
+        uint8_t* vrow = dyn0 + stage * S::kStageBytes;
+        if (mixed) {  // NaN codes of V: noted for the rows that see them, and zeroed
 #pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
-            const uint4 w = *reinterpret_cast<const uint4*>(vrow + swizzled<D>(kUnit, tok, c));
-            if (nan_bytes(w.x) | nan_bytes(w.y) | nan_bytes(w.z) | nan_bytes(w.w)) {
-              nan = true;
-              const uint32_t* u = reinterpret_cast<const uint32_t*>(&w);
+            uint32_t* u4 = reinterpret_cast<uint32_t*>(vrow + swizzled<D>(kUnit, tok, c));
+            if (nan_bytes(u4[0]) | nan_bytes(u4[1]) | nan_bytes(u4[2]) | nan_bytes(u4[3])) {
               uint32_t bits = 0;
-              for (int e = 0; e < 16; ++e) bits |= (nan_bytes(u[e >> 2]) >> (8 * (e & 3) + 7) & 1) << e;
-              for (int x = 0; x < NC; ++x)
-                if (see >> x & 1) atomicOr(&nan_s[c0 + x][c >> 1], bits << 16 * (c & 1));
-            }
-          }
-          if (nan) any_nan = 1;
-          soft_sync();
-          if (nan && side == 0) {
-            for (int c = 0; c < D / 16; ++c) {
-              uint4* w = reinterpret_cast<uint4*>(vrow + swizzled<D>(kUnit, tok, c));
-              uint32_t* u = reinterpret_cast<uint32_t*>(w);
-              for (int e = 0; e < 4; ++e) u[e] &= ~((nan_bytes(u[e]) >> 7) * 255u);
+              for (int e = 0; e < 16; ++e) bits |= (nan_bytes(u4[e >> 2]) >> (8 * (e & 3) + 7) & 1) << e;
+              for (int x = 0; x < RT; ++x)
+                if (see >> x & 1) atomicOr(&nan_s[x][c >> 1], bits << 16 * (c & 1));
+              for (int e = 0; e < 4; ++e) u4[e] &= ~((nan_bytes(u4[e]) >> 7) * 255u);
+              any_nan = 1;
             }
           }
         }
-        tmem_wait_ld();
-        // ---- exponents, relative to the rows' references
-        const uint64_t ks2 = f2_pack(ks, ks), lvs2 = f2_pack(lvs, lvs);
-        const uint64_t* sc2 = reinterpret_cast<const uint64_t*>(sc_s + c0);
-        const uint64_t* nm2 = reinterpret_cast<const uint64_t*>(neg_m + c0);
-        float a[NC];
-        auto exponents = [&]() {
-          float top = -INFINITY;
+        if constexpr (S::kHalfV) {  // this position's V as fp16, 64 dimensions a row
+          uint8_t* to = v16_0 + group * S::kVBytes + tok * 128;
 #pragma unroll
-          for (int i = 0; i < NC / 2; ++i) {
+          for (int c = 0; c < D / 16; ++c) {
+            const uint4 w = *reinterpret_cast<const uint4*>(vrow + swizzled<D>(kUnit, tok, c));
+            uint4 h0, h1;
+            h0.x = halves_of(w.x), h0.y = halves_of(w.x >> 16);
+            h0.z = halves_of(w.y), h0.w = halves_of(w.y >> 16);
+            h1.x = halves_of(w.z), h1.y = halves_of(w.z >> 16);
+            h1.z = halves_of(w.w), h1.w = halves_of(w.w >> 16);
+            uint8_t* half = to + (c >> 2) * (kUnit * 128);
+            const int c16 = 2 * (c & 3);
+            *reinterpret_cast<uint4*>(half + ((c16 ^ (tok & 7)) << 4)) = h0;
+            *reinterpret_cast<uint4*>(half + (((c16 + 1) ^ (tok & 7)) << 4)) = h1;
+          }
+        }
+        ok = ok && mbar_wait(&s_full[group], u >> 1 & 1, p.err, p.wait_ns);
+        tc_fence_after();
+        // ---- exponents of kC columns, relative to the rows' references
+        const uint64_t ks2 = f2_pack(ks, ks), lvs2 = f2_pack(lvs, lvs);
+        const uint32_t s_at = lanes + group * S::kSCols;
+        auto scores = [&](int c, uint32_t* s) {
+          tmem_ld<kC>(s_at + c, s);
+          if constexpr (S::kStack) {
+            uint32_t y[S::kParts - 1][kC];
+#pragma unroll
+            for (int part = 1; part < S::kParts; ++part) tmem_ld<kC>(s_at + part * RT + c, y[part - 1]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int part = 1; part < S::kParts; ++part)
+#pragma unroll
+              for (int i = 0; i < kC; ++i)
+                s[i] = __float_as_uint(__uint_as_float(s[i]) + __uint_as_float(y[part - 1][i]));
+          } else {
+            tmem_wait_ld();
+          }
+        };
+        auto exponents = [&](int c, const uint32_t* s, float* a) {
+          float top = -INFINITY;
+          const uint64_t* sc2 = reinterpret_cast<const uint64_t*>(sc_s + c);
+          const uint64_t* nm2 = reinterpret_cast<const uint64_t*>(neg_m[group] + c);
+#pragma unroll
+          for (int i = 0; i < kC / 2; ++i) {
             const uint64_t x =
                 f2_mul(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2[i]);
             f2_unpack(f2_fma(x, ks2, f2_add(lvs2, nm2[i])), a[2 * i], a[2 * i + 1]);
             if (mixed) {
-              a[2 * i] = see >> (2 * i) & 1 ? a[2 * i] : -INFINITY;
-              a[2 * i + 1] = see >> (2 * i + 1) & 1 ? a[2 * i + 1] : -INFINITY;
+              a[2 * i] = see >> (c + 2 * i) & 1 ? a[2 * i] : -INFINITY;
+              a[2 * i + 1] = see >> (c + 2 * i + 1) & 1 ? a[2 * i + 1] : -INFINITY;
             }
             top = fmax3(top, a[2 * i], a[2 * i + 1]);
           }
           return top;
         };
-        const float top = exponents();
-        if (soft_any(top > kTop || !ok)) {
-          if (soft_any(!ok)) break;  // (the same for all: everyone leaves the tile loop)
-          // ---- the references move: maxima over the tile's positions
-          float x[NC];
-#pragma unroll
-          for (int i = 0; i < NC; ++i) {
-            x[i] = __uint_as_float(s[i]) * sc_s[c0 + i] * ks + lvs;
-            if (mixed && !(see >> i & 1)) x[i] = -INFINITY;
-          }
-          int col;
-          const float m = over_lanes<NC>(x, lane, [](float u, float v) { return fmaxf(u, v); }, &col);
-          red[warp][col] = m;
-          soft_sync();
-          if (threadIdx.x < RT) {
-            const int n = threadIdx.x, w0 = n / NC * 4, c = n % NC;
-            float m4 = fmaxf(fmaxf(red[w0][c], red[w0 + 1][c]), fmaxf(red[w0 + 2][c], red[w0 + 3][c]));
-            const float old = -neg_m[n], now = m4 - old > kTop ? m4 - kBelow : old;
-            fac_s[n] = fast_exp2(old - now);
-            neg_m[n] = -now;
-          }
-          soft_sync();
-#pragma unroll
-          for (int i = 0; i < NC / 2; ++i)
-            l2[i] = f2_mul(l2[i], reinterpret_cast<const uint64_t*>(fac_s + c0)[i]);
-          if (j > 0) {
-            ok = mbar_wait(&pv_done[(g - 1) & 1], (g - 1) >> 1 & 1, p.err, p.wait_ns);
-            tc_fence_after();
+        // (K has been read, V and the scales have been taken over)
+        if constexpr (S::kHalfV) mbar_arrive(&empty[stage]);
+        // ---- weights and their sums; once more where a weight has passed 2^kTop
+        const uint64_t rvs2 = f2_pack(rvs, rvs);
+        uint8_t* w_at = dyn0 + (p_at - base) + group * S::kPBytes + tok * 16;
+        bool failed = false;
 #pragma unroll 1
-            for (int part = 0; part < (D == 256 ? 6 : 3); ++part)
+        for (int pass = begun ? 0 : 1;; ++pass) {
+          if (pass) {
+            // ---- the references move: maxima over the tile's positions
 #pragma unroll
-              for (int c = 0; c < NC; c += 8) {
-                const uint32_t at = lanes + S::kColO + part * RT + c0 + c;
+            for (int c = 0; c < RT; c += kC) {
+              uint32_t s[kC];
+              float x[kC];
+              scores(c, s);
+#pragma unroll
+              for (int i = 0; i < kC; ++i) {
+                x[i] = __uint_as_float(s[i]) * sc_s[c + i] * ks + lvs;
+                if (mixed && !(see >> (c + i) & 1)) x[i] = -INFINITY;
+              }
+              int col;
+              const float m = over_lanes<kC>(x, lane, [](float u, float v) { return fmaxf(u, v); }, &col);
+              red[warp][c + col] = m;
+            }
+            sync_of(bar, kGroup);
+            if (tok < RT) {
+              const int w0 = group * 4;
+              const float m4 = fmaxf(fmaxf(red[w0][tok], red[w0 + 1][tok]),
+                                     fmaxf(red[w0 + 2][tok], red[w0 + 3][tok]));
+              const float old = -neg_m[group][tok], now = m4 - old > S::kTop ? m4 - S::kBelow : old;
+              fac_s[group][tok] = fast_exp2(old - now);
+              neg_m[group][tok] = -now;
+            }
+            sync_of(bar, kGroup);
+            const float* fac = fac_s[group];
+#pragma unroll
+            for (int i = 0; i < RT / 2; ++i)
+              l2[i] = f2_mul(l2[i], reinterpret_cast<const uint64_t*>(fac)[i]);
+            if (begun) {
+#pragma unroll 1
+              for (int c = 0; c < S::kOCols; c += 8) {
+                const uint32_t at = lanes + S::kColO + group * S::kOCols + c;
                 uint32_t o[8];
                 tmem_ld<8>(at, o);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                  o[e] = __float_as_uint(__uint_as_float(o[e]) * fac_s[c0 + c + e]);
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) * fac[c % RT + e]);
                 tmem_st8(at, o);
               }
-            tmem_wait_st();
-          }
-          exponents();
-        }
-        // ---- weights, their sums, and their three parts
-        if constexpr (S::kPBufs == 1)
-          if (j > 0)
-            ok = ok && mbar_wait(&pv_done[(g - 1) & 1], (g - 1) >> 1 & 1, p.err, p.wait_ns);
-        const uint64_t rvs2 = f2_pack(rvs, rvs);
-        uint8_t* w_at = dyn0 + (p_at - base) + (S::kPBufs == 2 ? g & 1 : 0) * S::kPBytes +
-                        (c0 >> 4) * 2048 + tok * 16 + (c0 & 15);
-#pragma unroll
-        for (int c = 0; c < NC; c += 8) {
-          uint32_t p1[2], p2[2], p3[2];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int i = c + 2 * e;
-            const float w0 = fast_exp2(a[i]), w1 = fast_exp2(a[i + 1]);
-            l2[i / 2] = f2_fma(f2_pack(w0, w1), rvs2, l2[i / 2]);
-            const uint32_t h = f16x2(w0, w1), x1 = e4m3x2(h);
-            const uint32_t r1 = sub_mul(h, halves_of(x1), 0x4c004c00u);   // times 2^4
-            const uint32_t x2 = e4m3x2(r1);
-            const uint32_t x3 = e5m2x2(sub_mul(r1, halves_of(x2), 0x68006800u));  // times 2^11
-            if (e & 1) {
-              p1[e >> 1] |= x1 << 16, p2[e >> 1] |= x2 << 16, p3[e >> 1] |= x3 << 16;
-            } else {
-              p1[e >> 1] = x1, p2[e >> 1] = x2, p3[e >> 1] = x3;
+              tmem_wait_st();
             }
           }
-          uint8_t* to = w_at + (c >> 4) * 2048 + (c & 15);
-          *reinterpret_cast<uint2*>(to) = make_uint2(p1[0], p1[1]);
-          *reinterpret_cast<uint2*>(to + RT * kUnit) = make_uint2(p2[0], p2[1]);
-          *reinterpret_cast<uint2*>(to + 2 * RT * kUnit) = make_uint2(p3[0], p3[1]);
+          float top = -INFINITY;
+          uint64_t t2[RT / 2];  // sums with this tile
+#pragma unroll
+          for (int c = 0; c < RT; c += kC) {
+            uint32_t s[kC];
+            float a[kC];
+            scores(c, s);
+            top = fmaxf(top, exponents(c, s, a));
+            if constexpr (S::kHalfV) {
+              uint32_t h[kC / 2];
+#pragma unroll
+              for (int e = 0; e < kC / 2; ++e) {
+                const float w0 = fast_exp2(a[2 * e]), w1 = fast_exp2(a[2 * e + 1]);
+                t2[c / 2 + e] = f2_fma(f2_pack(w0, w1), rvs2, l2[c / 2 + e]);
+                h[e] = f16x2(w0, w1);
+              }
+#pragma unroll
+              for (int x = 0; x < kC / 8; ++x)
+                *reinterpret_cast<uint4*>(w_at + (c / 8 + x) * 2048) =
+                    make_uint4(h[4 * x], h[4 * x + 1], h[4 * x + 2], h[4 * x + 3]);
+            } else {
+              uint32_t p1[4], p2[4], p3[4];
+#pragma unroll
+              for (int e = 0; e < kC / 2; ++e) {
+                const float w0 = fast_exp2(a[2 * e]), w1 = fast_exp2(a[2 * e + 1]);
+                t2[c / 2 + e] = f2_fma(f2_pack(w0, w1), rvs2, l2[c / 2 + e]);
+                const uint32_t h = f16x2(w0, w1), x1 = e4m3x2(h);
+                const uint32_t r1 = sub_mul(h, halves_of(x1), 0x4c004c00u);   // times 2^4
+                const uint32_t x2 = e4m3x2(r1);
+                const uint32_t x3 = e5m2x2(sub_mul(r1, halves_of(x2), 0x68006800u));  // times 2^11
+                if (e & 1) {
+                  p1[e >> 1] |= x1 << 16, p2[e >> 1] |= x2 << 16, p3[e >> 1] |= x3 << 16;
+                } else {
+                  p1[e >> 1] = x1, p2[e >> 1] = x2, p3[e >> 1] = x3;
+                }
+              }
+              uint8_t* to = w_at + (c >> 4) * 2048;
+              *reinterpret_cast<uint4*>(to) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+              *reinterpret_cast<uint4*>(to + RT * kUnit) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+              *reinterpret_cast<uint4*>(to + 2 * RT * kUnit) = make_uint4(p3[0], p3[1], p3[2], p3[3]);
+            }
+          }
+          if (pass || !any_of(bar, kGroup, top > S::kTop || !ok)) {
+#pragma unroll
+            for (int i = 0; i < RT / 2; ++i) l2[i] = t2[i];
+            break;
+          }
+          if ((failed = any_of(bar, kGroup, !ok))) break;  // (the same for all of the group)
         }
+        if (failed) break;
+        begun = true;
         fence_proxy_async();
         tc_fence_before();
-        mbar_arrive(&p_full[g & 1]);
+        mbar_arrive(&p_full[group]);
       }
-      // ---- the segment's sums and outputs
-      ok = ok && mbar_wait(&pv_done[(g - 1) & 1], (g - 1) >> 1 & 1, p.err, p.wait_ns);
-      if (soft_any(!ok)) break;
+      g += n_units;
+      // ---- the segment's sums and outputs: the groups' states meet
+      ok = ok && mbar_wait(&o_full, seg & 1, p.err, p.wait_ns);
+      if (any_of(3, kSoft, !ok)) break;
       tc_fence_after();
-      {
-        float l[NC];
 #pragma unroll
-        for (int i = 0; i < NC / 2; ++i) f2_unpack(l2[i], l[2 * i], l[2 * i + 1]);
+      for (int c = 0; c < RT; c += kC) {
+        float l[kC];
+#pragma unroll
+        for (int i = 0; i < kC / 2; ++i) f2_unpack(l2[c / 2 + i], l[2 * i], l[2 * i + 1]);
         int col;
-        const float sum = over_lanes<NC>(l, lane, [](float u, float v) { return u + v; }, &col);
-        red[warp][col] = sum;
+        const float sum = over_lanes<kC>(l, lane, [](float u, float v) { return u + v; }, &col);
+        red[warp][c + col] = sum;
       }
-      soft_sync();
-      const Ranges ranges(walk.W * p.Hkv, p.teams);
-      const bool whole = n_units == walk.seq.units;
-      const size_t part = ((size_t)team * 2 + (walk.s == ranges.begin(team) ? 0 : 1)) * p.tiles + tile;
+      sync_of(3, kSoft);
+      if (threadIdx.x < RT) {  // weights of the two groups' states, the row's reference and sum
+        const int n = threadIdx.x;
+        const float m0 = -neg_m[0][n], m1 = -neg_m[1][n], m = fmaxf(m0, m1);
+        const float la = (red[0][n] + red[1][n]) + (red[2][n] + red[3][n]);
+        const float lb = (red[4][n] + red[5][n]) + (red[6][n] + red[7][n]);
+        // (a state without weights holds nothing, or what was there before it)
+        const float f0 = la == 0.f ? 0.f : fast_exp2(m0 - m), f1 = lb == 0.f ? 0.f : fast_exp2(m1 - m);
+        const float l = (la == 0.f ? 0.f : la * f0) + (lb == 0.f ? 0.f : lb * f1);
+        fac_s[0][n] = f0;
+        fac_s[1][n] = f1;
+        inv_s[n] = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        if (n < rows) {
+          if (!whole)
+            *reinterpret_cast<float2*>(p.part_ml + out_s[n] * 2) = make_float2(m, l);
+          else if (p.lse)
+            p.lse[out_s[n]] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        }
+      }
+      sync_of(3, kSoft);
 #pragma unroll 1
-      for (int c = 0; c < NC; c += 8) {
-        if (c0 + c >= rows) break;
-        float l8[8];
+      for (int c = group * 8; c < rows; c += 16) {  // (a group takes every other eight rows)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          l8[e] = (red[side * 4][c + e] + red[side * 4 + 1][c + e]) +
-                  (red[side * 4 + 2][c + e] + red[side * 4 + 3][c + e]);
+        for (int half = 0; half < S::kHalves; ++half) {
+          uint32_t o[2][S::kSums][8];
 #pragma unroll
-        for (int half = 0; half < (D == 256 ? 2 : 1); ++half) {
-          uint32_t o1[8], o2[8], o3[8];
-          const uint32_t at = lanes + S::kColO + half * S::kHalfCols + c0 + c;
-          tmem_ld<8>(at, o1);
-          tmem_ld<8>(at + RT, o2);
-          tmem_ld<8>(at + 2 * RT, o3);
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int y = 0; y < S::kSums; ++y)
+              tmem_ld<8>(lanes + S::kColO + x * S::kOCols + (half * S::kSums + y) * RT + c, o[x][y]);
           tmem_wait_ld();
           const int d = half * 128 + tok;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int n = c0 + c + e;
+            const int n = c + e;
             if (n >= rows || d >= D) continue;
-            float y = __uint_as_float(o1[e]) +
-                      (__uint_as_float(o2[e]) * 0x1p-4f + __uint_as_float(o3[e]) * 0x1p-15f);
-            if (any_nan && nan_s[n][d >> 5] >> (d & 31) & 1) y = NAN;
-            if (whole) {
-              const int row = tile * p.rows_per_tile + n, i = row / p.G;
-              const size_t to = (((size_t)b * p.R + i) * p.Hq + walk.kvh * p.G + row - i * p.G) * D + d;
-              y = l8[e] == 0.f ? 0.f : y / l8[e];
-              if constexpr (F16) reinterpret_cast<__half*>(p.out)[to] = __float2half_rn(y);
-              else reinterpret_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(y);
-            } else {
-              p.part_o[(part * RT + n) * D + d] = y;
-            }
-          }
-        }
-        if (tok < 8 && c0 + c + tok < rows) {
-          const int n = c0 + c + tok;
-          float lx = 0.f;
+            float y = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) lx = e == tok ? l8[e] : lx;
-          const float m = -neg_m[n];
-          if (!whole) {
-            *reinterpret_cast<float2*>(p.part_ml + (part * RT + n) * 2) = make_float2(m, lx);
-          } else if (p.lse) {
-            const int row = tile * p.rows_per_tile + n, i = row / p.G;
-            p.lse[((size_t)b * p.R + i) * p.Hq + walk.kvh * p.G + row - i * p.G] =
-                lx == 0.f ? -INFINITY : (m + log2f(lx)) * kLn2;
+            for (int x = 0; x < 2; ++x) {
+              float z = __uint_as_float(o[x][0][e]);
+              if constexpr (!S::kHalfV)
+                z += __uint_as_float(o[x][1][e]) * 0x1p-4f + __uint_as_float(o[x][2][e]) * 0x1p-15f;
+              const float f = fac_s[x][n];
+              y += f == 0.f ? 0.f : f * z;
+            }
+            if (any_nan && nan_s[n][d >> 5] >> (d & 31) & 1) y = NAN;
+            const float inv = inv_s[n];
+            y = inv == 0.f ? 0.f : y * inv;
+            const long long to = out_s[n] * D + d;
+            if (!whole) p.part_o[to] = y;
+            else if constexpr (F16) reinterpret_cast<__half*>(p.out)[to] = __float2half_rn(y);
+            else reinterpret_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(y);
           }
         }
       }
       tc_fence_before();
-      soft_sync();  // the rows' state is free
+      sync_of(3, kSoft);  // the rows' state is free
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, S::kAlloc);
+  if (warp == kScoreWarp) tmem_dealloc(tmem, S::kAlloc);
 }
 
 // The sequences that lie in more than one range (and rows that see nothing): a warp joins a row's parts, in
@@ -873,16 +1023,20 @@ spec_status launch_one(const Params& p, cudaStream_t st) {
   return launch_chained(attn_scaled_kernel<D, RT, F16>, p.teams * p.tiles, kThreads, S::kSmem, st, p);
 }
 
+// Query rows that a CTA takes at most: what two O of 3 parts leave room for in tensor memory.
+constexpr int most_rows(int D) { return D == 256 ? 32 : 64; }
+
 // rt: 16, 32 or 64 query rows of a CTA.  Each D is a translation unit of its own.
 template <int D>
 spec_status launch_d(const Params& p, int rt, bool f16, cudaStream_t st) {
+  constexpr int kMost = most_rows(D);
   spec_status rc;
   if (f16)
     rc = rt == 16 ? launch_one<D, 16, true>(p, st)
-                  : rt == 32 ? launch_one<D, 32, true>(p, st) : launch_one<D, 64, true>(p, st);
+                  : rt == 32 ? launch_one<D, 32, true>(p, st) : launch_one<D, kMost, true>(p, st);
   else
     rc = rt == 16 ? launch_one<D, 16, false>(p, st)
-                  : rt == 32 ? launch_one<D, 32, false>(p, st) : launch_one<D, 64, false>(p, st);
+                  : rt == 32 ? launch_one<D, 32, false>(p, st) : launch_one<D, kMost, false>(p, st);
   if (rc != SPEC_OK) return rc;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.B * ((p.R * p.Hq + kJoinWarps - 1) / kJoinWarps), 1, 1);
