@@ -119,6 +119,7 @@ extern "C" spec_status spec_verify_attn_scaled(
   p.head_stride = head_stride;
   p.P = FastDiv(page_size);
   p.block = FastDiv(block);
+  p.per_head = FastDiv(Hq / Hkv);
   p.B = B;
   p.R = R;
   p.Hq = Hq;
@@ -131,7 +132,7 @@ extern "C" spec_status spec_verify_attn_scaled(
   p.rows_per_tile = pl.rows_per_tile;
   p.teams = pl.teams;
   p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
-  p.wait_ns = SPEC_WAIT_NS;
+  p.polls = (uint32_t)(SPEC_WAIT_NS / 1000);
   p.withhold_stage = -1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f16 = q_dtype == SPEC_F16;

@@ -43,9 +43,10 @@
 namespace scaled_attn {
 
 constexpr int kUnit = 128;                       // positions of a tile
-constexpr int kGroup = 128;                      // threads of a soft group: one per position
+constexpr int kGroup = 128;                      // threads of a soft group
 constexpr int kSoftWarps = 8, kSoft = 2 * kGroup;
-constexpr int kScoreWarp = kSoftWarps, kSumWarp = kScoreWarp + 1;  // one thread each issues MMAs
+constexpr int kPrepWarp0 = kSoftWarps, kPrepWarps = 4, kPrep = 32 * kPrepWarps;
+constexpr int kScoreWarp = kPrepWarp0 + kPrepWarps, kSumWarp = kScoreWarp + 1;  // a thread each issues MMAs
 constexpr int kCopyWarp0 = kSumWarp + 1, kCopyWarps = 2;
 constexpr int kCopy = 32 * kCopyWarps;
 constexpr int kThreads = 32 * (kCopyWarp0 + kCopyWarps);
@@ -62,11 +63,11 @@ struct Params {
   int32_t* err;
   long long q_stride_b, q_stride_r, q_stride_h;       // elements
   long long page_stride, token_stride, head_stride;   // bytes
-  FastDiv P, block;
+  FastDiv P, block, per_head;        // page size, block, query heads of a KV head
   int B, R, Hq, Hkv, G, num_pages, max_pages, window;
   int tiles, rows_per_tile, teams;   // row tiles of a KV head, their query rows; ranges
   float scale_log2;
-  uint64_t wait_ns;
+  uint32_t polls;                    // of a wait, before it gives up
   int withhold_stage;
 };
 
@@ -105,10 +106,11 @@ struct Walk {
   SPEC_DEV bool more() const { return s < s1; }
   SPEC_DEV int first_unit() const { return s - kvh * W - at; }
   SPEC_DEV int count() const { return min(seq.units - first_unit(), s1 - s); }
-  SPEC_DEV void next(const Params& p) {
+  __device__ __noinline__ void next(const Params& p) {
     s += count();
     if (s >= s1) return;
     at += seq.units;
+#pragma unroll 1
     do {
       if (++b == p.B) b = 0, at = 0, ++kvh;
       seq = seq_of(p, b);
@@ -152,24 +154,42 @@ SPEC_DEV void mma_f16(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, u
       : "memory");
 }
 
+// 16 lanes x 8 N columns as accumulator fragments: registers 4 k, 4 k + 1 are columns 8 k + 2 (lane % 4),
+// + 1 of lane / 4, registers 4 k + 2, + 3 those of lane / 4 + 8.
 template <int N>
-SPEC_DEV void tmem_ld(uint32_t addr, uint32_t* r) {
-  static_assert(N == 8 || N == 16 || N == 32, "columns");
-  if constexpr (N == 8)
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+SPEC_DEV void tmem_ld_frag(uint32_t addr, uint32_t* r) {
+  static_assert(N == 1 || N == 2 || N == 4, "column groups");
+  if constexpr (N == 1)
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+  else if constexpr (N == 2)
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
                    "=r"(r[6]), "=r"(r[7])
                  : "r"(addr));
-  else if constexpr (N == 16)
+  else
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
         "%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
           "=r"(r[14]), "=r"(r[15])
         : "r"(addr));
-  else
-    tmem_ld32(addr, *reinterpret_cast<uint32_t(*)[32]>(r));
+}
+
+SPEC_DEV void tmem_ld8(uint32_t addr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                 "=r"(r[7])
+               : "r"(addr));
+}
+
+// Four 8 x 8 fragments of 16-bit elements; lane i has the address of row i % 8 of fragment i / 8.
+SPEC_DEV void store_frags(uint32_t addr, const uint32_t* r) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
 }
 
 SPEC_DEV void tmem_st8(uint32_t addr, const uint32_t* r) {
@@ -193,25 +213,16 @@ SPEC_DEV void sync_of(int id, int n) {
   asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
-// Columns combined over a warp's lanes in about N shuffles: lane holds column (lane * N / 32 ...)
-// of the result, N = 8, 16 or 32; returns the column that this lane's result belongs to.
-template <int N, class Op>
-SPEC_DEV float over_lanes(float* x, int lane, Op op, int* column) {
-  int col = 0;
-#pragma unroll
-  for (int n = N / 2, o = 16; n >= 1; n /= 2, o /= 2) {
-    const bool up = lane & o;
-#pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float give = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
-      x[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+// mbar_wait with little code (an instance holds a dozen, and what does not run still has to be
+// fetched): suspended polls of up to 1 us, `polls` of them.
+SPEC_DEV bool wait_for(uint64_t* bar, uint32_t parity, const Params& p) {
+#pragma unroll 1
+  for (uint32_t i = 0; !mbar_try_wait_ns(bar, parity, 1000); ++i)
+    if (i > p.polls) {
+      set_error(p.err, SPEC_ERR_MBAR_TIMEOUT);
+      return false;
     }
-    col += up ? n : 0;
-  }
-#pragma unroll
-  for (int o = 16 / N; o >= 1; o /= 2) x[0] = op(x[0], __shfl_xor_sync(0xffffffffu, x[0], o));
-  *column = col;
-  return x[0];
+  return true;
 }
 
 SPEC_DEV uint32_t f16x2(float lo, float hi) {
@@ -232,6 +243,12 @@ SPEC_DEV uint32_t halves_of(uint32_t codes) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
   return r;
+}
+SPEC_DEV void codes_to_halves(uint32_t w, uint32_t& lo, uint32_t& hi) {  // bytes 0, 1 and 2, 3
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 SPEC_DEV uint32_t sub_mul(uint32_t a, uint32_t b, uint32_t mul) {  // (a - b) * mul, halves
   uint32_t r;
@@ -261,21 +278,21 @@ struct Shape {
   static constexpr int kOCols = kSums * RT * kHalves;
   // weights stay at or below 2^kTop and begin at 2^kBelow
   static constexpr float kTop = kHalfV ? 15.f : 8.f, kBelow = kHalfV ? 8.f : 2.f;
-  // Q's parts as columns side by side, added up by the readers, where tensor memory has room: an
-  // MMA of 128 x N x 32 takes 61 cycles up to N = 96, and N / 2 above that
-  static constexpr bool kStack = 2 * kParts * RT + 2 * kOCols <= 512;
-  static constexpr int kSCols = kStack ? kParts * RT : RT;      // of a score buffer
   static constexpr int kStageBytes = 2 * kTileBytes + 1024;     // V, K, scales
-  static constexpr int kQBytes = kParts * RT * D;
+  static constexpr int kQBytes = kParts * RT * D;               // of one of two
   static constexpr int kPBytes = kHalfV ? RT * kUnit * 2 : 3 * RT * kUnit;
   static constexpr int kVBytes = kHalfV ? 2 * kTileBytes : 0;
-  static constexpr int kFixed = kQBytes + 2 * kPBytes + 2 * kVBytes + 1024;
-  static constexpr int kRoom = 225 * 1024 - 8 * 1024 - kFixed;  // (static shared memory: < 8 KB)
+  // buffers of Q (the next segment's is made while this one's is used) and of weights (with four, those
+  // who write them need not wait for the product two tiles back), where there is room
+  static constexpr int kQBufs = RT == 64 && F16 ? 1 : 2, kPBufs = RT == 64 || D == 256 ? 2 : 4;
+  static constexpr int kTokBytes = kUnit * 16;                  // a tile's scales, as the weights take them
+  static constexpr int kFixed = kQBufs * kQBytes + kPBufs * kPBytes + 2 * kVBytes + 4 * kTokBytes + 1024;
+  static constexpr int kRoom = 225 * 1024 - 11 * 1024 - kFixed; // (static shared memory: < 11 KB)
   static constexpr int kStages = kRoom / kStageBytes < 8 ? kRoom / kStageBytes : 8;
-  static_assert(kStages >= 2, "a ring needs two stages");
+  static_assert(kStages >= 1, "a ring needs a stage");
   static constexpr int kSmem = kFixed + kStages * kStageBytes;
   // tensor memory: a score buffer and an O for each soft group
-  static constexpr int kColO = 2 * kSCols, kCols = kColO + 2 * kOCols;
+  static constexpr int kColO = 2 * RT, kCols = kColO + 2 * kOCols;
   static constexpr int kAlloc = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static_assert(kCols <= 512, "tensor memory");
 };
@@ -287,31 +304,62 @@ SPEC_DEV uint32_t swizzled(int rows, int r, int c) {
   return (uint32_t)(c >> 3) * (rows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
+// NaN codes in a position's V row: noted for the query rows that see it, and zeroed (positions that only some
+// rows see; hardly ever anything to do).
+template <int D>
+__device__ __noinline__ bool note_nans(uint8_t* tile, int tok, int t, int jb, int rows, const uint64_t* see,
+                                       const int* from, uint32_t* notes) {
+  bool any = false;
+#pragma unroll 1
+  for (int c = 0; c < D / 16; ++c) {
+    uint32_t* u4 = reinterpret_cast<uint32_t*>(tile + swizzled<D>(kUnit, tok, c));
+#pragma unroll 1
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t nan = nan_bytes(u4[e]);
+      if (!nan) continue;
+      any = true;
+      const uint32_t bits = nan >> 7 & 1 | nan >> 14 & 2 | nan >> 21 & 4 | nan >> 28 & 8;
+#pragma unroll 1
+      for (int n = 0; n < rows; ++n)
+        if (jb < 0 ? t >= from[n] : jb < 64 && (see[n] >> jb & 1))
+          atomicOr(&notes[n * (D / 32) + (c >> 1)], bits << (16 * (c & 1) + 4 * e));
+      u4[e] &= ~((nan >> 7) * 255u);
+    }
+  }
+  return any;
+}
+
 template <int D, int RT, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
     const __grid_constant__ Params p) {
   using S = Shape<D, RT, F16>;
   constexpr int NS = S::kStages;
-  constexpr int kC = 16;  // columns that a soft thread works on at a time
+  constexpr int kGroups = RT / 8;                    // column groups of eight
+  constexpr int kB = kGroups < 4 ? kGroups : 4;      // of them between two votes
   extern __shared__ uint8_t dyn[];
-  __shared__ __align__(8) uint64_t full[NS], empty[NS], s_full[2], p_full[2], pv_done[2], q_full, o_full, fin;
-  __shared__ __align__(16) float sc_s[RT], neg_m[2][RT], fac_s[2][RT], red[kSoftWarps][RT];
-  __shared__ __align__(16) float inv_s[RT];
-  __shared__ uint64_t see_s[RT];
-  __shared__ long long out_s[RT];  // element of the row's output, or of its part's
-  __shared__ int from_s[RT];
-  __shared__ uint32_t nan_s[RT][D / 32];
+  __shared__ __align__(8) uint64_t full[NS], empty[NS], prep[4], v_full[2], s_full[2], p_full[2], pv_done[4],
+      q_full[2], seg_done[2], o_full, fin;
+  // per segment, two in flight: scale, block rows seen, first position, output row of a query row
+  __shared__ __align__(16) float sc_s[2][RT];
+  __shared__ uint64_t see_s[2][RT];
+  __shared__ long long out_s[2][RT];
+  __shared__ int from_s[2][RT], any_nan[2];
+  __shared__ uint32_t nan_s[2][RT][D / 32];
+  __shared__ __align__(16) float neg_m[2][RT], fac_s[2][RT], red[kSoftWarps][RT], inv_s[RT];
   __shared__ Walk start;
   __shared__ uint32_t tmem_base;
-  __shared__ int part_w[kThreads / 32], any_nan;
+  __shared__ int part_w[kThreads / 32];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int team = blockIdx.x / p.tiles, tile = blockIdx.x % p.tiles;
   // fp16 V, the stages, Q, the weights: whole swizzle atoms
   const uint32_t v16_at = (smem_u32(dyn) + 1023u) & ~1023u, base = v16_at + 2 * S::kVBytes;
-  const uint32_t q_at = base + NS * S::kStageBytes, p_at = q_at + S::kQBytes;
+  const uint32_t q_at = base + NS * S::kStageBytes, p_at = q_at + S::kQBufs * S::kQBytes;
   uint8_t* const v16_0 = dyn + (v16_at - smem_u32(dyn));
   uint8_t* const dyn0 = v16_0 + 2 * S::kVBytes;
+  uint8_t* const q_0 = dyn0 + NS * S::kStageBytes;
+  float4* const tok_s = reinterpret_cast<float4*>(q_0 + S::kQBufs * S::kQBytes + S::kPBufs * S::kPBytes);  // [4][kUnit]
+  const int rows = min(p.rows_per_tile, p.R * p.G - tile * p.rows_per_tile);
 
   chain_wait();
   // ---- this CTA's range, and the sequence it begins in: each thread sums consecutive sequences
@@ -349,14 +397,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
     if (threadIdx.x == 0) {
       for (int i = 0; i < NS; ++i) {
         mbar_init(&full[i], kCopy);
-        mbar_init(&empty[i], S::kHalfV ? kGroup : 1);
+        mbar_init(&empty[i], kPrep + (S::kHalfV ? 1 : 2));  // scales (and V) taken, K's (and V's) product
       }
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&s_full[i], 1);
-        mbar_init(&p_full[i], kGroup);
+      for (int i = 0; i < 4; ++i) {
+        mbar_init(&prep[i], kPrep);
         mbar_init(&pv_done[i], 1);
       }
-      mbar_init(&q_full, kSoft);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&v_full[i], kPrep);
+        mbar_init(&s_full[i], 1);
+        mbar_init(&p_full[i], kGroup);
+        mbar_init(&q_full[i], kPrep);
+        mbar_init(&seg_done[i], kSoft);
+      }
       mbar_init(&o_full, 1);
       mbar_init(&fin, 2);
       fence_mbar_init();
@@ -413,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         }
         // (the warp as one: the shuffles below need every lane)
         if (g >= NS)
-          ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], ((g / NS) - 1) & 1, p.err, p.wait_ns));
+          ok = __all_sync(0xffffffffu, wait_for(&empty[stage], ((g / NS) - 1) & 1, p));
         if (!ok) break;
         const uint32_t v_at = base + stage * S::kStageBytes, k_at = v_at + S::kTileBytes;
 #pragma unroll
@@ -453,62 +506,61 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == kScoreWarp) {
-    // ================================================================ the scores' MMA thread
+    // ================================================================ S^T = K Q^T, one thread
     if (lane == 0) {
-      constexpr uint32_t kId = idesc_f8(128, S::kSCols, false, false);
+      constexpr uint32_t kId = idesc_f8(128, RT, false, false);
       constexpr uint32_t kHi = desc_hi(S::kRows8, S::kLayout);
-      // (a part is RT rows: stacked parts are kParts * RT rows of one operand)
-      constexpr int kQRows = S::kStack ? S::kParts * RT : RT;
-      const uint32_t q_lo = desc_lo(q_at, 16);
       int g = 0, seg = 0;
       bool ok = true;
       for (Walk walk = start; walk.more() && ok; walk.next(p), ++seg) {
         const int n = walk.count();
-        if (!mbar_wait(&q_full, seg & 1, p.err, p.wait_ns)) break;
+        if (!wait_for(&q_full[seg & 1], seg >> 1 & 1, p)) break;
+        const uint32_t q_lo = desc_lo(q_at + seg % S::kQBufs * S::kQBytes, 16);
 #pragma unroll 1
         for (int j = 0; j < n; ++j, ++g) {
           const int stage = g % NS;
-          // the score buffer's last tile has been read, this tile has landed
-          if (g >= 2 && !(ok = mbar_wait(&p_full[g & 1], (g - 2) >> 1 & 1, p.err, p.wait_ns))) break;
-          if (!(ok = mbar_wait(&full[stage], (g / NS) & 1, p.err, p.wait_ns))) break;
+          // the score buffer's last tile has been read, the weights' last product is complete (both for
+          // who takes these scores), and this tile has landed
+          ok = (g < 2 || wait_for(&p_full[g & 1], (g - 2) >> 1 & 1, p)) &&
+               (S::kPBufs == 2 || g < 4 || wait_for(&pv_done[g & 3], (g - 4) >> 2 & 1, p)) &&
+               wait_for(&prep[g & 3], g >> 2 & 1, p);
+          if (!ok) break;
           fence_proxy_async();  // the copies' writes, for the tensor cores
           tc_fence_after();
           const uint32_t k_lo = desc_lo(base + stage * S::kStageBytes + S::kTileBytes, 16);
-          const uint32_t d = tmem + (g & 1) * S::kSCols;
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) {
             constexpr int kIn = D == 64 ? 2 : 4;  // steps within a swizzled row
 #pragma unroll
-            for (int part = 0; part < (S::kStack ? 1 : S::kParts); ++part)
-              mma_f8(d, k_lo + ((k / kIn) * (kUnit * 128) + k % kIn * 32) / 16, kHi,
-                     q_lo + (part * RT * D + (k / kIn) * (kQRows * 128) + k % kIn * 32) / 16, kHi, kId,
+            for (int part = 0; part < S::kParts; ++part)
+              mma_f8(tmem + (g & 1) * RT, k_lo + ((k / kIn) * (kUnit * 128) + k % kIn * 32) / 16, kHi,
+                     q_lo + (part * RT * D + (k / kIn) * (RT * 128) + k % kIn * 32) / 16, kHi, kId,
                      k > 0 || part > 0);
           }
           tc_commit(&s_full[g & 1]);
+          tc_commit(&empty[stage]);
         }
       }
       // nothing of this thread's is in flight when the tensor memory goes
       tc_commit(&fin);
-      mbar_wait(&fin, 0, nullptr);
+      wait_for(&fin, 0, p);
     }
     __syncwarp();
   } else if (warp == kSumWarp) {
-    // ================================================================ O^T += V^T W^T
+    // ================================================================ O^T += V^T W^T, one thread
     if (lane == 0) {
-      constexpr uint32_t kHi = desc_hi(S::kRows8, S::kLayout), kHiW = desc_hi(2048, 0);
+      constexpr uint32_t kHiW = desc_hi(2048, 0);
       int g = 0;
       bool ok = true;
       for (Walk walk = start; walk.more() && ok; walk.next(p)) {
         const int n = walk.count();
 #pragma unroll 1
         for (int j = 0; j < n; ++j, ++g) {
-          const int stage = g % NS;
-          if constexpr (!S::kHalfV) ok = mbar_wait(&full[stage], (g / NS) & 1, p.err, p.wait_ns);
-          ok = ok && mbar_wait(&p_full[g & 1], g >> 1 & 1, p.err, p.wait_ns);
+          ok = wait_for(&v_full[g & 1], g >> 1 & 1, p) && wait_for(&p_full[g & 1], g >> 1 & 1, p);
           if (!ok) break;
           if constexpr (!S::kHalfV) fence_proxy_async();
           tc_fence_after();
-          const uint32_t w_lo = desc_lo(p_at + (g & 1) * S::kPBytes, 128);
+          const uint32_t w_lo = desc_lo(p_at + g % S::kPBufs * S::kPBytes, 128);
           const uint32_t o = tmem + S::kColO + (g & 1) * S::kOCols;
           const uint32_t later = j >= 2;  // this group's O holds something
           if constexpr (S::kHalfV) {
@@ -521,6 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
           } else {
             constexpr uint32_t kIdP = idesc_f8(128, 2 * RT, false, true);
             constexpr uint32_t kIdL = idesc_f8(128, RT, true, true);
+            constexpr uint32_t kHi = desc_hi(S::kRows8, S::kLayout);
+            const int stage = g % NS;
             const uint32_t v_lo = desc_lo(base + stage * S::kStageBytes, 16384);
 #pragma unroll
             for (int half = 0; half < S::kHalves; ++half)
@@ -534,47 +588,39 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
               }
             tc_commit(&empty[stage]);
           }
-          tc_commit(&pv_done[g & 1]);
+          tc_commit(&pv_done[g & 3]);
         }
         if (ok) tc_commit(&o_full);
       }
       tc_commit(&fin);
-      mbar_wait(&fin, 0, nullptr);
+      wait_for(&fin, 0, p);
     }
     __syncwarp();
-  } else {
-    // ================================================================ scores into weights
-    // Two groups of four warps take the tiles in turn, each with references, sums and an O of its
-    // own: one tile's chain of waits lies under the other's work.
-    const int group = warp >> 2, bar = 1 + group;
-    const int tok = (warp & 3) * 32 + lane;      // a position of the tile, a dimension of O
-    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
-    const int rows = min(p.rows_per_tile, p.R * p.G - tile * p.rows_per_tile);
+  } else if (warp >= kPrepWarp0) {
+    // ================================================================ operands: Q, scales, fp16 V
+    const int tid = threadIdx.x - 32 * kPrepWarp0, tok = tid;  // a position of the tile
     const int range0 = start.s;
     int g = 0, seg = 0;
     bool ok = true;
     for (Walk walk = start; walk.more(); walk.next(p), ++seg) {
-      const int b = walk.b, n_units = walk.count(), ctx = walk.seq.ctx;
+      const int b = walk.b, n_units = walk.count(), ctx = walk.seq.ctx, sb = seg & 1;
       const bool whole = n_units == walk.seq.units;
-      const int part = (team * 2 + (walk.s == range0 ? 0 : 1)) * p.tiles + tile;
+      const int part_at = (team * 2 + (walk.s == range0 ? 0 : 1)) * p.tiles + tile;
+      // the segment before the last is done with this one's places
+      if (seg >= S::kQBufs)
+        ok = ok && wait_for(&seg_done[(seg - S::kQBufs) & 1], (seg - S::kQBufs) >> 1 & 1, p);
       // ---- Q as sums of e4m3 parts under a power of two per row
       {
-        constexpr int kPer = kSoft / RT;  // threads of a row
-        const int n = threadIdx.x / kPer, x0 = threadIdx.x % kPer;
-        const int row = tile * p.rows_per_tile + n, i = row / p.G;
+        constexpr int kPer = kPrep / RT;            // threads of a row
+        constexpr int kMine = D / 8 / kPer > 0 ? D / 8 / kPer : 1;  // 16-byte chunks of a thread
+        const int n = tid / kPer, x0 = tid % kPer;
+        const int row = tile * p.rows_per_tile + n, i = p.per_head.quot(row);
         const bool real = n < rows;
         const uint4* src = reinterpret_cast<const uint4*>(
             p.q + (b * p.q_stride_b + (real ? i : 0) * p.q_stride_r +
                    (walk.kvh * p.G + (real ? row - i * p.G : 0)) * p.q_stride_h) * 2);
-        constexpr int kMine = D / 8 / kPer > 0 ? D / 8 / kPer : 1;  // 16-byte chunks of a thread
-        uint4 raw[kMine];
-#pragma unroll
-        for (int m = 0; m < kMine; ++m) {
-          const int c = x0 + m * kPer;
-          raw[m] = real && c < D / 8 ? src[c] : make_uint4(0, 0, 0, 0);
-        }
-        auto values = [&](int m, float* x) {
-          const uint32_t* u = reinterpret_cast<const uint32_t*>(&raw[m]);
+        auto values = [&](const uint4& w, float* x) {
+          const uint32_t* u = reinterpret_cast<const uint32_t*>(&w);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if constexpr (F16) {
@@ -586,40 +632,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
             }
           }
         };
-        float big = 0.f;
+        // the largest magnitude as bits (of fp16 or bf16 pairs: what is not finite has all exponent bits)
+        constexpr uint32_t kInf = F16 ? 0x7c00u : 0x7f80u;
+        uint32_t big = 0;
         bool bad = false;
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
-          float x[8];
-          values(m, x);
+          const int c = x0 + m * kPer;
+          const uint4 w = real && c < D / 8 ? src[c] : make_uint4(0, 0, 0, 0);
+          const uint32_t u[4] = {w.x & 0x7fff7fffu, w.y & 0x7fff7fffu, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            big = fmaxf(big, finite_abs(x[e]));
-            bad = bad || !(fabsf(x[e]) < INFINITY);
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = u[e] & 0xffffu, hi = u[e] >> 16;
+            bad = bad || lo >= kInf || hi >= kInf;
+            big = max(big, max(lo >= kInf ? 0u : lo, hi >= kInf ? 0u : hi));
           }
         }
 #pragma unroll
         for (int o = 1; o < kPer; o <<= 1) {
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+          big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
           bad = __shfl_xor_sync(0xffffffffu, (int)bad, o) || bad;
         }
-        const float s = needed_scale(big), down = 1.f / s;
-#pragma unroll
+        const float s = needed_scale(F16 ? __half2float(__ushort_as_half((unsigned short)big))
+                                         : __uint_as_float(big << 16));
+        const float down = 1.f / s;
+#pragma unroll 1
         for (int m = 0; m < kMine; ++m) {
           const int c = x0 + m * kPer;
           if (c >= D / 8) break;
           float x[8];
-          values(m, x);
+          values(real ? src[c] : make_uint4(0, 0, 0, 0), x);
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] *= down;
-#pragma unroll
+          uint8_t* to = q_0 + seg % S::kQBufs * S::kQBytes + swizzled<D>(RT, n, c >> 1) + (c & 1) * 8;
+#pragma unroll 1
           for (int part = 0; part < S::kParts; ++part) {
-            const uint32_t to =
-                S::kStack ? swizzled<D>(S::kParts * RT, part * RT + n, c >> 1)
-                          : part * RT * D + swizzled<D>(RT, n, c >> 1);
             const uint2 w = make_uint2(e4m3_word(x[0], x[1], x[2], x[3]),
                                        e4m3_word(x[4], x[5], x[6], x[7]));
-            *reinterpret_cast<uint2*>(dyn0 + (q_at - base) + to + (c & 1) * 8) = w;
+            *reinterpret_cast<uint2*>(to + part * RT * D) = w;
             float y[8];
             e4m3_values(w.x, y);
             e4m3_values(w.y, y + 4);
@@ -628,225 +678,288 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
           }
         }
         if (x0 == 0) {
-          sc_s[n] = bad ? NAN : real ? p.scale_log2 * s : 0.f;
-          neg_m[0][n] = neg_m[1][n] = -kNone;
+          sc_s[sb][n] = bad ? NAN : real ? p.scale_log2 * s : 0.f;
           uint64_t m = 0;
           if (real) {
             m = p.mask ? p.mask[(size_t)b * p.R + i] : i >= 63 ? ~0ull : (2ull << i) - 1;
             if (p.R < 64) m &= (1ull << p.R) - 1;
           }
-          see_s[n] = m;
-          out_s[n] = whole ? ((long long)b * p.R + i) * p.Hq + walk.kvh * p.G + row - i * p.G
-                           : (long long)part * RT + n;
-          from_s[n] = p.window > 0 ? ctx + __popcll(m) - p.window : 0;
-#pragma unroll
-          for (int e = 0; e < D / 32; ++e) nan_s[n][e] = 0;
+          see_s[sb][n] = m;
+          out_s[sb][n] = whole ? ((long long)b * p.R + i) * p.Hq + walk.kvh * p.G + row - i * p.G
+                               : (long long)part_at * RT + n;
+          from_s[sb][n] = p.window > 0 ? ctx + __popcll(m) - p.window : 0;
+#pragma unroll 1
+          for (int e = 0; e < D / 32; ++e) nan_s[sb][n][e] = 0;
         }
-        if (threadIdx.x == 0) any_nan = 0;
+        if (tid == 0) any_nan[sb] = 0;
         fence_proxy_async();
-        mbar_arrive(&q_full);
+        mbar_arrive(&q_full[sb]);
+        sync_of(4, kPrep);
       }
-      sync_of(3, kSoft);
-
-      uint64_t l2[RT / 2];
-#pragma unroll
-      for (int i = 0; i < RT / 2; ++i) l2[i] = 0ull;
-      bool begun = false;  // this group's O holds something
-      const int t_seg = walk.seq.first + walk.first_unit() * kUnit;
+      int t0 = walk.seq.first + walk.first_unit() * kUnit;
 #pragma unroll 1
-      for (int j = (g ^ group) & 1; j < n_units; j += 2) {
-        const int u = g + j, stage = u % NS, t0 = t_seg + j * kUnit;
-        ok = ok && mbar_wait(&full[stage], (u / NS) & 1, p.err, p.wait_ns);
-        const float* scales =
-            reinterpret_cast<const float*>(dyn0 + stage * S::kStageBytes + 2 * S::kTileBytes);
-        float ks = scales[tok], vs = scales[kUnit + tok];
-        const bool here = ks != -INFINITY;
-        vs = !here ? 1.f : vs < 0x1p-100f ? 0x1p-100f : vs;
-        ks = here ? ks : 0.f;
-        const float lvs = here ? __log2f(vs) : -INFINITY, rvs = here ? __fdividef(1.f, vs) : 0.f;
-        // positions that some rows see and others do not
-        const bool mixed = (t0 + kUnit > ctx && (p.R > 1 || p.mask)) ||
-                           (p.window > 0 && t0 < ctx + p.R - p.window);
-        uint64_t see = ~0ull;  // columns that see this thread's position
-        if (mixed) {
-          const int t = t0 + tok, jb = t - ctx;
-          see = 0;
-#pragma unroll 1
-          for (int c = 0; c < RT; ++c)
-            if (jb < 0 ? t >= from_s[c] : jb < 64 && (see_s[c] >> jb & 1)) see |= 1ull << c;
-        }
-        // the group's last product is complete: its O and its operands' buffers are free
-        if (u >= 2) ok = ok && mbar_wait(&pv_done[group], (u - 2) >> 1 & 1, p.err, p.wait_ns);
+      for (int j = 0; j < n_units; ++j, ++g, t0 += kUnit) {
+        const int stage = g % NS;
+        ok = ok && wait_for(&full[stage], (g / NS) & 1, p);
         uint8_t* vrow = dyn0 + stage * S::kStageBytes;
-        if (mixed) {  // NaN codes of V: noted for the rows that see them, and zeroed
-#pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t* u4 = reinterpret_cast<uint32_t*>(vrow + swizzled<D>(kUnit, tok, c));
-            if (nan_bytes(u4[0]) | nan_bytes(u4[1]) | nan_bytes(u4[2]) | nan_bytes(u4[3])) {
-              uint32_t bits = 0;
-              for (int e = 0; e < 16; ++e) bits |= (nan_bytes(u4[e >> 2]) >> (8 * (e & 3) + 7) & 1) << e;
-              for (int x = 0; x < RT; ++x)
-                if (see >> x & 1) atomicOr(&nan_s[x][c >> 1], bits << 16 * (c & 1));
-              for (int e = 0; e < 4; ++e) u4[e] &= ~((nan_bytes(u4[e]) >> 7) * 255u);
-              any_nan = 1;
-            }
-          }
+        // ---- K's scale, the logarithm of V's and its inverse; nothing for positions that are not there
+        {
+          const float* scales = reinterpret_cast<const float*>(vrow + 2 * S::kTileBytes);
+          const float ks = scales[tok];
+          float vs = scales[kUnit + tok];
+          vs = vs < 0x1p-100f ? 0x1p-100f : vs;
+          tok_s[(g & 3) * kUnit + tok] = ks == -INFINITY
+                                             ? make_float4(0.f, -INFINITY, 0.f, 0.f)
+                                             : make_float4(ks, __log2f(vs), __fdividef(1.f, vs), 0.f);
+          mbar_arrive(&prep[g & 3]);
+        }
+        // positions that some rows see and others do not: NaN codes of V are noted for the rows that
+        // see them, and zeroed
+        if ((t0 + kUnit > ctx && (p.R > 1 || p.mask)) || (p.window > 0 && t0 < ctx + p.R - p.window)) {
+          const int t = t0 + tok;
+          if (note_nans<D>(vrow, tok, t, t - ctx, RT, see_s[sb], from_s[sb], nan_s[sb][0])) any_nan[sb] = 1;
         }
         if constexpr (S::kHalfV) {  // this position's V as fp16, 64 dimensions a row
-          uint8_t* to = v16_0 + group * S::kVBytes + tok * 128;
+          // (the product that read the buffer last is complete)
+          if (g >= 2) ok = ok && wait_for(&pv_done[(g - 2) & 3], (g - 2) >> 2 & 1, p);
+          uint8_t* to = v16_0 + (g & 1) * S::kVBytes + tok * 128;
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             const uint4 w = *reinterpret_cast<const uint4*>(vrow + swizzled<D>(kUnit, tok, c));
             uint4 h0, h1;
-            h0.x = halves_of(w.x), h0.y = halves_of(w.x >> 16);
-            h0.z = halves_of(w.y), h0.w = halves_of(w.y >> 16);
-            h1.x = halves_of(w.z), h1.y = halves_of(w.z >> 16);
-            h1.z = halves_of(w.w), h1.w = halves_of(w.w >> 16);
+            codes_to_halves(w.x, h0.x, h0.y);
+            codes_to_halves(w.y, h0.z, h0.w);
+            codes_to_halves(w.z, h1.x, h1.y);
+            codes_to_halves(w.w, h1.z, h1.w);
             uint8_t* half = to + (c >> 2) * (kUnit * 128);
             const int c16 = 2 * (c & 3);
             *reinterpret_cast<uint4*>(half + ((c16 ^ (tok & 7)) << 4)) = h0;
             *reinterpret_cast<uint4*>(half + (((c16 + 1) ^ (tok & 7)) << 4)) = h1;
           }
         }
-        ok = ok && mbar_wait(&s_full[group], u >> 1 & 1, p.err, p.wait_ns);
+        fence_proxy_async();
+        mbar_arrive(&v_full[g & 1]);
+        mbar_arrive(&empty[stage]);
+        if (__any_sync(0xffffffffu, !ok)) break;
+      }
+      if (any_of(4, kPrep, !ok)) break;
+    }
+  } else {
+    // ================================================================ scores into weights
+    // Two groups of four warps take the tiles in turn, each with references, sums and an O of its
+    // own: one tile's chain of waits lies under the other's work.
+    const int group = warp >> 2, bar = 1 + group, quad = warp & 3;
+    const int tid = threadIdx.x & (kGroup - 1);       // in the group; a dimension of O
+    const uint32_t lanes = tmem + ((uint32_t)quad << 21);
+    const int c2 = 2 * (lane & 3), t_lane = quad * 32 + (lane >> 2);  // first column and position of this lane
+    int g = 0, seg = 0;
+    bool ok = true;
+    for (Walk walk = start; walk.more(); walk.next(p), ++seg) {
+      const int n_units = walk.count(), ctx = walk.seq.ctx, sb = seg & 1;
+      const int t_seg = walk.seq.first + walk.first_unit() * kUnit;
+      const bool whole = n_units == walk.seq.units;
+      ok = ok && wait_for(&q_full[sb], seg >> 1 & 1, p);
+      // columns 8 k + c2, + 1: their scales, references and sums (over this lane's positions)
+      uint64_t sc2[kGroups], nm2[kGroups], l2[kGroups];
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        sc2[k] = *reinterpret_cast<const uint64_t*>(&sc_s[sb][8 * k + c2]);
+        nm2[k] = f2_pack(-kNone, -kNone);
+        l2[k] = 0ull;
+      }
+      if (tid < RT) neg_m[group][tid] = -kNone;
+      bool begun = false;  // this group's O holds something
+      bool failed = false;
+#pragma unroll 1
+      for (int j = (g ^ group) & 1; j < n_units; j += 2) {
+        const int u = g + j, t0 = t_seg + j * kUnit;
+        ok = ok && wait_for(&s_full[group], u >> 1 & 1, p);
         tc_fence_after();
-        // ---- exponents of kC columns, relative to the rows' references
-        const uint64_t ks2 = f2_pack(ks, ks), lvs2 = f2_pack(lvs, lvs);
-        const uint32_t s_at = lanes + group * S::kSCols;
-        auto scores = [&](int c, uint32_t* s) {
-          tmem_ld<kC>(s_at + c, s);
-          if constexpr (S::kStack) {
-            uint32_t y[S::kParts - 1][kC];
+        // positions t_lane + 8 r
+        uint64_t ks2[4], lvs2[4], rvs2[4];
 #pragma unroll
-            for (int part = 1; part < S::kParts; ++part) tmem_ld<kC>(s_at + part * RT + c, y[part - 1]);
+        for (int r = 0; r < 4; ++r) {
+          const float4 x = tok_s[(u & 3) * kUnit + t_lane + 8 * r];
+          ks2[r] = f2_pack(x.x, x.x), lvs2[r] = f2_pack(x.y, x.y), rvs2[r] = f2_pack(x.z, x.z);
+        }
+        // positions that some rows see and others do not
+        const bool mixed = (t0 + kUnit > ctx && (p.R > 1 || p.mask)) ||
+                           (p.window > 0 && t0 < ctx + p.R - p.window);
+        const uint32_t s_at = lanes + group * RT;
+        const uint32_t w_at = p_at + u % S::kPBufs * S::kPBytes + (quad * 32 + lane) * 16;
+#pragma unroll
+        for (int h = 0; h < kGroups; h += kB) {
+          if (8 * h >= rows) break;
+          // ---- exponents relative to the rows' references; these move where a weight would pass
+          // 2^kTop (column groups behind the last row are left out)
+          float a[4][2 * kB];
+          bool moved = false;
+#pragma unroll 1
+          while (true) {
+            uint32_t s[2][4 * kB];
+            tmem_ld_frag<kB>(s_at + 8 * h, s[0]);
+            tmem_ld_frag<kB>(s_at + 8 * h + (16u << 16), s[1]);
             tmem_wait_ld();
+            float top = -INFINITY;
 #pragma unroll
-            for (int part = 1; part < S::kParts; ++part)
+            for (int k = 0; k < kB; ++k) {
+              if (8 * (h + k) >= rows) break;
 #pragma unroll
-              for (int i = 0; i < kC; ++i)
-                s[i] = __float_as_uint(__uint_as_float(s[i]) + __uint_as_float(y[part - 1][i]));
-          } else {
-            tmem_wait_ld();
-          }
-        };
-        auto exponents = [&](int c, const uint32_t* s, float* a) {
-          float top = -INFINITY;
-          const uint64_t* sc2 = reinterpret_cast<const uint64_t*>(sc_s + c);
-          const uint64_t* nm2 = reinterpret_cast<const uint64_t*>(neg_m[group] + c);
-#pragma unroll
-          for (int i = 0; i < kC / 2; ++i) {
-            const uint64_t x =
-                f2_mul(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2[i]);
-            f2_unpack(f2_fma(x, ks2, f2_add(lvs2, nm2[i])), a[2 * i], a[2 * i + 1]);
+              for (int r = 0; r < 4; ++r) {
+                const uint32_t* y = &s[r >> 1][4 * k + 2 * (r & 1)];
+                const uint64_t x =
+                    f2_mul(f2_pack(__uint_as_float(y[0]), __uint_as_float(y[1])), sc2[h + k]);
+                f2_unpack(f2_fma(x, ks2[r], f2_add(lvs2[r], nm2[h + k])), a[r][2 * k], a[r][2 * k + 1]);
+              }
+            }
             if (mixed) {
-              a[2 * i] = see >> (c + 2 * i) & 1 ? a[2 * i] : -INFINITY;
-              a[2 * i + 1] = see >> (c + 2 * i + 1) & 1 ? a[2 * i + 1] : -INFINITY;
-            }
-            top = fmax3(top, a[2 * i], a[2 * i + 1]);
-          }
-          return top;
-        };
-        // (K has been read, V and the scales have been taken over)
-        if constexpr (S::kHalfV) mbar_arrive(&empty[stage]);
-        // ---- weights and their sums; once more where a weight has passed 2^kTop
-        const uint64_t rvs2 = f2_pack(rvs, rvs);
-        uint8_t* w_at = dyn0 + (p_at - base) + group * S::kPBytes + tok * 16;
-        bool failed = false;
+              uint32_t see = 0;  // 2 kB bits a position
 #pragma unroll 1
-        for (int pass = begun ? 0 : 1;; ++pass) {
-          if (pass) {
-            // ---- the references move: maxima over the tile's positions
-#pragma unroll
-            for (int c = 0; c < RT; c += kC) {
-              uint32_t s[kC];
-              float x[kC];
-              scores(c, s);
-#pragma unroll
-              for (int i = 0; i < kC; ++i) {
-                x[i] = __uint_as_float(s[i]) * sc_s[c + i] * ks + lvs;
-                if (mixed && !(see >> (c + i) & 1)) x[i] = -INFINITY;
+              for (int x = 0; x < 4 * 2 * kB; ++x) {
+                const int i = x & (2 * kB - 1), n = 8 * (h + (i >> 1)) + c2 + (i & 1);
+                const int t = t0 + t_lane + 8 * (x / (2 * kB)), jb = t - ctx;
+                if (jb < 0 ? t >= from_s[sb][n] : jb < 64 && (see_s[sb][n] >> jb & 1)) see |= 1u << x;
               }
-              int col;
-              const float m = over_lanes<kC>(x, lane, [](float u, float v) { return fmaxf(u, v); }, &col);
-              red[warp][c + col] = m;
-            }
-            sync_of(bar, kGroup);
-            if (tok < RT) {
-              const int w0 = group * 4;
-              const float m4 = fmaxf(fmaxf(red[w0][tok], red[w0 + 1][tok]),
-                                     fmaxf(red[w0 + 2][tok], red[w0 + 3][tok]));
-              const float old = -neg_m[group][tok], now = m4 - old > S::kTop ? m4 - S::kBelow : old;
-              fac_s[group][tok] = fast_exp2(old - now);
-              neg_m[group][tok] = -now;
-            }
-            sync_of(bar, kGroup);
-            const float* fac = fac_s[group];
 #pragma unroll
-            for (int i = 0; i < RT / 2; ++i)
-              l2[i] = f2_mul(l2[i], reinterpret_cast<const uint64_t*>(fac)[i]);
+              for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int i = 0; i < 2 * kB; ++i)
+                  a[r][i] = see >> (2 * kB * r + i) & 1 ? a[r][i] : -INFINITY;
+            }
+            if (moved) break;
+#pragma unroll
+            for (int k = 0; k < kB; ++k) {
+              if (8 * (h + k) >= rows) break;
+#pragma unroll
+              for (int r = 0; r < 4; ++r) top = fmax3(top, a[r][2 * k], a[r][2 * k + 1]);
+            }
             if (begun) {
+              if (!any_of(bar, kGroup, top > S::kTop || !ok)) break;
+              if ((failed = any_of(bar, kGroup, !ok))) break;  // (the same for all of the group)
+            }
+            moved = true;
+            // ---- maxima over the tile's positions
 #pragma unroll 1
-              for (int c = 0; c < S::kOCols; c += 8) {
-                const uint32_t at = lanes + S::kColO + group * S::kOCols + c;
-                uint32_t o[8];
-                tmem_ld<8>(at, o);
-                tmem_wait_ld();
+            for (int k = h; k < h + kB && 8 * k < rows; ++k) {
+              uint32_t y[2][4];
+              tmem_ld_frag<1>(s_at + 8 * k, y[0]);
+              tmem_ld_frag<1>(s_at + 8 * k + (16u << 16), y[1]);
+              tmem_wait_ld();
+              const float2 sc = *reinterpret_cast<const float2*>(&sc_s[sb][8 * k + c2]);
+              float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  o[e] = __float_as_uint(__uint_as_float(o[e]) * fac[c % RT + e]);
-                tmem_st8(at, o);
+              for (int r = 0; r < 4; ++r) {
+                const float4 x = tok_s[(u & 3) * kUnit + t_lane + 8 * r];
+                float z0 = __uint_as_float(y[r >> 1][2 * (r & 1)]) * sc.x * x.x + x.y;
+                float z1 = __uint_as_float(y[r >> 1][2 * (r & 1) + 1]) * sc.y * x.x + x.y;
+                if (mixed) {
+                  const int t = t0 + t_lane + 8 * r, jb = t - ctx, n = 8 * k + c2;
+                  if (!(jb < 0 ? t >= from_s[sb][n] : jb < 64 && (see_s[sb][n] >> jb & 1))) z0 = -INFINITY;
+                  if (!(jb < 0 ? t >= from_s[sb][n + 1] : jb < 64 && (see_s[sb][n + 1] >> jb & 1))) z1 = -INFINITY;
+                }
+                m0 = fmaxf(m0, z0);
+                m1 = fmaxf(m1, z1);
               }
+#pragma unroll
+              for (int o = 4; o <= 16; o *= 2) {
+                m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+                m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+              }
+              if (lane < 4) *reinterpret_cast<float2*>(&red[warp][8 * k + c2]) = make_float2(m0, m1);
+            }
+            sync_of(bar, kGroup);
+            if (tid < 8 * kB && 8 * h + (tid & ~7) < rows) {
+              const int w0 = group * 4, n = 8 * h + tid;
+              const float m4 = fmaxf(fmaxf(red[w0][n], red[w0 + 1][n]), fmaxf(red[w0 + 2][n], red[w0 + 3][n]));
+              const float old = -neg_m[group][n];
+              const float now = m4 - old > S::kTop ? m4 - S::kBelow : old;
+              fac_s[group][n] = fast_exp2(old - now);
+              neg_m[group][n] = -now;
+            }
+            sync_of(bar, kGroup);
+#pragma unroll
+            for (int k = 0; k < kB; ++k) {
+              if (8 * (h + k) >= rows) break;
+              nm2[h + k] = *reinterpret_cast<const uint64_t*>(&neg_m[group][8 * (h + k) + c2]);
+              if (begun)
+                l2[h + k] = f2_mul(l2[h + k],
+                                   *reinterpret_cast<const uint64_t*>(&fac_s[group][8 * (h + k) + c2]));
+            }
+            if (begun) {  // O, whose last product has to be complete
+              ok = ok && wait_for(&pv_done[(u - 2) & 3], (u - 2) >> 2 & 1, p);
+              tc_fence_after();
+#pragma unroll 1
+              for (int y = 0; y < S::kSums * S::kHalves; ++y)
+#pragma unroll 1
+                for (int k = h; k < h + kB && 8 * k < rows; ++k) {
+                  const uint32_t at = lanes + S::kColO + group * S::kOCols + y * RT;
+                  uint32_t o[8];
+                  if constexpr (S::kHalfV) {
+                    tmem_ld8(at + 8 * k, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                      o[e] = __float_as_uint(__uint_as_float(o[e]) * fac_s[group][8 * k + e]);
+                    tmem_st8(at + 8 * k, o);
+                  } else {  // (columns in the parts' order, sixteen at a time)
+                    if (k & 1) continue;
+#pragma unroll 1
+                    for (int x = 0; x < 2; ++x) {
+                      tmem_ld8(at + 8 * k + 8 * x, o);
+                      tmem_wait_ld();
+#pragma unroll
+                      for (int e = 0; e < 8; ++e) {
+                        const int q = 8 * x + e, n = 8 * k + 2 * (q >> 2) + (q & 1) + 8 * (q >> 1 & 1);
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) *
+                                               ((n & ~7) < rows ? fac_s[group][n] : 1.f));
+                      }
+                      tmem_st8(at + 8 * k + 8 * x, o);
+                    }
+                  }
+                }
               tmem_wait_st();
             }
           }
-          float top = -INFINITY;
-          uint64_t t2[RT / 2];  // sums with this tile
+          if (failed) break;
+          // ---- weights and their sums
+          if constexpr (S::kPBufs == 2)
+            if (h == 0 && u >= 2) ok = ok && wait_for(&pv_done[(u - 2) & 3], (u - 2) >> 2 & 1, p);
+          uint32_t w[kB][4];
 #pragma unroll
-          for (int c = 0; c < RT; c += kC) {
-            uint32_t s[kC];
-            float a[kC];
-            scores(c, s);
-            top = fmaxf(top, exponents(c, s, a));
-            if constexpr (S::kHalfV) {
-              uint32_t h[kC / 2];
+          for (int k = 0; k < kB; ++k) {
+            if (8 * (h + k) >= rows) break;
 #pragma unroll
-              for (int e = 0; e < kC / 2; ++e) {
-                const float w0 = fast_exp2(a[2 * e]), w1 = fast_exp2(a[2 * e + 1]);
-                t2[c / 2 + e] = f2_fma(f2_pack(w0, w1), rvs2, l2[c / 2 + e]);
-                h[e] = f16x2(w0, w1);
-              }
+            for (int r = 0; r < 4; ++r) {
+              const float w0 = fast_exp2(a[r][2 * k]), w1 = fast_exp2(a[r][2 * k + 1]);
+              l2[h + k] = f2_fma(f2_pack(w0, w1), rvs2[r], l2[h + k]);
+              w[k][r] = f16x2(w0, w1);
+            }
+            if constexpr (S::kHalfV) store_frags(w_at + (h + k) * 2048, w[k]);
+          }
+          if constexpr (!S::kHalfV) {  // three 8-bit parts, two column groups together
 #pragma unroll
-              for (int x = 0; x < kC / 8; ++x)
-                *reinterpret_cast<uint4*>(w_at + (c / 8 + x) * 2048) =
-                    make_uint4(h[4 * x], h[4 * x + 1], h[4 * x + 2], h[4 * x + 3]);
-            } else {
+            for (int k = 0; k < kB; k += 2) {
+              if (8 * (h + k) >= rows) break;
               uint32_t p1[4], p2[4], p3[4];
 #pragma unroll
-              for (int e = 0; e < kC / 2; ++e) {
-                const float w0 = fast_exp2(a[2 * e]), w1 = fast_exp2(a[2 * e + 1]);
-                t2[c / 2 + e] = f2_fma(f2_pack(w0, w1), rvs2, l2[c / 2 + e]);
-                const uint32_t h = f16x2(w0, w1), x1 = e4m3x2(h);
-                const uint32_t r1 = sub_mul(h, halves_of(x1), 0x4c004c00u);   // times 2^4
-                const uint32_t x2 = e4m3x2(r1);
-                const uint32_t x3 = e5m2x2(sub_mul(r1, halves_of(x2), 0x68006800u));  // times 2^11
-                if (e & 1) {
-                  p1[e >> 1] |= x1 << 16, p2[e >> 1] |= x2 << 16, p3[e >> 1] |= x3 << 16;
-                } else {
-                  p1[e >> 1] = x1, p2[e >> 1] = x2, p3[e >> 1] = x3;
+              for (int r = 0; r < 4; ++r) {
+                p1[r] = p2[r] = p3[r] = 0;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const uint32_t y = 8 * (h + k + x) < rows ? w[k + x][r] : 0u;
+                  const uint32_t x1 = e4m3x2(y);
+                  const uint32_t r1 = sub_mul(y, halves_of(x1), 0x4c004c00u);   // times 2^4
+                  const uint32_t x2 = e4m3x2(r1);
+                  const uint32_t x3 = e5m2x2(sub_mul(r1, halves_of(x2), 0x68006800u));  // times 2^11
+                  p1[r] |= x1 << 16 * x, p2[r] |= x2 << 16 * x, p3[r] |= x3 << 16 * x;
                 }
               }
-              uint8_t* to = w_at + (c >> 4) * 2048;
-              *reinterpret_cast<uint4*>(to) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-              *reinterpret_cast<uint4*>(to + RT * kUnit) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
-              *reinterpret_cast<uint4*>(to + 2 * RT * kUnit) = make_uint4(p3[0], p3[1], p3[2], p3[3]);
+              const uint32_t to = w_at + (h + k) / 2 * 2048;
+              store_frags(to, p1);
+              store_frags(to + RT * kUnit, p2);
+              store_frags(to + 2 * RT * kUnit, p3);
             }
           }
-          if (pass || !any_of(bar, kGroup, top > S::kTop || !ok)) {
-#pragma unroll
-            for (int i = 0; i < RT / 2; ++i) l2[i] = t2[i];
-            break;
-          }
-          if ((failed = any_of(bar, kGroup, !ok))) break;  // (the same for all of the group)
         }
         if (failed) break;
         begun = true;
@@ -856,19 +969,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
       }
       g += n_units;
       // ---- the segment's sums and outputs: the groups' states meet
-      ok = ok && mbar_wait(&o_full, seg & 1, p.err, p.wait_ns);
+#pragma unroll
+      for (int k = 0; k < kGroups; ++k) {
+        float l[2];
+        f2_unpack(l2[k], l[0], l[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          l[i] += __shfl_xor_sync(0xffffffffu, l[i], 4);
+          l[i] += __shfl_xor_sync(0xffffffffu, l[i], 8);
+          l[i] += __shfl_xor_sync(0xffffffffu, l[i], 16);
+          if (lane < 4) red[warp][8 * k + c2 + i] = l[i];
+        }
+      }
+      ok = ok && wait_for(&o_full, seg & 1, p);
       if (any_of(3, kSoft, !ok)) break;
       tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < RT; c += kC) {
-        float l[kC];
-#pragma unroll
-        for (int i = 0; i < kC / 2; ++i) f2_unpack(l2[c / 2 + i], l[2 * i], l[2 * i + 1]);
-        int col;
-        const float sum = over_lanes<kC>(l, lane, [](float u, float v) { return u + v; }, &col);
-        red[warp][c + col] = sum;
-      }
-      sync_of(3, kSoft);
       if (threadIdx.x < RT) {  // weights of the two groups' states, the row's reference and sum
         const int n = threadIdx.x;
         const float m0 = -neg_m[0][n], m1 = -neg_m[1][n], m = fmaxf(m0, m1);
@@ -882,14 +997,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         inv_s[n] = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
         if (n < rows) {
           if (!whole)
-            *reinterpret_cast<float2*>(p.part_ml + out_s[n] * 2) = make_float2(m, l);
+            *reinterpret_cast<float2*>(p.part_ml + out_s[sb][n] * 2) = make_float2(m, l);
           else if (p.lse)
-            p.lse[out_s[n]] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            p.lse[out_s[sb][n]] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
       }
       sync_of(3, kSoft);
 #pragma unroll 1
-      for (int c = group * 8; c < rows; c += 16) {  // (a group takes every other eight rows)
+      for (int c = group * 8; c < RT && (S::kHalfV ? c : c & ~15) < rows; c += 16) {
+        // (a group takes every other eight columns of O)
 #pragma unroll
         for (int half = 0; half < S::kHalves; ++half) {
           uint32_t o[2][S::kSums][8];
@@ -897,12 +1013,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
           for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int y = 0; y < S::kSums; ++y)
-              tmem_ld<8>(lanes + S::kColO + x * S::kOCols + (half * S::kSums + y) * RT + c, o[x][y]);
+              tmem_ld8(lanes + S::kColO + x * S::kOCols + (half * S::kSums + y) * RT + c, o[x][y]);
           tmem_wait_ld();
-          const int d = half * 128 + tok;
+          const int d = half * 128 + tid;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int n = c + e;
+            const int q = c + e;
+            const int n = S::kHalfV ? q : (q & ~15) + 2 * (q >> 2 & 3) + (q & 1) + 8 * (q >> 1 & 1);
             if (n >= rows || d >= D) continue;
             float y = 0.f;
 #pragma unroll
@@ -913,10 +1030,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
               const float f = fac_s[x][n];
               y += f == 0.f ? 0.f : f * z;
             }
-            if (any_nan && nan_s[n][d >> 5] >> (d & 31) & 1) y = NAN;
+            if (any_nan[sb] && nan_s[sb][n][d >> 5] >> (d & 31) & 1) y = NAN;
             const float inv = inv_s[n];
             y = inv == 0.f ? 0.f : y * inv;
-            const long long to = out_s[n] * D + d;
+            const long long to = out_s[sb][n] * D + d;
             if (!whole) p.part_o[to] = y;
             else if constexpr (F16) reinterpret_cast<__half*>(p.out)[to] = __float2half_rn(y);
             else reinterpret_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(y);
@@ -925,6 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
       }
       tc_fence_before();
       sync_of(3, kSoft);  // the rows' state is free
+      mbar_arrive(&seg_done[sb]);
     }
   }
   tc_fence_before();
