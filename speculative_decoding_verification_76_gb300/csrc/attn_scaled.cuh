@@ -178,6 +178,10 @@ SPEC_DEV void tmem_ld_frag(uint32_t addr, uint32_t* r) {
         : "r"(addr));
 }
 
+SPEC_DEV void tmem_ld2(uint32_t addr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+}
+
 SPEC_DEV void tmem_ld8(uint32_t addr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
@@ -213,16 +217,18 @@ SPEC_DEV void sync_of(int id, int n) {
   asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
-// mbar_wait with little code (an instance holds a dozen, and what does not run still has to be
-// fetched): suspended polls of up to 1 us, `polls` of them.
+// mbar_wait with little code (what an instance holds in its loops has to stay in the SM's instruction cache:
+// with waits, rare paths and unrolled loops written out, 64 ragged chains took 378 us against 293): suspended
+// polls of up to 1 us, `polls` of them.  The roles set the error word when they end.
 SPEC_DEV bool wait_for(uint64_t* bar, uint32_t parity, const Params& p) {
+  uint32_t left = p.polls;
 #pragma unroll 1
-  for (uint32_t i = 0; !mbar_try_wait_ns(bar, parity, 1000); ++i)
-    if (i > p.polls) {
-      set_error(p.err, SPEC_ERR_MBAR_TIMEOUT);
-      return false;
-    }
+  while (!mbar_try_wait_ns(bar, parity, 1000))
+    if (left-- == 0) return false;
   return true;
+}
+SPEC_DEV void report(bool ok, const Params& p) {
+  if (!ok) set_error(p.err, SPEC_ERR_MBAR_TIMEOUT);
 }
 
 SPEC_DEV uint32_t f16x2(float lo, float hi) {
@@ -441,44 +447,52 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
     bool ok = true;
     for (Walk walk = start; walk.more() && ok; walk.next(p)) {
       const int n = walk.count();
-      int t = walk.seq.first + walk.first_unit() * kUnit + first + lane;
       const int32_t* bt = p.table + (size_t)walk.b * p.max_pages;
       const char* kh = p.k + walk.kvh * p.head_stride;
       const char* vh = p.v + walk.kvh * p.head_stride;
-      int id[kMine];
+      // page and offset of this lane's positions of the next tile
+      int t = walk.seq.first + walk.first_unit() * kUnit + first + lane, id[kMine], off[kMine];
+      auto look_up = [&]() {
 #pragma unroll
-      for (int m = 0; m < kMine; ++m)
-        id[m] = t + 32 * m < walk.seq.end ? bt[p.P.quot(t + 32 * m)] : -1;
+        for (int m = 0; m < kMine; ++m) {
+          const int tm = t + 32 * m, page = p.P.quot(tm);
+          off[m] = tm - page * p.P.d;
+          id[m] = tm < walk.seq.end ? bt[page] : -1;
+        }
+      };
+      look_up();
 #pragma unroll 1
-      for (int j = 0; j < n; ++j, ++g, t += kUnit) {
+      for (int j = 0; j < n; ++j, ++g) {
         const int stage = g % NS;
         long long row[kMine], sc[kMine];
         uint32_t here[kMine];
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
-          const int tm = t + 32 * m, off = tm - p.P.quot(tm) * p.P.d;
-          const bool ok_id = id[m] >= 0 && id[m] < p.num_pages;
+          const bool ok_id = (uint32_t)id[m] < (uint32_t)p.num_pages;
           here[m] = __ballot_sync(0xffffffffu, ok_id);
-          row[m] = ok_id ? id[m] * p.page_stride + off * p.token_stride : 0;
-          sc[m] = ((long long)id[m] * nb + p.block.quot(off)) * p.Hkv + walk.kvh;
-          const int tn = tm + kUnit;
-          id[m] = j + 1 < n && tn < walk.seq.end ? bt[p.P.quot(tn)] : -1;
+          row[m] = ok_id ? id[m] * p.page_stride + off[m] * p.token_stride : 0;
+          sc[m] = ((long long)id[m] * nb + p.block.quot(off[m])) * p.Hkv + walk.kvh;
         }
+        t += kUnit;
+        if (j + 1 < n) look_up();
         // (the warp as one: the shuffles below need every lane)
         if (g >= NS)
           ok = __all_sync(0xffffffffu, wait_for(&empty[stage], ((g / NS) - 1) & 1, p));
         if (!ok) break;
         const uint32_t v_at = base + stage * S::kStageBytes, k_at = v_at + S::kTileBytes;
-#pragma unroll
+#pragma unroll 1
         for (int m = 0; m < kMine; ++m) {
+          const long long mine = m ? row[1] : row[0], my_sc = m ? sc[1] : sc[0];
+          const uint32_t there = m ? here[1] : here[0];
+          const int r0 = first + 32 * m;
 #pragma unroll
           for (int i = 0; i < L; ++i) {
             const int r = i * kRows + sub;
-            const long long from = __shfl_sync(0xffffffffu, row[m], r) + chunk * 16;
-            const uint32_t bytes = here[m] >> r & 1 ? 16u : 0u;
+            const long long from = __shfl_sync(0xffffffffu, mine, r) + chunk * 16;
+            const uint32_t bytes = there >> r & 1 ? 16u : 0u;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const uint32_t to = swizzled<D>(kUnit, first + 32 * m + r, chunk + x * L);
+              const uint32_t to = swizzled<D>(kUnit, r0 + r, chunk + x * L);
               asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(
                                k_at + to),
                            "l"(kh + from + x * L * 16), "r"(bytes), "l"(pol)
@@ -489,13 +503,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
                            : "memory");
             }
           }
-          const uint32_t s_at = v_at + 2 * S::kTileBytes + (first + 32 * m + lane) * 4;
-          const bool mine = here[m] >> lane & 1;
+          const uint32_t s_at = v_at + 2 * S::kTileBytes + (r0 + lane) * 4;
+          const bool is_there = there >> lane & 1;
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_at),
-                       "l"(mine ? p.ks + sc[m] : &g_unseen)
+                       "l"(is_there ? p.ks + my_sc : &g_unseen)
                        : "memory");
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_at + 512),
-                       "l"(mine ? p.vs + sc[m] : &g_unseen)
+                       "l"(is_there ? p.vs + my_sc : &g_unseen)
                        : "memory");
         }
         if (g != p.withhold_stage)  // (a test can withhold one: its waiters time out)
@@ -505,6 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    report(ok, p);
   } else if (warp == kScoreWarp) {
     // ================================================================ S^T = K Q^T, one thread
     if (lane == 0) {
@@ -514,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
       bool ok = true;
       for (Walk walk = start; walk.more() && ok; walk.next(p), ++seg) {
         const int n = walk.count();
-        if (!wait_for(&q_full[seg & 1], seg >> 1 & 1, p)) break;
+        if (!(ok = wait_for(&q_full[seg & 1], seg >> 1 & 1, p))) break;
         const uint32_t q_lo = desc_lo(q_at + seg % S::kQBufs * S::kQBytes, 16);
 #pragma unroll 1
         for (int j = 0; j < n; ++j, ++g) {
@@ -531,17 +546,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
 #pragma unroll
           for (int k = 0; k < D / 32; ++k) {
             constexpr int kIn = D == 64 ? 2 : 4;  // steps within a swizzled row
+            const uint32_t a = k_lo + ((k / kIn) * (kUnit * 128) + k % kIn * 32) / 16;
+            uint32_t b = q_lo + ((k / kIn) * (RT * 128) + k % kIn * 32) / 16;
 #pragma unroll
-            for (int part = 0; part < S::kParts; ++part)
-              mma_f8(tmem + (g & 1) * RT, k_lo + ((k / kIn) * (kUnit * 128) + k % kIn * 32) / 16, kHi,
-                     q_lo + (part * RT * D + (k / kIn) * (RT * 128) + k % kIn * 32) / 16, kHi, kId,
-                     k > 0 || part > 0);
+            for (int part = 0; part < S::kParts; ++part, b += RT * D / 16)
+              mma_f8(tmem + (g & 1) * RT, a, kHi, b, kHi, kId, k > 0 || part > 0);
           }
           tc_commit(&s_full[g & 1]);
           tc_commit(&empty[stage]);
         }
       }
-      // nothing of this thread's is in flight when the tensor memory goes
+      // (nothing of this thread's is in flight when the tensor memory goes)
+      report(ok, p);
       tc_commit(&fin);
       wait_for(&fin, 0, p);
     }
@@ -576,9 +592,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
             constexpr uint32_t kHi = desc_hi(S::kRows8, S::kLayout);
             const int stage = g % NS;
             const uint32_t v_lo = desc_lo(base + stage * S::kStageBytes, 16384);
-#pragma unroll
+#pragma unroll 1
             for (int half = 0; half < S::kHalves; ++half)
-#pragma unroll
+#pragma unroll 1
               for (int k = 0; k < kUnit / 32; ++k) {
                 const uint32_t a = v_lo + (half * (kUnit * 128) + k * 4 * S::kRows8) / 16;
                 const uint32_t d = o + half * 3 * RT;
@@ -592,6 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         }
         if (ok) tc_commit(&o_full);
       }
+      report(ok, p);
       tc_commit(&fin);
       wait_for(&fin, 0, p);
     }
@@ -632,27 +649,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
             }
           }
         };
-        // the largest magnitude as bits (of fp16 or bf16 pairs: what is not finite has all exponent bits)
-        constexpr uint32_t kInf = F16 ? 0x7c00u : 0x7f80u;
-        uint32_t big = 0;
-        bool bad = false;
+        // the largest magnitude, as bits; what is not finite has all exponent bits
+        uint32_t big2 = 0;
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
           const int c = x0 + m * kPer;
           const uint4 w = real && c < D / 8 ? src[c] : make_uint4(0, 0, 0, 0);
-          const uint32_t u[4] = {w.x & 0x7fff7fffu, w.y & 0x7fff7fffu, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t lo = u[e] & 0xffffu, hi = u[e] >> 16;
-            bad = bad || lo >= kInf || hi >= kInf;
-            big = max(big, max(lo >= kInf ? 0u : lo, hi >= kInf ? 0u : hi));
-          }
+          big2 = __vimax3_u16x2(big2, w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
+          big2 = __vimax3_u16x2(big2, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu);
         }
 #pragma unroll
-        for (int o = 1; o < kPer; o <<= 1) {
-          big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-          bad = __shfl_xor_sync(0xffffffffu, (int)bad, o) || bad;
-        }
+        for (int o = 1; o < kPer; o <<= 1) big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, o));
+        const uint32_t big = max(big2 & 0xffffu, big2 >> 16);
+        const bool bad = big >= (F16 ? 0x7c00u : 0x7f80u);  // (then only the row's scale matters)
         const float s = needed_scale(F16 ? __half2float(__ushort_as_half((unsigned short)big))
                                          : __uint_as_float(big << 16));
         const float down = 1.f / s;
@@ -723,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
           // (the product that read the buffer last is complete)
           if (g >= 2) ok = ok && wait_for(&pv_done[(g - 2) & 3], (g - 2) >> 2 & 1, p);
           uint8_t* to = v16_0 + (g & 1) * S::kVBytes + tok * 128;
-#pragma unroll
+#pragma unroll 4
           for (int c = 0; c < D / 16; ++c) {
             const uint4 w = *reinterpret_cast<const uint4*>(vrow + swizzled<D>(kUnit, tok, c));
             uint4 h0, h1;
@@ -744,6 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
       }
       if (any_of(4, kPrep, !ok)) break;
     }
+    report(ok, p);
   } else {
     // ================================================================ scores into weights
     // Two groups of four warps take the tiles in turn, each with references, sums and an O of its
@@ -1003,24 +1013,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         }
       }
       sync_of(3, kSoft);
+      // (a group takes every other two columns of O; of three 8-bit parts, a column and the next are rows n
+      // and n + 1)
 #pragma unroll 1
-      for (int c = group * 8; c < RT && (S::kHalfV ? c : c & ~15) < rows; c += 16) {
-        // (a group takes every other eight columns of O)
-#pragma unroll
+      for (int c = 2 * group; c < RT; c += 4) {
+        const int n0 = S::kHalfV ? c : (c & ~15) + 2 * (c >> 2 & 3) + 8 * (c >> 1 & 1);
+        if (n0 >= rows) continue;
+#pragma unroll 1
         for (int half = 0; half < S::kHalves; ++half) {
-          uint32_t o[2][S::kSums][8];
+          uint32_t o[2][S::kSums][2];
 #pragma unroll
           for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int y = 0; y < S::kSums; ++y)
-              tmem_ld8(lanes + S::kColO + x * S::kOCols + (half * S::kSums + y) * RT + c, o[x][y]);
+              tmem_ld2(lanes + S::kColO + x * S::kOCols + (half * S::kSums + y) * RT + c, o[x][y]);
           tmem_wait_ld();
           const int d = half * 128 + tid;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int q = c + e;
-            const int n = S::kHalfV ? q : (q & ~15) + 2 * (q >> 2 & 3) + (q & 1) + 8 * (q >> 1 & 1);
-            if (n >= rows || d >= D) continue;
+          for (int e = 0; e < 2; ++e) {
+            const int n = n0 + e;
+            if (n >= rows || d >= D) break;
             float y = 0.f;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -1044,6 +1056,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
       sync_of(3, kSoft);  // the rows' state is free
       mbar_arrive(&seg_done[sb]);
     }
+    report(ok, p);
   }
   tc_fence_before();
   __syncthreads();
