@@ -85,7 +85,13 @@ extern "C" spec_status spec_verify_attn_scaled(
   if ((((q_stride_b | q_stride_r | q_stride_h) * 2) & 15) ||
       ((page_stride | token_stride | head_stride) & 15))
     return SPEC_EINVAL;
-  // positions, and the batch's tiles over all KV heads, are counted in 31 bits
+  // cache rows are numbered in token strides, in 31 bits
+  if (token_stride < 1) return SPEC_EINVAL;
+  if (page_stride % token_stride || token_stride > UINT32_MAX) return SPEC_EUNSUPPORTED;
+  const int64_t page_rows = page_stride / token_stride;
+  if (page_rows > INT32_MAX || page_rows * (num_pages - 1) + page_size > INT32_MAX)
+    return SPEC_EUNSUPPORTED;
+  // so are positions, and the batch's tiles over all KV heads
   if ((long long)max_pages * page_size > INT32_MAX - 512 || B > INT32_MAX - 512)
     return SPEC_EUNSUPPORTED;
   const double units = ((double)max_pages * page_size / scaled_attn::kUnit + 1) * B * Hkv;
@@ -114,9 +120,9 @@ extern "C" spec_status spec_verify_attn_scaled(
   p.q_stride_b = q_stride_b;
   p.q_stride_r = q_stride_r;
   p.q_stride_h = q_stride_h;
-  p.page_stride = page_stride;
-  p.token_stride = token_stride;
   p.head_stride = head_stride;
+  p.token_stride = (uint32_t)token_stride;
+  p.page_rows = (uint32_t)page_rows;
   p.P = FastDiv(page_size);
   p.block = FastDiv(block);
   p.per_head = FastDiv(Hq / Hkv);

@@ -45,11 +45,10 @@ namespace scaled_attn {
 constexpr int kUnit = 128;                       // positions of a tile
 constexpr int kGroup = 128;                      // threads of a soft group
 constexpr int kSoftWarps = 8, kSoft = 2 * kGroup;
-constexpr int kPrepWarp0 = kSoftWarps, kPrepWarps = 4, kPrep = 32 * kPrepWarps;
-constexpr int kScoreWarp = kPrepWarp0 + kPrepWarps, kSumWarp = kScoreWarp + 1;  // a thread each issues MMAs
-constexpr int kCopyWarp0 = kSumWarp + 1, kCopyWarps = 2;
-constexpr int kCopy = 32 * kCopyWarps;
-constexpr int kThreads = 32 * (kCopyWarp0 + kCopyWarps);
+constexpr int kLoadWarp0 = kSoftWarps, kLoadWarps = 4, kLoad = 32 * kLoadWarps;
+constexpr int kScoreWarp = kLoadWarp0 + kLoadWarps, kSumWarp = kScoreWarp + 1;  // a thread each issues MMAs
+constexpr int kThreads = 32 * (kSumWarp + 1);
+static_assert(kLoad == kUnit, "a position of the tile for each");
 constexpr float kNone = -1e30f;                  // the reference of a row that has seen nothing
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -62,7 +61,8 @@ struct Params {
   float *lse, *part_o, *part_ml;
   int32_t* err;
   long long q_stride_b, q_stride_r, q_stride_h;       // elements
-  long long page_stride, token_stride, head_stride;   // bytes
+  long long head_stride;             // bytes
+  uint32_t token_stride, page_rows;  // bytes; page stride in token strides
   FastDiv P, block, per_head;        // page size, block, query heads of a KV head
   int B, R, Hq, Hkv, G, num_pages, max_pages, window;
   int tiles, rows_per_tile, teams;   // row tiles of a KV head, their query rows; ranges
@@ -290,9 +290,8 @@ struct Shape {
   static constexpr int kVBytes = kHalfV ? 2 * kTileBytes : 0;
   // buffers of Q (the next segment's is made while this one's is used) and of weights (with four, those
   // who write them need not wait for the product two tiles back), where there is room
-  static constexpr int kQBufs = RT == 64 && F16 ? 1 : 2, kPBufs = RT == 64 || D == 256 ? 2 : 4;
-  static constexpr int kTokBytes = kUnit * 16;                  // a tile's scales, as the weights take them
-  static constexpr int kFixed = kQBufs * kQBytes + kPBufs * kPBytes + 2 * kVBytes + 4 * kTokBytes + 1024;
+  static constexpr int kQBufs = RT == 64 && F16 ? 1 : 2, kPBufs = 2;
+  static constexpr int kFixed = kQBufs * kQBytes + kPBufs * kPBytes + 2 * kVBytes + 1024;
   static constexpr int kRoom = 225 * 1024 - 11 * 1024 - kFixed; // (static shared memory: < 11 KB)
   static constexpr int kStages = kRoom / kStageBytes < 8 ? kRoom / kStageBytes : 8;
   static_assert(kStages >= 1, "a ring needs a stage");
@@ -343,8 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
   constexpr int kGroups = RT / 8;                    // column groups of eight
   constexpr int kB = kGroups < 4 ? kGroups : 4;      // of them between two votes
   extern __shared__ uint8_t dyn[];
-  __shared__ __align__(8) uint64_t full[NS], empty[NS], prep[4], v_full[2], s_full[2], p_full[2], pv_done[4],
-      q_full[2], seg_done[2], o_full, fin;
+  __shared__ __align__(8) uint64_t full[NS], empty[NS], s_full[2], p_full[2], pv_done[4], q_full[2],
+      seg_done[2], o_full, fin;
   // per segment, two in flight: scale, block rows seen, first position, output row of a query row
   __shared__ __align__(16) float sc_s[2][RT];
   __shared__ uint64_t see_s[2][RT];
@@ -364,7 +363,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
   uint8_t* const v16_0 = dyn + (v16_at - smem_u32(dyn));
   uint8_t* const dyn0 = v16_0 + 2 * S::kVBytes;
   uint8_t* const q_0 = dyn0 + NS * S::kStageBytes;
-  float4* const tok_s = reinterpret_cast<float4*>(q_0 + S::kQBufs * S::kQBytes + S::kPBufs * S::kPBytes);  // [4][kUnit]
   const int rows = min(p.rows_per_tile, p.R * p.G - tile * p.rows_per_tile);
 
   chain_wait();
@@ -402,18 +400,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
     }
     if (threadIdx.x == 0) {
       for (int i = 0; i < NS; ++i) {
-        mbar_init(&full[i], kCopy);
-        mbar_init(&empty[i], kPrep + (S::kHalfV ? 1 : 2));  // scales (and V) taken, K's (and V's) product
+        mbar_init(&full[i], kLoad);
+        mbar_init(&empty[i], kGroup + (S::kHalfV ? 1 : 2));  // scales (and V) taken, K's (and V's) product
       }
-      for (int i = 0; i < 4; ++i) {
-        mbar_init(&prep[i], kPrep);
-        mbar_init(&pv_done[i], 1);
-      }
+      for (int i = 0; i < 4; ++i) mbar_init(&pv_done[i], 1);
       for (int i = 0; i < 2; ++i) {
-        mbar_init(&v_full[i], kPrep);
         mbar_init(&s_full[i], 1);
         mbar_init(&p_full[i], kGroup);
-        mbar_init(&q_full[i], kPrep);
+        mbar_init(&q_full[i], kLoad);
         mbar_init(&seg_done[i], kSoft);
       }
       mbar_init(&o_full, 1);
@@ -430,205 +424,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
   }
   const uint32_t tmem = tmem_base;
 
-  if (warp >= kCopyWarp0) {
-    // ================================================================ copy warps
-    // a lane copies chunks c and c + L of a row (L lanes of a row, 32 / L rows an instruction)
+  if (warp >= kLoadWarp0 && warp < kScoreWarp) {
+    // ================================================================ K, V, their scales, and Q
+    // a thread looks up one position; a lane copies chunks c and c + L of a row (L lanes of a row)
     constexpr int L = D / 32, kRows = 32 / L;
-    constexpr int kMine = kUnit / kCopy;       // positions of a lane: 32 apart
-    const int w = warp - kCopyWarp0, first = w * 32 * kMine;
+    const int tid = threadIdx.x - 32 * kLoadWarp0, r0 = tid & ~31;
     const int sub = lane / L, chunk = lane % L;
     uint64_t pol;
     if (p.tiles == 1)  // the only reader of these rows
       asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
     else
       asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
-    const int nb = p.P.d / p.block.d;
-    int g = 0;
-    bool ok = true;
-    for (Walk walk = start; walk.more() && ok; walk.next(p)) {
-      const int n = walk.count();
-      const int32_t* bt = p.table + (size_t)walk.b * p.max_pages;
-      const char* kh = p.k + walk.kvh * p.head_stride;
-      const char* vh = p.v + walk.kvh * p.head_stride;
-      // page and offset of this lane's positions of the next tile
-      int t = walk.seq.first + walk.first_unit() * kUnit + first + lane, id[kMine], off[kMine];
-      auto look_up = [&]() {
-#pragma unroll
-        for (int m = 0; m < kMine; ++m) {
-          const int tm = t + 32 * m, page = p.P.quot(tm);
-          off[m] = tm - page * p.P.d;
-          id[m] = tm < walk.seq.end ? bt[page] : -1;
-        }
-      };
-      look_up();
-#pragma unroll 1
-      for (int j = 0; j < n; ++j, ++g) {
-        const int stage = g % NS;
-        long long row[kMine], sc[kMine];
-        uint32_t here[kMine];
-#pragma unroll
-        for (int m = 0; m < kMine; ++m) {
-          const bool ok_id = (uint32_t)id[m] < (uint32_t)p.num_pages;
-          here[m] = __ballot_sync(0xffffffffu, ok_id);
-          row[m] = ok_id ? id[m] * p.page_stride + off[m] * p.token_stride : 0;
-          sc[m] = ((long long)id[m] * nb + p.block.quot(off[m])) * p.Hkv + walk.kvh;
-        }
-        t += kUnit;
-        if (j + 1 < n) look_up();
-        // (the warp as one: the shuffles below need every lane)
-        if (g >= NS)
-          ok = __all_sync(0xffffffffu, wait_for(&empty[stage], ((g / NS) - 1) & 1, p));
-        if (!ok) break;
-        const uint32_t v_at = base + stage * S::kStageBytes, k_at = v_at + S::kTileBytes;
-#pragma unroll 1
-        for (int m = 0; m < kMine; ++m) {
-          const long long mine = m ? row[1] : row[0], my_sc = m ? sc[1] : sc[0];
-          const uint32_t there = m ? here[1] : here[0];
-          const int r0 = first + 32 * m;
-#pragma unroll
-          for (int i = 0; i < L; ++i) {
-            const int r = i * kRows + sub;
-            const long long from = __shfl_sync(0xffffffffu, mine, r) + chunk * 16;
-            const uint32_t bytes = there >> r & 1 ? 16u : 0u;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t to = swizzled<D>(kUnit, r0 + r, chunk + x * L);
-              asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(
-                               k_at + to),
-                           "l"(kh + from + x * L * 16), "r"(bytes), "l"(pol)
-                           : "memory");
-              asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(
-                               v_at + to),
-                           "l"(vh + from + x * L * 16), "r"(bytes), "l"(pol)
-                           : "memory");
-            }
-          }
-          const uint32_t s_at = v_at + 2 * S::kTileBytes + (r0 + lane) * 4;
-          const bool is_there = there >> lane & 1;
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_at),
-                       "l"(is_there ? p.ks + my_sc : &g_unseen)
-                       : "memory");
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_at + 512),
-                       "l"(is_there ? p.vs + my_sc : &g_unseen)
-                       : "memory");
-        }
-        if (g != p.withhold_stage)  // (a test can withhold one: its waiters time out)
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                           smem_u32(&full[stage]))
-                       : "memory");
-      }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    report(ok, p);
-  } else if (warp == kScoreWarp) {
-    // ================================================================ S^T = K Q^T, one thread
-    if (lane == 0) {
-      constexpr uint32_t kId = idesc_f8(128, RT, false, false);
-      constexpr uint32_t kHi = desc_hi(S::kRows8, S::kLayout);
-      int g = 0, seg = 0;
-      bool ok = true;
-      for (Walk walk = start; walk.more() && ok; walk.next(p), ++seg) {
-        const int n = walk.count();
-        if (!(ok = wait_for(&q_full[seg & 1], seg >> 1 & 1, p))) break;
-        const uint32_t q_lo = desc_lo(q_at + seg % S::kQBufs * S::kQBytes, 16);
-#pragma unroll 1
-        for (int j = 0; j < n; ++j, ++g) {
-          const int stage = g % NS;
-          // the score buffer's last tile has been read, the weights' last product is complete (both for
-          // who takes these scores), and this tile has landed
-          ok = (g < 2 || wait_for(&p_full[g & 1], (g - 2) >> 1 & 1, p)) &&
-               (S::kPBufs == 2 || g < 4 || wait_for(&pv_done[g & 3], (g - 4) >> 2 & 1, p)) &&
-               wait_for(&prep[g & 3], g >> 2 & 1, p);
-          if (!ok) break;
-          fence_proxy_async();  // the copies' writes, for the tensor cores
-          tc_fence_after();
-          const uint32_t k_lo = desc_lo(base + stage * S::kStageBytes + S::kTileBytes, 16);
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            constexpr int kIn = D == 64 ? 2 : 4;  // steps within a swizzled row
-            const uint32_t a = k_lo + ((k / kIn) * (kUnit * 128) + k % kIn * 32) / 16;
-            uint32_t b = q_lo + ((k / kIn) * (RT * 128) + k % kIn * 32) / 16;
-#pragma unroll
-            for (int part = 0; part < S::kParts; ++part, b += RT * D / 16)
-              mma_f8(tmem + (g & 1) * RT, a, kHi, b, kHi, kId, k > 0 || part > 0);
-          }
-          tc_commit(&s_full[g & 1]);
-          tc_commit(&empty[stage]);
-        }
-      }
-      // (nothing of this thread's is in flight when the tensor memory goes)
-      report(ok, p);
-      tc_commit(&fin);
-      wait_for(&fin, 0, p);
-    }
-    __syncwarp();
-  } else if (warp == kSumWarp) {
-    // ================================================================ O^T += V^T W^T, one thread
-    if (lane == 0) {
-      constexpr uint32_t kHiW = desc_hi(2048, 0);
-      int g = 0;
-      bool ok = true;
-      for (Walk walk = start; walk.more() && ok; walk.next(p)) {
-        const int n = walk.count();
-#pragma unroll 1
-        for (int j = 0; j < n; ++j, ++g) {
-          ok = wait_for(&v_full[g & 1], g >> 1 & 1, p) && wait_for(&p_full[g & 1], g >> 1 & 1, p);
-          if (!ok) break;
-          if constexpr (!S::kHalfV) fence_proxy_async();
-          tc_fence_after();
-          const uint32_t w_lo = desc_lo(p_at + g % S::kPBufs * S::kPBytes, 128);
-          const uint32_t o = tmem + S::kColO + (g & 1) * S::kOCols;
-          const uint32_t later = j >= 2;  // this group's O holds something
-          if constexpr (S::kHalfV) {
-            // (D = 64: rows 64 .. 127 are what lies behind the tile, and are not used)
-            constexpr uint32_t kId = idesc_f16(128, RT), kHiV = desc_hi(1024, 2);
-            const uint32_t v_lo = desc_lo(v16_at + (g & 1) * S::kVBytes, kUnit * 128);
-#pragma unroll
-            for (int k = 0; k < kUnit / 16; ++k)
-              mma_f16(o, v_lo + k * 2048 / 16, kHiV, w_lo + k * 256 / 16, kHiW, kId, k > 0 ? 1u : later);
-          } else {
-            constexpr uint32_t kIdP = idesc_f8(128, 2 * RT, false, true);
-            constexpr uint32_t kIdL = idesc_f8(128, RT, true, true);
-            constexpr uint32_t kHi = desc_hi(S::kRows8, S::kLayout);
-            const int stage = g % NS;
-            const uint32_t v_lo = desc_lo(base + stage * S::kStageBytes, 16384);
-#pragma unroll 1
-            for (int half = 0; half < S::kHalves; ++half)
-#pragma unroll 1
-              for (int k = 0; k < kUnit / 32; ++k) {
-                const uint32_t a = v_lo + (half * (kUnit * 128) + k * 4 * S::kRows8) / 16;
-                const uint32_t d = o + half * 3 * RT;
-                mma_f8(d, a, kHi, w_lo + k * 512 / 16, kHiW, kIdP, k > 0 ? 1u : later);
-                mma_f8(d + 2 * RT, a, kHi, w_lo + (2 * RT * kUnit + k * 512) / 16, kHiW, kIdL,
-                       k > 0 ? 1u : later);
-              }
-            tc_commit(&empty[stage]);
-          }
-          tc_commit(&pv_done[g & 3]);
-        }
-        if (ok) tc_commit(&o_full);
-      }
-      report(ok, p);
-      tc_commit(&fin);
-      wait_for(&fin, 0, p);
-    }
-    __syncwarp();
-  } else if (warp >= kPrepWarp0) {
-    // ================================================================ operands: Q, scales, fp16 V
-    const int tid = threadIdx.x - 32 * kPrepWarp0, tok = tid;  // a position of the tile
-    const int range0 = start.s;
+    const int nb = p.P.d / p.block.d, range0 = start.s;
     int g = 0, seg = 0;
     bool ok = true;
-    for (Walk walk = start; walk.more(); walk.next(p), ++seg) {
-      const int b = walk.b, n_units = walk.count(), ctx = walk.seq.ctx, sb = seg & 1;
+    for (Walk walk = start; walk.more() && ok; walk.next(p), ++seg) {
+      const int b = walk.b, n_units = walk.count(), ctx = walk.seq.ctx, end = walk.seq.end, sb = seg & 1;
       const bool whole = n_units == walk.seq.units;
       const int part_at = (team * 2 + (walk.s == range0 ? 0 : 1)) * p.tiles + tile;
+      const int32_t* bt = p.table + (size_t)b * p.max_pages;
+      int t = walk.seq.first + walk.first_unit() * kUnit + tid;
+      int page = p.P.quot(t), off = t - page * p.P.d, id = t < end ? bt[page] : -1;
       // the segment before the last is done with this one's places
       if (seg >= S::kQBufs)
-        ok = ok && wait_for(&seg_done[(seg - S::kQBufs) & 1], (seg - S::kQBufs) >> 1 & 1, p);
+        ok = __all_sync(0xffffffffu,
+                        wait_for(&seg_done[(seg - S::kQBufs) & 1], (seg - S::kQBufs) >> 1 & 1, p));
+      if (!ok) break;
       // ---- Q as sums of e4m3 parts under a power of two per row
       {
-        constexpr int kPer = kPrep / RT;            // threads of a row
+        constexpr int kPer = kLoad / RT;            // threads of a row
         constexpr int kMine = D / 8 / kPer > 0 ? D / 8 / kPer : 1;  // 16-byte chunks of a thread
         const int n = tid / kPer, x0 = tid % kPer;
         const int row = tile * p.rows_per_tile + n, i = p.per_head.quot(row);
@@ -703,57 +527,148 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         if (tid == 0) any_nan[sb] = 0;
         fence_proxy_async();
         mbar_arrive(&q_full[sb]);
-        sync_of(4, kPrep);
       }
-      int t0 = walk.seq.first + walk.first_unit() * kUnit;
+      const char* kh = p.k + walk.kvh * p.head_stride + chunk * 16;
+      const char* vh = p.v + walk.kvh * p.head_stride + chunk * 16;
 #pragma unroll 1
-      for (int j = 0; j < n_units; ++j, ++g, t0 += kUnit) {
+      for (int j = 0; j < n_units; ++j, ++g) {
         const int stage = g % NS;
-        ok = ok && wait_for(&full[stage], (g / NS) & 1, p);
-        uint8_t* vrow = dyn0 + stage * S::kStageBytes;
-        // ---- K's scale, the logarithm of V's and its inverse; nothing for positions that are not there
-        {
-          const float* scales = reinterpret_cast<const float*>(vrow + 2 * S::kTileBytes);
-          const float ks = scales[tok];
-          float vs = scales[kUnit + tok];
-          vs = vs < 0x1p-100f ? 0x1p-100f : vs;
-          tok_s[(g & 3) * kUnit + tok] = ks == -INFINITY
-                                             ? make_float4(0.f, -INFINITY, 0.f, 0.f)
-                                             : make_float4(ks, __log2f(vs), __fdividef(1.f, vs), 0.f);
-          mbar_arrive(&prep[g & 3]);
-        }
-        // positions that some rows see and others do not: NaN codes of V are noted for the rows that
-        // see them, and zeroed
-        if ((t0 + kUnit > ctx && (p.R > 1 || p.mask)) || (p.window > 0 && t0 < ctx + p.R - p.window)) {
-          const int t = t0 + tok;
-          if (note_nans<D>(vrow, tok, t, t - ctx, RT, see_s[sb], from_s[sb], nan_s[sb][0])) any_nan[sb] = 1;
-        }
-        if constexpr (S::kHalfV) {  // this position's V as fp16, 64 dimensions a row
-          // (the product that read the buffer last is complete)
-          if (g >= 2) ok = ok && wait_for(&pv_done[(g - 2) & 3], (g - 2) >> 2 & 1, p);
-          uint8_t* to = v16_0 + (g & 1) * S::kVBytes + tok * 128;
-#pragma unroll 4
-          for (int c = 0; c < D / 16; ++c) {
-            const uint4 w = *reinterpret_cast<const uint4*>(vrow + swizzled<D>(kUnit, tok, c));
-            uint4 h0, h1;
-            codes_to_halves(w.x, h0.x, h0.y);
-            codes_to_halves(w.y, h0.z, h0.w);
-            codes_to_halves(w.z, h1.x, h1.y);
-            codes_to_halves(w.w, h1.z, h1.w);
-            uint8_t* half = to + (c >> 2) * (kUnit * 128);
-            const int c16 = 2 * (c & 3);
-            *reinterpret_cast<uint4*>(half + ((c16 ^ (tok & 7)) << 4)) = h0;
-            *reinterpret_cast<uint4*>(half + (((c16 + 1) ^ (tok & 7)) << 4)) = h1;
+        // (a position that is not there: zeros)
+        const bool is_there = (uint32_t)id < (uint32_t)p.num_pages;
+        const uint32_t there = __ballot_sync(0xffffffffu, is_there);
+        const uint32_t row = is_there ? id * p.page_rows + off : 0;  // in token strides
+        const long long sc = ((long long)id * nb + p.block.quot(off)) * p.Hkv + walk.kvh;
+        t += kUnit;
+        page = p.P.quot(t), off = t - page * p.P.d;
+        id = j + 1 < n_units && t < end ? bt[page] : -1;
+        // (the warp as one: the shuffles below need every lane)
+        if (g >= NS) ok = __all_sync(0xffffffffu, wait_for(&empty[stage], ((g / NS) - 1) & 1, p));
+        if (!ok) break;
+        const uint32_t v_at = base + stage * S::kStageBytes, k_at = v_at + S::kTileBytes;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+          const int r = i * kRows + sub;
+          const uint64_t from = (uint64_t)__shfl_sync(0xffffffffu, row, r) * p.token_stride;
+          const uint32_t bytes = there >> r & 1 ? 16u : 0u;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t to = swizzled<D>(kUnit, r0 + r, chunk + x * L);
+            asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(
+                             k_at + to),
+                         "l"(kh + from + x * L * 16), "r"(bytes), "l"(pol)
+                         : "memory");
+            asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(
+                             v_at + to),
+                         "l"(vh + from + x * L * 16), "r"(bytes), "l"(pol)
+                         : "memory");
           }
         }
-        fence_proxy_async();
-        mbar_arrive(&v_full[g & 1]);
-        mbar_arrive(&empty[stage]);
-        if (__any_sync(0xffffffffu, !ok)) break;
+        const uint32_t s_at = v_at + 2 * S::kTileBytes + tid * 4;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_at),
+                     "l"(is_there ? p.ks + sc : &g_unseen)
+                     : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_at + 512),
+                     "l"(is_there ? p.vs + sc : &g_unseen)
+                     : "memory");
+        if (g != p.withhold_stage)  // (a test can withhold one: its waiters time out)
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                           smem_u32(&full[stage]))
+                       : "memory");
       }
-      if (any_of(4, kPrep, !ok)) break;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     report(ok, p);
+  } else if (warp == kScoreWarp) {
+    // ================================================================ S^T = K Q^T, one thread
+    if (lane == 0) {
+      constexpr uint32_t kId = idesc_f8(128, RT, false, false);
+      constexpr uint32_t kHi = desc_hi(S::kRows8, S::kLayout);
+      int g = 0, seg = 0;
+      bool ok = true;
+      for (Walk walk = start; walk.more() && ok; walk.next(p), ++seg) {
+        const int n = walk.count();
+        if (!(ok = wait_for(&q_full[seg & 1], seg >> 1 & 1, p))) break;
+        const uint32_t q_lo = desc_lo(q_at + seg % S::kQBufs * S::kQBytes, 16);
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++g) {
+          const int stage = g % NS;
+          // the score buffer's last tile has been read, this tile has landed
+          ok = (g < 2 || wait_for(&p_full[g & 1], (g - 2) >> 1 & 1, p)) &&
+               wait_for(&full[stage], (g / NS) & 1, p);
+          if (!ok) break;
+          fence_proxy_async();  // the copies' writes, for the tensor cores
+          tc_fence_after();
+          const uint32_t k_lo = desc_lo(base + stage * S::kStageBytes + S::kTileBytes, 16);
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            constexpr int kIn = D == 64 ? 2 : 4;  // steps within a swizzled row
+            const uint32_t a = k_lo + ((k / kIn) * (kUnit * 128) + k % kIn * 32) / 16;
+            uint32_t b = q_lo + ((k / kIn) * (RT * 128) + k % kIn * 32) / 16;
+#pragma unroll
+            for (int part = 0; part < S::kParts; ++part, b += RT * D / 16)
+              mma_f8(tmem + (g & 1) * RT, a, kHi, b, kHi, kId, k > 0 || part > 0);
+          }
+          tc_commit(&s_full[g & 1]);
+          tc_commit(&empty[stage]);
+        }
+      }
+      // (nothing of this thread's is in flight when the tensor memory goes)
+      report(ok, p);
+      tc_commit(&fin);
+      wait_for(&fin, 0, p);
+    }
+    __syncwarp();
+  } else if (warp == kSumWarp) {
+    // ================================================================ O^T += V^T W^T, one thread
+    if (lane == 0) {
+      constexpr uint32_t kHiW = desc_hi(2048, 0);
+      int g = 0;
+      bool ok = true;
+      for (Walk walk = start; walk.more() && ok; walk.next(p)) {
+        const int n = walk.count();
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++g) {
+          ok = wait_for(&p_full[g & 1], g >> 1 & 1, p);
+          if (!ok) break;
+          if constexpr (!S::kHalfV) fence_proxy_async();
+          tc_fence_after();
+          const uint32_t w_lo = desc_lo(p_at + g % S::kPBufs * S::kPBytes, 128);
+          const uint32_t o = tmem + S::kColO + (g & 1) * S::kOCols;
+          const uint32_t later = j >= 2;  // this group's O holds something
+          if constexpr (S::kHalfV) {
+            // (D = 64: rows 64 .. 127 are what lies behind the tile, and are not used)
+            constexpr uint32_t kId = idesc_f16(128, RT), kHiV = desc_hi(1024, 2);
+            const uint32_t v_lo = desc_lo(v16_at + (g & 1) * S::kVBytes, kUnit * 128);
+#pragma unroll
+            for (int k = 0; k < kUnit / 16; ++k)
+              mma_f16(o, v_lo + k * 2048 / 16, kHiV, w_lo + k * 256 / 16, kHiW, kId, k > 0 ? 1u : later);
+          } else {
+            constexpr uint32_t kIdP = idesc_f8(128, 2 * RT, false, true);
+            constexpr uint32_t kIdL = idesc_f8(128, RT, true, true);
+            constexpr uint32_t kHi = desc_hi(S::kRows8, S::kLayout);
+            const int stage = g % NS;
+            const uint32_t v_lo = desc_lo(base + stage * S::kStageBytes, 16384);
+#pragma unroll 1
+            for (int half = 0; half < S::kHalves; ++half)
+#pragma unroll 1
+              for (int k = 0; k < kUnit / 32; ++k) {
+                const uint32_t a = v_lo + (half * (kUnit * 128) + k * 4 * S::kRows8) / 16;
+                const uint32_t d = o + half * 3 * RT;
+                mma_f8(d, a, kHi, w_lo + k * 512 / 16, kHiW, kIdP, k > 0 ? 1u : later);
+                mma_f8(d + 2 * RT, a, kHi, w_lo + (2 * RT * kUnit + k * 512) / 16, kHiW, kIdL,
+                       k > 0 ? 1u : later);
+              }
+            tc_commit(&empty[stage]);
+          }
+          tc_commit(&pv_done[g & 3]);
+        }
+        if (ok) tc_commit(&o_full);
+      }
+      report(ok, p);
+      tc_commit(&fin);
+      wait_for(&fin, 0, p);
+    }
+    __syncwarp();
   } else {
     // ================================================================ scores into weights
     // Two groups of four warps take the tiles in turn, each with references, sums and an O of its
@@ -783,18 +698,46 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
 #pragma unroll 1
       for (int j = (g ^ group) & 1; j < n_units; j += 2) {
         const int u = g + j, t0 = t_seg + j * kUnit;
-        ok = ok && wait_for(&s_full[group], u >> 1 & 1, p);
-        tc_fence_after();
-        // positions t_lane + 8 r
-        uint64_t ks2[4], lvs2[4], rvs2[4];
+        const int stage = u % NS;
+        ok = ok && wait_for(&full[stage], (u / NS) & 1, p);
+        // positions t_lane + 8 r: K's scale, the logarithm of V's and its inverse
+        uint8_t* vrow = dyn0 + stage * S::kStageBytes;
+        const float* scales = reinterpret_cast<const float*>(vrow + 2 * S::kTileBytes) + t_lane;
+        float ks[4], lvs[4], rvs[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float4 x = tok_s[(u & 3) * kUnit + t_lane + 8 * r];
-          ks2[r] = f2_pack(x.x, x.x), lvs2[r] = f2_pack(x.y, x.y), rvs2[r] = f2_pack(x.z, x.z);
+          float vs = scales[kUnit + 8 * r];
+          vs = vs < 0x1p-100f ? 0x1p-100f : vs;
+          ks[r] = scales[8 * r];
+          lvs[r] = __log2f(vs), rvs[r] = __fdividef(1.f, vs);
+          if (ks[r] == -INFINITY) ks[r] = 0.f, lvs[r] = -INFINITY, rvs[r] = 0.f;  // not there
         }
         // positions that some rows see and others do not
         const bool mixed = (t0 + kUnit > ctx && (p.R > 1 || p.mask)) ||
                            (p.window > 0 && t0 < ctx + p.R - p.window);
+        if (mixed && note_nans<D>(vrow, tid, t0 + tid, t0 + tid - ctx, RT, see_s[sb], from_s[sb], nan_s[sb][0]))
+          any_nan[sb] = 1;
+        if constexpr (S::kHalfV) {  // position tid's V as fp16, 64 dimensions a row
+          // (the product that read the buffer last is complete)
+          if (u >= 2) ok = ok && wait_for(&pv_done[(u - 2) & 3], (u - 2) >> 2 & 1, p);
+          uint8_t* to = v16_0 + group * S::kVBytes + tid * 128;
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            const uint4 w = *reinterpret_cast<const uint4*>(vrow + swizzled<D>(kUnit, tid, c));
+            uint4 h0, h1;
+            codes_to_halves(w.x, h0.x, h0.y);
+            codes_to_halves(w.y, h0.z, h0.w);
+            codes_to_halves(w.z, h1.x, h1.y);
+            codes_to_halves(w.w, h1.z, h1.w);
+            uint8_t* half = to + (c >> 2) * (kUnit * 128);
+            const int c16 = 2 * (c & 3);
+            *reinterpret_cast<uint4*>(half + ((c16 ^ (tid & 7)) << 4)) = h0;
+            *reinterpret_cast<uint4*>(half + (((c16 + 1) ^ (tid & 7)) << 4)) = h1;
+          }
+        }
+        ok = ok && wait_for(&s_full[group], u >> 1 & 1, p);
+        tc_fence_after();
+        mbar_arrive(&empty[stage]);
         const uint32_t s_at = lanes + group * RT;
         const uint32_t w_at = p_at + u % S::kPBufs * S::kPBytes + (quad * 32 + lane) * 16;
 #pragma unroll
@@ -819,7 +762,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
                 const uint32_t* y = &s[r >> 1][4 * k + 2 * (r & 1)];
                 const uint64_t x =
                     f2_mul(f2_pack(__uint_as_float(y[0]), __uint_as_float(y[1])), sc2[h + k]);
-                f2_unpack(f2_fma(x, ks2[r], f2_add(lvs2[r], nm2[h + k])), a[r][2 * k], a[r][2 * k + 1]);
+                f2_unpack(f2_fma(x, f2_pack(ks[r], ks[r]), f2_add(f2_pack(lvs[r], lvs[r]), nm2[h + k])), a[r][2 * k],
+                          a[r][2 * k + 1]);
               }
             }
             if (mixed) {
@@ -859,9 +803,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
               float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-                const float4 x = tok_s[(u & 3) * kUnit + t_lane + 8 * r];
-                float z0 = __uint_as_float(y[r >> 1][2 * (r & 1)]) * sc.x * x.x + x.y;
-                float z1 = __uint_as_float(y[r >> 1][2 * (r & 1) + 1]) * sc.y * x.x + x.y;
+                float z0 = __uint_as_float(y[r >> 1][2 * (r & 1)]) * sc.x * ks[r] + lvs[r];
+                float z1 = __uint_as_float(y[r >> 1][2 * (r & 1) + 1]) * sc.y * ks[r] + lvs[r];
                 if (mixed) {
                   const int t = t0 + t_lane + 8 * r, jb = t - ctx, n = 8 * k + c2;
                   if (!(jb < 0 ? t >= from_s[sb][n] : jb < 64 && (see_s[sb][n] >> jb & 1))) z0 = -INFINITY;
@@ -932,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
           }
           if (failed) break;
           // ---- weights and their sums
-          if constexpr (S::kPBufs == 2)
+          if constexpr (S::kPBufs == 2 && !S::kHalfV)
             if (h == 0 && u >= 2) ok = ok && wait_for(&pv_done[(u - 2) & 3], (u - 2) >> 2 & 1, p);
           uint32_t w[kB][4];
 #pragma unroll
@@ -941,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const float w0 = fast_exp2(a[r][2 * k]), w1 = fast_exp2(a[r][2 * k + 1]);
-              l2[h + k] = f2_fma(f2_pack(w0, w1), rvs2[r], l2[h + k]);
+              l2[h + k] = f2_fma(f2_pack(w0, w1), f2_pack(rvs[r], rvs[r]), l2[h + k]);
               w[k][r] = f16x2(w0, w1);
             }
             if constexpr (S::kHalfV) store_frags(w_at + (h + k) * 2048, w[k]);
