@@ -10,7 +10,8 @@
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kMostThreads = 256;
+constexpr int kFlight = 2;  // items of a thread in flight
 constexpr int kMaxPairs = kMaxRopePairs;
 
 struct RotateParams {
@@ -18,41 +19,57 @@ struct RotateParams {
   char *q_out, *k_out;
   const int32_t* pos;
   long long q_stride, k_stride, q_out_stride, k_out_stride;  // elements
-  FastDiv per, items;  // work items of a token; of a head
-  int T, Hq, Hkv, D;
+  FastDiv items;  // work items of a head
+  int Hq, Hkv, D;
   RopeTable<> rope;
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ RotateParams p) {
+__global__ void __launch_bounds__(kMostThreads) rotate_kernel(
+    const __grid_constant__ RotateParams p) {
   __shared__ __align__(16) float cs[kMaxPairs], sn[kMaxPairs];
-  const int t = blockIdx.x;
+  const int t = blockIdx.x, n = (p.Hq + p.Hkv) * p.items.d;
   chain_wait();
   const int at = p.pos[t];
+  Chunk8<T> a[kFlight], b[kFlight];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int i = i0 + f * blockDim.x;
+      if (i >= n) break;
+      const int h = p.items.quot(i), j = i - h * p.items.d;
+      const int2 c = rope_chunks(p.rope, j);
+      const T* src = h < p.Hq ? reinterpret_cast<const T*>(p.q) + t * p.q_stride + h * p.D
+                              : reinterpret_cast<const T*>(p.k) + t * p.k_stride + (h - p.Hq) * p.D;
+      a[f] = reinterpret_cast<const Chunk8<T>*>(src)[c.x];
+      b[f] = reinterpret_cast<const Chunk8<T>*>(src)[c.y];
+    }
+  };
+  load(threadIdx.x);  // (the rows are on their way while the angles are worked out)
   if (at < 0) return;
-  for (int i = threadIdx.x; i < p.D / 2; i += kThreads) {
+  for (int i = threadIdx.x; i < p.D / 2; i += blockDim.x) {
     const float2 e = rope_entry(p.rope, at, i);
     cs[i] = e.x;
     sn[i] = e.y;
   }
   __syncthreads();
-  const int n = (p.Hq + p.Hkv) * p.items.d;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int h = p.items.quot(i), j = i - h * p.items.d;
-    const bool is_q = h < p.Hq;
-    const int2 c = rope_chunks(p.rope, j);
-    const long long from = is_q ? t * p.q_stride + (long long)h * p.D
-                                : t * p.k_stride + (long long)(h - p.Hq) * p.D;
-    const long long to = is_q ? t * p.q_out_stride + (long long)h * p.D
-                              : t * p.k_out_stride + (long long)(h - p.Hq) * p.D;
-    const char* src = (is_q ? p.q : p.k) + from * (long long)sizeof(T);
-    char* dst = (is_q ? p.q_out : p.k_out) + to * (long long)sizeof(T);
-    float a[8], b[8];
-    unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(src + c.x * 8 * sizeof(T)), a);
-    unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(src + c.y * 8 * sizeof(T)), b);
-    rope_turn(p.rope.interleaved, a, b, cs + 8 * j, sn + 8 * j);
-    *reinterpret_cast<Chunk8<T>*>(dst + c.x * 8 * sizeof(T)) = pack_chunk<T>(a);
-    *reinterpret_cast<Chunk8<T>*>(dst + c.y * 8 * sizeof(T)) = pack_chunk<T>(b);
+  for (int i0 = threadIdx.x; i0 < n; i0 += kFlight * blockDim.x) {
+    if (i0 != threadIdx.x) load(i0);
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int i = i0 + f * blockDim.x;
+      if (i >= n) break;
+      const int h = p.items.quot(i), j = i - h * p.items.d;
+      const int2 c = rope_chunks(p.rope, j);
+      T* dst = h < p.Hq ? reinterpret_cast<T*>(p.q_out) + t * p.q_out_stride + h * p.D
+                        : reinterpret_cast<T*>(p.k_out) + t * p.k_out_stride + (h - p.Hq) * p.D;
+      float x[8], y[8];
+      unpack_chunk<T>(a[f], x);
+      unpack_chunk<T>(b[f], y);
+      rope_turn(p.rope.interleaved, x, y, cs + 8 * j, sn + 8 * j);
+      reinterpret_cast<Chunk8<T>*>(dst)[c.x] = pack_chunk<T>(x);
+      reinterpret_cast<Chunk8<T>*>(dst)[c.y] = pack_chunk<T>(y);
+    }
   }
 }
 
@@ -88,15 +105,15 @@ extern "C" spec_status spec_rotate(const void* q, int64_t q_stride, void* q_out,
   p.k_stride = k_stride;
   p.q_out_stride = q_out_stride;
   p.k_out_stride = k_out_stride;
-  p.T = T;
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.D = D;
   p.items = FastDiv(D / 16);
-  p.per = FastDiv((Hq + Hkv) * (D / 16));
+  const int n = (Hq + Hkv) * (D / 16);
+  const int threads = std::min(kMostThreads, ((n + kFlight - 1) / kFlight + 31) / 32 * 32);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == SPEC_F32) return launch_chained(rotate_kernel<float>, T, kThreads, 0, st, p);
+  if (dtype == SPEC_F32) return launch_chained(rotate_kernel<float>, T, threads, 0, st, p);
   if (dtype == SPEC_BF16)
-    return launch_chained(rotate_kernel<__nv_bfloat16>, T, kThreads, 0, st, p);
-  return launch_chained(rotate_kernel<__half>, T, kThreads, 0, st, p);
+    return launch_chained(rotate_kernel<__nv_bfloat16>, T, threads, 0, st, p);
+  return launch_chained(rotate_kernel<__half>, T, threads, 0, st, p);
 }
