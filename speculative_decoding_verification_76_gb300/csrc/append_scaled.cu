@@ -25,7 +25,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 16;        // rows of a CTA where there are many
 constexpr int kFewRows = 2432;   // up to sixteen per SM: a CTA per row
-constexpr int kPasses = 4;       // row groups that a warp keeps in registers
+constexpr int kPasses = 4;       // row groups (items) that a warp (thread) keeps in registers
 
 struct AppendParams {
   const char *k, *v, *q;
@@ -35,7 +35,7 @@ struct AppendParams {
   const int32_t* pos;                                        // null: no rotation
   long long k_stride, v_stride, q_stride, q_out_stride;      // elements
   long long page_stride, token_stride, head_stride;          // bytes
-  FastDiv P, block;
+  FastDiv P, block, heads, per;                              // KV heads; items of a row's queries
   int T, Hq, Hkv, W, num_slots;
   RopeTable<128> rope;
 };
@@ -46,31 +46,39 @@ SPEC_DEV long long slot_offset(const FastDiv& P, long long page_stride, long lon
   return page * page_stride + (slot - page * P.d) * token_stride;
 }
 
-// The codes of a block's rows that are not in `written`, under a new scale: a warp's work.
+SPEC_DEV void team_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// The codes of a block's rows that are not in `written`, under a new scale: the work of `threads` threads
+// (whole warps), of which this is number i.
 template <int D>
 SPEC_DEV void move_others(char* cache, long long token_stride, int block, uint64_t written,
-                          float ratio, int lane) {
-  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
-  for (int o = lane / kLanes; o < block; o += kRows)
+                          float ratio, int i, int threads) {
+  constexpr int kLanes = D / 16;
+  for (int o = i / kLanes; o < block; o += threads / kLanes)
     if (!(written >> o & 1)) {
-      uint4* p = reinterpret_cast<uint4*>(cache + o * token_stride + lane % kLanes * 16);
+      uint4* p = reinterpret_cast<uint4*>(cache + o * token_stride + i % kLanes * 16);
       *p = moved_codes(*p, ratio);
     }
 }
 
 // T: type of the rows
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) append_scaled_kernel(
+__global__ void __launch_bounds__(kThreads, 3) append_scaled_kernel(
     const __grid_constant__ AppendParams p) {
-  constexpr int kItems = D / 16;             // of a row
-  constexpr int kRows = 32 / kItems;         // rows of a warp's pass
-  constexpr int kMost = kTile + kMaxBlock;   // rows looked at
+  constexpr int kItems = D / 16;               // of a row
+  constexpr int kRows = 32 / kItems;           // rows of a warp's pass
+  constexpr int kWarpRows = kPasses * kRows;   // that a warp holds
+  constexpr int kMost = kTile + kMaxBlock;     // rows looked at
   extern __shared__ __align__(16) float table[];  // [rows][2][D/2]: cosines, sines
   __shared__ int slot_s[kMost + 1];               // of row t0 - 1 + i; -1: none
   __shared__ int pos_s[kMost + 1];
   __shared__ int run_at[kTile], run_n[kTile];     // the runs that begin here
-  __shared__ int runs, rows_end;
-  const int t0 = blockIdx.x * p.W, t1 = min(t0 + p.W, p.T);
+  __shared__ int runs, rows_end, longest;
+  __shared__ float big_s[2][kWarps];
+  const int parts = p.Hq ? 3 : 2, part = blockIdx.x % parts;  // keys, values, queries
+  const int t0 = blockIdx.x / parts * p.W, t1 = min(t0 + p.W, p.T);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   chain_wait();
   const int look = min(t1 - 1 + p.block.d, p.T);  // past the last row a run from here may have
@@ -85,34 +93,39 @@ __global__ void __launch_bounds__(kThreads) append_scaled_kernel(
     slot_s[threadIdx.x] = s;
     pos_s[threadIdx.x] = at;
   }
-  if (threadIdx.x == 0) runs = 0, rows_end = t1;
+  if (threadIdx.x == 0) runs = 0, rows_end = part == 2 ? t1 : t0, longest = 0;
   __syncthreads();
   // ---- the runs that begin in t0 .. t1 - 1, in order
-  if (warp == 0) {
-    const int t = t0 + lane;
-    bool first = false;
-    int n = 0;
-    if (t < t1 && slot_s[lane + 1] >= 0) {
-      const int b = p.block.quot(slot_s[lane + 1]), before = slot_s[lane];
-      first = before < 0 || p.block.quot(before) != b;
-      if (first) {
-        n = 1;
-        while (n < p.block.d && t + n < look && slot_s[lane + 1 + n] >= 0 &&
-               p.block.quot(slot_s[lane + 1 + n]) == b)
-          ++n;
+  if (part < 2) {
+    if (warp == 0) {
+      const int t = t0 + lane;
+      bool first = false;
+      int n = 0;
+      if (t < t1 && slot_s[lane + 1] >= 0) {
+        const int b = p.block.quot(slot_s[lane + 1]), before = slot_s[lane];
+        first = before < 0 || p.block.quot(before) != b;
+        if (first) {
+          n = 1;
+          while (n < p.block.d && t + n < look && slot_s[lane + 1 + n] >= 0 &&
+                 p.block.quot(slot_s[lane + 1 + n]) == b)
+            ++n;
+        }
       }
+      const uint32_t who = __ballot_sync(0xffffffffu, first);
+      if (first) {
+        const int i = __popc(who & ((1u << lane) - 1));
+        run_at[i] = t;
+        run_n[i] = n;
+        atomicMax(&rows_end, t + n);
+        atomicMax(&longest, n);
+      }
+      if (lane == 0) runs = __popc(who);
     }
-    const uint32_t who = __ballot_sync(0xffffffffu, first);
-    if (first) {
-      const int i = __popc(who & ((1u << lane) - 1));
-      run_at[i] = t;
-      run_n[i] = n;
-      atomicMax(&rows_end, t + n);
-    }
-    if (lane == 0) runs = __popc(who);
+    __syncthreads();
+    if (runs == 0) return;
   }
-  __syncthreads();
-  if (p.rope.pairs > 0) {
+  const bool turn = part != 1 && p.rope.pairs > 0;
+  if (turn) {
     const int n = (rows_end - t0) * (D / 2);
     for (int i = threadIdx.x; i < n; i += kThreads) {
       const int u = i / (D / 2), j = i % (D / 2);
@@ -123,112 +136,125 @@ __global__ void __launch_bounds__(kThreads) append_scaled_kernel(
     __syncthreads();
   }
 
-  // ---- keys and values: a warp takes a run of one head
-  const int items = runs * p.Hkv * 2;
+  if (part == 2) {
+    // ---- this tile's queries
+    const int n = (t1 - t0) * p.per.d;
+    for (int i0 = threadIdx.x; i0 < n; i0 += kPasses * kThreads) {
+      uint4 raw[kPasses][2];
+      bool some[kPasses];
+#pragma unroll
+      for (int x = 0; x < kPasses; ++x) {
+        const int i = i0 + x * kThreads, u = p.per.quot(i), y = i - u * p.per.d;
+        some[x] = i < n && slot_s[u + 1] >= 0;
+        if (!some[x]) continue;
+        const int2 c = rope_chunks(p.rope, y % kItems);
+        const uint4* row = reinterpret_cast<const uint4*>(
+            reinterpret_cast<const T*>(p.q) + (t0 + u) * p.q_stride + y / kItems * D);
+        raw[x][0] = __ldcs(row + c.x);
+        raw[x][1] = __ldcs(row + c.y);
+      }
+#pragma unroll
+      for (int x = 0; x < kPasses; ++x) {
+        if (!some[x]) continue;
+        const int i = i0 + x * kThreads, u = p.per.quot(i), y = i - u * p.per.d, j = y % kItems;
+        const int2 c = rope_chunks(p.rope, j);
+        uint4* to = reinterpret_cast<uint4*>(
+            reinterpret_cast<T*>(p.q_out) + (t0 + u) * p.q_out_stride + y / kItems * D);
+        float a[8], e[8];
+        unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&raw[x][0]), a);
+        unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&raw[x][1]), e);
+        if (turn)
+          rope_turn(p.rope.interleaved, a, e, table + u * D + 8 * j, table + u * D + D / 2 + 8 * j);
+        to[c.x] = pack_chunk<T>(a).w[0];
+        to[c.y] = pack_chunk<T>(e).w[0];
+      }
+    }
+    return;
+  }
+
+  // ---- keys or values: a team of warps, as many as hold the longest run, takes a run of one head
+  int team_warps = 1;
+  while (team_warps * kWarpRows < longest) team_warps *= 2;
+  const int team = warp / team_warps, mine = warp % team_warps, threads = 32 * team_warps;
+  const int items = runs * p.Hkv, step = kWarps / team_warps;
   const int j = lane % kItems, sub = lane / kItems;   // item of a row, row of a pass
-  for (int i = warp; i < items; i += kWarps) {
-    const int r = i / (2 * p.Hkv), w = i - r * 2 * p.Hkv;
-    const bool is_k = w < p.Hkv;
-    const int h = is_k ? w : w - p.Hkv;
-    const int at = run_at[r], n = run_n[r], s0 = slot_s[at - t0 + 1];
-    const int b = p.block.quot(s0);
+  const bool is_k = part == 0;
+  const int2 c = is_k ? rope_chunks(p.rope, j) : make_int2(j, j + kItems);
+  int buf = 0;
+  for (int i = team; i < items; i += step, buf ^= 1) {
+    const int r = p.heads.quot(i), h = i - r * p.Hkv;
+    const int at = run_at[r], n = run_n[r], first = at - t0 + 1;
+    const int b = p.block.quot(slot_s[first]);
     const T* src = reinterpret_cast<const T*>(is_k ? p.k : p.v) + h * D;
     const long long stride = is_k ? p.k_stride : p.v_stride;
     float* scale = (is_k ? p.ks : p.vs) + (long long)b * p.Hkv + h;
     const float stored = *scale;
-    const bool turn = is_k && p.rope.pairs > 0;
-    const int2 c = is_k ? rope_chunks(p.rope, j) : make_int2(j, j + kItems);
+    const int base = mine * kWarpRows;
     uint4 raw[kPasses][2];
-    // rows base .. of the run, kPasses groups of kRows (rows behind the last: the last again)
-    auto load = [&](int base) {
 #pragma unroll
-      for (int x = 0; x < kPasses; ++x) {
-        if (base + x * kRows >= n) break;
-        const int t = at + min(base + x * kRows + sub, n - 1);
-        const uint4* row = reinterpret_cast<const uint4*>(src + t * stride);
-        raw[x][0] = row[c.x];
-        raw[x][1] = row[c.y];
-      }
-    };
-    auto values = [&](int x, int base, float* a, float* e) {
+    for (int x = 0; x < kPasses; ++x) {  // (rows behind the last: the last again)
+      if (base + x * kRows >= n) break;
+      const int t = at + min(base + x * kRows + sub, n - 1);
+      const uint4* row = reinterpret_cast<const uint4*>(src + t * stride);
+      raw[x][0] = __ldcs(row + c.x);
+      raw[x][1] = __ldcs(row + c.y);
+    }
+    auto values = [&](int x, float* a, float* e) {
       unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&raw[x][0]), a);
       unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&raw[x][1]), e);
       if (turn) {
-        const float* cs = table + (at - t0 + min(base + x * kRows + sub, n - 1)) * D + 8 * j;
+        const float* cs = table + (first - 1 + min(base + x * kRows + sub, n - 1)) * D + 8 * j;
         rope_turn(p.rope.interleaved, a, e, cs, cs + D / 2);
       }
     };
-    float big = 0.f;
     uint32_t lo = 0, hi = 0;  // written places of the block
     for (int u = lane; u < n; u += 32) {
-      const int o = slot_s[at - t0 + 1 + u] - b * p.block.d;
+      const int o = slot_s[first + u] - b * p.block.d;
       if (o < 32) lo |= 1u << o; else hi |= 1u << (o - 32);
     }
     const uint64_t written = (uint64_t)__reduce_or_sync(0xffffffffu, hi) << 32 |
                              __reduce_or_sync(0xffffffffu, lo);
-    for (int base = 0; base < n; base += kPasses * kRows) {
-      load(base);
+    float big = 0.f;
 #pragma unroll
-      for (int x = 0; x < kPasses; ++x) {
-        if (base + x * kRows >= n) break;
-        float a[8], e[8];
-        values(x, base, a, e);
+    for (int x = 0; x < kPasses; ++x) {
+      if (base + x * kRows >= n) break;
+      float a[8], e[8];
+      values(x, a, e);
 #pragma unroll
-        for (int y = 0; y < 8; ++y) big = fmaxf(big, fmaxf(finite_abs(a[y]), finite_abs(e[y])));
-      }
+      for (int y = 0; y < 8; ++y) big = fmaxf(big, fmaxf(finite_abs(a[y]), finite_abs(e[y])));
     }
     big = warp_max(big);
-    const bool fresh = written & 1;
-    const float held = fresh ? 0.f : held_scale(stored);
+    if (team_warps > 1) {
+      if (lane == 0) big_s[buf][warp] = big;
+      team_sync(1 + team, threads);
+      for (int w = 0; w < team_warps; ++w) big = fmaxf(big, big_s[buf][team * team_warps + w]);
+    }
+    const float held = written & 1 ? 0.f : held_scale(stored);  // (a block begun anew: its own)
     const float s = fmaxf(held, needed_scale(big));
     char* cache = (is_k ? p.kc : p.vc) + h * p.head_stride;
     if (held > 0.f && s != stored)
       move_others<D>(cache + slot_offset(p.P, p.page_stride, p.token_stride, b * p.block.d),
-                     p.token_stride, p.block.d, written, stored / s, lane);
-    if (lane == 0 && s != stored) *scale = s;
+                     p.token_stride, p.block.d, written, stored / s, mine * 32 + lane, threads);
+    if (mine == 0 && lane == 0 && s != stored) *scale = s;
     const float by = 1.f / s;  // (a power of two)
-    const bool once = n <= kPasses * kRows;
-    for (int base = 0; base < n; base += kPasses * kRows) {
-      if (!once) load(base);
 #pragma unroll
-      for (int x = 0; x < kPasses; ++x) {
-        const int u = base + x * kRows + sub;
-        if (base + x * kRows >= n) break;
-        float a[8], e[8];
-        values(x, base, a, e);
-        if (u < n) {
-          char* to = cache + slot_offset(p.P, p.page_stride, p.token_stride,
-                                         slot_s[at - t0 + 1 + u]);
+    for (int x = 0; x < kPasses; ++x) {
+      const int u = base + x * kRows + sub;
+      if (base + x * kRows >= n) break;
+      float a[8], e[8];
+      values(x, a, e);
+      if (u < n) {
+        char* to = cache + slot_offset(p.P, p.page_stride, p.token_stride, slot_s[first + u]);
 #pragma unroll
-          for (int y = 0; y < 8; ++y) a[y] *= by, e[y] *= by;
-          *reinterpret_cast<uint2*>(to + c.x * 8) =
-              make_uint2(e4m3_word(a[0], a[1], a[2], a[3]), e4m3_word(a[4], a[5], a[6], a[7]));
-          *reinterpret_cast<uint2*>(to + c.y * 8) =
-              make_uint2(e4m3_word(e[0], e[1], e[2], e[3]), e4m3_word(e[4], e[5], e[6], e[7]));
-        }
+        for (int y = 0; y < 8; ++y) a[y] *= by, e[y] *= by;
+        const uint2 first8 =
+            make_uint2(e4m3_word(a[0], a[1], a[2], a[3]), e4m3_word(a[4], a[5], a[6], a[7]));
+        const uint2 other8 =
+            make_uint2(e4m3_word(e[0], e[1], e[2], e[3]), e4m3_word(e[4], e[5], e[6], e[7]));
+        *reinterpret_cast<uint2*>(to + c.x * 8) = first8;
+        *reinterpret_cast<uint2*>(to + c.y * 8) = other8;
       }
     }
-  }
-
-  // ---- this tile's queries
-  if (p.Hq == 0) return;
-  const int per = p.Hq * kItems, n = (t1 - t0) * per;
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const int u = i / per, y = i - u * per, h = y / kItems, x = y % kItems;
-    if (slot_s[u + 1] < 0) continue;
-    const int2 c = rope_chunks(p.rope, x);
-    const uint4* row = reinterpret_cast<const uint4*>(
-        reinterpret_cast<const T*>(p.q) + (t0 + u) * p.q_stride + h * D);
-    uint4* to = reinterpret_cast<uint4*>(
-        reinterpret_cast<T*>(p.q_out) + (t0 + u) * p.q_out_stride + h * D);
-    float a[8], e[8];
-    const uint4 ra = row[c.x], re = row[c.y];
-    unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&ra), a);
-    unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&re), e);
-    if (p.rope.pairs > 0)
-      rope_turn(p.rope.interleaved, a, e, table + u * D + 8 * x, table + u * D + D / 2 + 8 * x);
-    to[c.x] = pack_chunk<T>(a).w[0];
-    to[c.y] = pack_chunk<T>(e).w[0];
   }
 }
 
@@ -240,39 +266,43 @@ struct ReadParams {
   char *k_out, *v_out;
   long long page_stride, token_stride, head_stride;  // bytes
   long long k_stride, v_stride;                      // elements
-  FastDiv P, block, chunks, heads;                   // 16-byte chunks of a row's head; heads
-  long long n;                                       // chunks in all
-  int num_slots;
+  FastDiv P, block, chunks, per;                     // 16-byte chunks of a row's head; of a row
+  int T, Hkv, W, num_slots;                          // rows of a CTA
 };
 
+// A thread takes 16 codes of a key and of the value beside it.
 template <typename O>
 __global__ void __launch_bounds__(kThreads) read_scaled_kernel(const __grid_constant__ ReadParams p) {
   chain_wait();
-  const int per = p.chunks.d * p.heads.d;
-  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < p.n;
-       i += (long long)gridDim.x * kThreads) {
-    const long long row = i / per;
-    const int y = (int)(i - row * per), h = p.chunks.quot(y), x = y - h * p.chunks.d;
-    const int64_t slot = p.slots[row];
+  const int t0 = blockIdx.x * p.W, n = min(p.W, p.T - t0) * p.per.d;
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const int u = p.per.quot(i), y = i - u * p.per.d, h = p.chunks.quot(y), x = y - h * p.chunks.d;
+    const int64_t slot = p.slots[t0 + u];
     if (slot < 0 || slot >= p.num_slots) continue;
     const long long from = slot_offset(p.P, p.page_stride, p.token_stride, (int)slot) +
                            h * p.head_stride + x * 16;
-    const long long sc = (long long)p.block.quot((int)slot) * p.heads.d + h;
+    const long long sc = (long long)p.block.quot((int)slot) * p.Hkv + h;
+    uint4 w[2];
+    float s[2];
+    w[0] = *reinterpret_cast<const uint4*>(p.kc + from);
+    s[0] = p.ks[sc];
+    if (p.vc) {
+      w[1] = *reinterpret_cast<const uint4*>(p.vc + from);
+      s[1] = p.vs[sc];
+    }
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       if (kv && !p.vc) break;
-      const uint4 w = *reinterpret_cast<const uint4*>((kv ? p.vc : p.kc) + from);
-      const float s = (kv ? p.vs : p.ks)[sc];
       float v[16];
-      e4m3_values(w.x, v);
-      e4m3_values(w.y, v + 4);
-      e4m3_values(w.z, v + 8);
-      e4m3_values(w.w, v + 12);
+      e4m3_values(w[kv].x, v);
+      e4m3_values(w[kv].y, v + 4);
+      e4m3_values(w[kv].z, v + 8);
+      e4m3_values(w[kv].w, v + 12);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] *= s;
+      for (int e = 0; e < 16; ++e) v[e] *= s[kv];
       Chunk8<O>* to = reinterpret_cast<Chunk8<O>*>(
-          reinterpret_cast<O*>(kv ? p.v_out : p.k_out) + row * (kv ? p.v_stride : p.k_stride) +
-          (h * p.chunks.d + x) * 16);
+          reinterpret_cast<O*>(kv ? p.v_out : p.k_out) +
+          (t0 + u) * (kv ? p.v_stride : p.k_stride) + y * 16);
       to[0] = pack_chunk<O>(v);
       to[1] = pack_chunk<O>(v + 8);
     }
@@ -370,7 +400,7 @@ __global__ void __launch_bounds__(kThreads) commit_scaled_kernel(
       const uint64_t written =
           (hi - lo == 64 ? ~0ull : (1ull << (hi - lo)) - 1) << (lo - begin);
       move_others<D>(code_at(kv, slot_of(begin)), (long long)p.Hkv * D, p.block.d, written,
-                     stored / s, lane);
+                     stored / s, lane, 32);
     }
     __syncwarp();
     if (lane == 0 && s != stored) *scale = s;
@@ -391,7 +421,9 @@ spec_status launch_append(const AppendParams& p, cudaStream_t st) {
   const spec_status rc = ensure_smem_limit(once, (const void*)append_scaled_kernel<T, D>,
                                            (kTile - 1 + kMaxBlock) * D * (int)sizeof(float));
   if (rc != SPEC_OK) return rc;
-  return launch_chained(append_scaled_kernel<T, D>, (p.T + p.W - 1) / p.W, kThreads, smem, st, p);
+  const int parts = p.Hq ? 3 : 2;
+  return launch_chained(append_scaled_kernel<T, D>, (p.T + p.W - 1) / p.W * parts, kThreads, smem, st,
+                        p);
 }
 
 template <typename T>
@@ -463,6 +495,8 @@ extern "C" spec_status spec_append_scaled(
   p.head_stride = head_stride;
   p.P = FastDiv(page_size);
   p.block = FastDiv(block);
+  p.heads = FastDiv(Hkv);
+  p.per = FastDiv(std::max(1, Hq * (D / 16)));
   p.T = T;
   p.Hq = q ? Hq : 0;
   p.Hkv = Hkv;
@@ -511,10 +545,12 @@ extern "C" spec_status spec_read_scaled(const void* k_cache, const void* v_cache
   p.P = FastDiv(page_size);
   p.block = FastDiv(block);
   p.chunks = FastDiv(D / 16);
-  p.heads = FastDiv(Hkv);
-  p.n = (long long)T * Hkv * (D / 16);
+  p.per = FastDiv(Hkv * (D / 16));
+  p.T = T;
+  p.Hkv = Hkv;
+  p.W = std::max(1, kThreads / p.per.d);
   p.num_slots = num_pages * page_size;
-  const int grid = (int)std::min<long long>((p.n + kThreads - 1) / kThreads, 1 << 20);
+  const int grid = (int)(((long long)T + p.W - 1) / p.W);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (out_dtype == SPEC_F32) return launch_chained(read_scaled_kernel<float>, grid, kThreads, 0, st, p);
   if (out_dtype == SPEC_BF16)
