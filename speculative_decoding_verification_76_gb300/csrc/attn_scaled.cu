@@ -2,25 +2,12 @@
 // workspace.  The kernels and the reasons for them are in attn_scaled.cuh; each head size is a
 // translation unit of its own.
 #include <algorithm>
-#include <atomic>
 
 #include "attn_scaled.cuh"
 
 namespace {
 
 using scaled_attn::Params;
-
-// SMs of the current device, asked once per device (the query costs host time)
-int num_sms() {
-  static std::atomic<int> known[64];
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
-  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
-    return 152;
-  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
 
 struct Plan {
   int tiles, rows_per_tile, rt, teams;
@@ -36,7 +23,7 @@ bool make_plan(int B, int R, int Hq, int Hkv, int D, Plan* pl) {
   pl->tiles = (int)((rows + most - 1) / most);
   pl->rows_per_tile = (int)((rows + pl->tiles - 1) / pl->tiles);
   pl->rt = pl->rows_per_tile <= 16 ? 16 : pl->rows_per_tile <= 32 ? 32 : 64;
-  pl->teams = std::max(1, num_sms() / pl->tiles);
+  pl->teams = std::max(1, sm_count() / pl->tiles);
   return true;
 }
 

@@ -16,6 +16,8 @@
 // either touches in a bitmap, and walks its rows: a thread takes four ids that are one 16-byte
 // store, and looks at counts and biases only where the bitmap has a bit.  From row to row only the
 // block tokens that differ are counted up or down.
+#include <algorithm>
+
 #include <cuda_fp16.h>
 
 #include "serving.cuh"
@@ -24,7 +26,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kFlight = 4;                  // groups of four ids of a thread in flight
 constexpr uint32_t kPrompt = 0x80000000u;   // of a count: the id stands in the prompt
 constexpr int kHalo = 32;                   // ids behind a slice that its last group may touch
 
@@ -46,28 +47,39 @@ SPEC_DEV float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 SPEC_DEV float to_float(__half x) { return __half2float(x); }
 
 template <typename T>
-struct alignas(4 * sizeof(T)) Group {  // four logits, as they come
-  T x[4];
+struct alignas(8 * sizeof(T)) Unit {  // eight logits, as they come
+  T x[8];
 };
 
-// Four logits from src on: all of them in one load where the row has them and they are aligned, else
-// those of `want`.
 template <typename T>
-SPEC_DEV void load_group(const T* src, uint32_t want, bool all, Group<T>& g) {
-  if (all && ((uintptr_t)src & (4 * sizeof(T) - 1)) == 0) {
-    if constexpr (sizeof(T) == 4)
-      *reinterpret_cast<float4*>(&g) = __ldcs(reinterpret_cast<const float4*>(src));
-    else
-      *reinterpret_cast<uint2*>(&g) = __ldcs(reinterpret_cast<const uint2*>(src));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (want >> i & 1) g.x[i] = src[i];
-  }
+SPEC_DEV void load_unit(const T* src, Unit<T>& u) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+  if constexpr (sizeof(T) == 4)
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                   "=r"(w[6]), "=r"(w[7])
+                 : "l"(src));
+  else
+    *reinterpret_cast<uint4*>(w) = __ldcs(reinterpret_cast<const uint4*>(src));
+}
+
+SPEC_DEV void store_unit(float* out, const float* y) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "f"(y[0]),
+               "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
+               : "memory");
+}
+
+// Bits at .. at + 7 (at > -8; bits in front of the first and behind byte `last`: 0).
+SPEC_DEV uint32_t eight_bits(const uint8_t* w, int at, int last) {
+  const int i = at >> 3, sh = at & 7;
+  uint32_t v = at >= 0 ? w[i] : 0u;
+  if (sh && i < last) v |= (uint32_t)w[i + 1] << 8;
+  return v >> sh & 255u;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant__ LogitsParams p) {
+__global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_constant__ LogitsParams p) {
+  constexpr int kFlight = sizeof(T) == 4 ? 2 : 4;            // units of a thread in flight
   extern __shared__ __align__(16) uint32_t sm[];
   const int S = p.slice + kHalo;
   uint32_t* touched = sm;                                   // S / 32 + 1 words
@@ -85,10 +97,63 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
   if (any) {
     const int n = (int)((p.biases ? add + S : reinterpret_cast<float*>(count) + S) -
                         reinterpret_cast<float*>(sm));
-    for (int i = threadIdx.x; i < n; i += kThreads) sm[i] = 0u;
+    for (int i = threadIdx.x; i < n / 4; i += kThreads)
+      reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
   }
   chain_wait();
-  __syncthreads();
+
+  // ---- a row, and eight ids of it at a time: a unit is one aligned store of 32 bytes, so units start
+  // at ids -off, 8 - off, ...
+  const T* src;
+  float* out;
+  const uint8_t* mask;
+  int off, k0, k1;
+  bool aligned;
+  auto begin_row = [&](int r) {
+    const long long row = (long long)b * p.R + r;
+    out = p.out + row * p.V;
+    src = reinterpret_cast<const T*>(p.logits) + row * p.stride;
+    mask = nullptr;
+    if (p.mask) {
+      const long long m = p.mask_row ? p.mask_row[row] : row;
+      if (m >= 0 && m < p.n_masks) mask = reinterpret_cast<const uint8_t*>(p.mask + m * p.words);
+    }
+    off = (int)(((uintptr_t)out >> 2) & 7);
+    aligned = (((uintptr_t)src - off * sizeof(T)) & (8 * sizeof(T) - 1)) == 0;
+    k0 = base == 0 ? 0 : (base + off + 7) >> 3;
+    k1 = (min(base + p.slice, p.V) + off + 7) >> 3;
+  };
+  Unit<T> g[kFlight];
+  uint32_t ok[kFlight];  // ids that may be drawn
+  auto live = [&](int id) {
+    uint32_t m = 255u;
+    if (id < 0) m = 255u << -id & 255u;
+    if (id + 8 > p.V) m &= (1u << (p.V - id)) - 1;
+    return m;
+  };
+  auto load = [&](int k) {
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int kk = k + f * kThreads, id = 8 * kk - off;
+      ok[f] = 0;
+      if (kk < k1) ok[f] = mask ? eight_bits(mask, id, 4 * p.words - 1) : 255u;
+    }
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int id = 8 * (k + f * kThreads) - off;
+      if (!ok[f] || p.in_place) continue;
+      if (aligned && id >= 0 && id + 8 <= p.V) {
+        load_unit(src + id, g[f]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if ((unsigned)(id + i) < (unsigned)p.V) g[f].x[i] = src[id + i];
+      }
+    }
+  };
+  begin_row(r0);
+  load(k0 + threadIdx.x);  // (on their way while the ids are counted)
+  if (any) __syncthreads();
   auto mark = [&](int i) { atomicOr(touched + (i >> 5), 1u << (i & 31)); };
   float rep = 1.f, freq = 0.f, pres = 0.f;
   if (p.counts) {
@@ -97,13 +162,19 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
     pres = p.presence ? p.presence[b] : 0.f;
     const int prompt = p.prompt_len ? p.prompt_len[b] : 0;
     const int32_t* h = p.history + (size_t)b * p.H;
-    for (int i = threadIdx.x; i < p.H; i += kThreads) {
-      const uint32_t id = (uint32_t)h[i] - (uint32_t)base;
-      if (id < (uint32_t)top) {
-        if (i < prompt) atomicOr(count + id, kPrompt);
-        else atomicAdd(count + id, 1u);
-        mark(id);
-      }
+    constexpr int kAtOnce = 8;
+    for (int i0 = threadIdx.x; i0 < p.H; i0 += kAtOnce * kThreads) {
+      uint32_t id[kAtOnce];
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x)
+        id[x] = i0 + x * kThreads < p.H ? (uint32_t)h[i0 + x * kThreads] - (uint32_t)base : ~0u;
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x)
+        if (id[x] < (uint32_t)top) {
+          if (i0 + x * kThreads < prompt) atomicOr(count + id[x], kPrompt);
+          else atomicAdd(count + id[x], 1u);
+          mark(id[x]);
+        }
     }
     // the block's tokens and each row's ancestors
     if (threadIdx.x < p.R) {
@@ -163,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
         }
     }
   }
-  __syncthreads();
+  if (any) __syncthreads();
 
   uint64_t counted = 0;  // block tokens that the counts hold
   const uint64_t here = p.counts ? here_s : 0;
@@ -179,72 +250,58 @@ __global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant_
       counted = want;
       __syncthreads();
     }
-    const long long row = (long long)b * p.R + r;
-    float* out = p.out + row * p.V;
-    const T* src = reinterpret_cast<const T*>(p.logits) + row * p.stride;
-    const uint32_t* mask = nullptr;
-    if (p.mask) {
-      const long long m = p.mask_row ? p.mask_row[row] : row;
-      if (m >= 0 && m < p.n_masks) mask = p.mask + m * p.words;
-    }
+    if (r > r0) begin_row(r);
     if (p.in_place && !any && !mask) continue;
-    // groups of four ids start where the store is aligned: at -off, 4 - off, ...
-    const int off = (int)(((uintptr_t)out >> 2) & 3);
-    const int k0 = base == 0 ? 0 : (base + off + 3) >> 2;
-    const int end = min(base + p.slice, p.V);                 // groups that start in front of it
-    const int k1 = (end + off + 3) >> 2;
     for (int k = k0 + threadIdx.x; k < k1; k += kThreads * kFlight) {
-      Group<T> g[kFlight];
-      uint32_t live[kFlight], hit[kFlight], ok[kFlight];
+      if (r > r0 || k >= k0 + kThreads * kFlight) load(k);
 #pragma unroll
       for (int f = 0; f < kFlight; ++f) {
-        const int kk = k + f * kThreads, id = 4 * kk - off;
-        live[f] = hit[f] = ok[f] = 0;
-        if (kk >= k1) continue;
-        live[f] = 15u;
-        if (id < 0) live[f] = 15u << -id & 15u;
-        if (id + 4 > p.V) live[f] &= (1u << (p.V - id)) - 1;
-        auto bits = [&](const uint32_t* w, int at, int last) {  // four, from bit at on
-          const int i = at < 0 ? 0 : at;
-          uint32_t v = w[i >> 5] >> (i & 31);
-          if ((i & 31) > 28 && (i >> 5) < last) v |= w[(i >> 5) + 1] << (32 - (i & 31));
-          return at < 0 ? v << -at : v;
-        };
-        ok[f] = mask ? bits(mask, id, p.words - 1) & live[f] : live[f];
-        if (any) hit[f] = bits(touched, id - base, S / 32) & ok[f];
-        const uint32_t need = p.in_place ? hit[f] : ok[f];
-        if (need) load_group(src + id, need, live[f] == 15u, g[f]);
-      }
+        if (k + f * kThreads >= k1) break;
+        const int id = 8 * (k + f * kThreads) - off;
+        float y[8];
+        if (p.in_place) {
 #pragma unroll
-      for (int f = 0; f < kFlight; ++f) {
-        if (!live[f]) continue;
-        const int id = 4 * (k + f * kThreads) - off;
-        float y[4];
+          for (int i = 0; i < 8; ++i) y[i] = -INFINITY;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = ok[f] >> i & 1 ? to_float(g[f].x[i]) : -INFINITY;
-        if (hit[f]) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (hit[f] >> i & 1) {
-              const int e = id + i - base;
-              if (p.counts) {
-                const uint32_t c = count[e], n = c & ~kPrompt;
-                if (c && p.repetition) y[i] = y[i] > 0.f ? __fdiv_rn(y[i], rep) : y[i] * rep;
-                if (n) {
-                  if (p.frequency) y[i] = __fsub_rn(y[i], __fmul_rn(freq, (float)n));
-                  if (p.presence) y[i] = __fsub_rn(y[i], pres);
-                }
-              }
-              if (p.biases) y[i] += add[e];
-            }
+          for (int i = 0; i < 8; ++i) y[i] = ok[f] >> i & 1 ? to_float(g[f].x[i]) : -INFINITY;
         }
-        const uint32_t put = p.in_place ? hit[f] | (live[f] & ~ok[f]) : live[f];
-        if (put == 15u)
-          __stcs(reinterpret_cast<float4*>(out + id), make_float4(y[0], y[1], y[2], y[3]));
-        else
+        const uint32_t in = live(id);
+        uint32_t put = p.in_place ? in & ~ok[f] : in;
+        if (any) {
+          uint32_t hit =
+              eight_bits(reinterpret_cast<const uint8_t*>(touched), id - base, S / 8) & ok[f] & in;
+          put |= hit;
+          while (hit) {
+            const int i = __ffs(hit) - 1, e = id + i - base;
+            hit &= hit - 1;
+            float x = y[0];
+            if (p.in_place) {
+              x = out[id + i];
+            } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+              for (int j = 1; j < 8; ++j) x = i == j ? y[j] : x;
+            }
+            if (p.counts) {
+              const uint32_t c = count[e], n = c & ~kPrompt;
+              if (c && p.repetition) x = x > 0.f ? __fdiv_rn(x, rep) : x * rep;
+              if (n) {
+                if (p.frequency) x = __fsub_rn(x, __fmul_rn(freq, (float)n));
+                if (p.presence) x = __fsub_rn(x, pres);
+              }
+            }
+            if (p.biases) x += add[e];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = i == j ? x : y[j];
+          }
+        }
+        if (put == 255u) {
+          store_unit(out + id, y);
+        } else if (put) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
             if (put >> i & 1) out[id + i] = y[i];
+        }
       }
     }
   }
@@ -324,9 +381,13 @@ extern "C" spec_status spec_logits_process(
   p.counts = (repetition || frequency || presence) && (H > 0 || block_tokens);
   p.biases = n_bias > 0;
   p.in_place = in_place;
-  p.slice = 4096;
-  p.rows = R;
-  p.row_groups = 1;
+  // A CTA per sequence and slice walks all rows where that fills the GPU; else the rows are dealt out
+  // too, and where even that leaves SMs idle the slices are shorter.
+  const int sms = sm_count();
+  p.slice = (long long)B * R * ((V + 4095) / 4096) >= sms ? 4096 : 1024;
+  const long long ctas = (long long)B * ((V + p.slice - 1) / p.slice);
+  p.rows = std::max<int>(1, (int)std::min<long long>(R, R * ctas / (2 * sms)));
+  p.row_groups = (R + p.rows - 1) / p.rows;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == SPEC_F32) return launch<float>(p, st);
   if (dtype == SPEC_BF16) return launch<__nv_bfloat16>(p, st);

@@ -1,6 +1,8 @@
 // What the kernels of the cache's side of a decoding step share (tables.cu,
 // append_tokens.cu, decode.cu).
 #pragma once
+#include <atomic>
+
 #include "common.cuh"
 
 // x / d for 0 <= x < 2^31 and a divisor the host knows: with 2^s >= d the
@@ -24,6 +26,18 @@ struct FastDiv {
     return q + (q * d != x);
   }
 };
+
+// SMs of the current device, asked once per device (the query costs host time)
+static inline int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 152;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
 
 // Programmatic dependent launch: a kernel started by launch_chained is set up while the
 // kernel in front of it on the stream still runs, and chain_wait() holds it until that
