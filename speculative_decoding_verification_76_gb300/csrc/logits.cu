@@ -12,10 +12,12 @@
 //
 // Design: a CTA takes a slice of the vocabulary for some rows of one sequence.  It counts the
 // history's ids of its slice in shared memory (integer atomics: the order does not matter), sums
-// the biases there (ids are dealt to threads, each adds its own in the list's order), marks what
-// either touches in a bitmap, and walks its rows: a thread takes four ids that are one 16-byte
-// store, and looks at counts and biases only where the bitmap has a bit.  From row to row only the
-// block tokens that differ are counted up or down.
+// the biases there (ids are dealt to threads, each adds its own in the list's order) and lists what
+// either touches.  A row is then written as it comes, eight ids a thread and store, with -inf where
+// the mask forbids; behind that the touched ids, a thread each, are computed and written over
+// it, while the next row is on its way.  (With the touched ids looked for within the stores, most warps
+// met some: twice the instructions, 105 us against the present 0 at 64 sequences of 5 rows.)  From row
+// to row only the block tokens that differ are counted up or down.
 #include <algorithm>
 
 #include <cuda_fp16.h>
@@ -27,7 +29,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr uint32_t kPrompt = 0x80000000u;   // of a count: the id stands in the prompt
-constexpr int kHalo = 32;                   // ids behind a slice that its last group may touch
+constexpr int kFlight = 2;                  // units (of eight ids) of a thread
+constexpr int kMostSlice = 8 * kFlight * kThreads;
+constexpr int kHalo = 8;                    // ids in front of a slice that a row's first unit may hold
 
 struct LogitsParams {
   const char* logits;
@@ -77,38 +81,41 @@ SPEC_DEV uint32_t eight_bits(const uint8_t* w, int at, int last) {
   return v >> sh & 255u;
 }
 
+__host__ __device__ constexpr int touched_words(int slice) {  // whole 16 bytes
+  return ((slice + kHalo + 31) / 32 + 3) / 4 * 4;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_constant__ LogitsParams p) {
-  constexpr int kFlight = sizeof(T) == 4 ? 2 : 4;            // units of a thread in flight
   extern __shared__ __align__(16) uint32_t sm[];
   const int S = p.slice + kHalo;
-  uint32_t* touched = sm;                                   // S / 32 + 1 words
-  uint32_t* count = touched + (S / 32 + 1 + 3) / 4 * 4;      // S, if counts
+  uint32_t* touched = sm;                                   // a bit for each id: in the list
+  uint32_t* count = touched + touched_words(p.slice);       // S, if counts
   float* add = reinterpret_cast<float*>(count + (p.counts ? S : 0));  // S, if biases
+  uint16_t* list = reinterpret_cast<uint16_t*>(add + (p.biases ? S : 0));  // S
   __shared__ uint64_t anc[64], here_s;
   __shared__ int32_t tok[64], list_id[kThreads];
   __shared__ float list_x[kThreads];
-  __shared__ int warp_n[kWarps];
-  const int b = blockIdx.y, base = blockIdx.x * p.slice;
+  __shared__ int warp_n[kWarps], listed;
+  const int b = blockIdx.y, first = blockIdx.x * p.slice;
+  const int base = first - kHalo;                            // id of the first counter
   const int r0 = blockIdx.z * p.rows, r1 = min(r0 + p.rows, p.R);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int top = min(p.V - base, S);                        // ids of this CTA
   const bool any = p.counts || p.biases;
   if (any) {
-    const int n = (int)((p.biases ? add + S : reinterpret_cast<float*>(count) + S) -
-                        reinterpret_cast<float*>(sm));
+    const int n = (int)(reinterpret_cast<uint32_t*>(list) - sm);
     for (int i = threadIdx.x; i < n / 4; i += kThreads)
       reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) listed = 0;
   }
   chain_wait();
 
-  // ---- a row, and eight ids of it at a time: a unit is one aligned store of 32 bytes, so units start
-  // at ids -off, 8 - off, ...
+  // ---- a row, eight ids of it at a time: a unit is one aligned store of 32 bytes, so the CTA's units
+  // start at ids first - off, first + 8 - off, ...
   const T* src;
   float* out;
-  const uint8_t* mask;
-  int off, k0, k1;
-  bool aligned;
+  const uint32_t* mask;
+  int off;
   auto begin_row = [&](int r) {
     const long long row = (long long)b * p.R + r;
     out = p.out + row * p.V;
@@ -116,32 +123,30 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
     mask = nullptr;
     if (p.mask) {
       const long long m = p.mask_row ? p.mask_row[row] : row;
-      if (m >= 0 && m < p.n_masks) mask = reinterpret_cast<const uint8_t*>(p.mask + m * p.words);
+      if (m >= 0 && m < p.n_masks) mask = p.mask + m * p.words;
     }
     off = (int)(((uintptr_t)out >> 2) & 7);
-    aligned = (((uintptr_t)src - off * sizeof(T)) & (8 * sizeof(T) - 1)) == 0;
-    k0 = base == 0 ? 0 : (base + off + 7) >> 3;
-    k1 = (min(base + p.slice, p.V) + off + 7) >> 3;
   };
   Unit<T> g[kFlight];
   uint32_t ok[kFlight];  // ids that may be drawn
-  auto live = [&](int id) {
-    uint32_t m = 255u;
-    if (id < 0) m = 255u << -id & 255u;
-    if (id + 8 > p.V) m &= (1u << (p.V - id)) - 1;
-    return m;
+  auto unit_id = [&](int f) { return first + 8 * (int)(threadIdx.x + f * kThreads) - off; };
+  auto there = [&](int f, int id) {  // (id: the unit's first)
+    return 8 * (threadIdx.x + f * kThreads) < p.slice && id < p.V;
   };
-  auto load = [&](int k) {
+  auto load = [&]() {
+    const bool aligned = (((uintptr_t)src - off * sizeof(T)) & (8 * sizeof(T) - 1)) == 0;
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
-      const int kk = k + f * kThreads, id = 8 * kk - off;
-      ok[f] = 0;
-      if (kk < k1) ok[f] = mask ? eight_bits(mask, id, 4 * p.words - 1) : 255u;
+      const int id = unit_id(f);
+      ok[f] = 255u;
+      if (mask && there(f, id))
+        ok[f] = eight_bits(reinterpret_cast<const uint8_t*>(mask), id, 4 * p.words - 1);
     }
+    if (p.in_place) return;
 #pragma unroll
     for (int f = 0; f < kFlight; ++f) {
-      const int id = 8 * (k + f * kThreads) - off;
-      if (!ok[f] || p.in_place) continue;
+      const int id = unit_id(f);
+      if (!ok[f] || !there(f, id)) continue;
       if (aligned && id >= 0 && id + 8 <= p.V) {
         load_unit(src + id, g[f]);
       } else {
@@ -152,29 +157,39 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
     }
   };
   begin_row(r0);
-  load(k0 + threadIdx.x);  // (on their way while the ids are counted)
-  if (any) __syncthreads();
-  auto mark = [&](int i) { atomicOr(touched + (i >> 5), 1u << (i & 31)); };
+  load();  // (on its way while the ids are counted)
+
+  auto mark = [&](int i) {
+    const uint32_t bit = 1u << (i & 31);
+    if (!(atomicOr(touched + (i >> 5), bit) & bit)) list[atomicAdd(&listed, 1)] = (uint16_t)i;
+  };
   float rep = 1.f, freq = 0.f, pres = 0.f;
+  uint64_t here = 0;  // block tokens that are ids of this slice
+  if (any) __syncthreads();
   if (p.counts) {
     rep = p.repetition ? p.repetition[b] : 1.f;
     freq = p.frequency ? p.frequency[b] : 0.f;
     pres = p.presence ? p.presence[b] : 0.f;
     const int prompt = p.prompt_len ? p.prompt_len[b] : 0;
     const int32_t* h = p.history + (size_t)b * p.H;
+    auto index = [&](int32_t id) {  // of an id's counter, ~0 if there is none
+      const uint32_t i = (uint32_t)id - (uint32_t)base;
+      return i < (uint32_t)S && (uint32_t)id < (uint32_t)p.V ? i : ~0u;
+    };
     constexpr int kAtOnce = 8;
     for (int i0 = threadIdx.x; i0 < p.H; i0 += kAtOnce * kThreads) {
-      uint32_t id[kAtOnce];
+      int32_t id[kAtOnce];
 #pragma unroll
       for (int x = 0; x < kAtOnce; ++x)
-        id[x] = i0 + x * kThreads < p.H ? (uint32_t)h[i0 + x * kThreads] - (uint32_t)base : ~0u;
+        id[x] = i0 + x * kThreads < p.H ? h[i0 + x * kThreads] : -1;
 #pragma unroll
-      for (int x = 0; x < kAtOnce; ++x)
-        if (id[x] < (uint32_t)top) {
-          if (i0 + x * kThreads < prompt) atomicOr(count + id[x], kPrompt);
-          else atomicAdd(count + id[x], 1u);
-          mark(id[x]);
-        }
+      for (int x = 0; x < kAtOnce; ++x) {
+        const uint32_t i = index(id[x]);
+        if (i == ~0u) continue;
+        if (i0 + x * kThreads < prompt) atomicOr(count + i, kPrompt);
+        else atomicAdd(count + i, 1u);
+        mark(i);
+      }
     }
     // the block's tokens and each row's ancestors
     if (threadIdx.x < p.R) {
@@ -182,7 +197,9 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
       int t = -1;
       if (p.tokens && i > 0)
         t = p.parent ? p.tokens[(size_t)b * p.R + i] : p.tokens[(size_t)b * (p.R - 1) + i - 1];
+      t = (int)index(t);
       tok[i] = t;
+      if (t >= 0) mark(t);
       uint64_t m = 0;
       if (p.parent) {
         int v = i;
@@ -197,12 +214,9 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
       anc[i] = m;
     }
     __syncthreads();
-    if (warp == 0) {  // which of them are ids of this slice
-      auto inside = [&](int i) {
-        return i < p.R && tok[i] >= 0 && (uint32_t)tok[i] - (uint32_t)base < (uint32_t)top;
-      };
-      const uint32_t lo = __ballot_sync(0xffffffffu, inside(lane));
-      const uint32_t hi = __ballot_sync(0xffffffffu, inside(lane + 32));
+    if (warp == 0) {
+      const uint32_t lo = __ballot_sync(0xffffffffu, lane < p.R && tok[lane] >= 0);
+      const uint32_t hi = __ballot_sync(0xffffffffu, lane + 32 < p.R && tok[lane + 32] >= 0);
       if (lane == 0) here_s = (uint64_t)hi << 32 | lo;
     }
   }
@@ -211,8 +225,8 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
     const float* xs = p.bias + (size_t)b * p.n_bias;
     for (int i0 = 0; i0 < p.n_bias; i0 += kThreads) {
       const int i = i0 + threadIdx.x;
-      const uint32_t id = i < p.n_bias ? (uint32_t)ids[i] - (uint32_t)base : ~0u;
-      const bool in = id < (uint32_t)top;
+      const int32_t id = i < p.n_bias ? ids[i] : -1;
+      const bool in = (uint32_t)id - (uint32_t)base < (uint32_t)S && (uint32_t)id < (uint32_t)p.V;
       const uint32_t who = __ballot_sync(0xffffffffu, in);
       if (lane == 0) warp_n[warp] = __popc(who);
       __syncthreads();
@@ -223,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
         n += warp_n[w];
       }
       if (in) {
-        list_id[at] = (int)id;
+        list_id[at] = id - base;
         list_x[at] = xs[i];
       }
       __syncthreads();
@@ -235,81 +249,71 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
     }
   }
   if (any) __syncthreads();
+  if (p.counts) here = here_s;
+  const int n_listed = any ? listed : 0;
 
   uint64_t counted = 0;  // block tokens that the counts hold
-  const uint64_t here = p.counts ? here_s : 0;
   for (int r = r0; r < r1; ++r) {
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int id = unit_id(f);
+      if (!there(f, id)) continue;
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = !p.in_place && (ok[f] >> i & 1) ? to_float(g[f].x[i]) : -INFINITY;
+      uint32_t put = 255u;
+      if (id < 0) put = 255u << -id & 255u;
+      if (id + 8 > p.V) put &= (1u << (p.V - id)) - 1;
+      if (p.in_place) put &= ~ok[f];
+      if (put == 255u) {
+        store_unit(out + id, y);
+      } else if (put) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (put >> i & 1) out[id + i] = y[i];
+      }
+    }
+    const T* const from = src;
+    float* const to = out;
+    const uint32_t* const allowed = mask;
+    const int begin = first - off;
+    if (r + 1 < r1) {
+      begin_row(r + 1);
+      load();
+    }
+    if (n_listed == 0) continue;
+    // ---- what the counts and biases touch, behind the stores of the other threads
+    __syncthreads();
     const uint64_t want = p.counts ? anc[r] & here : 0, change = want ^ counted;
     if (change) {
-      __syncthreads();
-      if (threadIdx.x < 64 && change >> threadIdx.x & 1) {
-        const int id = tok[threadIdx.x] - base;
-        atomicAdd(count + id, want >> threadIdx.x & 1 ? 1u : ~0u);
-        mark(id);
-      }
+      if (threadIdx.x < 64 && change >> threadIdx.x & 1)
+        atomicAdd(count + tok[threadIdx.x], want >> threadIdx.x & 1 ? 1u : ~0u);
       counted = want;
       __syncthreads();
     }
-    if (r > r0) begin_row(r);
-    if (p.in_place && !any && !mask) continue;
-    for (int k = k0 + threadIdx.x; k < k1; k += kThreads * kFlight) {
-      if (r > r0 || k >= k0 + kThreads * kFlight) load(k);
-#pragma unroll
-      for (int f = 0; f < kFlight; ++f) {
-        if (k + f * kThreads >= k1) break;
-        const int id = 8 * (k + f * kThreads) - off;
-        float y[8];
-        if (p.in_place) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = -INFINITY;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = ok[f] >> i & 1 ? to_float(g[f].x[i]) : -INFINITY;
-        }
-        const uint32_t in = live(id);
-        uint32_t put = p.in_place ? in & ~ok[f] : in;
-        if (any) {
-          uint32_t hit =
-              eight_bits(reinterpret_cast<const uint8_t*>(touched), id - base, S / 8) & ok[f] & in;
-          put |= hit;
-          while (hit) {
-            const int i = __ffs(hit) - 1, e = id + i - base;
-            hit &= hit - 1;
-            float x = y[0];
-            if (p.in_place) {
-              x = out[id + i];
-            } else {
-#pragma unroll
-              for (int j = 1; j < 8; ++j) x = i == j ? y[j] : x;
-            }
-            if (p.counts) {
-              const uint32_t c = count[e], n = c & ~kPrompt;
-              if (c && p.repetition) x = x > 0.f ? __fdiv_rn(x, rep) : x * rep;
-              if (n) {
-                if (p.frequency) x = __fsub_rn(x, __fmul_rn(freq, (float)n));
-                if (p.presence) x = __fsub_rn(x, pres);
-              }
-            }
-            if (p.biases) x += add[e];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = i == j ? x : y[j];
-          }
-        }
-        if (put == 255u) {
-          store_unit(out + id, y);
-        } else if (put) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (put >> i & 1) out[id + i] = y[i];
+    for (int e = threadIdx.x; e < n_listed; e += kThreads) {
+      const int i = list[e], id = base + i;
+      if ((unsigned)(id - begin) >= (unsigned)p.slice) continue;  // (a neighbour's, in this row)
+      if (allowed && !(allowed[id >> 5] >> (id & 31) & 1)) continue;
+      float x = p.in_place ? to[id] : to_float(from[id]);
+      if (p.counts) {
+        const uint32_t c = count[i], n = c & ~kPrompt;
+        if (c && p.repetition) x = x > 0.f ? __fdiv_rn(x, rep) : x * rep;
+        if (n) {
+          if (p.frequency) x = __fsub_rn(x, __fmul_rn(freq, (float)n));
+          if (p.presence) x = __fsub_rn(x, pres);
         }
       }
+      if (p.biases) x += add[i];
+      to[id] = x;
     }
   }
 }
 
 size_t smem_bytes(const LogitsParams& p) {
+  if (!p.counts && !p.biases) return 0;
   const size_t S = p.slice + kHalo;
-  return ((S / 32 + 1 + 3) / 4 * 4 + (p.counts ? S : 0) + (p.biases ? S : 0)) * 4;
+  return (touched_words(p.slice) + (p.counts ? S : 0) + (p.biases ? S : 0)) * 4 + S * 2;
 }
 
 template <typename T>
@@ -317,13 +321,13 @@ spec_status launch(const LogitsParams& p, cudaStream_t st) {
   const size_t smem = smem_bytes(p);
   static PerDeviceOnce<int> once;
   LogitsParams most = p;
-  most.slice = 8192;
+  most.slice = kMostSlice;
   most.counts = most.biases = 1;
   const spec_status rc =
       ensure_smem_limit(once, (const void*)logits_kernel<T>, (int)smem_bytes(most));
   if (rc != SPEC_OK) return rc;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.V + p.slice - 1) / p.slice, p.B, p.row_groups);
+  cfg.gridDim = dim3((p.V + 7 + p.slice - 1) / p.slice, p.B, p.row_groups);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -346,7 +350,7 @@ extern "C" spec_status spec_logits_process(
     const int32_t* mask_row, void* stream) {
   if (B < 0 || R < 1 || R > 64 || V < 1 || H < 0 || n_bias < 0 || n_masks < 0) return SPEC_EINVAL;
   if (dtype != SPEC_F32 && dtype != SPEC_BF16 && dtype != SPEC_F16) return SPEC_EINVAL;
-  if (V > INT32_MAX - 4096 || H > INT32_MAX - 4096 || n_bias > INT32_MAX - 4096 || B > 65535)
+  if (V > INT32_MAX - 4 * kMostSlice || H > INT32_MAX - 4096 || n_bias > INT32_MAX - 4096 || B > 65535)
     return SPEC_EUNSUPPORTED;
   if ((H > 0 && !history) || (parent && !block_tokens) || (n_bias > 0 && (!bias_ids || !bias)) ||
       (n_masks > 0 && !mask))
@@ -384,7 +388,7 @@ extern "C" spec_status spec_logits_process(
   // A CTA per sequence and slice walks all rows where that fills the GPU; else the rows are dealt out
   // too, and where even that leaves SMs idle the slices are shorter.
   const int sms = sm_count();
-  p.slice = (long long)B * R * ((V + 4095) / 4096) >= sms ? 4096 : 1024;
+  p.slice = (long long)B * R * ((V + kMostSlice - 1) / kMostSlice) >= sms ? kMostSlice : 1024;
   const long long ctas = (long long)B * ((V + p.slice - 1) / p.slice);
   p.rows = std::max<int>(1, (int)std::min<long long>(R, R * ctas / (2 * sms)));
   p.row_groups = (R + p.rows - 1) / p.rows;
