@@ -29,6 +29,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr uint32_t kPrompt = 0x80000000u;   // of a count: the id stands in the prompt
+constexpr uint32_t kBlock = 0x40000000u;    // a block token
+constexpr int kRows = 2;                    // rows of a CTA in flight
 constexpr int kFlight = 2;                  // units (of eight ids) of a thread
 constexpr int kMostSlice = 8 * kFlight * kThreads;
 constexpr int kHalo = 8;                    // ids in front of a slice that a row's first unit may hold
@@ -93,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
   uint32_t* count = touched + touched_words(p.slice);       // S, if counts
   float* add = reinterpret_cast<float*>(count + (p.counts ? S : 0));  // S, if biases
   uint16_t* list = reinterpret_cast<uint16_t*>(add + (p.biases ? S : 0));  // S
-  __shared__ uint64_t anc[64], here_s;
+  __shared__ uint64_t anc[64];
   __shared__ int32_t tok[64], list_id[kThreads];
   __shared__ float list_x[kThreads];
   __shared__ int warp_n[kWarps], listed;
@@ -112,59 +114,61 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
 
   // ---- a row, eight ids of it at a time: a unit is one aligned store of 32 bytes, so the CTA's units
   // start at ids first - off, first + 8 - off, ...
-  const T* src;
-  float* out;
-  const uint32_t* mask;
-  int off;
-  auto begin_row = [&](int r) {
-    const long long row = (long long)b * p.R + r;
-    out = p.out + row * p.V;
-    src = reinterpret_cast<const T*>(p.logits) + row * p.stride;
-    mask = nullptr;
-    if (p.mask) {
-      const long long m = p.mask_row ? p.mask_row[row] : row;
-      if (m >= 0 && m < p.n_masks) mask = p.mask + m * p.words;
-    }
-    off = (int)(((uintptr_t)out >> 2) & 7);
+  struct Row {
+    const T* src;
+    float* out;
+    const uint32_t* mask;
+    int off;
   };
-  Unit<T> g[kFlight];
-  uint32_t ok[kFlight];  // ids that may be drawn
-  auto unit_id = [&](int f) { return first + 8 * (int)(threadIdx.x + f * kThreads) - off; };
+  auto row_of = [&](int r) {
+    const long long at = (long long)b * p.R + r;
+    Row row{reinterpret_cast<const T*>(p.logits) + at * p.stride, p.out + at * p.V, nullptr, 0};
+    if (p.mask) {
+      const long long m = p.mask_row ? p.mask_row[at] : at;
+      if (m >= 0 && m < p.n_masks) row.mask = p.mask + m * p.words;
+    }
+    row.off = (int)(((uintptr_t)row.out >> 2) & 7);
+    return row;
+  };
+  Unit<T> g[kRows][kFlight];
+  uint32_t ok[kRows][kFlight];  // ids that may be drawn
+  auto unit_id = [&](const Row& row, int f) {
+    return first + 8 * (int)(threadIdx.x + f * kThreads) - row.off;
+  };
   auto there = [&](int f, int id) {  // (id: the unit's first)
     return 8 * (threadIdx.x + f * kThreads) < p.slice && id < p.V;
   };
-  auto load = [&]() {
-    const bool aligned = (((uintptr_t)src - off * sizeof(T)) & (8 * sizeof(T) - 1)) == 0;
+  auto load = [&](int r) {  // rows r .. r + kRows - 1
 #pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      const int id = unit_id(f);
-      ok[f] = 255u;
-      if (mask && there(f, id))
-        ok[f] = eight_bits(reinterpret_cast<const uint8_t*>(mask), id, 4 * p.words - 1);
-    }
-    if (p.in_place) return;
+    for (int x = 0; x < kRows; ++x) {
+      if (r + x >= r1) break;
+      const Row row = row_of(r + x);
+      const bool aligned = (((uintptr_t)row.src - row.off * sizeof(T)) & (8 * sizeof(T) - 1)) == 0;
 #pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      const int id = unit_id(f);
-      if (!ok[f] || !there(f, id)) continue;
-      if (aligned && id >= 0 && id + 8 <= p.V) {
-        load_unit(src + id, g[f]);
-      } else {
+      for (int f = 0; f < kFlight; ++f) {
+        const int id = unit_id(row, f);
+        uint32_t m = 255u;
+        if (row.mask && there(f, id))
+          m = eight_bits(reinterpret_cast<const uint8_t*>(row.mask), id, 4 * p.words - 1);
+        ok[x][f] = m;
+        if (!m || p.in_place || !there(f, id)) continue;
+        if (aligned && id >= 0 && id + 8 <= p.V) {
+          load_unit(row.src + id, g[x][f]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if ((unsigned)(id + i) < (unsigned)p.V) g[f].x[i] = src[id + i];
+          for (int i = 0; i < 8; ++i)
+            if ((unsigned)(id + i) < (unsigned)p.V) g[x][f].x[i] = row.src[id + i];
+        }
       }
     }
   };
-  begin_row(r0);
-  load();  // (on its way while the ids are counted)
+  load(r0);  // (on its way while the ids are counted)
 
   auto mark = [&](int i) {
     const uint32_t bit = 1u << (i & 31);
     if (!(atomicOr(touched + (i >> 5), bit) & bit)) list[atomicAdd(&listed, 1)] = (uint16_t)i;
   };
   float rep = 1.f, freq = 0.f, pres = 0.f;
-  uint64_t here = 0;  // block tokens that are ids of this slice
   if (any) __syncthreads();
   if (p.counts) {
     rep = p.repetition ? p.repetition[b] : 1.f;
@@ -199,7 +203,10 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
         t = p.parent ? p.tokens[(size_t)b * p.R + i] : p.tokens[(size_t)b * (p.R - 1) + i - 1];
       t = (int)index(t);
       tok[i] = t;
-      if (t >= 0) mark(t);
+      if (t >= 0) {
+        atomicOr(count + t, kBlock);
+        mark(t);
+      }
       uint64_t m = 0;
       if (p.parent) {
         int v = i;
@@ -212,12 +219,6 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
         m = (i >= 63 ? ~0ull : (2ull << i) - 1) & ~1ull;
       }
       anc[i] = m;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      const uint32_t lo = __ballot_sync(0xffffffffu, lane < p.R && tok[lane] >= 0);
-      const uint32_t hi = __ballot_sync(0xffffffffu, lane + 32 < p.R && tok[lane + 32] >= 0);
-      if (lane == 0) here_s = (uint64_t)hi << 32 | lo;
     }
   }
   if (p.biases) {
@@ -248,65 +249,61 @@ __global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_consta
         }
     }
   }
-  if (any) __syncthreads();
-  if (p.counts) here = here_s;
-  const int n_listed = any ? listed : 0;
 
-  uint64_t counted = 0;  // block tokens that the counts hold
-  for (int r = r0; r < r1; ++r) {
+  for (int r = r0; r < r1; r += kRows) {
+    if (r > r0) load(r);
 #pragma unroll
-    for (int f = 0; f < kFlight; ++f) {
-      const int id = unit_id(f);
-      if (!there(f, id)) continue;
-      float y[8];
+    for (int x = 0; x < kRows; ++x) {
+      if (r + x >= r1) break;
+      const long long at = (long long)b * p.R + r + x;
+      float* out = p.out + at * p.V;
+      const int off = (int)(((uintptr_t)out >> 2) & 7);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = !p.in_place && (ok[f] >> i & 1) ? to_float(g[f].x[i]) : -INFINITY;
-      uint32_t put = 255u;
-      if (id < 0) put = 255u << -id & 255u;
-      if (id + 8 > p.V) put &= (1u << (p.V - id)) - 1;
-      if (p.in_place) put &= ~ok[f];
-      if (put == 255u) {
-        store_unit(out + id, y);
-      } else if (put) {
+      for (int f = 0; f < kFlight; ++f) {
+        const int id = first + 8 * (int)(threadIdx.x + f * kThreads) - off;
+        if (!there(f, id)) continue;
+        float y[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (put >> i & 1) out[id + i] = y[i];
-      }
-    }
-    const T* const from = src;
-    float* const to = out;
-    const uint32_t* const allowed = mask;
-    const int begin = first - off;
-    if (r + 1 < r1) {
-      begin_row(r + 1);
-      load();
-    }
-    if (n_listed == 0) continue;
-    // ---- what the counts and biases touch, behind the stores of the other threads
-    __syncthreads();
-    const uint64_t want = p.counts ? anc[r] & here : 0, change = want ^ counted;
-    if (change) {
-      if (threadIdx.x < 64 && change >> threadIdx.x & 1)
-        atomicAdd(count + tok[threadIdx.x], want >> threadIdx.x & 1 ? 1u : ~0u);
-      counted = want;
-      __syncthreads();
-    }
-    for (int e = threadIdx.x; e < n_listed; e += kThreads) {
-      const int i = list[e], id = base + i;
-      if ((unsigned)(id - begin) >= (unsigned)p.slice) continue;  // (a neighbour's, in this row)
-      if (allowed && !(allowed[id >> 5] >> (id & 31) & 1)) continue;
-      float x = p.in_place ? to[id] : to_float(from[id]);
-      if (p.counts) {
-        const uint32_t c = count[i], n = c & ~kPrompt;
-        if (c && p.repetition) x = x > 0.f ? __fdiv_rn(x, rep) : x * rep;
-        if (n) {
-          if (p.frequency) x = __fsub_rn(x, __fmul_rn(freq, (float)n));
-          if (p.presence) x = __fsub_rn(x, pres);
+          y[i] = !p.in_place && (ok[x][f] >> i & 1) ? to_float(g[x][f].x[i]) : -INFINITY;
+        uint32_t put = 255u;
+        if (id < 0) put = 255u << -id & 255u;
+        if (id + 8 > p.V) put &= (1u << (p.V - id)) - 1;
+        if (p.in_place) put &= ~ok[x][f];
+        if (put == 255u) {
+          store_unit(out + id, y);
+        } else if (put) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (put >> i & 1) out[id + i] = y[i];
         }
       }
-      if (p.biases) x += add[i];
-      to[id] = x;
     }
+  }
+  if (!any) return;
+
+  // ---- what the counts and biases touch, behind the stores of the other threads
+  __syncthreads();
+  const int n_listed = listed, n = n_listed * (r1 - r0);
+  for (int j = threadIdx.x; j < n; j += kThreads) {
+    const int u = j / n_listed, i = list[j - u * n_listed], id = base + i;
+    const Row row = row_of(r0 + u);
+    if ((unsigned)(id - first + row.off) >= (unsigned)p.slice) continue;  // (a neighbour's, in this row)
+    if (row.mask && !(row.mask[id >> 5] >> (id & 31) & 1)) continue;
+    float x = p.in_place ? row.out[id] : to_float(row.src[id]);
+    if (p.counts) {
+      const uint32_t c = count[i];
+      uint64_t before = c & kBlock ? anc[r0 + u] : 0;  // rows of the block in front of this one
+      int n = c & (kBlock - 1);
+      for (; before; before &= before - 1) n += tok[__ffsll((long long)before) - 1] == i;
+      if ((n > 0 || (c & kPrompt)) && p.repetition) x = x > 0.f ? __fdiv_rn(x, rep) : x * rep;
+      if (n > 0) {
+        if (p.frequency) x = __fsub_rn(x, __fmul_rn(freq, (float)n));
+        if (p.presence) x = __fsub_rn(x, pres);
+      }
+    }
+    if (p.biases) x += add[i];
+    row.out[id] = x;
   }
 }
 
@@ -350,7 +347,7 @@ extern "C" spec_status spec_logits_process(
     const int32_t* mask_row, void* stream) {
   if (B < 0 || R < 1 || R > 64 || V < 1 || H < 0 || n_bias < 0 || n_masks < 0) return SPEC_EINVAL;
   if (dtype != SPEC_F32 && dtype != SPEC_BF16 && dtype != SPEC_F16) return SPEC_EINVAL;
-  if (V > INT32_MAX - 4 * kMostSlice || H > INT32_MAX - 4096 || n_bias > INT32_MAX - 4096 || B > 65535)
+  if (V > INT32_MAX - 4 * kMostSlice || H >= (int)kBlock || n_bias > INT32_MAX - 4096 || B > 65535)
     return SPEC_EUNSUPPORTED;
   if ((H > 0 && !history) || (parent && !block_tokens) || (n_bias > 0 && (!bias_ids || !bias)) ||
       (n_masks > 0 && !mask))
