@@ -26,7 +26,7 @@
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr uint32_t kPrompt = 0x80000000u;   // of a count: the id stands in the prompt
 constexpr uint32_t kBlock = 0x40000000u;    // a block token
@@ -88,7 +88,7 @@ __host__ __device__ constexpr int touched_words(int slice) {  // whole 16 bytes
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) logits_kernel(const __grid_constant__ LogitsParams p) {
+__global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_constant__ LogitsParams p) {
   extern __shared__ __align__(16) uint32_t sm[];
   const int S = p.slice + kHalo;
   uint32_t* touched = sm;                                   // a bit for each id: in the list
@@ -385,7 +385,8 @@ extern "C" spec_status spec_logits_process(
   // A CTA per sequence and slice walks all rows where that fills the GPU; else the rows are dealt out
   // too, and where even that leaves SMs idle the slices are shorter.
   const int sms = sm_count();
-  p.slice = (long long)B * R * ((V + kMostSlice - 1) / kMostSlice) >= sms ? kMostSlice : 1024;
+  p.slice = kMostSlice;
+  while (p.slice > 1024 && (long long)B * R * ((V + p.slice - 1) / p.slice) < sms) p.slice /= 2;
   const long long ctas = (long long)B * ((V + p.slice - 1) / p.slice);
   p.rows = std::max<int>(1, (int)std::min<long long>(R, R * ctas / (2 * sms)));
   p.row_groups = (R + p.rows - 1) / p.rows;
