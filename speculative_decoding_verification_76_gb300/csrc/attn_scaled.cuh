@@ -309,12 +309,31 @@ SPEC_DEV uint32_t swizzled(int rows, int r, int c) {
   return (uint32_t)(c >> 3) * (rows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
+template <bool kWide>
+struct RowBits {
+  using T = uint32_t;
+};
+template <>
+struct RowBits<true> {
+  using T = uint64_t;
+};
+
+// Whether a position's V row has NaN codes.
+template <int D>
+SPEC_DEV bool has_nans(const uint8_t* tile, int tok) {
+  uint32_t nan = 0;
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    const uint4 w = *reinterpret_cast<const uint4*>(tile + swizzled<D>(kUnit, tok, c));
+    nan |= nan_bytes(w.x) | nan_bytes(w.y) | nan_bytes(w.z) | nan_bytes(w.w);
+  }
+  return nan != 0;
+}
+
 // NaN codes in a position's V row: noted for the query rows that see it, and zeroed (positions that only some
 // rows see; hardly ever anything to do).
 template <int D>
-__device__ __noinline__ bool note_nans(uint8_t* tile, int tok, int t, int jb, int rows, const uint64_t* see,
-                                       const int* from, uint32_t* notes) {
-  bool any = false;
+__device__ __noinline__ void note_nans(uint8_t* tile, int tok, uint64_t rows, uint32_t* notes) {
 #pragma unroll 1
   for (int c = 0; c < D / 16; ++c) {
     uint32_t* u4 = reinterpret_cast<uint32_t*>(tile + swizzled<D>(kUnit, tok, c));
@@ -322,16 +341,14 @@ __device__ __noinline__ bool note_nans(uint8_t* tile, int tok, int t, int jb, in
     for (int e = 0; e < 4; ++e) {
       const uint32_t nan = nan_bytes(u4[e]);
       if (!nan) continue;
-      any = true;
       const uint32_t bits = nan >> 7 & 1 | nan >> 14 & 2 | nan >> 21 & 4 | nan >> 28 & 8;
 #pragma unroll 1
-      for (int n = 0; n < rows; ++n)
-        if (jb < 0 ? t >= from[n] : jb < 64 && (see[n] >> jb & 1))
-          atomicOr(&notes[n * (D / 32) + (c >> 1)], bits << (16 * (c & 1) + 4 * e));
+      for (uint64_t left = rows; left; left &= left - 1)
+        atomicOr(&notes[(__ffsll((long long)left) - 1) * (D / 32) + (c >> 1)],
+                 bits << (16 * (c & 1) + 4 * e));
       u4[e] &= ~((nan >> 7) * 255u);
     }
   }
-  return any;
 }
 
 template <int D, int RT, bool F16>
@@ -351,6 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
   __shared__ int from_s[2][RT], any_nan[2];
   __shared__ uint32_t nan_s[2][RT][D / 32];
   __shared__ __align__(16) float neg_m[2][RT], fac_s[2][RT], red[kSoftWarps][RT], inv_s[RT];
+  // the rows that see a position, for tiles where not all of them do: of a group's last two tiles
+  using Rows = typename RowBits<(RT > 32)>::T;
+  __shared__ Rows seen_by[2][2][kUnit];
   __shared__ Walk start;
   __shared__ uint32_t tmem_base;
   __shared__ int part_w[kThreads / 32];
@@ -366,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
   const int rows = min(p.rows_per_tile, p.R * p.G - tile * p.rows_per_tile);
 
   chain_wait();
+  chain_next();  // (the joining kernel may be set up)
   // ---- this CTA's range, and the sequence it begins in: each thread sums consecutive sequences
   {
     const int per = (p.B + kThreads - 1) / kThreads;
@@ -445,89 +466,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
       const int32_t* bt = p.table + (size_t)b * p.max_pages;
       int t = walk.seq.first + walk.first_unit() * kUnit + tid;
       int page = p.P.quot(t), off = t - page * p.P.d, id = t < end ? bt[page] : -1;
-      // the segment before the last is done with this one's places
-      if (seg >= S::kQBufs)
-        ok = __all_sync(0xffffffffu,
-                        wait_for(&seg_done[(seg - S::kQBufs) & 1], (seg - S::kQBufs) >> 1 & 1, p));
-      if (!ok) break;
-      // ---- Q as sums of e4m3 parts under a power of two per row
-      {
-        constexpr int kPer = kLoad / RT;            // threads of a row
-        constexpr int kMine = D / 8 / kPer > 0 ? D / 8 / kPer : 1;  // 16-byte chunks of a thread
-        const int n = tid / kPer, x0 = tid % kPer;
-        const int row = tile * p.rows_per_tile + n, i = p.per_head.quot(row);
-        const bool real = n < rows;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (b * p.q_stride_b + (real ? i : 0) * p.q_stride_r +
-                   (walk.kvh * p.G + (real ? row - i * p.G : 0)) * p.q_stride_h) * 2);
-        auto values = [&](const uint4& w, float* x) {
-          const uint32_t* u = reinterpret_cast<const uint32_t*>(&w);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if constexpr (F16) {
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(u + e));
-              x[2 * e] = f.x, x[2 * e + 1] = f.y;
-            } else {
-              x[2 * e] = __uint_as_float(u[e] << 16);
-              x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-            }
-          }
-        };
-        // the largest magnitude, as bits; what is not finite has all exponent bits
-        uint32_t big2 = 0;
-#pragma unroll
-        for (int m = 0; m < kMine; ++m) {
-          const int c = x0 + m * kPer;
-          const uint4 w = real && c < D / 8 ? src[c] : make_uint4(0, 0, 0, 0);
-          big2 = __vimax3_u16x2(big2, w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
-          big2 = __vimax3_u16x2(big2, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu);
-        }
-#pragma unroll
-        for (int o = 1; o < kPer; o <<= 1) big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, o));
-        const uint32_t big = max(big2 & 0xffffu, big2 >> 16);
-        const bool bad = big >= (F16 ? 0x7c00u : 0x7f80u);  // (then only the row's scale matters)
-        const float s = needed_scale(F16 ? __half2float(__ushort_as_half((unsigned short)big))
-                                         : __uint_as_float(big << 16));
-        const float down = 1.f / s;
-#pragma unroll 1
-        for (int m = 0; m < kMine; ++m) {
-          const int c = x0 + m * kPer;
-          if (c >= D / 8) break;
-          float x[8];
-          values(real ? src[c] : make_uint4(0, 0, 0, 0), x);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= down;
-          uint8_t* to = q_0 + seg % S::kQBufs * S::kQBytes + swizzled<D>(RT, n, c >> 1) + (c & 1) * 8;
-#pragma unroll 1
-          for (int part = 0; part < S::kParts; ++part) {
-            const uint2 w = make_uint2(e4m3_word(x[0], x[1], x[2], x[3]),
-                                       e4m3_word(x[4], x[5], x[6], x[7]));
-            *reinterpret_cast<uint2*>(to + part * RT * D) = w;
-            float y[8];
-            e4m3_values(w.x, y);
-            e4m3_values(w.y, y + 4);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] -= y[e];
-          }
-        }
-        if (x0 == 0) {
-          sc_s[sb][n] = bad ? NAN : real ? p.scale_log2 * s : 0.f;
-          uint64_t m = 0;
-          if (real) {
-            m = p.mask ? p.mask[(size_t)b * p.R + i] : i >= 63 ? ~0ull : (2ull << i) - 1;
-            if (p.R < 64) m &= (1ull << p.R) - 1;
-          }
-          see_s[sb][n] = m;
-          out_s[sb][n] = whole ? ((long long)b * p.R + i) * p.Hq + walk.kvh * p.G + row - i * p.G
-                               : (long long)part_at * RT + n;
-          from_s[sb][n] = p.window > 0 ? ctx + __popcll(m) - p.window : 0;
-#pragma unroll 1
-          for (int e = 0; e < D / 32; ++e) nan_s[sb][n][e] = 0;
-        }
-        if (tid == 0) any_nan[sb] = 0;
-        fence_proxy_async();
-        mbar_arrive(&q_full[sb]);
-      }
       const char* kh = p.k + walk.kvh * p.head_stride + chunk * 16;
       const char* vh = p.v + walk.kvh * p.head_stride + chunk * 16;
 #pragma unroll 1
@@ -574,6 +512,90 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
                            smem_u32(&full[stage]))
                        : "memory");
+        if (j > 0) continue;
+        // ---- behind the segment's first tile: Q as sums of e4m3 parts under a power of two per row
+        // (the segment before the last is done with the places)
+        if (seg >= S::kQBufs)
+          ok = __all_sync(0xffffffffu,
+                          wait_for(&seg_done[(seg - S::kQBufs) & 1], (seg - S::kQBufs) >> 1 & 1, p));
+        if (!ok) break;
+        {
+          constexpr int kPer = kLoad / RT;            // threads of a row
+          constexpr int kMine = D / 8 / kPer > 0 ? D / 8 / kPer : 1;  // 16-byte chunks of a thread
+          const int n = tid / kPer, x0 = tid % kPer;
+          const int row = tile * p.rows_per_tile + n, i = p.per_head.quot(row);
+          const bool real = n < rows;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              p.q + (b * p.q_stride_b + (real ? i : 0) * p.q_stride_r +
+                     (walk.kvh * p.G + (real ? row - i * p.G : 0)) * p.q_stride_h) * 2);
+          auto values = [&](const uint4& w, float* x) {
+            const uint32_t* u = reinterpret_cast<const uint32_t*>(&w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if constexpr (F16) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(u + e));
+                x[2 * e] = f.x, x[2 * e + 1] = f.y;
+              } else {
+                x[2 * e] = __uint_as_float(u[e] << 16);
+                x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+              }
+            }
+          };
+          // the largest magnitude, as bits; what is not finite has all exponent bits
+          uint32_t big2 = 0;
+#pragma unroll
+          for (int m = 0; m < kMine; ++m) {
+            const int c = x0 + m * kPer;
+            const uint4 w = real && c < D / 8 ? src[c] : make_uint4(0, 0, 0, 0);
+            big2 = __vimax3_u16x2(big2, w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
+            big2 = __vimax3_u16x2(big2, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu);
+          }
+#pragma unroll
+          for (int o = 1; o < kPer; o <<= 1) big2 = __vmaxu2(big2, __shfl_xor_sync(0xffffffffu, big2, o));
+          const uint32_t big = max(big2 & 0xffffu, big2 >> 16);
+          const bool bad = big >= (F16 ? 0x7c00u : 0x7f80u);  // (then only the row's scale matters)
+          const float s = needed_scale(F16 ? __half2float(__ushort_as_half((unsigned short)big))
+                                           : __uint_as_float(big << 16));
+          const float down = 1.f / s;
+#pragma unroll 1
+          for (int m = 0; m < kMine; ++m) {
+            const int c = x0 + m * kPer;
+            if (c >= D / 8) break;
+            float x[8];
+            values(real ? src[c] : make_uint4(0, 0, 0, 0), x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= down;
+            uint8_t* to = q_0 + seg % S::kQBufs * S::kQBytes + swizzled<D>(RT, n, c >> 1) + (c & 1) * 8;
+#pragma unroll 1
+            for (int part = 0; part < S::kParts; ++part) {
+              const uint2 w = make_uint2(e4m3_word(x[0], x[1], x[2], x[3]),
+                                         e4m3_word(x[4], x[5], x[6], x[7]));
+              *reinterpret_cast<uint2*>(to + part * RT * D) = w;
+              float y[8];
+              e4m3_values(w.x, y);
+              e4m3_values(w.y, y + 4);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] -= y[e];
+            }
+          }
+          if (x0 == 0) {
+            sc_s[sb][n] = bad ? NAN : real ? p.scale_log2 * s : 0.f;
+            uint64_t m = 0;
+            if (real) {
+              m = p.mask ? p.mask[(size_t)b * p.R + i] : i >= 63 ? ~0ull : (2ull << i) - 1;
+              if (p.R < 64) m &= (1ull << p.R) - 1;
+            }
+            see_s[sb][n] = m;
+            out_s[sb][n] = whole ? ((long long)b * p.R + i) * p.Hq + walk.kvh * p.G + row - i * p.G
+                                 : (long long)part_at * RT + n;
+            from_s[sb][n] = p.window > 0 ? ctx + __popcll(m) - p.window : 0;
+#pragma unroll 1
+            for (int e = 0; e < D / 32; ++e) nan_s[sb][n][e] = 0;
+          }
+          if (tid == 0) any_nan[sb] = 0;
+          fence_proxy_async();
+          mbar_arrive(&q_full[sb]);
+        }
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -715,8 +737,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         // positions that some rows see and others do not
         const bool mixed = (t0 + kUnit > ctx && (p.R > 1 || p.mask)) ||
                            (p.window > 0 && t0 < ctx + p.R - p.window);
-        if (mixed && note_nans<D>(vrow, tid, t0 + tid, t0 + tid - ctx, RT, see_s[sb], from_s[sb], nan_s[sb][0]))
-          any_nan[sb] = 1;
+        // (a buffer's last readers are done: all of them have handed over weights behind it, or the scores
+        // that this group took last would not be there)
+        Rows* const seen = seen_by[group][u >> 1 & 1];
+        if (mixed) {
+          const int t = t0 + tid, jb = t - ctx;
+          Rows m = 0;
+#pragma unroll 8
+          for (int n = 0; n < RT; ++n)
+            m |= (Rows)(jb < 0 ? t >= from_s[sb][n] : jb < 64 && (see_s[sb][n] >> (jb & 63) & 1)) << n;
+          seen[tid] = m;
+          if (has_nans<D>(vrow, tid)) {
+            note_nans<D>(vrow, tid, m, nan_s[sb][0]);
+            any_nan[sb] = 1;
+          }
+          sync_of(bar, kGroup);
+        }
         if constexpr (S::kHalfV) {  // position tid's V as fp16, 64 dimensions a row
           // (the product that read the buffer last is complete)
           if (u >= 2) ok = ok && wait_for(&pv_done[(u - 2) & 3], (u - 2) >> 2 & 1, p);
@@ -767,18 +803,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
               }
             }
             if (mixed) {
-              uint32_t see = 0;  // 2 kB bits a position
-#pragma unroll 1
-              for (int x = 0; x < 4 * 2 * kB; ++x) {
-                const int i = x & (2 * kB - 1), n = 8 * (h + (i >> 1)) + c2 + (i & 1);
-                const int t = t0 + t_lane + 8 * (x / (2 * kB)), jb = t - ctx;
-                if (jb < 0 ? t >= from_s[sb][n] : jb < 64 && (see_s[sb][n] >> jb & 1)) see |= 1u << x;
-              }
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
+              for (int r = 0; r < 4; ++r) {
+                const uint32_t see = (uint32_t)(seen[t_lane + 8 * r] >> (8 * h + c2));
 #pragma unroll
                 for (int i = 0; i < 2 * kB; ++i)
-                  a[r][i] = see >> (2 * kB * r + i) & 1 ? a[r][i] : -INFINITY;
+                  a[r][i] = see >> (8 * (i >> 1) + (i & 1)) & 1 ? a[r][i] : -INFINITY;
+              }
             }
             if (moved) break;
 #pragma unroll
@@ -806,9 +837,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
                 float z0 = __uint_as_float(y[r >> 1][2 * (r & 1)]) * sc.x * ks[r] + lvs[r];
                 float z1 = __uint_as_float(y[r >> 1][2 * (r & 1) + 1]) * sc.y * ks[r] + lvs[r];
                 if (mixed) {
-                  const int t = t0 + t_lane + 8 * r, jb = t - ctx, n = 8 * k + c2;
-                  if (!(jb < 0 ? t >= from_s[sb][n] : jb < 64 && (see_s[sb][n] >> jb & 1))) z0 = -INFINITY;
-                  if (!(jb < 0 ? t >= from_s[sb][n + 1] : jb < 64 && (see_s[sb][n + 1] >> jb & 1))) z1 = -INFINITY;
+                  const Rows see = seen[t_lane + 8 * r] >> (8 * k + c2);
+                  if (!(see & 1)) z0 = -INFINITY;
+                  if (!(see & 2)) z1 = -INFINITY;
                 }
                 m0 = fmaxf(m0, z0);
                 m1 = fmaxf(m1, z1);
@@ -1018,7 +1049,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per_seq = (p.R * p.Hq + kJoinWarps - 1) / kJoinWarps;
   const int b = blockIdx.x / per_seq, r = blockIdx.x % per_seq * kJoinWarps + warp;
-  chain_wait();
+  // (in front of its wait it reads the lengths only: what wrote them the kernel in front has waited for)
   int before = 0, W = 0;
   for (int x = threadIdx.x; x < p.B; x += 32 * kJoinWarps) {
     const int u = seq_of(p, x).units;
@@ -1035,6 +1066,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   W = before = 0;
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) W += sums[w][0], before += sums[w][1];
+  chain_wait();
   if (r >= p.R * p.Hq) return;
   const int i = r / p.Hq, h = r % p.Hq, kvh = h / p.G, row = i * p.G + h % p.G;
   const size_t at = (size_t)b * p.R * p.Hq + r;
@@ -1052,28 +1084,39 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
       return (((size_t)(first + x) * 2 + (x == 0 && late)) * p.tiles + tile) * RT + n;
     };
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-    for (int x = lane; x < np; x += 32) M = fmaxf(M, __ldcg(ml + part(x)).x);
-    M = warp_max(M);
-    constexpr int kFlight = 8;
+    constexpr int kFlight = D == 256 ? 8 : 16;
 #pragma unroll 1
     for (int x0 = 0; x0 < np; x0 += kFlight) {
-      float y[kFlight][kPer], e[kFlight];
+      float2 w[kFlight], y[kFlight][kPer / 2];
+      float now = M;
 #pragma unroll
       for (int x = 0; x < kFlight; ++x) {
-        const size_t from = part(min(x0 + x, np - 1));
-        const float2 w = __ldcg(ml + from);
-        e[x] = x0 + x < np ? fast_exp2(w.x - M) : 0.f;
-        L += e[x] * w.y;
+        if (x0 + x >= np) break;
+        const size_t from = part(x0 + x);
+        w[x] = __ldcg(ml + from);
 #pragma unroll
-        for (int c = 0; c < kPer; c += 2) {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(p.part_o + from * D + kPer * lane + c));
-          y[x][c] = v.x, y[x][c + 1] = v.y;
-        }
+        for (int c = 0; c < kPer / 2; ++c)
+          y[x][c] = __ldcg(reinterpret_cast<const float2*>(p.part_o + from * D + kPer * lane) + c);
       }
 #pragma unroll
       for (int x = 0; x < kFlight; ++x)
+        if (x0 + x < np) now = fmaxf(now, w[x].x);
+      const float f = fast_exp2(M - now);
+      M = now;
+      L *= f;
 #pragma unroll
-        for (int c = 0; c < kPer; ++c) acc[c] += x0 + x < np ? e[x] * y[x][c] : 0.f;
+      for (int c = 0; c < kPer; ++c) acc[c] *= f;
+#pragma unroll
+      for (int x = 0; x < kFlight; ++x) {
+        if (x0 + x >= np) break;
+        const float e = fast_exp2(w[x].x - M);
+        L += e * w[x].y;
+#pragma unroll
+        for (int c = 0; c < kPer / 2; ++c) {
+          acc[2 * c] += e * y[x][c].x;
+          acc[2 * c + 1] += e * y[x][c].y;
+        }
+      }
     }
   }
   const float f = L == 0.f ? 0.f : 1.f / L;
