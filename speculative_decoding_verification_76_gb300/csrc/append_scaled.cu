@@ -24,7 +24,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 16;        // rows of a CTA where there are many
-constexpr int kFewRows = 2432;   // up to sixteen per SM: a CTA per row
 constexpr int kPasses = 4;       // row groups (items) that a warp (thread) keeps in registers
 
 struct AppendParams {
@@ -36,7 +35,7 @@ struct AppendParams {
   long long k_stride, v_stride, q_stride, q_out_stride;      // elements
   long long page_stride, token_stride, head_stride;          // bytes
   FastDiv P, block, heads, per;                              // KV heads; items of a row's queries
-  int T, Hq, Hkv, W, num_slots;
+  int T, Hq, Hkv, W, Wq, tiles, num_slots;                   // rows of a CTA; CTAs of the keys
   RopeTable<128> rope;
 };
 
@@ -63,6 +62,59 @@ SPEC_DEV void move_others(char* cache, long long token_stride, int block, uint64
     }
 }
 
+// Queries: a CTA turns Wq rows; what its threads hold at once is on its way while the angles are worked out.
+template <typename T, int D>
+SPEC_DEV void turn_queries(const AppendParams& p, int t0, float* table, int* live) {
+  constexpr int kItems = D / 16;
+  const int rows = min(p.Wq, p.T - t0), n = rows * p.per.d;
+  uint4 raw[kPasses][2];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int x = 0; x < kPasses; ++x) {
+      const int i = i0 + x * kThreads, u = p.per.quot(i), y = i - u * p.per.d;
+      if (i >= n) break;
+      const int2 c = rope_chunks(p.rope, y % kItems);
+      const uint4* row = reinterpret_cast<const uint4*>(
+          reinterpret_cast<const T*>(p.q) + (t0 + u) * p.q_stride + y / kItems * D);
+      raw[x][0] = __ldcs(row + c.x);
+      raw[x][1] = __ldcs(row + c.y);
+    }
+  };
+  load(threadIdx.x);
+  for (int i = threadIdx.x; i < rows * (D / 2); i += kThreads) {
+    const int u = i / (D / 2), j = i % (D / 2);
+    const int at = p.pos ? p.pos[t0 + u] : 0;
+    if (j == 0) {
+      const int64_t slot = p.slots[t0 + u];
+      live[u] = slot >= 0 && slot < p.num_slots && at >= 0;
+    }
+    if (p.rope.pairs == 0) continue;
+    const float2 e = rope_entry(p.rope, at, j);
+    table[u * D + j] = e.x;
+    table[u * D + D / 2 + j] = e.y;
+  }
+  __syncthreads();
+  for (int i0 = threadIdx.x; i0 < n; i0 += kPasses * kThreads) {
+    if (i0 != threadIdx.x) load(i0);
+#pragma unroll
+    for (int x = 0; x < kPasses; ++x) {
+      const int i = i0 + x * kThreads, u = p.per.quot(i), y = i - u * p.per.d, j = y % kItems;
+      if (i >= n) break;
+      if (!live[u]) continue;
+      const int2 c = rope_chunks(p.rope, j);
+      uint4* to = reinterpret_cast<uint4*>(
+          reinterpret_cast<T*>(p.q_out) + (t0 + u) * p.q_out_stride + y / kItems * D);
+      float a[8], e[8];
+      unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&raw[x][0]), a);
+      unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&raw[x][1]), e);
+      if (p.rope.pairs > 0)
+        rope_turn(p.rope.interleaved, a, e, table + u * D + 8 * j, table + u * D + D / 2 + 8 * j);
+      to[c.x] = pack_chunk<T>(a).w[0];
+      to[c.y] = pack_chunk<T>(e).w[0];
+    }
+  }
+}
+
 // T: type of the rows
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 3) append_scaled_kernel(
@@ -77,10 +129,14 @@ __global__ void __launch_bounds__(kThreads, 3) append_scaled_kernel(
   __shared__ int run_at[kTile], run_n[kTile];     // the runs that begin here
   __shared__ int runs, rows_end, longest;
   __shared__ float big_s[2][kWarps];
-  const int parts = p.Hq ? 3 : 2, part = blockIdx.x % parts;  // keys, values, queries
-  const int t0 = blockIdx.x / parts * p.W, t1 = min(t0 + p.W, p.T);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   chain_wait();
+  if ((int)blockIdx.x >= 2 * p.tiles) {
+    turn_queries<T, D>(p, (blockIdx.x - 2 * p.tiles) * p.Wq, table, slot_s);
+    return;
+  }
+  const bool is_k = (blockIdx.x & 1) == 0;
+  const int t0 = (int)(blockIdx.x >> 1) * p.W, t1 = min(t0 + p.W, p.T);
   const int look = min(t1 - 1 + p.block.d, p.T);  // past the last row a run from here may have
   if (threadIdx.x <= look - t0) {
     const int t = t0 - 1 + (int)threadIdx.x;
@@ -93,38 +149,62 @@ __global__ void __launch_bounds__(kThreads, 3) append_scaled_kernel(
     slot_s[threadIdx.x] = s;
     pos_s[threadIdx.x] = at;
   }
-  if (threadIdx.x == 0) runs = 0, rows_end = part == 2 ? t1 : t0, longest = 0;
+  if (threadIdx.x == 0) runs = 0, rows_end = t0, longest = 0;
   __syncthreads();
   // ---- the runs that begin in t0 .. t1 - 1, in order
-  if (part < 2) {
-    if (warp == 0) {
-      const int t = t0 + lane;
-      bool first = false;
-      int n = 0;
-      if (t < t1 && slot_s[lane + 1] >= 0) {
-        const int b = p.block.quot(slot_s[lane + 1]), before = slot_s[lane];
-        first = before < 0 || p.block.quot(before) != b;
-        if (first) {
-          n = 1;
-          while (n < p.block.d && t + n < look && slot_s[lane + 1 + n] >= 0 &&
-                 p.block.quot(slot_s[lane + 1 + n]) == b)
-            ++n;
-        }
-      }
-      const uint32_t who = __ballot_sync(0xffffffffu, first);
+  if (warp == 0) {
+    const int t = t0 + lane;
+    bool first = false;
+    int n = 0;
+    if (t < t1 && slot_s[lane + 1] >= 0) {
+      const int b = p.block.quot(slot_s[lane + 1]), before = slot_s[lane];
+      first = before < 0 || p.block.quot(before) != b;
       if (first) {
-        const int i = __popc(who & ((1u << lane) - 1));
-        run_at[i] = t;
-        run_n[i] = n;
-        atomicMax(&rows_end, t + n);
-        atomicMax(&longest, n);
+        n = 1;
+        while (n < p.block.d && t + n < look && slot_s[lane + 1 + n] >= 0 &&
+               p.block.quot(slot_s[lane + 1 + n]) == b)
+          ++n;
       }
-      if (lane == 0) runs = __popc(who);
     }
-    __syncthreads();
-    if (runs == 0) return;
+    const uint32_t who = __ballot_sync(0xffffffffu, first);
+    if (first) {
+      const int i = __popc(who & ((1u << lane) - 1));
+      run_at[i] = t;
+      run_n[i] = n;
+      atomicMax(&rows_end, t + n);
+      atomicMax(&longest, n);
+    }
+    if (lane == 0) runs = __popc(who);
   }
-  const bool turn = part != 1 && p.rope.pairs > 0;
+  __syncthreads();
+  if (runs == 0) return;
+
+  // ---- keys or values: a team of warps, as many as hold the longest run, takes a run of one head
+  int team_warps = 1;
+  while (team_warps * kWarpRows < longest) team_warps *= 2;
+  const int team = warp / team_warps, mine = warp % team_warps, threads = 32 * team_warps;
+  const int items = runs * p.Hkv, step = kWarps / team_warps;
+  const int j = lane % kItems, sub = lane / kItems;   // item of a row, row of a pass
+  const int2 c = is_k ? rope_chunks(p.rope, j) : make_int2(j, j + kItems);
+  const bool turn = is_k && p.rope.pairs > 0;
+  const int base = mine * kWarpRows;
+  uint4 raw[kPasses][2];
+  float stored = 0.f;
+  auto load = [&](int i) {  // an item's rows (behind the last: the last again) and scale
+    const int r = p.heads.quot(i), h = i - r * p.Hkv, at = run_at[r], n = run_n[r];
+    const T* src = reinterpret_cast<const T*>(is_k ? p.k : p.v) + h * D;
+    const long long stride = is_k ? p.k_stride : p.v_stride;
+    stored = (is_k ? p.ks : p.vs)[(long long)p.block.quot(slot_s[at - t0 + 1]) * p.Hkv + h];
+#pragma unroll
+    for (int x = 0; x < kPasses; ++x) {
+      if (base + x * kRows >= n) break;
+      const int t = at + min(base + x * kRows + sub, n - 1);
+      const uint4* row = reinterpret_cast<const uint4*>(src + t * stride);
+      raw[x][0] = __ldcs(row + c.x);
+      raw[x][1] = __ldcs(row + c.y);
+    }
+  };
+  if (team < items) load(team);  // (on its way while the angles are worked out)
   if (turn) {
     const int n = (rows_end - t0) * (D / 2);
     for (int i = threadIdx.x; i < n; i += kThreads) {
@@ -135,70 +215,13 @@ __global__ void __launch_bounds__(kThreads, 3) append_scaled_kernel(
     }
     __syncthreads();
   }
-
-  if (part == 2) {
-    // ---- this tile's queries
-    const int n = (t1 - t0) * p.per.d;
-    for (int i0 = threadIdx.x; i0 < n; i0 += kPasses * kThreads) {
-      uint4 raw[kPasses][2];
-      bool some[kPasses];
-#pragma unroll
-      for (int x = 0; x < kPasses; ++x) {
-        const int i = i0 + x * kThreads, u = p.per.quot(i), y = i - u * p.per.d;
-        some[x] = i < n && slot_s[u + 1] >= 0;
-        if (!some[x]) continue;
-        const int2 c = rope_chunks(p.rope, y % kItems);
-        const uint4* row = reinterpret_cast<const uint4*>(
-            reinterpret_cast<const T*>(p.q) + (t0 + u) * p.q_stride + y / kItems * D);
-        raw[x][0] = __ldcs(row + c.x);
-        raw[x][1] = __ldcs(row + c.y);
-      }
-#pragma unroll
-      for (int x = 0; x < kPasses; ++x) {
-        if (!some[x]) continue;
-        const int i = i0 + x * kThreads, u = p.per.quot(i), y = i - u * p.per.d, j = y % kItems;
-        const int2 c = rope_chunks(p.rope, j);
-        uint4* to = reinterpret_cast<uint4*>(
-            reinterpret_cast<T*>(p.q_out) + (t0 + u) * p.q_out_stride + y / kItems * D);
-        float a[8], e[8];
-        unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&raw[x][0]), a);
-        unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&raw[x][1]), e);
-        if (turn)
-          rope_turn(p.rope.interleaved, a, e, table + u * D + 8 * j, table + u * D + D / 2 + 8 * j);
-        to[c.x] = pack_chunk<T>(a).w[0];
-        to[c.y] = pack_chunk<T>(e).w[0];
-      }
-    }
-    return;
-  }
-
-  // ---- keys or values: a team of warps, as many as hold the longest run, takes a run of one head
-  int team_warps = 1;
-  while (team_warps * kWarpRows < longest) team_warps *= 2;
-  const int team = warp / team_warps, mine = warp % team_warps, threads = 32 * team_warps;
-  const int items = runs * p.Hkv, step = kWarps / team_warps;
-  const int j = lane % kItems, sub = lane / kItems;   // item of a row, row of a pass
-  const bool is_k = part == 0;
-  const int2 c = is_k ? rope_chunks(p.rope, j) : make_int2(j, j + kItems);
   int buf = 0;
   for (int i = team; i < items; i += step, buf ^= 1) {
     const int r = p.heads.quot(i), h = i - r * p.Hkv;
     const int at = run_at[r], n = run_n[r], first = at - t0 + 1;
     const int b = p.block.quot(slot_s[first]);
-    const T* src = reinterpret_cast<const T*>(is_k ? p.k : p.v) + h * D;
-    const long long stride = is_k ? p.k_stride : p.v_stride;
     float* scale = (is_k ? p.ks : p.vs) + (long long)b * p.Hkv + h;
-    const float stored = *scale;
-    const int base = mine * kWarpRows;
-    uint4 raw[kPasses][2];
-#pragma unroll
-    for (int x = 0; x < kPasses; ++x) {  // (rows behind the last: the last again)
-      if (base + x * kRows >= n) break;
-      const int t = at + min(base + x * kRows + sub, n - 1);
-      const uint4* row = reinterpret_cast<const uint4*>(src + t * stride);
-      raw[x][0] = __ldcs(row + c.x);
-      raw[x][1] = __ldcs(row + c.y);
-    }
+    if (i != team) load(i);
     auto values = [&](int x, float* a, float* e) {
       unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&raw[x][0]), a);
       unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&raw[x][1]), e);
@@ -416,14 +439,13 @@ __global__ void __launch_bounds__(kThreads) commit_scaled_kernel(
 template <typename T, int D>
 spec_status launch_append(const AppendParams& p, cudaStream_t st) {
   const size_t smem =
-      p.rope.pairs ? (size_t)(p.W - 1 + p.block.d) * D * sizeof(float) : 0;
+      p.rope.pairs ? (size_t)std::max(p.W - 1 + p.block.d, p.Wq) * D * sizeof(float) : 0;
   static PerDeviceOnce<int> once;
   const spec_status rc = ensure_smem_limit(once, (const void*)append_scaled_kernel<T, D>,
                                            (kTile - 1 + kMaxBlock) * D * (int)sizeof(float));
   if (rc != SPEC_OK) return rc;
-  const int parts = p.Hq ? 3 : 2;
-  return launch_chained(append_scaled_kernel<T, D>, (p.T + p.W - 1) / p.W * parts, kThreads, smem, st,
-                        p);
+  const int grid = 2 * p.tiles + (p.Hq ? (p.T + p.Wq - 1) / p.Wq : 0);
+  return launch_chained(append_scaled_kernel<T, D>, grid, kThreads, smem, st, p);
 }
 
 template <typename T>
@@ -500,7 +522,12 @@ extern "C" spec_status spec_append_scaled(
   p.T = T;
   p.Hq = q ? Hq : 0;
   p.Hkv = Hkv;
-  p.W = T <= kFewRows ? 1 : kTile;
+  // rows of a CTA: few where there are few, else a run's share of a block, and for the queries what its
+  // threads hold at once
+  const int sms = sm_count();
+  p.W = std::min(kTile, std::max(1, T / (2 * sms)));
+  p.tiles = (T + p.W - 1) / p.W;
+  p.Wq = std::max(1, std::min({kPasses * kThreads / p.per.d, T / (2 * sms), kTile}));
   p.num_slots = num_pages * page_size;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return new_dtype == SPEC_BF16 ? launch_append_d<__nv_bfloat16>(p, D, st)
