@@ -90,8 +90,9 @@ SPEC_DEV void turn_queries(const AppendParams& p, int t0, float* table, int* liv
     }
     if (p.rope.pairs == 0) continue;
     const float2 e = rope_entry(p.rope, at, j);
-    table[u * D + j] = e.x;
-    table[u * D + D / 2 + j] = e.y;
+    float* to = table + u * D + rope_place(kItems, j);
+    to[0] = e.x;
+    to[D / 2] = e.y;
   }
   __syncthreads();
   for (int i0 = threadIdx.x; i0 < n; i0 += kPasses * kThreads) {
@@ -108,7 +109,7 @@ SPEC_DEV void turn_queries(const AppendParams& p, int t0, float* table, int* liv
       unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&raw[x][0]), a);
       unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&raw[x][1]), e);
       if (p.rope.pairs > 0)
-        rope_turn(p.rope.interleaved, a, e, table + u * D + 8 * j, table + u * D + D / 2 + 8 * j);
+        rope_turn(p.rope.interleaved, a, e, table + u * D, table + u * D + D / 2, kItems, j);
       to[c.x] = pack_chunk<T>(a).w[0];
       to[c.y] = pack_chunk<T>(e).w[0];
     }
@@ -210,8 +211,9 @@ __global__ void __launch_bounds__(kThreads, 3) append_scaled_kernel(
     for (int i = threadIdx.x; i < n; i += kThreads) {
       const int u = i / (D / 2), j = i % (D / 2);
       const float2 e = rope_entry(p.rope, pos_s[u + 1], j);
-      table[u * D + j] = e.x;
-      table[u * D + D / 2 + j] = e.y;
+      float* to = table + u * D + rope_place(kItems, j);
+      to[0] = e.x;
+      to[D / 2] = e.y;
     }
     __syncthreads();
   }
@@ -226,8 +228,8 @@ __global__ void __launch_bounds__(kThreads, 3) append_scaled_kernel(
       unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&raw[x][0]), a);
       unpack_chunk<T>(*reinterpret_cast<const Chunk8<T>*>(&raw[x][1]), e);
       if (turn) {
-        const float* cs = table + (first - 1 + min(base + x * kRows + sub, n - 1)) * D + 8 * j;
-        rope_turn(p.rope.interleaved, a, e, cs, cs + D / 2);
+        const float* cs = table + (first - 1 + min(base + x * kRows + sub, n - 1)) * D;
+        rope_turn(p.rope.interleaved, a, e, cs, cs + D / 2, kItems, j);
       }
     };
     uint32_t lo = 0, hi = 0;  // written places of the block

@@ -132,8 +132,23 @@ SPEC_DEV int2 rope_chunks(const RopeTable<N>& r, int j) {
   return j < half ? make_int2(j, j + half) : make_int2(2 * j, 2 * j + 1);
 }
 
-// The item's pairs, turned: cs[x], sn[x] of pair 8 j + x.
-SPEC_DEV void rope_turn(bool interleaved, float* a, float* b, const float* cs, const float* sn) {
+// A position's table of cosines (or sines) in shared memory, D / 2 of them: pairs 8 j + x of all items j with
+// x < 4 lie in front of those with x >= 4, so that the lanes' 16-byte reads stand next to each other.
+SPEC_DEV int rope_place(int items, int pair) {
+  return (((pair >> 2 & 1) * items + (pair >> 3)) << 2) + (pair & 3);
+}
+
+// The pairs of item j of `items`, turned.
+SPEC_DEV void rope_turn(bool interleaved, float* a, float* b, const float* cosines,
+                        const float* sines, int items, int j) {
+  float cs[8], sn[8];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    *reinterpret_cast<float4*>(cs + 4 * x) =
+        *reinterpret_cast<const float4*>(cosines + ((x * items + j) << 2));
+    *reinterpret_cast<float4*>(sn + 4 * x) =
+        *reinterpret_cast<const float4*>(sines + ((x * items + j) << 2));
+  }
   if (interleaved) {
 #pragma unroll
     for (int x = 0; x < 8; ++x) {

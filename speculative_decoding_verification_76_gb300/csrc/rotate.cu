@@ -49,8 +49,9 @@ __global__ void __launch_bounds__(kMostThreads) rotate_kernel(
   if (at < 0) return;
   for (int i = threadIdx.x; i < p.D / 2; i += blockDim.x) {
     const float2 e = rope_entry(p.rope, at, i);
-    cs[i] = e.x;
-    sn[i] = e.y;
+    const int to = rope_place(p.items.d, i);
+    cs[to] = e.x;
+    sn[to] = e.y;
   }
   __syncthreads();
   for (int i0 = threadIdx.x; i0 < n; i0 += kFlight * blockDim.x) {
@@ -66,7 +67,7 @@ __global__ void __launch_bounds__(kMostThreads) rotate_kernel(
       float x[8], y[8];
       unpack_chunk<T>(a[f], x);
       unpack_chunk<T>(b[f], y);
-      rope_turn(p.rope.interleaved, x, y, cs + 8 * j, sn + 8 * j);
+      rope_turn(p.rope.interleaved, x, y, cs, sn, p.items.d, j);
       reinterpret_cast<Chunk8<T>*>(dst)[c.x] = pack_chunk<T>(x);
       reinterpret_cast<Chunk8<T>*>(dst)[c.y] = pack_chunk<T>(y);
     }
