@@ -35,7 +35,7 @@ struct AppendParams {
   long long k_stride, v_stride, q_stride, q_out_stride;      // elements
   long long page_stride, token_stride, head_stride;          // bytes
   FastDiv P, block, heads, per;                              // KV heads; items of a row's queries
-  int T, Hq, Hkv, W, Wq, tiles, num_slots;                   // rows of a CTA; CTAs of the keys
+  int T, Hq, Hkv, W, Wq, kv_ctas, num_slots;                 // rows of a CTA; CTAs of keys and values
   RopeTable<128> rope;
 };
 
@@ -81,15 +81,17 @@ SPEC_DEV void turn_queries(const AppendParams& p, int t0, float* table, int* liv
     }
   };
   load(threadIdx.x);
-  for (int i = threadIdx.x; i < rows * (D / 2); i += kThreads) {
-    const int u = i / (D / 2), j = i % (D / 2);
+  const int j = threadIdx.x % (D / 2);
+  const bool turns = j < p.rope.pairs;
+  const uint64_t by = turns ? p.rope.turn[j] : 0;
+  for (int u = threadIdx.x / (D / 2); u < rows; u += kThreads / (D / 2)) {
     const int at = p.pos ? p.pos[t0 + u] : 0;
     if (j == 0) {
       const int64_t slot = p.slots[t0 + u];
       live[u] = slot >= 0 && slot < p.num_slots && at >= 0;
     }
     if (p.rope.pairs == 0) continue;
-    const float2 e = rope_entry(p.rope, at, j);
+    const float2 e = turns ? rope_angle(by, p.rope.magnitude, at) : make_float2(1.f, 0.f);
     float* to = table + u * D + rope_place(kItems, j);
     to[0] = e.x;
     to[D / 2] = e.y;
@@ -124,54 +126,63 @@ __global__ void __launch_bounds__(kThreads, 3) append_scaled_kernel(
   constexpr int kRows = 32 / kItems;           // rows of a warp's pass
   constexpr int kWarpRows = kPasses * kRows;   // that a warp holds
   constexpr int kMost = kTile + kMaxBlock;     // rows looked at
+  constexpr int kWords = kMost / 32 + 1;
   extern __shared__ __align__(16) float table[];  // [rows][2][D/2]: cosines, sines
   __shared__ int slot_s[kMost + 1];               // of row t0 - 1 + i; -1: none
   __shared__ int pos_s[kMost + 1];
+  __shared__ long long at_s[kMost + 1];           // its place in a cache
+  __shared__ uint32_t same[kWords];               // rows whose block is that of the row in front
   __shared__ int run_at[kTile], run_n[kTile];     // the runs that begin here
+  __shared__ uint64_t run_to[kTile];              // places of their blocks that they write
   __shared__ int runs, rows_end, longest;
   __shared__ float big_s[2][kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   chain_wait();
-  if ((int)blockIdx.x >= 2 * p.tiles) {
-    turn_queries<T, D>(p, (blockIdx.x - 2 * p.tiles) * p.Wq, table, slot_s);
+  if ((int)blockIdx.x >= p.kv_ctas) {
+    turn_queries<T, D>(p, (blockIdx.x - p.kv_ctas) * p.Wq, table, slot_s);
     return;
   }
   const bool is_k = (blockIdx.x & 1) == 0;
   const int t0 = (int)(blockIdx.x >> 1) * p.W, t1 = min(t0 + p.W, p.T);
   const int look = min(t1 - 1 + p.block.d, p.T);  // past the last row a run from here may have
-  if (threadIdx.x <= look - t0) {
+  if (threadIdx.x <= kMost) {
     const int t = t0 - 1 + (int)threadIdx.x;
     int s = -1, at = 0;
-    if (t >= 0) {
+    if (t >= 0 && t < look) {
       const int64_t slot = p.slots[t];
       at = p.pos ? p.pos[t] : 0;
       if (slot >= 0 && slot < p.num_slots && at >= 0) s = (int)slot;
     }
     slot_s[threadIdx.x] = s;
     pos_s[threadIdx.x] = at;
+    at_s[threadIdx.x] = s < 0 ? 0 : slot_offset(p.P, p.page_stride, p.token_stride, s);
   }
-  if (threadIdx.x == 0) runs = 0, rows_end = t0, longest = 0;
+  if (threadIdx.x == 0) rows_end = t0, longest = 0;
+  __syncthreads();
+  if (warp < kWords) {
+    const int i = threadIdx.x;
+    const bool joined = i > 0 && i <= kMost && slot_s[i] >= 0 && slot_s[i - 1] >= 0 &&
+                        p.block.quot(slot_s[i]) == p.block.quot(slot_s[i - 1]);
+    const uint32_t word = __ballot_sync(0xffffffffu, joined);
+    if (lane == 0) same[warp] = word;
+  }
   __syncthreads();
   // ---- the runs that begin in t0 .. t1 - 1, in order
   if (warp == 0) {
-    const int t = t0 + lane;
-    bool first = false;
-    int n = 0;
-    if (t < t1 && slot_s[lane + 1] >= 0) {
-      const int b = p.block.quot(slot_s[lane + 1]), before = slot_s[lane];
-      first = before < 0 || p.block.quot(before) != b;
-      if (first) {
-        n = 1;
-        while (n < p.block.d && t + n < look && slot_s[lane + 1 + n] >= 0 &&
-               p.block.quot(slot_s[lane + 1 + n]) == b)
-          ++n;
-      }
-    }
+    const int i = lane + 1, t = t0 + lane;
+    const bool first = t < t1 && slot_s[i] >= 0 && !(same[i >> 5] >> (i & 31) & 1u);
     const uint32_t who = __ballot_sync(0xffffffffu, first);
     if (first) {
-      const int i = __popc(who & ((1u << lane) - 1));
-      run_at[i] = t;
-      run_n[i] = n;
+      int n = 1;
+      for (int y = i + 1; n < p.block.d && y <= kMost;) {
+        const int left = 32 - (y & 31), more = __clz(__brev(~(same[y >> 5] >> (y & 31))));
+        n += min(more, left), y += left;
+        if (more < left) break;
+      }
+      n = min(n, p.block.d);  // (a slot that comes twice)
+      const int r = __popc(who & ((1u << lane) - 1));
+      run_at[r] = t;
+      run_n[r] = n;
       atomicMax(&rows_end, t + n);
       atomicMax(&longest, n);
     }
@@ -179,6 +190,26 @@ __global__ void __launch_bounds__(kThreads, 3) append_scaled_kernel(
   }
   __syncthreads();
   if (runs == 0) return;
+  for (int r = warp; r < runs; r += kWarps) {
+    const int first = run_at[r] - t0 + 1, n = run_n[r], b0 = p.block.quot(slot_s[first]) * p.block.d;
+    uint32_t lo = 0, hi = 0;
+    for (int u = lane; u < n; u += 32) {
+      const int o = slot_s[first + u] - b0;
+      if (o < 32) lo |= 1u << o; else hi |= 1u << (o - 32);
+    }
+    lo = __reduce_or_sync(0xffffffffu, lo), hi = __reduce_or_sync(0xffffffffu, hi);
+    if (lane == 0) run_to[r] = (uint64_t)hi << 32 | lo;
+  }
+  __syncthreads();
+  // the heads of a row stand together and are used one after the other: on their way to L2 whole
+  if (p.Hkv * D >= 512)
+    for (int u = threadIdx.x; u < rows_end - t0; u += kThreads) {
+      const char* row = (is_k ? p.k : p.v) + (t0 + u) * (is_k ? p.k_stride : p.v_stride) * (int)sizeof(T);
+      if (slot_s[u + 1] >= 0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row),
+                     "r"(p.Hkv * D * (int)sizeof(T))
+                     : "memory");
+    }
 
   // ---- keys or values: a team of warps, as many as hold the longest run, takes a run of one head
   int team_warps = 1;
@@ -207,10 +238,12 @@ __global__ void __launch_bounds__(kThreads, 3) append_scaled_kernel(
   };
   if (team < items) load(team);  // (on its way while the angles are worked out)
   if (turn) {
-    const int n = (rows_end - t0) * (D / 2);
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      const int u = i / (D / 2), j = i % (D / 2);
-      const float2 e = rope_entry(p.rope, pos_s[u + 1], j);
+    const int j = threadIdx.x % (D / 2), n = rows_end - t0;
+    const bool turns = j < p.rope.pairs;
+    const uint64_t by = turns ? p.rope.turn[j] : 0;
+#pragma unroll 4
+    for (int u = threadIdx.x / (D / 2); u < n; u += kThreads / (D / 2)) {
+      const float2 e = turns ? rope_angle(by, p.rope.magnitude, pos_s[u + 1]) : make_float2(1.f, 0.f);
       float* to = table + u * D + rope_place(kItems, j);
       to[0] = e.x;
       to[D / 2] = e.y;
@@ -232,21 +265,35 @@ __global__ void __launch_bounds__(kThreads, 3) append_scaled_kernel(
         rope_turn(p.rope.interleaved, a, e, cs, cs + D / 2, kItems, j);
       }
     };
-    uint32_t lo = 0, hi = 0;  // written places of the block
-    for (int u = lane; u < n; u += 32) {
-      const int o = slot_s[first + u] - b * p.block.d;
-      if (o < 32) lo |= 1u << o; else hi |= 1u << (o - 32);
-    }
-    const uint64_t written = (uint64_t)__reduce_or_sync(0xffffffffu, hi) << 32 |
-                             __reduce_or_sync(0xffffffffu, lo);
+    const uint64_t written = run_to[r];
     float big = 0.f;
+    bool packed = !turn;
+    if (packed) {  // magnitudes compare as their bits do, two at a time
+      uint32_t m = 0;
 #pragma unroll
-    for (int x = 0; x < kPasses; ++x) {
-      if (base + x * kRows >= n) break;
-      float a[8], e[8];
-      values(x, a, e);
+      for (int x = 0; x < kPasses; ++x) {
+        if (base + x * kRows >= n) break;
 #pragma unroll
-      for (int y = 0; y < 8; ++y) big = fmaxf(big, fmaxf(finite_abs(a[y]), finite_abs(e[y])));
+        for (int y = 0; y < 2; ++y) {
+          const uint4 w = raw[x][y];
+          m = __vimax3_u16x2(m, w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
+          m = __vimax3_u16x2(m, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu);
+        }
+      }
+      const unsigned short top = (unsigned short)max(m & 0xffffu, m >> 16);
+      big = static_cast<float>(*reinterpret_cast<const T*>(&top));
+      packed = big < INFINITY;  // (else some value is not finite, and does not count)
+    }
+    if (!packed) {
+      big = 0.f;
+#pragma unroll
+      for (int x = 0; x < kPasses; ++x) {
+        if (base + x * kRows >= n) break;
+        float a[8], e[8];
+        values(x, a, e);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) big = fmaxf(big, fmaxf(finite_abs(a[y]), finite_abs(e[y])));
+      }
     }
     big = warp_max(big);
     if (team_warps > 1) {
@@ -269,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_scaled_kernel(
       float a[8], e[8];
       values(x, a, e);
       if (u < n) {
-        char* to = cache + slot_offset(p.P, p.page_stride, p.token_stride, slot_s[first + u]);
+        char* to = cache + at_s[first + u];
 #pragma unroll
         for (int y = 0; y < 8; ++y) a[y] *= by, e[y] *= by;
         const uint2 first8 =
@@ -446,7 +493,7 @@ spec_status launch_append(const AppendParams& p, cudaStream_t st) {
   const spec_status rc = ensure_smem_limit(once, (const void*)append_scaled_kernel<T, D>,
                                            (kTile - 1 + kMaxBlock) * D * (int)sizeof(float));
   if (rc != SPEC_OK) return rc;
-  const int grid = 2 * p.tiles + (p.Hq ? (p.T + p.Wq - 1) / p.Wq : 0);
+  const int grid = p.kv_ctas + (p.Hq ? (p.T + p.Wq - 1) / p.Wq : 0);
   return launch_chained(append_scaled_kernel<T, D>, grid, kThreads, smem, st, p);
 }
 
@@ -519,7 +566,6 @@ extern "C" spec_status spec_append_scaled(
   p.head_stride = head_stride;
   p.P = FastDiv(page_size);
   p.block = FastDiv(block);
-  p.heads = FastDiv(Hkv);
   p.per = FastDiv(std::max(1, Hq * (D / 16)));
   p.T = T;
   p.Hq = q ? Hq : 0;
@@ -528,7 +574,8 @@ extern "C" spec_status spec_append_scaled(
   // threads hold at once
   const int sms = sm_count();
   p.W = std::min(kTile, std::max(1, T / (2 * sms)));
-  p.tiles = (T + p.W - 1) / p.W;
+  p.heads = FastDiv(Hkv);
+  p.kv_ctas = 2 * ((T + p.W - 1) / p.W);
   p.Wq = std::max(1, std::min({kPasses * kThreads / p.per.d, T / (2 * sms), kTile}));
   p.num_slots = num_pages * page_size;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

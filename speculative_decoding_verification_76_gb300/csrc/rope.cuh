@@ -103,16 +103,14 @@ static inline spec_status rope_table(const spec_rope* r, int D, RopeTable<N>* ou
   return SPEC_OK;
 }
 
-// Cosine and sine of pair i at position t, times the magnitude (identity behind the pairs).
+// Cosine and sine of a pair that turns by `turn` at position t, times the magnitude.
 //
 // The angle as a 32-bit fraction of a turn is split into the nearest quarter and a rest of at most an
 // eighth of a turn, d + e with d what fp32 holds of it: sin and cos of d, and e (below 2^-26 of a turn)
 // by the first term of its series.  An fp32 angle of up to half a turn alone would be off by 2^-24,
 // twice what rounding the result costs, and shows in the codes of a cache that is written from it.
-template <int N>
-SPEC_DEV float2 rope_entry(const RopeTable<N>& r, int t, int i) {
-  if (i >= r.pairs) return make_float2(1.f, 0.f);
-  const uint32_t frac = (uint32_t)(((uint64_t)(uint32_t)t * r.turn[i]) >> 32);
+SPEC_DEV float2 rope_angle(uint64_t turn, float magnitude, int t) {
+  const uint32_t frac = (uint32_t)(((uint64_t)(uint32_t)t * turn) >> 32);
   const uint32_t quarter = (frac + 0x20000000u) >> 30;
   const int32_t rest = (int32_t)(frac - (quarter << 30));
   const float d = (float)rest;
@@ -121,8 +119,15 @@ SPEC_DEV float2 rope_entry(const RopeTable<N>& r, int t, int i) {
   sincospif(d * 0x1p-31f, &s, &c);
   const float s1 = fmaf(c, e, s), c1 = fmaf(-s, e, c);
   const float x = quarter & 1 ? -s1 : c1, y = quarter & 1 ? c1 : s1;
-  const float m = quarter & 2 ? -r.magnitude : r.magnitude;
+  const float m = quarter & 2 ? -magnitude : magnitude;
   return make_float2(x * m, y * m);
+}
+
+// The same of pair i (identity behind the pairs).  Lanes ask for different pairs, and constant memory serves them
+// one after the other: where a thread needs a pair at many positions it reads its turn once.
+template <int N>
+SPEC_DEV float2 rope_entry(const RopeTable<N>& r, int t, int i) {
+  return i < r.pairs ? rope_angle(r.turn[i], r.magnitude, t) : make_float2(1.f, 0.f);
 }
 
 // First and second chunk of item j.
