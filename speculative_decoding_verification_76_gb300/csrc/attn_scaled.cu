@@ -81,7 +81,8 @@ extern "C" spec_status spec_verify_attn_scaled(
   // so are positions, and the batch's tiles over all KV heads
   if ((long long)max_pages * page_size > INT32_MAX - 512 || B > INT32_MAX - 512)
     return SPEC_EUNSUPPORTED;
-  const double units = ((double)max_pages * page_size / scaled_attn::kUnit + 1) * B * Hkv;
+  const double units =
+      ((double)max_pages * page_size / scaled_attn::kUnit + 1 + scaled_attn::kSwitch) * B * Hkv;
   if (units > INT32_MAX - 1024.0) return SPEC_EUNSUPPORTED;
   if ((double)B * ((double)R * Hq / scaled_attn::kJoinWarps + 1) > INT32_MAX) return SPEC_EUNSUPPORTED;
   Plan pl;

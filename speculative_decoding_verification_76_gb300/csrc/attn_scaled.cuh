@@ -73,8 +73,13 @@ struct Params {
 
 __device__ const float g_unseen = -INFINITY;  // K's scale of a position that is not there
 
+// What beginning and ending a segment costs (Q, sums, outputs), in tiles: a sequence counts as that many more
+// when the ranges are cut, so that those that meet an end take fewer.
+constexpr int kSwitch = 8;
+
 struct Seq {  // positions first .. end - 1 of a sequence are looked at
   int ctx, first, end, units;
+  SPEC_DEV int span() const { return units > 0 ? units + kSwitch : 0; }
 };
 
 SPEC_DEV Seq seq_of(const Params& p, int b) {
@@ -101,20 +106,25 @@ struct Ranges {
 
 // A walk over the segments (pieces of one sequence of one KV head) of a range.
 struct Walk {
-  int W, s, s1, kvh, b, at;  // batch's units; next unit and end; where it lies
+  int W, s, s1, kvh, b, at;  // batch's span; next unit and end; where it lies
   Seq seq;
+  int s0;                    // the range's first unit
   SPEC_DEV bool more() const { return s < s1; }
   SPEC_DEV int first_unit() const { return s - kvh * W - at; }
   SPEC_DEV int count() const { return min(seq.units - first_unit(), s1 - s); }
-  __device__ __noinline__ void next(const Params& p) {
-    s += count();
+  __device__ __noinline__ void next_seq(const Params& p) {
+    at += seq.span();
+    s = kvh * W + at;
     if (s >= s1) return;
-    at += seq.units;
 #pragma unroll 1
     do {
       if (++b == p.B) b = 0, at = 0, ++kvh;
       seq = seq_of(p, b);
     } while (seq.units == 0);
+  }
+  SPEC_DEV void next(const Params& p) {
+    s += count();
+    if (s < s1) next_seq(p);
   }
 };
 
@@ -393,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
     const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
     int mine = 0;
 #pragma unroll 1
-    for (int b = b0; b < b1; ++b) mine += seq_of(p, b).units;
+    for (int b = b0; b < b1; ++b) mine += seq_of(p, b).span();
     int x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -416,8 +426,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
       int b = b0;
       Seq seq = seq_of(p, b);
 #pragma unroll 1
-      while (at + seq.units <= u) at += seq.units, seq = seq_of(p, ++b);
-      start = {W, s0, ranges.begin(team + 1), kvh, b, at, seq};
+      while (at + seq.span() <= u) at += seq.span(), seq = seq_of(p, ++b);
+      Walk walk{W, s0, ranges.begin(team + 1), kvh, b, at, seq, s0};
+      if (walk.first_unit() >= seq.units) walk.next_seq(p);  // (nothing is left of this one)
+      start = walk;
     }
     if (threadIdx.x == 0) {
       for (int i = 0; i < NS; ++i) {
@@ -456,13 +468,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
       asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
     else
       asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
-    const int nb = p.P.d / p.block.d, range0 = start.s;
+    const int nb = p.P.d / p.block.d;
     int g = 0, seg = 0;
     bool ok = true;
     for (Walk walk = start; walk.more() && ok; walk.next(p), ++seg) {
       const int b = walk.b, n_units = walk.count(), ctx = walk.seq.ctx, end = walk.seq.end, sb = seg & 1;
       const bool whole = n_units == walk.seq.units;
-      const int part_at = (team * 2 + (walk.s == range0 ? 0 : 1)) * p.tiles + tile;
+      const int part_at = (team * 2 + (walk.s == walk.s0 ? 0 : 1)) * p.tiles + tile;
       const int32_t* bt = p.table + (size_t)b * p.max_pages;
       int t = walk.seq.first + walk.first_unit() * kUnit + tid;
       int page = p.P.quot(t), off = t - page * p.P.d, id = t < end ? bt[page] : -1;
@@ -1052,7 +1064,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   // (in front of its wait it reads the lengths only: what wrote them the kernel in front has waited for)
   int before = 0, W = 0;
   for (int x = threadIdx.x; x < p.B; x += 32 * kJoinWarps) {
-    const int u = seq_of(p, x).units;
+    const int u = seq_of(p, x).span();
     W += u;
     if (x < b) before += u;
   }
