@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
 #pragma unroll
       for (int k = 0; k < kGroups; ++k) {
         sc2[k] = *reinterpret_cast<const uint64_t*>(&sc_s[sb][8 * k + c2]);
-        nm2[k] = f2_pack(-kNone, -kNone);
+        nm2[k] = 0ull;  // (the segment's first references come from its first exponents)
         l2[k] = 0ull;
       }
       if (tid < RT) neg_m[group][tid] = -kNone;
@@ -824,16 +824,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
               }
             }
             if (moved) break;
+            if (!begun) {  // the first tile: references below the maxima of its positions
+#pragma unroll
+              for (int k = 0; k < kB; ++k) {
+                if (8 * (h + k) >= rows) break;
+                float m0 = fmaxf(fmaxf(a[0][2 * k], a[1][2 * k]), fmaxf(a[2][2 * k], a[3][2 * k]));
+                float m1 = fmaxf(fmaxf(a[0][2 * k + 1], a[1][2 * k + 1]), fmaxf(a[2][2 * k + 1], a[3][2 * k + 1]));
+#pragma unroll
+                for (int o = 4; o <= 16; o *= 2) {
+                  m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+                  m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+                }
+                if (lane < 4) *reinterpret_cast<float2*>(&red[warp][8 * (h + k) + c2]) = make_float2(m0, m1);
+              }
+              sync_of(bar, kGroup);
+              if (tid < 8 * kB && 8 * h + (tid & ~7) < rows) {
+                const int w0 = group * 4, n = 8 * h + tid;
+                const float m4 = fmaxf(fmaxf(red[w0][n], red[w0 + 1][n]), fmaxf(red[w0 + 2][n], red[w0 + 3][n]));
+                neg_m[group][n] = m4 > kNone ? S::kBelow - m4 : -kNone;
+              }
+              sync_of(bar, kGroup);
+#pragma unroll
+              for (int k = 0; k < kB; ++k) {
+                if (8 * (h + k) >= rows) break;
+                nm2[h + k] = *reinterpret_cast<const uint64_t*>(&neg_m[group][8 * (h + k) + c2]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  f2_unpack(f2_add(f2_pack(a[r][2 * k], a[r][2 * k + 1]), nm2[h + k]), a[r][2 * k], a[r][2 * k + 1]);
+              }
+              break;
+            }
 #pragma unroll
             for (int k = 0; k < kB; ++k) {
               if (8 * (h + k) >= rows) break;
 #pragma unroll
               for (int r = 0; r < 4; ++r) top = fmax3(top, a[r][2 * k], a[r][2 * k + 1]);
             }
-            if (begun) {
-              if (!any_of(bar, kGroup, top > S::kTop || !ok)) break;
-              if ((failed = any_of(bar, kGroup, !ok))) break;  // (the same for all of the group)
-            }
+            if (!any_of(bar, kGroup, top > S::kTop || !ok)) break;
+            if ((failed = any_of(bar, kGroup, !ok))) break;  // (the same for all of the group)
             moved = true;
             // ---- maxima over the tile's positions
 #pragma unroll 1
@@ -877,44 +905,42 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
             for (int k = 0; k < kB; ++k) {
               if (8 * (h + k) >= rows) break;
               nm2[h + k] = *reinterpret_cast<const uint64_t*>(&neg_m[group][8 * (h + k) + c2]);
-              if (begun)
-                l2[h + k] = f2_mul(l2[h + k],
-                                   *reinterpret_cast<const uint64_t*>(&fac_s[group][8 * (h + k) + c2]));
+              l2[h + k] = f2_mul(l2[h + k],
+                                 *reinterpret_cast<const uint64_t*>(&fac_s[group][8 * (h + k) + c2]));
             }
-            if (begun) {  // O, whose last product has to be complete
-              ok = ok && wait_for(&pv_done[(u - 2) & 3], (u - 2) >> 2 & 1, p);
-              tc_fence_after();
+            // O, whose last product has to be complete
+            ok = ok && wait_for(&pv_done[(u - 2) & 3], (u - 2) >> 2 & 1, p);
+            tc_fence_after();
 #pragma unroll 1
-              for (int y = 0; y < S::kSums * S::kHalves; ++y)
+            for (int y = 0; y < S::kSums * S::kHalves; ++y)
 #pragma unroll 1
-                for (int k = h; k < h + kB && 8 * k < rows; ++k) {
-                  const uint32_t at = lanes + S::kColO + group * S::kOCols + y * RT;
-                  uint32_t o[8];
-                  if constexpr (S::kHalfV) {
-                    tmem_ld8(at + 8 * k, o);
+              for (int k = h; k < h + kB && 8 * k < rows; ++k) {
+                const uint32_t at = lanes + S::kColO + group * S::kOCols + y * RT;
+                uint32_t o[8];
+                if constexpr (S::kHalfV) {
+                  tmem_ld8(at + 8 * k, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 8; ++e)
+                    o[e] = __float_as_uint(__uint_as_float(o[e]) * fac_s[group][8 * k + e]);
+                  tmem_st8(at + 8 * k, o);
+                } else {  // (columns in the parts' order, sixteen at a time)
+                  if (k & 1) continue;
+#pragma unroll 1
+                  for (int x = 0; x < 2; ++x) {
+                    tmem_ld8(at + 8 * k + 8 * x, o);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                      o[e] = __float_as_uint(__uint_as_float(o[e]) * fac_s[group][8 * k + e]);
-                    tmem_st8(at + 8 * k, o);
-                  } else {  // (columns in the parts' order, sixteen at a time)
-                    if (k & 1) continue;
-#pragma unroll 1
-                    for (int x = 0; x < 2; ++x) {
-                      tmem_ld8(at + 8 * k + 8 * x, o);
-                      tmem_wait_ld();
-#pragma unroll
-                      for (int e = 0; e < 8; ++e) {
-                        const int q = 8 * x + e, n = 8 * k + 2 * (q >> 2) + (q & 1) + 8 * (q >> 1 & 1);
-                        o[e] = __float_as_uint(__uint_as_float(o[e]) *
-                                               ((n & ~7) < rows ? fac_s[group][n] : 1.f));
-                      }
-                      tmem_st8(at + 8 * k + 8 * x, o);
+                    for (int e = 0; e < 8; ++e) {
+                      const int q = 8 * x + e, n = 8 * k + 2 * (q >> 2) + (q & 1) + 8 * (q >> 1 & 1);
+                      o[e] = __float_as_uint(__uint_as_float(o[e]) *
+                                             ((n & ~7) < rows ? fac_s[group][n] : 1.f));
                     }
+                    tmem_st8(at + 8 * k + 8 * x, o);
                   }
                 }
-              tmem_wait_st();
-            }
+              }
+            tmem_wait_st();
           }
           if (failed) break;
           // ---- weights and their sums
@@ -1001,7 +1027,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
       sync_of(3, kSoft);
       // (a group takes every other two columns of O; of three 8-bit parts, a column and the next are rows n
       // and n + 1)
-#pragma unroll 1
+#pragma unroll 2
       for (int c = 2 * group; c < RT; c += 4) {
         const int n0 = S::kHalfV ? c : (c & ~15) + 2 * (c >> 2 & 3) + 8 * (c >> 1 & 1);
         if (n0 >= rows) continue;
