@@ -476,6 +476,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
       const bool whole = n_units == walk.seq.units;
       const int part_at = (team * 2 + (walk.s == walk.s0 ? 0 : 1)) * p.tiles + tile;
       const int32_t* bt = p.table + (size_t)b * p.max_pages;
+      // a query row for kPer threads; what a thread has of it is on its way before anything else
+      constexpr int kPer = kLoad / RT;
+      constexpr int kMine = D / 8 / kPer > 0 ? D / 8 / kPer : 1;  // 16-byte chunks of a thread
+      constexpr bool kHeld = kMine <= 4;                          // (more of them: read where they are used)
+      const int n = tid / kPer, x0 = tid % kPer;
+      const int q_row = tile * p.rows_per_tile + n, i_row = p.per_head.quot(q_row);
+      const bool real = n < rows;
+      const uint4* const q_src = reinterpret_cast<const uint4*>(
+          p.q + (b * p.q_stride_b + (real ? i_row : 0) * p.q_stride_r +
+                 (walk.kvh * p.G + (real ? q_row - i_row * p.G : 0)) * p.q_stride_h) * 2);
+      auto q_chunk = [&](int m) {
+        const int c = x0 + m * kPer;
+        return real && c < D / 8 ? q_src[c] : make_uint4(0, 0, 0, 0);
+      };
+      uint4 held[kHeld ? kMine : 1];
+      if constexpr (kHeld) {
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) held[m] = q_chunk(m);
+      }
       int t = walk.seq.first + walk.first_unit() * kUnit + tid;
       int page = p.P.quot(t), off = t - page * p.P.d, id = t < end ? bt[page] : -1;
       const char* kh = p.k + walk.kvh * p.head_stride + chunk * 16;
@@ -532,14 +551,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
                           wait_for(&seg_done[(seg - S::kQBufs) & 1], (seg - S::kQBufs) >> 1 & 1, p));
         if (!ok) break;
         {
-          constexpr int kPer = kLoad / RT;            // threads of a row
-          constexpr int kMine = D / 8 / kPer > 0 ? D / 8 / kPer : 1;  // 16-byte chunks of a thread
-          const int n = tid / kPer, x0 = tid % kPer;
-          const int row = tile * p.rows_per_tile + n, i = p.per_head.quot(row);
-          const bool real = n < rows;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              p.q + (b * p.q_stride_b + (real ? i : 0) * p.q_stride_r +
-                     (walk.kvh * p.G + (real ? row - i * p.G : 0)) * p.q_stride_h) * 2);
           auto values = [&](const uint4& w, float* x) {
             const uint32_t* u = reinterpret_cast<const uint32_t*>(&w);
 #pragma unroll
@@ -557,8 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
           uint32_t big2 = 0;
 #pragma unroll
           for (int m = 0; m < kMine; ++m) {
-            const int c = x0 + m * kPer;
-            const uint4 w = real && c < D / 8 ? src[c] : make_uint4(0, 0, 0, 0);
+            uint4 w;
+            if constexpr (kHeld) w = held[m];
+            else w = q_chunk(m);
             big2 = __vimax3_u16x2(big2, w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
             big2 = __vimax3_u16x2(big2, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu);
           }
@@ -569,12 +581,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
           const float s = needed_scale(F16 ? __half2float(__ushort_as_half((unsigned short)big))
                                            : __uint_as_float(big << 16));
           const float down = 1.f / s;
-#pragma unroll 1
+#pragma unroll(kHeld ? kMine : 1)
           for (int m = 0; m < kMine; ++m) {
             const int c = x0 + m * kPer;
             if (c >= D / 8) break;
             float x[8];
-            values(real ? src[c] : make_uint4(0, 0, 0, 0), x);
+            if constexpr (kHeld) values(held[m], x);
+            else values(q_chunk(m), x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] *= down;
             uint8_t* to = q_0 + seg % S::kQBufs * S::kQBytes + swizzled<D>(RT, n, c >> 1) + (c & 1) * 8;
@@ -594,11 +607,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
             sc_s[sb][n] = bad ? NAN : real ? p.scale_log2 * s : 0.f;
             uint64_t m = 0;
             if (real) {
-              m = p.mask ? p.mask[(size_t)b * p.R + i] : i >= 63 ? ~0ull : (2ull << i) - 1;
+              m = p.mask ? p.mask[(size_t)b * p.R + i_row] : i_row >= 63 ? ~0ull : (2ull << i_row) - 1;
               if (p.R < 64) m &= (1ull << p.R) - 1;
             }
             see_s[sb][n] = m;
-            out_s[sb][n] = whole ? ((long long)b * p.R + i) * p.Hq + walk.kvh * p.G + row - i * p.G
+            out_s[sb][n] = whole ? ((long long)b * p.R + i_row) * p.Hq + walk.kvh * p.G + q_row - i_row * p.G
                                  : (long long)part_at * RT + n;
             from_s[sb][n] = p.window > 0 ? ctx + __popcll(m) - p.window : 0;
 #pragma unroll 1
