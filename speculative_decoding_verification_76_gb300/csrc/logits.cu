@@ -162,7 +162,27 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
       }
     }
   };
-  load(r0);  // (on its way while the ids are counted)
+  // ---- on their way while the ids are counted: the first rows; and the first ids of all lists
+  load(r0);
+  constexpr int kAtOnce = 8;
+  const int32_t* const history = p.history + (size_t)b * p.H;
+  int32_t past[kAtOnce], bias_id = -1, token = -1;
+  float bias = 0.f;
+  auto load_past = [&](int i0) {
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x)
+      past[x] = i0 + x * kThreads < p.H ? history[i0 + x * kThreads] : -1;
+  };
+  auto load_bias = [&](int i) {
+    bias_id = i < p.n_bias ? p.bias_ids[(size_t)b * p.n_bias + i] : -1;
+    bias = i < p.n_bias ? p.bias[(size_t)b * p.n_bias + i] : 0.f;
+  };
+  if (p.counts) {
+    load_past(threadIdx.x);
+    if (p.tokens && threadIdx.x > 0 && threadIdx.x < p.R)
+      token = p.tokens[p.parent ? (size_t)b * p.R + threadIdx.x : (size_t)b * (p.R - 1) + threadIdx.x - 1];
+  }
+  if (p.biases) load_bias(threadIdx.x);
 
   auto mark = [&](int i) {
     const uint32_t bit = 1u << (i & 31);
@@ -175,20 +195,15 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
     freq = p.frequency ? p.frequency[b] : 0.f;
     pres = p.presence ? p.presence[b] : 0.f;
     const int prompt = p.prompt_len ? p.prompt_len[b] : 0;
-    const int32_t* h = p.history + (size_t)b * p.H;
     auto index = [&](int32_t id) {  // of an id's counter, ~0 if there is none
       const uint32_t i = (uint32_t)id - (uint32_t)base;
       return i < (uint32_t)S && (uint32_t)id < (uint32_t)p.V ? i : ~0u;
     };
-    constexpr int kAtOnce = 8;
     for (int i0 = threadIdx.x; i0 < p.H; i0 += kAtOnce * kThreads) {
-      int32_t id[kAtOnce];
-#pragma unroll
-      for (int x = 0; x < kAtOnce; ++x)
-        id[x] = i0 + x * kThreads < p.H ? h[i0 + x * kThreads] : -1;
+      if (i0 != threadIdx.x) load_past(i0);
 #pragma unroll
       for (int x = 0; x < kAtOnce; ++x) {
-        const uint32_t i = index(id[x]);
+        const uint32_t i = index(past[x]);
         if (i == ~0u) continue;
         if (i0 + x * kThreads < prompt) atomicOr(count + i, kPrompt);
         else atomicAdd(count + i, 1u);
@@ -198,10 +213,7 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
     // the block's tokens and each row's ancestors
     if (threadIdx.x < p.R) {
       const int i = threadIdx.x;
-      int t = -1;
-      if (p.tokens && i > 0)
-        t = p.parent ? p.tokens[(size_t)b * p.R + i] : p.tokens[(size_t)b * (p.R - 1) + i - 1];
-      t = (int)index(t);
+      const int t = (int)index(token);
       tok[i] = t;
       if (t >= 0) {
         atomicOr(count + t, kBlock);
@@ -222,12 +234,9 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
     }
   }
   if (p.biases) {
-    const int32_t* ids = p.bias_ids + (size_t)b * p.n_bias;
-    const float* xs = p.bias + (size_t)b * p.n_bias;
     for (int i0 = 0; i0 < p.n_bias; i0 += kThreads) {
-      const int i = i0 + threadIdx.x;
-      const int32_t id = i < p.n_bias ? ids[i] : -1;
-      const bool in = (uint32_t)id - (uint32_t)base < (uint32_t)S && (uint32_t)id < (uint32_t)p.V;
+      if (i0 > 0) load_bias(i0 + threadIdx.x);
+      const bool in = (uint32_t)bias_id - (uint32_t)base < (uint32_t)S && (uint32_t)bias_id < (uint32_t)p.V;
       const uint32_t who = __ballot_sync(0xffffffffu, in);
       if (lane == 0) warp_n[warp] = __popc(who);
       __syncthreads();
@@ -238,8 +247,8 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
         n += warp_n[w];
       }
       if (in) {
-        list_id[at] = id - base;
-        list_x[at] = xs[i];
+        list_id[at] = bias_id - base;
+        list_x[at] = bias;
       }
       __syncthreads();
       for (int e = 0; e < n; ++e)
