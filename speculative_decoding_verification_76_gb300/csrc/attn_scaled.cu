@@ -82,7 +82,7 @@ extern "C" spec_status spec_verify_attn_scaled(
   if ((long long)max_pages * page_size > INT32_MAX - 512 || B > INT32_MAX - 512)
     return SPEC_EUNSUPPORTED;
   const double units =
-      ((double)max_pages * page_size / scaled_attn::kUnit + 1 + scaled_attn::kSwitch) * B * Hkv;
+      ((double)max_pages * page_size / scaled_attn::kUnit + 1 + scaled_attn::kMostEnds) * B * Hkv;
   if (units > INT32_MAX - 1024.0) return SPEC_EUNSUPPORTED;
   if ((double)B * ((double)R * Hq / scaled_attn::kJoinWarps + 1) > INT32_MAX) return SPEC_EUNSUPPORTED;
   Plan pl;
@@ -125,9 +125,9 @@ extern "C" spec_status spec_verify_attn_scaled(
   p.tiles = pl.tiles;
   p.rows_per_tile = pl.rows_per_tile;
   p.teams = pl.teams;
+  p.ends = pl.rt == 64 ? scaled_attn::kMostEnds : 8;
   p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
   p.polls = (uint32_t)(SPEC_WAIT_NS / 1000);
-  p.withhold_stage = -1;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f16 = q_dtype == SPEC_F16;
   return D == 64 ? scaled_attn::launch_d64(p, pl.rt, f16, st)

@@ -51,6 +51,7 @@ constexpr int kThreads = 32 * (kSumWarp + 1);
 static_assert(kLoad == kUnit, "a position of the tile for each");
 constexpr float kNone = -1e30f;                  // the reference of a row that has seen nothing
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMostEnds = 16;                    // of Params::ends
 
 struct Params {
   const char *q, *k, *v;
@@ -66,20 +67,17 @@ struct Params {
   FastDiv P, block, per_head;        // page size, block, query heads of a KV head
   int B, R, Hq, Hkv, G, num_pages, max_pages, window;
   int tiles, rows_per_tile, teams;   // row tiles of a KV head, their query rows; ranges
+  // What beginning and ending a segment costs (Q, sums, outputs), in tiles: a sequence counts as that many
+  // more when the ranges are cut, so that those that meet an end take fewer.
+  int ends;
   float scale_log2;
   uint32_t polls;                    // of a wait, before it gives up
-  int withhold_stage;
 };
 
 __device__ const float g_unseen = -INFINITY;  // K's scale of a position that is not there
 
-// What beginning and ending a segment costs (Q, sums, outputs), in tiles: a sequence counts as that many more
-// when the ranges are cut, so that those that meet an end take fewer.
-constexpr int kSwitch = 8;
-
 struct Seq {  // positions first .. end - 1 of a sequence are looked at
-  int ctx, first, end, units;
-  SPEC_DEV int span() const { return units > 0 ? units + kSwitch : 0; }
+  int ctx, first, end, units, span;
 };
 
 SPEC_DEV Seq seq_of(const Params& p, int b) {
@@ -89,6 +87,7 @@ SPEC_DEV Seq seq_of(const Params& p, int b) {
   s.end = s.ctx < 0 ? 0 : (int)end;
   s.first = p.window > 0 && s.ctx > p.window ? s.ctx - p.window : 0;
   s.units = s.end > s.first ? (s.end - s.first + kUnit - 1) / kUnit : 0;
+  s.span = s.units > 0 ? s.units + p.ends : 0;
   return s;
 }
 
@@ -113,7 +112,7 @@ struct Walk {
   SPEC_DEV int first_unit() const { return s - kvh * W - at; }
   SPEC_DEV int count() const { return min(seq.units - first_unit(), s1 - s); }
   __device__ __noinline__ void next_seq(const Params& p) {
-    at += seq.span();
+    at += seq.span;
     s = kvh * W + at;
     if (s >= s1) return;
 #pragma unroll 1
@@ -403,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
     const int b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
     int mine = 0;
 #pragma unroll 1
-    for (int b = b0; b < b1; ++b) mine += seq_of(p, b).span();
+    for (int b = b0; b < b1; ++b) mine += seq_of(p, b).span;
     int x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -426,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
       int b = b0;
       Seq seq = seq_of(p, b);
 #pragma unroll 1
-      while (at + seq.span() <= u) at += seq.span(), seq = seq_of(p, ++b);
+      while (at + seq.span <= u) at += seq.span, seq = seq_of(p, ++b);
       Walk walk{W, s0, ranges.begin(team + 1), kvh, b, at, seq, s0};
       if (walk.first_unit() >= seq.units) walk.next_seq(p);  // (nothing is left of this one)
       start = walk;
@@ -539,10 +538,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_at + 512),
                      "l"(is_there ? p.vs + sc : &g_unseen)
                      : "memory");
-        if (g != p.withhold_stage)  // (a test can withhold one: its waiters time out)
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                           smem_u32(&full[stage]))
-                       : "memory");
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                         smem_u32(&full[stage]))
+                     : "memory");
         if (j > 0) continue;
         // ---- behind the segment's first tile: Q as sums of e4m3 parts under a power of two per row
         // (the segment before the last is done with the places)
@@ -1103,7 +1101,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
   // (in front of its wait it reads the lengths only: what wrote them the kernel in front has waited for)
   int before = 0, W = 0;
   for (int x = threadIdx.x; x < p.B; x += 32 * kJoinWarps) {
-    const int u = seq_of(p, x).span();
+    const int u = seq_of(p, x).span;
     W += u;
     if (x < b) before += u;
   }
