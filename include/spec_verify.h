@@ -735,13 +735,15 @@ spec_status spec_commit_scaled(void* k_cache, void* v_cache, float* k_scale, flo
  *   out      [B,R,Hq,D] q_dtype; lse_out [B,R,Hq] fp32 natural log (nullable).
  *            Neither shares memory with an input.
  *   workspace >= spec_verify_attn_scaled_workspace_size(...) bytes, 256-byte
- *            aligned; it keeps nothing from call to call.
+ *            aligned, its first 256 zeroed once: it keeps the error word
+ *            (spec_workspace_error) and nothing else from call to call.
  *
  * The result of a sequence may depend on the rest of the batch (by where the
  * cache is split) within rounding, and never on timing.
  * 1 <= R <= 64, D in {64,128,256}, Hkv * ceil(R * Hq / Hkv / 64) <= 4096 (/ 32 for D = 256); caches,
- * strides and q 16-byte aligned; max_pages * page_size and B at most 2^31 - 513;
- * B * Hkv * (max_pages * page_size / 128 + 1) < 2^31.
+ * strides and q 16-byte aligned; page_stride a multiple of token_stride, which is positive, and the
+ * cache's rows, counted in token strides, at most 2^31 - 1; max_pages * page_size and B at most
+ * 2^31 - 513; B * Hkv * (max_pages * page_size / 128 + 17) <= 2^31 - 1025.
  * ---------------------------------------------------------------------- */
 size_t spec_verify_attn_scaled_workspace_size(int B, int R, int Hq, int Hkv, int D);
 
@@ -782,8 +784,8 @@ spec_status spec_verify_attn_scaled(const void* q, int64_t q_stride_b, int64_t q
  *            allowed; any other becomes -inf, whatever it was.  mask_row [B,R] int32:
  *            the mask of each row, outside 0 .. n_masks - 1: none (NULL: row i of
  *            sequence b has mask b * R + i).
- *   1 <= R <= 64; V < 2^31 - 4096; a parent row that is no tree in storage order
- *   (0 <= parent[i] < i) ends the walk there.
+ *   1 <= R <= 64; V < 2^31 - 32768; H < 2^30; n_bias < 2^31 - 4096; B <= 65535; a parent
+ *   row that is no tree in storage order (0 <= parent[i] < i) ends the walk there.
  * ---------------------------------------------------------------------- */
 spec_status spec_logits_process(const void* logits, int64_t logits_stride, spec_dtype dtype,
                                 float* out, int B, int R, int V, const int32_t* history, int H,

@@ -5,32 +5,51 @@
 // a_t, c_t:
 //   x_t = scale a_t (q . k_t),  out = sum_t e^(x_t) c_t v_t / l,  l = sum_t e^(x_t),  lse = ln l.
 // V's scale goes into the weight, w_t = 2^(x_t + log2 c_t - m) with a reference m per row, and
-// l = sum w_t / c_t.  So weights stay below 2^8 whatever the scales are, and a row's sum keeps the
+// l = sum w_t / c_t.  So weights keep to a narrow range whatever the scales are, and a row's sum keeps the
 // precision of its own largest contribution.  Parts of the positions give (m, l, sum w v) each and
 // join by 2^(m_i - M) ("Speculative Token Decoupling: Asynchronous Verification via
 // Flash-Decoding", section 03: split-K attention).
 //
-// What bounds it: HBM up to some 100 query rows per KV head (2 D bytes per position and head are
-// read once); the tensor cores and the exponentials above that.
+// What bounds it: HBM in principle up to some 100 query rows per KV head (2 D bytes per position and head
+// are read once); measured, the chain of waits of a tile (below).
 //
 // Design.  Both products are taken transposed, positions (or dimensions) as the MMA's 128 rows and
 // query rows as its columns, so that a few query rows cost a few columns:
 //   S^T = K Q^T: a tile of 128 positions, as it lies in the cache: the codes go to the tensor cores
 //     (tcgen05 kind::f8f6f4) as they are, without a conversion.  Q is a sum of e4m3 parts (two hold a
 //     bf16 number's 8 bits, three an fp16's 11) under a power of two per row.
-//   O^T = V^T W^T: A is the V tile, positions along K.  W is a sum of three 8-bit parts: two e4m3 (the
-//     second times 2^4) and one e5m2 (times 2^15), 11 bits down to 2^-27 of a row's largest weight; the
-//     parts are columns of their own and are added up at the end.
-// In S^T a thread owns one position: its scales are two numbers, unseen positions one comparison,
-// and the sum over positions is left to the end.  The reference of a row moves only when a weight
-// passes 2^8 (one vote a tile); then O is rescaled in tensor memory.
+//   O^T = V^T W^T: up to D = 128 the V tile is converted to fp16 in shared memory (exact) and the weights
+//     are fp16 (2^-11), from 2^8 at a row's first maximum up to 2^15, so that what lies 2^32 below a row's
+//     largest is what is lost.  At D = 256, where shared memory has no room for it, V goes as it lies and a
+//     weight is a sum of three 8-bit parts, two e4m3 (the second times 2^4) and one e5m2 (times 2^15), 11
+//     bits down to 2^-27 of a row's largest weight; the parts are columns of their own, added up at the end.
+//     (Three parts at every D: 64 ragged chains 339 us against 307, draft trees 766 against 703.)
+// In S^T a lane owns four positions of eight columns: their scales are a few registers, unseen positions a
+// bit, and the sum over positions is left to the end.  The reference of a row moves only when a weight
+// would pass the largest (one vote a tile); then O is rescaled in tensor memory.
 //
-// A CTA (one per SM) takes up to 64 query rows of a KV head and one contiguous range of (KV head, batch's
-// positions), cut evenly in tiles of 128 over all SMs on the device, so that ragged batches, one long
-// sequence and captured graphs whose lengths change fill the GPU alike.  Four copy warps stream K, V and
-// their scales into a ring of stages (16-byte cp.async, zeros where nothing is seen) and run ahead
-// over the ends of sequences; one thread issues the MMAs; eight warps turn scores into weights.
-// Sequences cut over several CTAs leave parts, joined by a second kernel in their order.
+// A CTA (one per SM) takes up to 64 query rows of a KV head (32 at D = 256) and one contiguous range of (KV
+// head, batch's positions), cut in tiles of 128 over all SMs on the device, so that ragged batches, one
+// long sequence and captured graphs whose lengths change fill the GPU alike; the cut counts what a
+// sequence's ends cost (8 tiles, 16 for 64 rows: 64 ragged chains 256 -> 244 us, one chain of 8 rows on 8192
+// tokens 24.5 -> 20.5, a chain of 16 on 131072 167 -> 154).  Four warps stream K, V and their scales into a
+// ring of stages (16-byte cp.async, zeros where nothing is seen), run ahead over the ends of sequences and
+// make Q's parts behind a segment's first tile; one thread each issues the two products; two groups of four
+// warps take the tiles in turn and turn scores into weights, each with references, sums and an O of its
+// own, so that one tile's chain of waits lies under the other's work.  Sequences cut over several CTAs leave
+// parts, joined by a second kernel in their order, which is set up early.
+//
+// What a tile costs (cycles of a group, at 32 rows / 64): scales, V's conversion and the wait for it 1750 /
+// 1450, the wait for the scores 190 / 200, exponents and vote 770 / 790, weights 360 / 1670, the next tile 600;
+// 1870 / 2540 a tile with both groups, against 490 / 1000 of tensor-core time.  Issue slots are 42 % full: it
+// is latency that is left.  Tried: three groups (96 registers a thread: 280 us against 244 for 64 ragged
+// chains), two CTAs an SM (294), conversion by warps of its own beside two copy warps (draft trees 10 %
+// faster, 64 ragged chains 13 % slower), one vote behind the weights instead of one in front (278).
+//
+// Measured (replays of a captured graph; bf16, 32/8 heads of 128 unless given): 64 ragged chains of 5 rows
+// (540 K positions) 237 us, 4.7 TB/s; one chain of 8 on 8192 tokens 19.5; draft trees of 64 on 4 x 32768, 64/8
+// heads, 577, 475 TFLOP/s; a chain of 16 on 131072, 64/8 heads, fp16, 154; single tokens of 37 sequences, window
+// 1000, 16/4 heads of 64, fp16, 15.6.
 //
 // What is seen by some rows only (block rows, the edge of a window) gets weight 0 elsewhere; as 0 times a
 // NaN code would be NaN, such tiles' NaN codes of V are zeroed and noted per row.

@@ -7,17 +7,21 @@
 // and the real sampler": p must include the transforms actually served).  A row's text is the
 // history behind the prompt and the block tokens in front of the row.
 //
-// What bounds it: the logits are read once and written once, so HBM; what a mask forbids in
-// groups of four is not read.
+// What bounds it: the logits are read once and written once, so HBM (what a mask forbids in groups of
+// eight is not read), and the counting in front of it where histories are long.
 //
 // Design: a CTA takes a slice of the vocabulary for some rows of one sequence.  It counts the
 // history's ids of its slice in shared memory (integer atomics: the order does not matter), sums
 // the biases there (ids are dealt to threads, each adds its own in the list's order) and lists what
-// either touches.  A row is then written as it comes, eight ids a thread and store, with -inf where
-// the mask forbids; behind that the touched ids, a thread each, are computed and written over
-// it, while the next row is on its way.  (With the touched ids looked for within the stores, most warps
-// met some: twice the instructions, 105 us against the present 0 at 64 sequences of 5 rows.)  From row
-// to row only the block tokens that differ are counted up or down.
+// either touches; the first rows' logits and the lists' first ids are on their way meanwhile.  Rows are
+// written as they come, eight ids a thread and store, with -inf where the mask forbids; behind them the
+// touched ids, a thread each, are computed and written over it.  (Touched ids looked for within the
+// stores: most warps met some, twice the instructions.)
+//
+// Measured: 64 sequences of 5 rows, fp32, 152064 ids, histories of 4099, a mask on a quarter 85.5 us, 4.6 TB/s
+// (the copy alone 58.5, penalties 14 us more, biases 6, masks 6; simplest form 113, touched ids behind each
+// row's stores 99, two rows in flight 89); one sequence of 8 rows, bf16, 128256 ids 5.7 us (19.4 before its
+// rows were dealt out).  Copying first in every other wave of CTAs, so that not all count at once: 100 us.
 #include <algorithm>
 
 #include <cuda_fp16.h>

@@ -4,8 +4,12 @@
 // b cos u), u = t f_i (rope.cuh), in fp32 with one rounding.
 //
 // What bounds it: every row is read once and written once, so HBM, and for the rows of a verify
-// block the launch.  A thread takes 8 + 8 elements whose pairs lie within them (two 16-byte loads
-// and stores); a token's sines and cosines serve all its heads from shared memory.
+// block the launch.  A CTA turns a token: its sines and cosines serve all heads from shared memory, and are
+// worked out while the rows are on their way.  A thread takes items of 8 + 8 elements whose pairs lie within
+// them (two 16-byte loads and stores), two in flight.
+//
+// Measured: 16384 rows of 32/8 heads of 128 in bf16 52.9 us, 6.3 TB/s, 0.94 of the copy (66 with the angles in
+// front of the loads); 320 rows 2.8 us, one 2.3.
 #include "rope.cuh"
 
 namespace {
