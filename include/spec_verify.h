@@ -170,8 +170,9 @@ spec_status spec_verify_attn_combine(const void* q, const void* k_cache, const v
  * counterpart; this exists so that a test can show that a wait that runs out
  * ends the kernel with an error word instead of hanging the GPU.
  *
- *   withhold_stage  >= 0: in every partial-pass CTA launched from now on, the
- *                   copy warps never signal that K/V stage withhold_stage has
+ *   withhold_stage  >= 0: in every partial-pass CTA (and CTA of
+ *                   spec_verify_attn_scaled) launched from now on, the copy
+ *                   warps never signal that K/V stage withhold_stage has
  *                   landed, so the waits on it (and those behind it) run out;
  *                   -1: normal operation.
  *   wait_limit_ns   bound of every wait of the partial passes; 0 restores the

@@ -812,6 +812,11 @@ extern "C" spec_status spec_debug_attn_fault(int withhold_stage, unsigned long l
   return SPEC_OK;
 }
 
+void attn_fault_setting(int* withhold_stage, unsigned long long* wait_ns) {
+  *withhold_stage = g_withhold_stage.load(std::memory_order_relaxed);
+  *wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+}
+
 extern "C" spec_status spec_verify_attn(SPEC_ATTN_ARGS, void* out, float* lse_out, void* stream) {
   return verify_attn_impl(SPEC_ATTN_FWD, out, lse_out, stream, kBoth);
 }

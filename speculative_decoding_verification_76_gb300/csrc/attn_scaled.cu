@@ -127,7 +127,9 @@ extern "C" spec_status spec_verify_attn_scaled(
   p.teams = pl.teams;
   p.ends = pl.rt == 64 ? scaled_attn::kMostEnds : 8;
   p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.4426950408889634f;
-  p.polls = (uint32_t)(SPEC_WAIT_NS / 1000);
+  unsigned long long wait_ns;
+  attn_fault_setting(&p.withhold_stage, &wait_ns);
+  p.polls = (uint32_t)std::min<unsigned long long>(wait_ns / 1000 + 1, UINT32_MAX);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool f16 = q_dtype == SPEC_F16;
   return D == 64 ? scaled_attn::launch_d64(p, pl.rt, f16, st)

@@ -91,6 +91,7 @@ struct Params {
   int ends;
   float scale_log2;
   uint32_t polls;                    // of a wait, before it gives up
+  int withhold_stage;                // -1; a test sets a tile whose arrival the load warps withhold
 };
 
 __device__ const float g_unseen = -INFINITY;  // K's scale of a position that is not there
@@ -557,9 +558,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_at + 512),
                      "l"(is_there ? p.vs + sc : &g_unseen)
                      : "memory");
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                         smem_u32(&full[stage]))
-                     : "memory");
+        if (g != p.withhold_stage)
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                           smem_u32(&full[stage]))
+                       : "memory");
         if (j > 0) continue;
         // ---- behind the segment's first tile: Q as sums of e4m3 parts under a power of two per row
         // (the segment before the last is done with the places)
@@ -815,7 +817,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         }
         ok = ok && wait_for(&s_full[group], u >> 1 & 1, p);
         tc_fence_after();
-        mbar_arrive(&empty[stage]);
+        // (only what has been handed over is given back: a phase must not get more arrivals than it waits for)
+        if (ok) mbar_arrive(&empty[stage]);
         const uint32_t s_at = lanes + group * RT;
         const uint32_t w_at = p_at + u % S::kPBufs * S::kPBytes + (quad * 32 + lane) * 16;
 #pragma unroll
@@ -1017,7 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         begun = true;
         fence_proxy_async();
         tc_fence_before();
-        mbar_arrive(&p_full[group]);
+        if (ok) mbar_arrive(&p_full[group]);
       }
       g += n_units;
       // ---- the segment's sums and outputs: the groups' states meet
@@ -1198,6 +1201,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
 }
 
 // ---------------------------------------------------------------- host side
+}  // namespace scaled_attn
+void attn_fault_setting(int* withhold_stage, unsigned long long* wait_ns);  // spec_debug_attn_fault's
+namespace scaled_attn {
+
 template <int D, int RT, bool F16>
 spec_status launch_one(const Params& p, cudaStream_t st) {
   using S = Shape<D, RT, F16>;
