@@ -18,12 +18,14 @@
 //   S^T = K Q^T: a tile of 128 positions, as it lies in the cache: the codes go to the tensor cores
 //     (tcgen05 kind::f8f6f4) as they are, without a conversion.  Q is a sum of e4m3 parts (two hold a
 //     bf16 number's 8 bits, three an fp16's 11) under a power of two per row.
-//   O^T = V^T W^T: up to D = 128 the V tile is converted to fp16 in shared memory (exact) and the weights
-//     are fp16 (2^-11), from 2^8 at a row's first maximum up to 2^15, so that what lies 2^32 below a row's
-//     largest is what is lost.  At D = 256, where shared memory has no room for it, V goes as it lies and a
-//     weight is a sum of three 8-bit parts, two e4m3 (the second times 2^4) and one e5m2 (times 2^15), 11
-//     bits down to 2^-27 of a row's largest weight; the parts are columns of their own, added up at the end.
-//     (Three parts at every D: 64 ragged chains 339 us against 307, draft trees 766 against 703.)
+//   O^T = V^T W^T, in one of two forms.  V goes as it lies, and a weight is a sum of three 8-bit parts, two
+//     e4m3 (the second times 2^4) and one e5m2 (times 2^15), 11 bits down to 2^-27 of a row's largest
+//     weight; the parts are columns of their own, added up at the end.  Or the V tile is converted to fp16
+//     in shared memory (exact) and the weights are fp16 (2^-11), from 2^8 at a row's first maximum up to 2^15, so
+//     that what lies 2^32 below a row's largest is what is lost.  The first costs conversions per weight, the
+//     second per code, and room that D = 256 does not have: the second is taken for 64 rows (draft trees
+//     703 us against 766) and at D = 64 (64 ragged chains 199 against 214, single tokens 15.4 against 16.4), the
+//     first else (one row at D = 128 187 against 200, 5 rows 232 against 235.5).
 // In S^T a lane owns four positions of eight columns: their scales are a few registers, unseen positions a
 // bit, and the sum over positions is left to the end.  The reference of a row moves only when a weight
 // would pass the largest (one vote a tile); then O is rescaled in tensor memory.
@@ -39,17 +41,18 @@
 // own, so that one tile's chain of waits lies under the other's work.  Sequences cut over several CTAs leave
 // parts, joined by a second kernel in their order, which is set up early.
 //
-// What a tile costs (cycles of a group, at 32 rows / 64): scales, V's conversion and the wait for it 1750 /
-// 1450, the wait for the scores 190 / 200, exponents and vote 770 / 790, weights 360 / 1670, the next tile 600;
-// 1870 / 2540 a tile with both groups, against 490 / 1000 of tensor-core time.  Issue slots are 42 % full: it
-// is latency that is left.  Tried: three groups (96 registers a thread: 280 us against 244 for 64 ragged
-// chains), two CTAs an SM (294), conversion by warps of its own beside two copy warps (draft trees 10 %
-// faster, 64 ragged chains 13 % slower), one vote behind the weights instead of one in front (278).
+// What a tile costs (cycles of a group, at 32 rows with V as it lies): scales 260, the wait for the scores 200,
+// exponents and vote 890, weights 1060, up to the next tile 670; 1590 a tile with both groups, against some 500
+// of tensor-core time.  At 64 rows V's conversion adds 1200 and the weights take 1670: 2540 a tile against 1000.
+// Issue slots are 42 % full: it is latency that is left.  Tried: three groups (96 registers a thread: 280 us
+// against 244 for 64 ragged chains), two CTAs an SM (294), conversion by warps of its own beside two copy
+// warps (draft trees 10 % faster, 64 ragged chains 13 % slower), one vote behind the weights instead of
+// one in front (278), one score buffer a group instead of two (232 against 228).
 //
 // Measured (replays of a captured graph; bf16, 32/8 heads of 128 unless given): 64 ragged chains of 5 rows
-// (540 K positions) 237 us, 4.7 TB/s; one chain of 8 on 8192 tokens 19.5; draft trees of 64 on 4 x 32768, 64/8
-// heads, 577, 475 TFLOP/s; a chain of 16 on 131072, 64/8 heads, fp16, 154; single tokens of 37 sequences, window
-// 1000, 16/4 heads of 64, fp16, 15.6.
+// (540 K positions) 228 us, 4.9 TB/s, of one row 196; one chain of 8 on 8192 tokens 19.4; draft trees of 64 on
+// 4 x 32768, 64/8 heads, 580, 473 TFLOP/s; a chain of 16 on 131072, 64/8 heads, fp16, 155; single tokens of 37
+// sequences, window 1000, 16/4 heads of 64, fp16, 15.5.
 //
 // What is seen by some rows only (block rows, the edge of a window) gets weight 0 elsewhere; as 0 times a
 // NaN code would be NaN, such tiles' NaN codes of V are zeroed and noted per row.
@@ -305,9 +308,9 @@ struct Shape {
   static constexpr uint32_t kRows8 = 8 * kRowBytes;             // bytes of 8 rows
   static constexpr int kTileBytes = kUnit * D;
   static constexpr int kParts = F16 ? 3 : 2;                    // of Q
-  // V as fp16, converted in shared memory, and the weights with it; else (no room at D = 256) V as it
-  // lies, and the weights as three 8-bit parts
-  static constexpr bool kHalfV = D <= 128;
+  // V as fp16, converted in shared memory, and the weights with it; else V as it lies, and the weights as
+  // three 8-bit parts (above)
+  static constexpr bool kHalfV = D == 64 || (D == 128 && RT == 64);
   static constexpr int kSums = kHalfV ? 1 : 3;                  // columns of O per row and 128 dimensions
   static constexpr int kHalves = D == 256 ? 2 : 1;
   static constexpr int kOCols = kSums * RT * kHalves;
@@ -325,8 +328,9 @@ struct Shape {
   static constexpr int kStages = kRoom / kStageBytes < 8 ? kRoom / kStageBytes : 8;
   static_assert(kStages >= 1, "a ring needs a stage");
   static constexpr int kSmem = kFixed + kStages * kStageBytes;
-  // tensor memory: a score buffer and an O for each soft group
-  static constexpr int kColO = 2 * RT, kCols = kColO + 2 * kOCols;
+  // tensor memory: two score buffers and an O for each soft group (the next tile's scores are made while one's
+  // are read)
+  static constexpr int kColO = 4 * RT, kCols = kColO + 2 * kOCols;
   static constexpr int kAlloc = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static_assert(kCols <= 512, "tensor memory");
 };
@@ -388,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
   constexpr int kGroups = RT / 8;                    // column groups of eight
   constexpr int kB = kGroups < 4 ? kGroups : 4;      // of them between two votes
   extern __shared__ uint8_t dyn[];
-  __shared__ __align__(8) uint64_t full[NS], empty[NS], s_full[2], p_full[2], pv_done[4], q_full[2],
+  __shared__ __align__(8) uint64_t full[NS], empty[NS], s_full[4], p_full[4], pv_done[4], q_full[2],
       seg_done[2], o_full, fin;
   // per segment, two in flight: scale, block rows seen, first position, output row of a query row
   __shared__ __align__(16) float sc_s[2][RT];
@@ -455,10 +459,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         mbar_init(&full[i], kLoad);
         mbar_init(&empty[i], kGroup + (S::kHalfV ? 1 : 2));  // scales (and V) taken, K's (and V's) product
       }
-      for (int i = 0; i < 4; ++i) mbar_init(&pv_done[i], 1);
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4; ++i) {  // tile u's is u & 3
         mbar_init(&s_full[i], 1);
         mbar_init(&p_full[i], kGroup);
+        mbar_init(&pv_done[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
         mbar_init(&q_full[i], kLoad);
         mbar_init(&seg_done[i], kSoft);
       }
@@ -659,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         for (int j = 0; j < n; ++j, ++g) {
           const int stage = g % NS;
           // the score buffer's last tile has been read, this tile has landed
-          ok = (g < 2 || wait_for(&p_full[g & 1], (g - 2) >> 1 & 1, p)) &&
+          ok = (g < 4 || wait_for(&p_full[g & 3], (g - 4) >> 2 & 1, p)) &&
                wait_for(&full[stage], (g / NS) & 1, p);
           if (!ok) break;
           fence_proxy_async();  // the copies' writes, for the tensor cores
@@ -672,9 +678,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
             uint32_t b = q_lo + ((k / kIn) * (RT * 128) + k % kIn * 32) / 16;
 #pragma unroll
             for (int part = 0; part < S::kParts; ++part, b += RT * D / 16)
-              mma_f8(tmem + (g & 1) * RT, a, kHi, b, kHi, kId, k > 0 || part > 0);
+              mma_f8(tmem + (g & 3) * RT, a, kHi, b, kHi, kId, k > 0 || part > 0);
           }
-          tc_commit(&s_full[g & 1]);
+          tc_commit(&s_full[g & 3]);
           tc_commit(&empty[stage]);
         }
       }
@@ -694,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         const int n = walk.count();
 #pragma unroll 1
         for (int j = 0; j < n; ++j, ++g) {
-          ok = wait_for(&p_full[g & 1], g >> 1 & 1, p);
+          ok = wait_for(&p_full[g & 3], g >> 2 & 1, p);
           if (!ok) break;
           if constexpr (!S::kHalfV) fence_proxy_async();
           tc_fence_after();
@@ -781,8 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         // positions that some rows see and others do not
         const bool mixed = (t0 + kUnit > ctx && (p.R > 1 || p.mask)) ||
                            (p.window > 0 && t0 < ctx + p.R - p.window);
-        // (a buffer's last readers are done: all of them have handed over weights behind it, or the scores
-        // that this group took last would not be there)
+        // (a buffer's last readers are done: the product of their weights was waited for a tile ago)
         Rows* const seen = seen_by[group][u >> 1 & 1];
         if (mixed) {
           const int t = t0 + tid, jb = t - ctx;
@@ -815,11 +820,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
             *reinterpret_cast<uint4*>(half + (((c16 + 1) ^ (tid & 7)) << 4)) = h1;
           }
         }
-        ok = ok && wait_for(&s_full[group], u >> 1 & 1, p);
+        ok = ok && wait_for(&s_full[u & 3], u >> 2 & 1, p);
         tc_fence_after();
         // (only what has been handed over is given back: a phase must not get more arrivals than it waits for)
         if (ok) mbar_arrive(&empty[stage]);
-        const uint32_t s_at = lanes + group * RT;
+        const uint32_t s_at = lanes + (u & 3) * RT;
         const uint32_t w_at = p_at + u % S::kPBufs * S::kPBytes + (quad * 32 + lane) * 16;
 #pragma unroll
         for (int h = 0; h < kGroups; h += kB) {
@@ -1020,7 +1025,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         begun = true;
         fence_proxy_async();
         tc_fence_before();
-        if (ok) mbar_arrive(&p_full[group]);
+        if (ok) mbar_arrive(&p_full[u & 3]);
       }
       g += n_units;
       // ---- the segment's sums and outputs: the groups' states meet
