@@ -504,7 +504,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
       // a query row for kPer threads; what a thread has of it is on its way before anything else
       constexpr int kPer = kLoad / RT;
       constexpr int kMine = D / 8 / kPer > 0 ? D / 8 / kPer : 1;  // 16-byte chunks of a thread
-      constexpr bool kHeld = kMine <= 4;                          // (more of them: read where they are used)
       const int n = tid / kPer, x0 = tid % kPer;
       const int q_row = tile * p.rows_per_tile + n, i_row = p.per_head.quot(q_row);
       const bool real = n < rows;
@@ -515,11 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         const int c = x0 + m * kPer;
         return real && c < D / 8 ? q_src[c] : make_uint4(0, 0, 0, 0);
       };
-      uint4 held[kHeld ? kMine : 1];
-      if constexpr (kHeld) {
+      uint4 held[kMine];
 #pragma unroll
-        for (int m = 0; m < kMine; ++m) held[m] = q_chunk(m);
-      }
+      for (int m = 0; m < kMine; ++m) held[m] = q_chunk(m);
       int t = walk.seq.first + walk.first_unit() * kUnit + tid;
       int page = p.P.quot(t), off = t - page * p.P.d, id = t < end ? bt[page] : -1;
       const char* kh = p.k + walk.kvh * p.head_stride + chunk * 16;
@@ -593,9 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
           uint32_t big2 = 0;
 #pragma unroll
           for (int m = 0; m < kMine; ++m) {
-            uint4 w;
-            if constexpr (kHeld) w = held[m];
-            else w = q_chunk(m);
+            const uint4 w = held[m];
             big2 = __vimax3_u16x2(big2, w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
             big2 = __vimax3_u16x2(big2, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu);
           }
@@ -606,13 +601,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
           const float s = needed_scale(F16 ? __half2float(__ushort_as_half((unsigned short)big))
                                            : __uint_as_float(big << 16));
           const float down = 1.f / s;
-#pragma unroll(kHeld ? kMine : 1)
+#pragma unroll
           for (int m = 0; m < kMine; ++m) {
             const int c = x0 + m * kPer;
             if (c >= D / 8) break;
             float x[8];
-            if constexpr (kHeld) values(held[m], x);
-            else values(q_chunk(m), x);
+            values(held[m], x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] *= down;
             uint8_t* to = q_0 + seg % S::kQBufs * S::kQBytes + swizzled<D>(RT, n, c >> 1) + (c & 1) * 8;
@@ -1065,7 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
       sync_of(3, kSoft);
       // (a group takes every other two columns of O; of three 8-bit parts, a column and the next are rows n
       // and n + 1)
-#pragma unroll 2
+#pragma unroll(S::kHalfV ? 4 : 2)
       for (int c = 2 * group; c < RT; c += 4) {
         const int n0 = S::kHalfV ? c : (c & ~15) + 2 * (c >> 2 & 3) + 8 * (c >> 1 & 1);
         if (n0 >= rows) continue;
