@@ -401,9 +401,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
   __shared__ int from_s[2][RT], any_nan[2];
   __shared__ uint32_t nan_s[2][RT][D / 32];
   __shared__ __align__(16) float neg_m[2][RT], fac_s[2][RT], red[kSoftWarps][RT], inv_s[RT];
-  // the rows that see a position, for tiles where not all of them do: of a group's last two tiles
+  // the rows that see a position, for tiles where not all of them do (a warp's positions are its own)
   using Rows = typename RowBits<(RT > 32)>::T;
-  __shared__ Rows seen_by[2][2][kUnit];
+  __shared__ Rows seen_by[2][kUnit];
   __shared__ Walk start;
   __shared__ uint32_t tmem_base;
   __shared__ int part_w[kThreads / 32];
@@ -781,20 +781,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         // positions that some rows see and others do not
         const bool mixed = (t0 + kUnit > ctx && (p.R > 1 || p.mask)) ||
                            (p.window > 0 && t0 < ctx + p.R - p.window);
-        // (a buffer's last readers are done: the product of their weights was waited for a tile ago)
-        Rows* const seen = seen_by[group][u >> 1 & 1];
-        if (mixed) {
-          const int t = t0 + tid, jb = t - ctx;
+        Rows* const seen = seen_by[group];
+        if (mixed) {  // a lane holds a row (or two), a vote gives a position's (of 16 rows, two positions')
+          constexpr int kAt = RT < 32 ? 16 : 32;  // positions from one of a vote to the next
+          const int first = t0 + quad * 32;
           Rows m = 0;
-#pragma unroll 8
-          for (int n = 0; n < RT; ++n)
-            m |= (Rows)(jb < 0 ? t >= from_s[sb][n] : jb < 64 && (see_s[sb][n] >> (jb & 63) & 1)) << n;
+          if (first + 31 < ctx && p.window == 0) {
+            m = ~(Rows)0;
+          } else if (first < ctx + p.R) {
+            const int n0 = lane & (kAt - 1), n1 = RT > 32 ? lane + 32 : n0;
+            const uint64_t see0 = see_s[sb][n0], see1 = see_s[sb][n1];
+            const int from0 = from_s[sb][n0], from1 = from_s[sb][n1];
+#pragma unroll 4
+            for (int i = 0; i < kAt; ++i) {
+              const int t = first + i + (lane & ~(kAt - 1)), jb = t - ctx;
+              const bool sees0 = jb < 0 ? t >= from0 : jb < 64 && (see0 >> (jb & 63) & 1);
+              Rows rows_of = __ballot_sync(0xffffffffu, sees0);
+              if constexpr (RT > 32) {
+                const bool sees1 = jb < 0 ? t >= from1 : jb < 64 && (see1 >> (jb & 63) & 1);
+                rows_of |= (Rows)__ballot_sync(0xffffffffu, sees1) << 32;
+              }
+              if (n0 == i) m = kAt < 32 ? rows_of >> (lane & 16) : rows_of;
+            }
+          }
+          if constexpr (RT < 32) m &= (1u << RT) - 1;
+          __syncwarp();
           seen[tid] = m;
           if (has_nans<D>(vrow, tid)) {
             note_nans<D>(vrow, tid, m, nan_s[sb][0]);
             any_nan[sb] = 1;
           }
-          sync_of(bar, kGroup);
+          __syncwarp();
         }
         if constexpr (S::kHalfV) {  // position tid's V as fp16, 64 dimensions a row
           // (the product that read the buffer last is complete)
