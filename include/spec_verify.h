@@ -744,7 +744,7 @@ spec_status spec_commit_scaled(void* k_cache, void* v_cache, float* k_scale, flo
  * 1 <= R <= 64, D in {64,128,256}, Hkv * ceil(R * Hq / Hkv / 64) <= 4096 (/ 32 for D = 256); caches,
  * strides and q 16-byte aligned; page_stride a multiple of token_stride, which is positive, and the
  * cache's rows, counted in token strides, at most 2^31 - 1; max_pages * page_size and B at most
- * 2^31 - 513; B * Hkv * (max_pages * page_size / 128 + 17) <= 2^31 - 1025.
+ * 2^31 - 513; B * Hkv * (max_pages * page_size / 128 + 11) <= 2^31 - 1025.
  * ---------------------------------------------------------------------- */
 size_t spec_verify_attn_scaled_workspace_size(int B, int R, int Hq, int Hkv, int D);
 

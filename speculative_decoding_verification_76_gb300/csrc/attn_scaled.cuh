@@ -33,8 +33,8 @@
 // A CTA (one per SM) takes up to 64 query rows of a KV head (32 at D = 256) and one contiguous range of (KV
 // head, batch's positions), cut in tiles of 128 over all SMs on the device, so that ragged batches, one
 // long sequence and captured graphs whose lengths change fill the GPU alike; the cut counts what a
-// sequence's ends cost (8 tiles, 16 for 64 rows: 64 ragged chains 256 -> 244 us, one chain of 8 rows on 8192
-// tokens 24.5 -> 20.5, a chain of 16 on 131072 167 -> 154).  Four warps stream K, V and their scales into a
+// sequence's ends cost (8 tiles, 10 for 64 rows: 64 ragged chains 256 -> 244 us, one chain of 8 rows on 8192
+// tokens 24.5 -> 20.5, a chain of 16 on 131072 168 -> 160).  Four warps stream K, V and their scales into a
 // ring of stages (16-byte cp.async, zeros where nothing is seen), run ahead over the ends of sequences and
 // make Q's parts behind a segment's first tile; one thread each issues the two products; two groups of four
 // warps take the tiles in turn and turn scores into weights, each with references, sums and an O of its
@@ -43,16 +43,18 @@
 //
 // What a tile costs (cycles of a group, at 32 rows with V as it lies): scales 260, the wait for the scores 200,
 // exponents and vote 890, weights 1060, up to the next tile 670; 1590 a tile with both groups, against some 500
-// of tensor-core time.  At 64 rows V's conversion adds 1200 and the weights take 1670: 2540 a tile against 1000.
+// of tensor-core time.  At 64 rows V's conversion adds 1200 and the weights take 1670: 2500 a tile against 1000.
 // Issue slots are 42 % full: it is latency that is left.  Tried: three groups (96 registers a thread: 280 us
 // against 244 for 64 ragged chains), two CTAs an SM (294), conversion by warps of its own beside two copy
 // warps (draft trees 10 % faster, 64 ragged chains 13 % slower), one vote behind the weights instead of
-// one in front (278), one score buffer a group instead of two (232 against 228).
+// one in front (278), one score buffer a group instead of two (232 against 228), the rows that see a position
+// by a thread's loop over them instead of votes (228 against 221, draft trees 562 against 551), outputs with
+// twice the rows in flight (247 against 221).
 //
 // Measured (replays of a captured graph; bf16, 32/8 heads of 128 unless given): 64 ragged chains of 5 rows
-// (540 K positions) 228 us, 4.9 TB/s, of one row 196; one chain of 8 on 8192 tokens 19.4; draft trees of 64 on
-// 4 x 32768, 64/8 heads, 580, 473 TFLOP/s; a chain of 16 on 131072, 64/8 heads, fp16, 155; single tokens of 37
-// sequences, window 1000, 16/4 heads of 64, fp16, 15.5.
+// (540 K positions) 221 us, 5.0 TB/s; one chain of 8 on 8192 tokens 18.5; draft trees of 64 on 4 x 32768, 64/8
+// heads, 546, 503 TFLOP/s; a chain of 16 on 131072, 64/8 heads, fp16, 154; single tokens of 37 sequences, window
+// 1000, 16/4 heads of 64, fp16, 15.5.
 //
 // What is seen by some rows only (block rows, the edge of a window) gets weight 0 elsewhere; as 0 times a
 // NaN code would be NaN, such tiles' NaN codes of V are zeroed and noted per row.
@@ -73,7 +75,7 @@ constexpr int kThreads = 32 * (kSumWarp + 1);
 static_assert(kLoad == kUnit, "a position of the tile for each");
 constexpr float kNone = -1e30f;                  // the reference of a row that has seen nothing
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMostEnds = 16;                    // of Params::ends
+constexpr int kMostEnds = 10;                    // of Params::ends
 
 struct Params {
   const char *q, *k, *v;
