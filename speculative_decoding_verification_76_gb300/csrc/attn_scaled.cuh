@@ -44,7 +44,7 @@
 // What a tile costs (cycles of a group, at 32 rows with V as it lies): scales 260, the wait for the scores 200,
 // exponents and vote 890, weights 1060, up to the next tile 670; 1590 a tile with both groups, against some 500
 // of tensor-core time.  At 64 rows V's conversion adds 1200 and the weights take 1670: 2500 a tile against 1000.
-// Issue slots are 42 % full: it is latency that is left.  Tried: three groups (96 registers a thread: 280 us
+// Issue slots are 42 to 52 % full: it is latency that is left.  Tried: three groups (96 registers a thread: 280 us
 // against 244 for 64 ragged chains), two CTAs an SM (294), conversion by warps of its own beside two copy
 // warps (draft trees 10 % faster, 64 ragged chains 13 % slower), one vote behind the weights instead of
 // one in front (278), one score buffer a group instead of two (232 against 228), the rows that see a position
