@@ -52,8 +52,8 @@
 // twice the rows in flight (247 against 221).
 //
 // Measured (replays of a captured graph; bf16, 32/8 heads of 128 unless given): 64 ragged chains of 5 rows
-// (540 K positions) 221 us, 5.0 TB/s; one chain of 8 on 8192 tokens 18.5; draft trees of 64 on 4 x 32768, 64/8
-// heads, 546, 503 TFLOP/s; a chain of 16 on 131072, 64/8 heads, fp16, 154; single tokens of 37 sequences, window
+// (540 K positions) 219 us, 5.1 TB/s; one chain of 8 on 8192 tokens 18.5; draft trees of 64 on 4 x 32768, 64/8
+// heads, 543, 506 TFLOP/s; a chain of 16 on 131072, 64/8 heads, fp16, 154; single tokens of 37 sequences, window
 // 1000, 16/4 heads of 64, fp16, 15.5.
 //
 // What is seen by some rows only (block rows, the edge of a window) gets weight 0 elsewhere; as 0 times a
@@ -1131,7 +1131,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
 // their order.
 constexpr int kJoinWarps = 8;
 
-template <int D, bool F16>
+template <int D, bool F16, int kFlight>  // kFlight parts are on their way at once
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_constant__ Params p, int RT) {
   constexpr int kPer = D / 32;
   __shared__ int sums[kJoinWarps][2];
@@ -1173,7 +1173,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const __grid_cons
       return (((size_t)(first + x) * 2 + (x == 0 && late)) * p.tiles + tile) * RT + n;
     };
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-    constexpr int kFlight = D == 256 ? 8 : 16;
 #pragma unroll 1
     for (int x0 = 0; x0 < np; x0 += kFlight) {
       float2 w[kFlight], y[kFlight][kPer / 2];
@@ -1257,8 +1256,13 @@ spec_status launch_d(const Params& p, int rt, bool f16, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = f16 ? cudaLaunchKernelEx(&cfg, join_kernel<D, true>, p, rt)
-                            : cudaLaunchKernelEx(&cfg, join_kernel<D, false>, p, rt);
+  // Sequences in many parts: one round trip for sixteen (one chain 18.6 us against 19.4 with eight); else eight,
+  // whose registers leave room for twice the rows (draft trees 5 us less).
+  constexpr int kMany = D == 256 ? 8 : 16, kFew = kMany / 2;
+  const bool many = p.teams > 8ll * p.B * p.Hkv;
+  const auto join = f16 ? many ? join_kernel<D, true, kMany> : join_kernel<D, true, kFew>
+                        : many ? join_kernel<D, false, kMany> : join_kernel<D, false, kFew>;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, join, p, rt);
   return e == cudaSuccess ? launch_status() : SPEC_ECUDA;
 }
 
