@@ -774,10 +774,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         float ks[4], lvs[4], rvs[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          float vs = scales[kUnit + 8 * r];
-          vs = vs < 0x1p-100f ? 0x1p-100f : vs;
+          const float stored = scales[kUnit + 8 * r], vs = fmaxf(stored, 0x1p-100f);
           ks[r] = scales[8 * r];
-          lvs[r] = __log2f(vs), rvs[r] = __fdividef(1.f, vs);
+          // (of a NaN scale the logarithm alone is NaN: where the weight is 0 the inverse must not make the sum NaN)
+          lvs[r] = stored == stored ? __log2f(vs) : NAN, rvs[r] = __fdividef(1.f, vs);
           if (ks[r] == -INFINITY) ks[r] = 0.f, lvs[r] = -INFINITY, rvs[r] = 0.f;  // not there
         }
         // positions that some rows see and others do not
