@@ -717,9 +717,15 @@ spec_status spec_commit_scaled(void* k_cache, void* v_cache, float* k_scale, flo
  *
  *   q        [B,R,Hq,D] q_dtype (bf16 or fp16); element (b,i,h,d) at b * q_stride_b
  *            + i * q_stride_r + h * q_stride_h + d.
- *   k_cache, v_cache, k_scale, v_scale: a scaled cache as above (any positive
- *            finite scales); block row j of sequence b is stored at position
- *            ctx_len[b] + j (append it first).
+ *   k_cache, v_cache, k_scale, v_scale: a scaled cache as above, its scales any
+ *            positive finite k_scale (powers of two or not) and v_scale from 2^-80 to
+ *            2^120, those that a row sees within 2^110 of one another: of a position
+ *            whose v_scale lies further below the largest, what 2^-126 cannot hold
+ *            beside the largest e^x v_scale is lost from the row's sum.  (Scales made by
+ *            spec_append_scaled lie within that while values of V stay below 2^54.)  A
+ *            v_scale below 2^-80 counts as 2^-80 (its values are below 2^-71); one above
+ *            2^120 makes NaN where it is seen.  Block row j of sequence b is stored at
+ *            position ctx_len[b] + j (append it first).
  *   block_table [B,max_pages] int32; ctx_len [B] int32: tokens stored in front of
  *            the block (R = 1: one less than a decoded sequence's length).  A
  *            negative one is an idle row of the batch.  Both stay as they are

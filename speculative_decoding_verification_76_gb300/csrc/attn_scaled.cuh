@@ -76,6 +76,9 @@ static_assert(kLoad == kUnit, "a position of the tile for each");
 constexpr float kNone = -1e30f;                  // the reference of a row that has seen nothing
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMostEnds = 10;                    // of Params::ends
+// V's scales: a row's sum adds weights of up to 2^15 over them, of up to 2^31 positions (2^126 at the least scale);
+// over the most, a row's first weight of 2^8 or more still leaves 2^-112.
+constexpr float kLeastV = 0x1p-80f, kMostV = 0x1p120f;
 
 struct Params {
   const char *q, *k, *v;
@@ -774,10 +777,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
         float ks[4], lvs[4], rvs[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float stored = scales[kUnit + 8 * r], vs = fmaxf(stored, 0x1p-100f);
+          const float stored = scales[kUnit + 8 * r], vs = fmaxf(stored, kLeastV);
           ks[r] = scales[8 * r];
-          // (of a NaN scale the logarithm alone is NaN: where the weight is 0 the inverse must not make the sum NaN)
-          lvs[r] = stored == stored ? __log2f(vs) : NAN, rvs[r] = __fdividef(1.f, vs);
+          // (of a NaN scale, or one too large, the logarithm alone is NaN: where the weight is 0 the inverse must
+          // not make the sum NaN)
+          lvs[r] = stored <= kMostV ? __log2f(vs) : NAN, rvs[r] = __fdividef(1.f, vs);
           if (ks[r] == -INFINITY) ks[r] = 0.f, lvs[r] = -INFINITY, rvs[r] = 0.f;  // not there
         }
         // positions that some rows see and others do not
