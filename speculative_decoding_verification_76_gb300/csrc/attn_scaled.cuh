@@ -18,14 +18,15 @@
 //   S^T = K Q^T: a tile of 128 positions, as it lies in the cache: the codes go to the tensor cores
 //     (tcgen05 kind::f8f6f4) as they are, without a conversion.  Q is a sum of e4m3 parts (two hold a
 //     bf16 number's 8 bits, three an fp16's 11) under a power of two per row.
-//   O^T = V^T W^T, in one of two forms.  V goes as it lies, and a weight is a sum of three 8-bit parts, two
-//     e4m3 (the second times 2^4) and one e5m2 (times 2^15), 11 bits down to 2^-27 of a row's largest
-//     weight; the parts are columns of their own, added up at the end.  Or the V tile is converted to fp16
-//     in shared memory (exact) and the weights are fp16 (2^-11), from 2^8 at a row's first maximum up to 2^15, so
-//     that what lies 2^32 below a row's largest is what is lost.  The first costs conversions per weight, the
-//     second per code, and room that D = 256 does not have: the second is taken for 64 rows (draft trees
-//     703 us against 766) and at D = 64 (64 ragged chains 199 against 214, single tokens 15.4 against 16.4), the
-//     first else (one row at D = 128 187 against 200, 5 rows 232 against 235.5).
+//   O^T = V^T W^T, with weights rounded to fp16, from 2^8 at a row's first maximum up to 2^15: 2^-11 relative down
+//     to 2^-22 of the row's largest, and 2^-33 of it below that.  In one of two forms, both exact behind that
+//     rounding.  V goes as it lies, and a weight is a sum of three e5m2 parts, the second times 2^4 and the third
+//     times 2^8: e5m2 has fp16's exponents, and 3 bits, 3 behind a sign and 3 behind another are fp16's 11.  The parts
+//     are columns of their own, added up at the end.  Or the V tile is converted to fp16 in shared memory.
+//     The first costs three columns per row, the second conversions per code and room in shared memory: the second
+//     is taken for 64 rows, where tensor memory has no room for three columns each, and at D = 64 (64 ragged chains
+//     199 us against 214, with costlier parts than these), the first else (one row at D = 128 196 against 202, 5 rows
+//     212 against 278).
 // In S^T a lane owns four positions of eight columns: their scales are a few registers, unseen positions a
 // bit, and the sum over positions is left to the end.  The reference of a row moves only when a weight
 // would pass the largest (one vote a tile); then O is rescaled in tensor memory.
@@ -77,7 +78,7 @@ constexpr float kNone = -1e30f;                  // the reference of a row that 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMostEnds = 10;                    // of Params::ends
 // V's scales: a row's sum adds weights of up to 2^15 over them, of up to 2^31 positions (2^126 at the least scale);
-// over the most, 2^120, a row's first weight of 2^2 or more still leaves 2^-118.  The most times the factor is the
+// over the most, 2^120, a row's first weight of 2^8 or more still leaves 2^-112.  The most times the factor is the
 // largest fp32 number.
 constexpr float kLeastV = 0x1p-80f, kPastMostV = 0x1.fffffep7f;
 
@@ -273,21 +274,9 @@ SPEC_DEV uint32_t f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-SPEC_DEV uint32_t e4m3x2(uint32_t h2) {  // two halves to two codes (low 16 bits)
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
-  return r;
-}
-SPEC_DEV uint32_t e5m2x2(uint32_t h2) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h2));
-  return r;
-}
-SPEC_DEV uint32_t halves_of(uint32_t codes) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
-  return r;
-}
+// Two halves rounded to the nearest e5m2 number, which is a half whose lower byte is zero (ties away from zero;
+// a NaN becomes a zero, and stays what the subtraction behind it makes).
+SPEC_DEV uint32_t e5m2_of(uint32_t h2) { return (h2 + 0x00800080u) & 0xff00ff00u; }
 SPEC_DEV void codes_to_halves(uint32_t w, uint32_t& lo, uint32_t& hi) {  // bytes 0, 1 and 2, 3
   asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
       " cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
@@ -321,7 +310,7 @@ struct Shape {
   static constexpr int kHalves = D == 256 ? 2 : 1;
   static constexpr int kOCols = kSums * RT * kHalves;
   // weights stay at or below 2^kTop and begin at 2^kBelow
-  static constexpr float kTop = kHalfV ? 15.f : 8.f, kBelow = kHalfV ? 8.f : 2.f;
+  static constexpr float kTop = 15.f, kBelow = 8.f;
   static constexpr int kStageBytes = 2 * kTileBytes + 1024;     // V, K, scales
   static constexpr int kQBytes = kParts * RT * D;               // of one of two
   static constexpr int kPBytes = kHalfV ? RT * kUnit * 2 : 3 * RT * kUnit;
@@ -715,8 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
             for (int k = 0; k < kUnit / 16; ++k)
               mma_f16(o, v_lo + k * 2048 / 16, kHiV, w_lo + k * 256 / 16, kHiW, kId, k > 0 ? 1u : later);
           } else {
-            constexpr uint32_t kIdP = idesc_f8(128, 2 * RT, false, true);
-            constexpr uint32_t kIdL = idesc_f8(128, RT, true, true);
+            constexpr uint32_t kId = idesc_f8(128, 3 * RT, true, true);
             constexpr uint32_t kHi = desc_hi(S::kRows8, S::kLayout);
             const int stage = g % NS;
             const uint32_t v_lo = desc_lo(base + stage * S::kStageBytes, 16384);
@@ -725,10 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
 #pragma unroll 1
               for (int k = 0; k < kUnit / 32; ++k) {
                 const uint32_t a = v_lo + (half * (kUnit * 128) + k * 4 * S::kRows8) / 16;
-                const uint32_t d = o + half * 3 * RT;
-                mma_f8(d, a, kHi, w_lo + k * 512 / 16, kHiW, kIdP, k > 0 ? 1u : later);
-                mma_f8(d + 2 * RT, a, kHi, w_lo + (2 * RT * kUnit + k * 512) / 16, kHiW, kIdL,
-                       k > 0 ? 1u : later);
+                mma_f8(o + half * 3 * RT, a, kHi, w_lo + k * 512 / 16, kHiW, kId, k > 0 ? 1u : later);
               }
             tc_commit(&empty[stage]);
           }
@@ -1021,16 +1006,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
               uint32_t p1[4], p2[4], p3[4];
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-                p1[r] = p2[r] = p3[r] = 0;
+                uint32_t x1[2], x2[2], x3[2];
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                   const uint32_t y = 8 * (h + k + x) < rows ? w[k + x][r] : 0u;
-                  const uint32_t x1 = e4m3x2(y);
-                  const uint32_t r1 = sub_mul(y, halves_of(x1), 0x4c004c00u);   // times 2^4
-                  const uint32_t x2 = e4m3x2(r1);
-                  const uint32_t x3 = e5m2x2(sub_mul(r1, halves_of(x2), 0x68006800u));  // times 2^11
-                  p1[r] |= x1 << 16 * x, p2[r] |= x2 << 16 * x, p3[r] |= x3 << 16 * x;
+                  x1[x] = e5m2_of(y);
+                  const uint32_t r1 = sub_mul(y, x1[x], 0x4c004c00u);  // times 2^4
+                  x2[x] = e5m2_of(r1);
+                  x3[x] = sub_mul(r1, x2[x], 0x4c004c00u);             // (an e5m2 number as it is)
                 }
+                p1[r] = __byte_perm(x1[0], x1[1], 0x7531);  // the upper bytes
+                p2[r] = __byte_perm(x2[0], x2[1], 0x7531);
+                p3[r] = __byte_perm(x3[0], x3[1], 0x7531);
               }
               const uint32_t to = w_at + (h + k) / 2 * 2048;
               store_frags(to, p1);
@@ -1106,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_scaled_kernel(
             for (int x = 0; x < 2; ++x) {
               float z = __uint_as_float(o[x][0][e]);
               if constexpr (!S::kHalfV)
-                z += __uint_as_float(o[x][1][e]) * 0x1p-4f + __uint_as_float(o[x][2][e]) * 0x1p-15f;
+                z += __uint_as_float(o[x][1][e]) * 0x1p-4f + __uint_as_float(o[x][2][e]) * 0x1p-8f;
               const float f = fac_s[x][n];
               y += f == 0.f ? 0.f : f * z;
             }
