@@ -619,7 +619,8 @@ PyObject* logits_process(PyObject* const* a) {
   if (x.dim() != 3) refuse("logits must be [B, R, V]");
   const int64_t B = x.size(0), R = x.size(1), V = x.size(2);
   if (B > INT_MAX || R > INT_MAX || V > INT_MAX) refuse("sizes must be below 2^31");
-  if (x.stride(2) != 1 || (B > 1 && R > 0 && x.stride(0) != R * x.stride(1)))
+  // (one row per sequence: the distance from row to row is the batch's, whatever stands in between)
+  if ((V > 1 && x.stride(2) != 1) || (B > 1 && R > 1 && x.stride(0) != R * x.stride(1)))
     refuse("logits: rows must be equally far apart, contiguous over V");
   const int64_t stride = R > 1 ? x.stride(1) : B > 1 ? x.stride(0) : V;
   auto width = [&](int i, const char* name) -> int64_t {  // of a [B, n] array; 0: not given
