@@ -673,8 +673,9 @@ spec_status spec_rotate(const void* q, int64_t q_stride, void* q_out, int64_t q_
  *   type's normal numbers is rounded.  x / scale is rounded to nearest even;
  *   infinities become +-448 * scale, NaN stays NaN.
  *   D in {64,128,256}; Hq, Hkv at most 4096; num_pages * page_size and T below
- *   2^31 - 64; rows, strides and caches 16-byte aligned.  The caches share no memory
- *   with the rows.
+ *   2^31 - 64; rows, strides and caches 16-byte aligned.  Caches and scales share no
+ *   memory with anything else that is passed (K's and V's may lie between one another),
+ *   nor does q_out, but that it may be q with its stride (in place).
  * ---------------------------------------------------------------------- */
 spec_status spec_append_scaled(const void* k_new, int64_t k_stride, const void* v_new,
                                int64_t v_stride, const void* q, int64_t q_stride, void* q_out,
@@ -702,7 +703,8 @@ spec_status spec_read_scaled(const void* k_cache, const void* v_cache, const flo
  * tree move to the next logical prefix, into blocks of other scales, as if
  * spec_append_scaled stored the values they stand for (a block whose first token
  * is among the moved rows begins anew).  Arguments as there; contiguous caches
- * and scales as above.  Pages of one sequence are not another's. */
+ * and scales as above.  Pages of one sequence are not another's.  What is written shares no
+ * memory with what is read: new_len is not ctx_len (SPEC_EINVAL). */
 spec_status spec_commit_scaled(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
                                int num_pages, int page_size, int block, int Hkv, int D,
                                const int32_t* block_table, int max_pages, const int32_t* ctx_len,

@@ -279,7 +279,7 @@ def kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.T
     rows move in place to positions ctx + 1 .. ctx + accepted_len.  parent [B,R]
     (optional) lets the kernel check that the path follows the tree.  For a scaled cache
     (append_scaled) k_scale and v_scale are its scales: rows move between blocks of
-    different ones.  Returns (new_len, keep_pages, status)."""
+    different ones, and new_len must not be ctx_len.  Returns (new_len, keep_pages, status)."""
     lib = load()
     if k_cache.dtype not in (torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn):
         raise ValueError("caches must be bf16, fp16, fp32 or float8_e4m3fn")

@@ -554,6 +554,9 @@ extern "C" spec_status spec_append_scaled(
   if (k_stride < 0 || v_stride < 0 || q_stride < 0 || q_out_stride < 0) return SPEC_EINVAL;
   if (((k_stride | v_stride | (q ? q_stride | q_out_stride : 0)) * 2) & 15) return SPEC_EINVAL;
   if (q && q == q_out && q_stride != q_out_stride) return SPEC_EINVAL;
+  // (K's and V's caches may lie between one another; their scales are contiguous)
+  const size_t scales = (size_t)num_pages * (page_size / block) * Hkv * sizeof(float);
+  if (k_cache == v_cache || share({{k_scale, scales}, {v_scale, scales}}, {})) return SPEC_EINVAL;
   p.k = static_cast<const char*>(k_new);
   p.v = static_cast<const char*>(v_new);
   p.q = static_cast<const char*>(q);
@@ -657,6 +660,14 @@ extern "C" spec_status spec_commit_scaled(void* k_cache, void* v_cache, float* k
   if (B == 0) return SPEC_OK;
   if (!k_cache || !v_cache || !k_scale || !v_scale || !block_table || !ctx_len || !accepted_len ||
       !path || !new_len)
+    return SPEC_EINVAL;
+  // A sequence's lengths are read by the CTAs of all its heads and written by one.
+  const size_t slots = (size_t)num_pages * page_size, seqs = (size_t)B * sizeof(int32_t);
+  const size_t scales = slots / block * Hkv * sizeof(float);
+  if (share({{k_cache, slots * Hkv * D}, {v_cache, slots * Hkv * D}, {k_scale, scales},
+             {v_scale, scales}, {new_len, seqs}, {keep_pages, seqs}, {status_per_seq, seqs}},
+            {{block_table, seqs * max_pages}, {ctx_len, seqs}, {accepted_len, seqs},
+             {path, seqs * R}, {parent, seqs * R}}))
     return SPEC_EINVAL;
   CommitParams p{};
   p.kc = static_cast<char*>(k_cache);

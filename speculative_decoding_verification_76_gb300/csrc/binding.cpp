@@ -357,7 +357,8 @@ const spec_rope* rope_of(PyObject* o, Rope* r) {
 
 // Bytes that a tensor spans, for outputs that must not lie over inputs.
 struct Span {
-  uintptr_t from, to;
+  uintptr_t from = 0, to = 0;
+  Span() = default;
   explicit Span(const Tensor& t) : from((uintptr_t)t.data_ptr()), to(from) {
     if (t.numel() == 0) return;
     int64_t last = 0;
@@ -502,6 +503,22 @@ PyObject* append_scaled(PyObject* const* a) {
     if (!made) out_apart(out, "q_out", a[8], {a[8], a[0], a[1]});
   } else if (given(out)) {
     refuse("q_out without q");
+  }
+  // What is written: caches and scales share memory with nothing else (K's and V's caches may lie
+  // between one another), q_out with none of them nor with slots and positions.
+  Span span[9];
+  for (int i = 0; i < 9; ++i)
+    if (given(a[i])) span[i] = Span(THPVariable_Unpack(a[i]));
+  static const char* const names[4] = {"k_cache", "v_cache", "k_scale", "v_scale"};
+  for (int i = 2; i < 6; ++i)
+    for (int j = 0; j < 9; ++j)
+      if (j != i && !(i < 4 && (j == 2 || j == 3)) && span[i].meets(span[j]))
+        refuse(names[i - 2], " must not share memory with another argument");
+  if (c.k == c.v) refuse("k_cache must not share memory with v_cache");
+  if (qo && !made) {
+    const Span o(THPVariable_Unpack(out));
+    for (int j = 2; j < 8; ++j)
+      if (o.meets(span[j])) refuse("q_out must not share memory with another argument");
   }
   check("spec_append_scaled",
         spec_append_scaled(k, ks, v, vs, q, qs, qo, os, code_of(type), c.k, c.v, c.ks, c.vs,

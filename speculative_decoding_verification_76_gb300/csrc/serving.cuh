@@ -2,6 +2,7 @@
 // append_tokens.cu, decode.cu).
 #pragma once
 #include <atomic>
+#include <initializer_list>
 
 #include "common.cuh"
 
@@ -26,6 +27,26 @@ struct FastDiv {
     return q + (q * d != x);
   }
 };
+
+// Outputs that share memory with an input or with one another, in part or in whole: some
+// blocks would read what others have written.
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+static inline bool meet(const Span& a, const Span& b) {
+  const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
+  return a.at && b.at && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+static inline bool share(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span& o : outs) {
+    for (const Span& i : ins)
+      if (meet(o, i)) return true;
+    for (const Span& other : outs)
+      if (&other != &o && meet(o, other)) return true;
+  }
+  return false;
+}
 
 // SMs of the current device, asked once per device (the query costs host time)
 static inline int sm_count() {

@@ -305,26 +305,6 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const ReleasePa
   }
 }
 
-// Outputs that share memory with an input or with one another, in part or in whole: some
-// blocks would read what others have written.
-struct Span {
-  const void* at;
-  size_t bytes;
-};
-bool meet(const Span& a, const Span& b) {
-  const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
-  return a.at && b.at && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
-}
-bool share(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
-  for (const Span& o : outs) {
-    for (const Span& i : ins)
-      if (meet(o, i)) return true;
-    for (const Span& other : outs)
-      if (&other != &o && meet(o, other)) return true;
-  }
-  return false;
-}
-
 // CTAs of `threads`: a warp per sequence, four rows per thread, at most two per SM
 int grid_for(int B, long long tokens, int threads) {
   const int warps = threads / 32;
