@@ -659,10 +659,13 @@ spec_status spec_rotate(const void* q, int64_t q_stride, void* q_out, int64_t q_
  *
  *   k_new, v_new, q, q_out, slot_map, positions, T: as in spec_append_tokens
  *            (16-bit rows).  rope NULL: no rotation (positions are not read).
- *   Rows of one block stand next to each other (spec_extend_tables' slot_map
- *   does that); of rows that do not, and of rows with the same slot, what is
- *   stored is unspecified.  Rows whose slot is outside 0 .. num_pages *
- *   page_size - 1, or whose position is negative, are skipped whole.
+ *   Rows whose slot is outside 0 .. num_pages * page_size - 1, or (with a rope)
+ *   whose position is negative, are skipped whole.
+ *   Rows of one block stand next to each other, with no skipped row between
+ *   them (spec_extend_tables' slot_map does that; padding belongs behind a
+ *   sequence's rows).  Of blocks whose rows do not, and of rows with the same
+ *   slot, what is stored is unspecified: every run of rows makes the block's
+ *   scale anew, at the same time as the others.
  *   Scales are powers of two.  What a block needs is the smallest 2^k >= 2^-64
  *   with |x| <= 448 * 2^k for all finite x that the call stores to it (keys after
  *   their rotation, in fp32).  A block whose first token is among the rows begins

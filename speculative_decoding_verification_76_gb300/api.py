@@ -669,8 +669,9 @@ def append_scaled(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_map, po
     from what is stored (powers of two; a block whose first token is among the rows
     begins anew, another's scale only grows).  Keys, and q [T, Hq, D] into q_out, turn
     for `positions` as `rope` says (None: not).  A block's rows stand next to each other
-    in the call, as extend_tables' slot_map has them; rows with a slot outside the cache
-    are skipped.  Returns q_out (None without q)."""
+    in the call, as extend_tables' slot_map has them, and not with a skipped row between
+    them: such a block's contents are unspecified.  Rows with a slot outside the cache, or
+    (with a rope) a negative position, are skipped.  Returns q_out (None without q)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return append_scaled(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_map,
