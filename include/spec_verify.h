@@ -613,8 +613,10 @@ spec_status spec_decode_attn(const void* q, int64_t q_stride_b, int64_t q_stride
  *               all of that (NULL: base, scaling and its numbers).
  *   base > 1; factor >= 1; low < high and original_len > 0 (PARTS); dim > 2 (NTK);
  *   freqs finite; magnitude finite.
- * Angles are kept as 64-bit fractions of a turn, so that they are as exact at
- * position 2^31 - 1 as at 1; sine, cosine and the rotation are in fp32.
+ * Angles are kept as 64-bit fractions of a turn, so that taking whole turns off costs
+ * nothing, however far the position.  What is left is the error of the frequencies, which
+ * are doubles, times the position: up to t * 2^-54 of a turn for the fastest pairs (2^-37
+ * at 131072, 2^-23 at 2^31 - 1).  Sine, cosine and the rotation are in fp32.
  * ---------------------------------------------------------------------- */
 enum { SPEC_ROPE_NONE = 0, SPEC_ROPE_LINEAR = 1, SPEC_ROPE_NTK = 2, SPEC_ROPE_PARTS = 3 };
 
