@@ -704,7 +704,8 @@ def verify_attn_scaled(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_l
     Hq as it comes), block row j of sequence b stored at position ctx_len[b] + j; anc_mask
     [B, R] (tree_prepare's) or None for a chain.  With R = 1 it is the attention of single
     tokens (ctx_len: what is stored in front of them; negative: an idle row).  window:
-    each row sees the last `window` tokens of its own text.  Returns (out, lse)."""
+    each row sees the last `window` tokens of its own text.  k_scale: any positive finite
+    numbers; v_scale: 2^-80 to 2^120.  Returns (out, lse)."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return verify_attn_scaled(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_len,

@@ -35,16 +35,18 @@
 // head, batch's positions), cut in tiles of 128 over all SMs on the device, so that ragged batches, one
 // long sequence and captured graphs whose lengths change fill the GPU alike; the cut counts what a
 // sequence's ends cost (8 tiles, 10 for 64 rows: 64 ragged chains 256 -> 244 us, one chain of 8 rows on 8192
-// tokens 24.5 -> 20.5, a chain of 16 on 131072 168 -> 160).  Four warps stream K, V and their scales into a
+// tokens 24.5 -> 20.5, a chain of 16 on 131072 168 -> 163).  Four warps stream K, V and their scales into a
 // ring of stages (16-byte cp.async, zeros where nothing is seen), run ahead over the ends of sequences and
 // make Q's parts behind a segment's first tile; one thread each issues the two products; two groups of four
 // warps take the tiles in turn and turn scores into weights, each with references, sums and an O of its
 // own, so that one tile's chain of waits lies under the other's work.  Sequences cut over several CTAs leave
 // parts, joined by a second kernel in their order, which is set up early.
 //
-// What a tile costs (cycles of a group, at 32 rows with V as it lies): scales 260, the wait for the scores 200,
-// exponents and vote 890, weights 1060, up to the next tile 670; 1590 a tile with both groups, against some 500
-// of tensor-core time.  At 64 rows V's conversion adds 1200 and the weights take 1670: 2500 a tile against 1000.
+// What a tile costs (cycles of a group, at 32 rows with V as it lies): the wait for it 220, scales and who sees
+// it 440, the wait for the scores 240, exponents and vote 950, weights 1000; 2980 with the rest, so 1490 a tile
+// with both groups.  At 64 rows: 190, 510, V's conversion 1100, 150, 1600, 900; 4400, so 2200 a tile.  The products'
+// arithmetic is 320 of the 1490 and 512 of the 2200 at the tensor cores' full rate, as their pipe's counter says
+// (17 and 21 %); N = 64 columns do not reach that rate, and are under way for about twice as long.
 // Issue slots are 42 to 52 % full: it is latency that is left.  Tried: three groups (96 registers a thread: 280 us
 // against 244 for 64 ragged chains), two CTAs an SM (294), conversion by warps of its own beside two copy
 // warps (draft trees 10 % faster, 64 ragged chains 13 % slower), one vote behind the weights instead of
@@ -53,9 +55,10 @@
 // twice the rows in flight (247 against 221).
 //
 // Measured (replays of a captured graph; bf16, 32/8 heads of 128 unless given): 64 ragged chains of 5 rows
-// (540 K positions) 219 us, 5.1 TB/s; one chain of 8 on 8192 tokens 18.5; draft trees of 64 on 4 x 32768, 64/8
-// heads, 543, 506 TFLOP/s; a chain of 16 on 131072, 64/8 heads, fp16, 154; single tokens of 37 sequences, window
-// 1000, 16/4 heads of 64, fp16, 15.5.
+// (540 K positions) 210 us, 5.3 TB/s (218 with weights in two e4m3 parts and one e5m2, of less range); one chain of 8
+// on 8192 tokens 18.5; draft trees of 64 on 4 x 32768, 64/8 heads, 544, 505 TFLOP/s; a chain of 16 on 131072, 64/8
+// heads, fp16, 154; single tokens of 37 sequences, window 1000, 16/4 heads of 64, fp16, 16.0.  (1 to 2 % from one
+// GPU to the next.)
 //
 // What is seen by some rows only (block rows, the edge of a window) gets weight 0 elsewhere; as 0 times a
 // NaN code would be NaN, such tiles' NaN codes of V are zeroed and noted per row.
