@@ -744,7 +744,7 @@ spec_status spec_commit_scaled(void* k_cache, void* v_cache, float* k_scale, flo
  *   Positions past the table, or whose page id is not in [0, num_pages), are not
  *   seen.  What a row does not see does not reach its output, whatever it
  *   holds (NaN codes or scales included).  A row that sees nothing has zeros and
- *   -inf.  A NaN that is seen, or a q that is not finite, makes NaN.
+ *   -inf, if its q is finite.  A NaN that is seen, or a q that is not finite, makes NaN.
  *   scale    softmax scale; <= 0 selects 1/sqrt(D).
  *   out      [B,R,Hq,D] q_dtype; lse_out [B,R,Hq] fp32 natural log (nullable).
  *            Neither shares memory with an input.
